@@ -364,6 +364,147 @@ DT_API dt_status dt_tp_mlp_static_workspace(const dt_dtensor* x, const dt_dtenso
                                             const dt_dtensor* w_down, const dt_dtensor* y, int32_t mode,
                                             int32_t tp_mesh_dim, int32_t* d_status, dt_stream_t stream);
 
+/* ---- between the q/k/v projections and the o projection ----
+ *
+ * These operators take activations as the column-parallel q/k/v projections
+ * leave them: [..., H * head_dim], Shard(-1) on tp (every shard holding whole
+ * heads, else DT_ERR_SHAPE) or Replicate on tp (tp_mesh_dim < 0: Replicate
+ * everywhere), Replicate on the other mesh dims, leading dims collapsible to
+ * one token dim, unit inner stride.  bf16 or fp32; all arithmetic is fp32 and
+ * each result is rounded once.  All heads of all shards run in one launch.
+ * Outputs must not have materialised replicas.
+ */
+
+/*
+ * Norms of queries and keys for each head, with the position rotation:
+ *   z = x / sqrt(mean(x^2) + eps) * weight       (per token and head)
+ *   y = z with its first R channels rotated by the angles of row
+ *       positions[t] of cos_sin
+ *   q, k       [..., Hq * head_dim], [..., Hk * head_dim]; k may be NULL
+ *   q_weight, k_weight  [head_dim] Replicate, bf16 or fp32; NULL: no norm
+ *   cos_sin    fp32 [rows, R] Replicate: R/2 cosines, then R/2 sines; R even,
+ *              at most head_dim; NULL (with positions NULL): no rotation
+ *   positions  int32 Replicate, one per token; a position outside
+ *              [0, rows) zero-fills its token's outputs and sets
+ *              DT_DEV_ERR_INDEX
+ *   interleaved  0: channel i is paired with i + R/2; else 2i with 2i + 1
+ *   q_out, k_out  shape and dtype of q and k
+ * head_dim 2 .. 1024.  Heads of a multiple of 16 channels (rotations too) on
+ * 16-byte boundaries run on a vector kernel, all others on a kernel of one
+ * element per lane.
+ */
+DT_API dt_status dt_tp_qk_norm_rope(const dt_dtensor* q, const dt_dtensor* k, const dt_dtensor* q_weight,
+                                    const dt_dtensor* k_weight, const dt_dtensor* cos_sin,
+                                    const dt_dtensor* positions, const dt_dtensor* q_out, const dt_dtensor* k_out,
+                                    int32_t head_dim, float eps, int32_t interleaved, int32_t tp_mesh_dim,
+                                    int32_t* d_status, dt_stream_t stream);
+
+/*
+ * Its gradients: from dq_out, dk_out (gradients of q_out, k_out) and the
+ * forward's inputs,
+ *   dq, dk                 gradients of q and k (shape and dtype of q, k)
+ *   dq_weight, dk_weight   [head_dim] Replicate, bf16 or fp32: summed over all
+ *                          tokens and the heads of all shards, in an order
+ *                          fixed by the shapes (the same inputs give the same
+ *                          bits); given exactly where the weight is
+ * Tokens whose position is out of range get dq = dk = 0 and add nothing.
+ * workspace: 256-byte aligned device memory of the queried size for the
+ * weights' partial sums (not needed without weights).
+ */
+DT_API dt_status dt_tp_qk_norm_rope_backward(const dt_dtensor* dq_out, const dt_dtensor* dk_out, const dt_dtensor* q,
+                                             const dt_dtensor* k, const dt_dtensor* q_weight,
+                                             const dt_dtensor* k_weight, const dt_dtensor* cos_sin,
+                                             const dt_dtensor* positions, const dt_dtensor* dq, const dt_dtensor* dk,
+                                             const dt_dtensor* dq_weight, const dt_dtensor* dk_weight,
+                                             int32_t head_dim, float eps, int32_t interleaved, int32_t tp_mesh_dim,
+                                             void* workspace, size_t workspace_bytes, int32_t* d_status,
+                                             dt_stream_t stream);
+DT_API dt_status dt_tp_qk_norm_rope_backward_workspace_size(int32_t head_dim, size_t* bytes);
+
+/*
+ * The paged cache of keys and values in 4 bits: int32
+ * [pages, kv heads, page_size, words], Shard(1) on tp (or Replicate), with
+ * words = dt_kv4_record_words(head_dim, group); head_dim 64, 128 or 256 in
+ * groups of 32 or 64 channels.  The record of one token and kv head:
+ *   head_dim/8 words      key codes, nibble i of word w = channel 8 w + i
+ *   head_dim/8 words      value codes
+ *   head_dim/group words  key parameters, one per group: bf16 step in the
+ *                         low half, bf16 minimum in the high half
+ *   head_dim/group words  value parameters
+ *   padding to a multiple of 4 words
+ * A code c stands for minimum + c * step.  Page and head strides are free
+ * (multiples of 16 bytes); the records of a page and head are contiguous.
+ *
+ * The batch, shared by dt_tp_kv4_append and dt_tp_kv4_attention, all int32
+ * and Replicate:
+ *   page_table [batch, n]     page of keys [i * page_size, (i + 1) * page_size)
+ *   kv_lens    [batch]        keys of each sequence, the new tokens included
+ *   q_starts   [batch + 1]    rows [q_starts[b], q_starts[b + 1]) of the
+ *                             activations are sequence b's new tokens; NULL:
+ *                             the same number for each sequence
+ * They are read on the device, at the call's turn in its stream: a captured
+ * graph replays with new lengths and pages.  New token i of n is key number
+ * kv_len - n + i, which is also its position.  Lengths beyond the page table
+ * are clamped to it, entries of the page table that are used but are no page
+ * are skipped; both set DT_DEV_ERR_INDEX.  Rows of no sequence are not
+ * written.
+ */
+DT_API dt_status dt_kv4_record_words(int32_t head_dim, int32_t group, int32_t* words);
+
+/*
+ * Append: the new tokens' keys (rotated) and values into the cache, and the
+ * rotated queries into q_out.
+ *   k, v       [..., Hkv * head_dim], Hkv = the cache's heads
+ *   cos_sin    as in dt_tp_qk_norm_rope, R a multiple of 16; NULL: no
+ *              rotation (keys that are rotated already)
+ *   q, q_out   [..., Hq * head_dim] or both NULL
+ *   k_stored, v_stored  shape and dtype of k, or both NULL: the keys and
+ *              values as the cache now holds them, for a prompt whose own
+ *              tokens attend to each other outside the cache
+ * Per group of a rotated key or a value, in fp32, each operation rounded on
+ * its own:
+ *   minimum = bf16(min), step = bf16((max - min) * fp32(1/15)),
+ *   code = clamp(rint((x - minimum) * (1 / step)), 0, 15)
+ * A step below the least normal fp32 number gives codes 0; a group with a
+ * value, minimum or step that is not finite is held as NaN.  Tokens whose
+ * position lies outside cos_sin are not stored and get zeros in q_out.
+ * Rows of k, v, q and the outputs must be 16-byte aligned (DT_ERR_ALIGNMENT).
+ */
+DT_API dt_status dt_tp_kv4_append(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor* cache,
+                                  const dt_dtensor* page_table, const dt_dtensor* kv_lens, const dt_dtensor* q_starts,
+                                  const dt_dtensor* cos_sin, const dt_dtensor* q, const dt_dtensor* q_out,
+                                  const dt_dtensor* k_stored, const dt_dtensor* v_stored, int32_t head_dim,
+                                  int32_t group, int32_t interleaved, int32_t tp_mesh_dim, int32_t* d_status,
+                                  dt_stream_t stream);
+
+/*
+ * Attention of each sequence's new tokens over its keys in the cache:
+ *   out = softmax(scale * q K^T + mask) V, query head h on kv head h / (Hq / Hkv)
+ *   q     [..., Hq * head_dim], Hq a multiple of the cache's heads
+ *   out   shape and dtype of q
+ *   lse   fp32 [..., Hq], sharded like q's heads, or NULL: the logarithm of
+ *         the softmax's denominator (natural, scale included)
+ *   causal  0: every key of the sequence; else keys at or before the query's
+ *         position; window > 0 (causal only): of those the last `window`
+ * A query that sees no key gets out = 0 and lse = -inf.  Whatever the hidden
+ * keys, or places of the pages beyond a sequence's length, hold (infinities
+ * and NaN too) does not reach the result.
+ * The softmax and all sums are fp32; for bf16 activations the probabilities
+ * times the value steps are rounded to bf16 before their product (fp32
+ * activations: three bf16 parts, 24 bits).
+ * workspace: 256-byte aligned device memory of the queried size, which
+ * depends on the current device; its contents between calls are the
+ * caller's.  Waits for copies are bounded (DT_DEV_ERR_TIMEOUT).
+ */
+DT_API dt_status dt_tp_kv4_attention(const dt_dtensor* q, const dt_dtensor* cache, const dt_dtensor* page_table,
+                                     const dt_dtensor* kv_lens, const dt_dtensor* q_starts, const dt_dtensor* out,
+                                     const dt_dtensor* lse, int32_t head_dim, int32_t group, float scale,
+                                     int32_t causal, int32_t window, int32_t tp_mesh_dim, void* workspace,
+                                     size_t workspace_bytes, int32_t* d_status, dt_stream_t stream);
+DT_API dt_status dt_tp_kv4_attention_workspace_size(const dt_dtensor* q, const dt_dtensor* cache,
+                                                    const dt_dtensor* page_table, int32_t head_dim, int32_t group,
+                                                    int32_t tp_mesh_dim, size_t* bytes);
+
 /* ---- utilities ---- */
 
 /* Static description of a status code. */

@@ -59,6 +59,8 @@ EXPORTS = [
     "dt_tp_mlp_workspace_size", "dt_tp_mlp", "dt_status_string",
     "dt_last_error", "dt_read_device_status", "dt_clear_cache", "dt_version", "dt_launch_count",
     "dt_cuda_core_gemm_count", "dt_tp_mlp_static_workspace",
+    "dt_tp_qk_norm_rope", "dt_tp_qk_norm_rope_backward", "dt_tp_qk_norm_rope_backward_workspace_size",
+    "dt_kv4_record_words", "dt_tp_kv4_append", "dt_tp_kv4_attention", "dt_tp_kv4_attention_workspace_size",
 ]
 
 _lib = None
@@ -110,6 +112,16 @@ def load(path: str = LIB_PATH) -> C.CDLL:
             "dt_launch_count": (C.c_uint64, []),
             "dt_cuda_core_gemm_count": (C.c_uint64, []),
             "dt_tp_mlp_static_workspace": (st, [D, D, D, D, D, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
+            "dt_tp_qk_norm_rope": (st, [D] * 8 + [C.c_int32, C.c_float, C.c_int32, C.c_int32, C.c_void_p,
+                                                  C.c_void_p]),
+            "dt_tp_qk_norm_rope_backward": (st, [D] * 12 + [C.c_int32, C.c_float, C.c_int32, C.c_int32, C.c_void_p,
+                                                            C.c_size_t, C.c_void_p, C.c_void_p]),
+            "dt_tp_qk_norm_rope_backward_workspace_size": (st, [C.c_int32, P(C.c_size_t)]),
+            "dt_kv4_record_words": (st, [C.c_int32, C.c_int32, P(C.c_int32)]),
+            "dt_tp_kv4_append": (st, [D] * 11 + [C.c_int32] * 4 + [C.c_void_p, C.c_void_p]),
+            "dt_tp_kv4_attention": (st, [D] * 7 + [C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_int32, C.c_int32,
+                                                   C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
+            "dt_tp_kv4_attention_workspace_size": (st, [D] * 3 + [C.c_int32] * 3 + [P(C.c_size_t)]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)

@@ -527,6 +527,139 @@ def tp_attention_projections(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, 
     return o, q, k, v
 
 
+# ---------------------------------------------------------------- between q/k/v and o
+
+def _ref(t: Optional[DTensor]):
+    """A descriptor argument (NULL for None); the DTensor keeps the descriptor alive."""
+    return None if t is None else C.byref(t._desc())
+
+
+def _like(t: DTensor, dtype=None) -> DTensor:
+    return DTensor.empty(t.mesh, t.placements, t.gshape, dtype or t.dtype, device=t.slots[0].device)
+
+
+def tp_qk_norm_rope(q: DTensor, k: Optional[DTensor] = None, q_weight: Optional[DTensor] = None,
+                    k_weight: Optional[DTensor] = None, cos_sin: Optional[DTensor] = None,
+                    positions: Optional[DTensor] = None, *, head_dim: int, eps: float = 1e-6,
+                    interleaved: bool = False, tp_dim="tp", out=None):
+    """Per head: x / sqrt(mean(x^2) + eps) * weight, then the position rotation, in one launch.
+
+    q, k [..., heads * head_dim] as the q/k/v projections leave them; weights
+    [head_dim] (None: no norm); cos_sin fp32 [rows, rotary], cosines then
+    sines, with int32 ``positions`` per token (both None: no rotation).
+    Returns (q_out, k_out); ``out`` = (q_out, k_out) to write into."""
+    qo, ko = out if out is not None else (_like(q), None if k is None else _like(k))
+    L.check(L.load().dt_tp_qk_norm_rope(_ref(q), _ref(k), _ref(q_weight), _ref(k_weight), _ref(cos_sin),
+                                        _ref(positions), _ref(qo), _ref(ko), head_dim, eps, int(interleaved),
+                                        _tp_index(q.mesh, tp_dim), None, _stream_handle()), "tp_qk_norm_rope")
+    return qo, ko
+
+
+def tp_qk_norm_rope_backward_workspace_bytes(q: DTensor, k: Optional[DTensor] = None, *, head_dim: int) -> int:
+    """dt_tp_qk_norm_rope_backward_workspace_size (it depends on head_dim alone)."""
+    n = C.c_size_t()
+    L.check(L.load().dt_tp_qk_norm_rope_backward_workspace_size(head_dim, C.byref(n)),
+            "tp_qk_norm_rope_backward_workspace_size")
+    return n.value
+
+
+def tp_qk_norm_rope_backward(dq_out: DTensor, dk_out: Optional[DTensor], q: DTensor, k: Optional[DTensor] = None,
+                             q_weight: Optional[DTensor] = None, k_weight: Optional[DTensor] = None,
+                             cos_sin: Optional[DTensor] = None, positions: Optional[DTensor] = None, *,
+                             head_dim: int, eps: float = 1e-6, interleaved: bool = False, tp_dim="tp", out=None,
+                             workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``tp_qk_norm_rope`` from those of its outputs and its inputs.
+
+    Returns (dq, dk, dq_weight, dk_weight), None where the operand is; the
+    weights' gradients (in their weight's dtype) are sums over all tokens and
+    the heads of all shards.  ``out``: the four to write into."""
+    if out is None:
+        out = (_like(q), None if k is None else _like(k), None if q_weight is None else _like(q_weight),
+               None if k_weight is None else _like(k_weight))
+    if workspace is None and (q_weight is not None or k_weight is not None):
+        workspace = _workspace(tp_qk_norm_rope_backward_workspace_bytes(q, k, head_dim=head_dim), q.slots[0].device)
+    L.check(L.load().dt_tp_qk_norm_rope_backward(
+        _ref(dq_out), _ref(dk_out), _ref(q), _ref(k), _ref(q_weight), _ref(k_weight), _ref(cos_sin), _ref(positions),
+        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), head_dim, eps, int(interleaved),
+        _tp_index(q.mesh, tp_dim), *_ws_args(workspace), None, _stream_handle()), "tp_qk_norm_rope_backward")
+    return tuple(out)
+
+
+def kv4_record_words(head_dim: int, group: int = 64) -> int:
+    """int32 words of one token's record in the 4-bit cache (dt_kv4_record_words)."""
+    n = C.c_int32()
+    L.check(L.load().dt_kv4_record_words(head_dim, group, C.byref(n)), "kv4_record_words")
+    return n.value
+
+
+def kv4_cache(mesh: DeviceMesh, pages: int, kv_heads: int, page_size: int, *, head_dim: int, group: int = 64,
+              tp_dim="tp", device=None) -> DTensor:
+    """A paged 4-bit cache for ``tp_kv4_append`` and ``tp_kv4_attention``: int32
+    [pages, kv_heads, page_size, words], heads sharded on tp, not initialised."""
+    pls = [Replicate()] * mesh.ndim
+    tp = _tp_index(mesh, tp_dim)
+    if tp >= 0:
+        pls[tp] = Shard(1)
+    return DTensor.empty(mesh, pls, (pages, kv_heads, page_size, kv4_record_words(head_dim, group)), torch.int32,
+                         device=device)
+
+
+def tp_kv4_append(k: DTensor, v: DTensor, cache: DTensor, page_table: DTensor, kv_lens: DTensor,
+                  q_starts: Optional[DTensor] = None, *, q: Optional[DTensor] = None,
+                  cos_sin: Optional[DTensor] = None, head_dim: int, group: int = 64, interleaved: bool = False,
+                  tp_dim="tp", q_out: Optional[DTensor] = None, stored=None) -> Optional[DTensor]:
+    """Write the new tokens' keys (rotated by ``cos_sin``) and values into the
+    paged 4-bit cache, and return the rotated queries (None without ``q``).
+
+    ``kv_lens`` count the new tokens; ``q_starts`` [batch + 1] delimit each
+    sequence's rows (None: the same number each).  ``stored`` = (k, v) outputs
+    that receive the keys and values as the cache holds them."""
+    if q is not None and q_out is None:
+        q_out = _like(q)
+    ks, vs = stored if stored is not None else (None, None)
+    L.check(L.load().dt_tp_kv4_append(_ref(k), _ref(v), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
+                                      _ref(cos_sin), _ref(q), _ref(q_out), _ref(ks), _ref(vs), head_dim, group,
+                                      int(interleaved), _tp_index(k.mesh, tp_dim), None, _stream_handle()),
+            "tp_kv4_append")
+    return q_out
+
+
+def tp_kv4_attention_workspace_bytes(q: DTensor, cache: DTensor, page_table: DTensor, *, head_dim: int,
+                                     group: int = 64, tp_dim="tp") -> int:
+    """dt_tp_kv4_attention_workspace_size, for the current device."""
+    tp = _tp_index(q.mesh, tp_dim)
+
+    def query():
+        n = C.c_size_t()
+        L.check(L.load().dt_tp_kv4_attention_workspace_size(_ref(q), _ref(cache), _ref(page_table), head_dim, group,
+                                                            tp, C.byref(n)), "tp_kv4_attention_workspace_size")
+        return n.value
+
+    return _ws_size(_op_key("kv4_attention", [q, cache, page_table], head_dim, group, tp), query)
+
+
+def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: DTensor,
+                     q_starts: Optional[DTensor] = None, *, head_dim: int, group: int = 64,
+                     scale: Optional[float] = None, causal: bool = True, window: int = 0, tp_dim="tp",
+                     out: Optional[DTensor] = None, lse: Optional[DTensor] = None,
+                     workspace: Optional[torch.Tensor] = None) -> DTensor:
+    """Attention of each sequence's new tokens (its last keys' queries) over its
+    keys in the 4-bit cache; ``scale`` defaults to head_dim ** -0.5.
+
+    ``window`` > 0 keeps the last ``window`` keys of each query; ``lse`` (fp32
+    [..., heads]) receives the log of the softmax's denominator."""
+    y = out if out is not None else _like(q)
+    if workspace is None:
+        workspace = _workspace(tp_kv4_attention_workspace_bytes(q, cache, page_table, head_dim=head_dim, group=group,
+                                                                tp_dim=tp_dim), q.slots[0].device)
+    L.check(L.load().dt_tp_kv4_attention(_ref(q), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
+                                         _ref(y), _ref(lse), head_dim, group,
+                                         head_dim ** -0.5 if scale is None else scale, int(causal), window,
+                                         _tp_index(q.mesh, tp_dim), *_ws_args(workspace), None, _stream_handle()),
+            "tp_kv4_attention")
+    return y
+
+
 # ---------------------------------------------------------------- DTorch-style layers
 
 class Linear:

@@ -1,0 +1,102 @@
+// Device helpers shared by the kernels on attention heads: bf16 and fp32
+// vectors of 8 channels, the rotation of one pair, and the sequence that a
+// token of a ragged batch belongs to.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "head_operands.h"
+
+namespace dt {
+
+// 8 consecutive channels (16-byte aligned) as fp32, and back with one
+// rounding.  Activations are read once and outputs written once, so both
+// use the streaming cache hint.
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                                                 pack_bf16(v[6], v[7])));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
+}
+// The same from a table that many warps re-read.
+__device__ __forceinline__ void load8_keep(const float* p, float (&v)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_f32(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_f32(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// The pair (a, b) turned by the angle with cosine c and sine s.  Products
+// and sums round one by one, never fused: the 4-bit codes of a rotated key
+// are then a function of the formula alone, not of the compiler's choice of
+// fused multiply-adds.
+__device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s) {
+  const float x = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
+  b = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
+  a = x;
+}
+
+// A batch of sequences with new tokens: sequence b's are rows
+// [q_starts[b], q_starts[b + 1]) of the activations (without q_starts, each
+// sequence has q_len of them) and its keys, the new ones included, number
+// kv_lens[b].  Every value read from the device is clamped to what the
+// operands hold, so no length can send a kernel out of bounds.
+struct SeqTable {
+  const int32_t* q_starts;  // NULL: q_len rows each
+  const int32_t* kv_lens;
+  int32_t batch, q_len, tokens;
+  int32_t capacity;  // keys one page table row can address
+
+  __device__ __forceinline__ int start(int b) const {
+    if (!q_starts) return b * q_len;
+    return min(max(__ldg(q_starts + b), 0), tokens);
+  }
+  __device__ __forceinline__ int keys(int b) const { return min(max(__ldg(kv_lens + b), 0), capacity); }
+};
+
+// Sequence of token t (all lanes of a converged warp call this with one t):
+// the last b with start(b) <= t, found 32 candidates a step.  Returns -1 for
+// tokens before the first or after the last sequence.
+__device__ __forceinline__ int warp_seq_of_token(const SeqTable& s, int t, int lane) {
+  if (!s.q_starts) {
+    const int b = t / s.q_len;
+    return b < s.batch ? b : -1;
+  }
+  int lo = 0, n = s.batch + 1;  // candidates lo .. lo + n - 1 (entry `batch` is the end)
+  while (n > 1) {
+    const int step = (n + 31) / 32;
+    const int at = lane * step;
+    const bool le = at < n && s.start(lo + at) <= t;
+    const unsigned m = __ballot_sync(0xffffffffu, le);
+    if (m == 0) return -1;
+    const int top = 31 - __clz(m);
+    lo += top * step;
+    n = min(step, n - top * step);
+  }
+  return (lo < s.batch && s.start(lo) <= t) ? lo : -1;
+}
+
+}  // namespace dt

@@ -1,0 +1,57 @@
+// Host and device description of one attention call over the 4-bit cache.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "heads_sm103.cuh"
+#include "kv4.h"
+
+namespace dt {
+namespace kv4 {
+
+constexpr int WARPS = 4;             // each takes every fourth tile of 32 keys
+constexpr int THREADS = 32 * WARPS;
+constexpr int TILE = 32;             // keys of a warp's tile
+constexpr int BLOCK = TILE * WARPS;  // keys of a unit of the schedule
+
+// What a CTA left unfinished: the unit whose keys begin in its range and end
+// in CTA `last`'s (unit < 0: none).  The join kernel adds those pieces.
+struct Split {
+  int32_t unit;  // >= 0: the row block below is split
+  int32_t q_row; // first (query, head) row of the block
+  int32_t rows;  // rows of the block
+  int32_t q0;    // first token of the sequence
+  int32_t head;  // kv head
+  int32_t last;  // CTA that holds the last piece
+};
+
+struct AttnParams {
+  HeadMap q, out, lse;
+  CacheMap cache;
+  SeqTable seq;
+  const int32_t* page_table;
+  int32_t table_width;
+  int32_t g;  // query heads per kv head
+  int32_t causal, window;
+  int32_t want_lse;
+  float scale_log2;  // softmax scale * log2(e)
+  float* part;       // [2 CTAs][rows][D + 2]: sums, then maximum (log2 units) and denominator
+  Split* split;      // [CTA]
+  int32_t* status;
+  unsigned long long wait_limit_ns;
+};
+
+// Grid of the device-filling launch, rows of a unit and workspace of one
+// variant; and its launch (defined per head_dim).
+struct Variant {
+  int grid = 0;
+  int rows = 0;
+  size_t bytes = 0;
+};
+template <int D>
+cudaError_t variant(int G, bool fp32, int64_t rows_per_seq, Variant* out);
+template <int D>
+cudaError_t launch(const AttnParams& p, int G, bool fp32, int64_t rows_per_seq, int grid, cudaStream_t s);
+
+}  // namespace kv4
+}  // namespace dt

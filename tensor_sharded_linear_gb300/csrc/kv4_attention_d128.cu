@@ -1,0 +1,13 @@
+// The attention kernels over the 4-bit cache for heads of 128 channels.
+#include <exception>
+
+#include "kv4_attention.cuh"
+
+namespace dt {
+namespace kv4 {
+
+template cudaError_t variant<128>(int, bool, int64_t, Variant*);
+template cudaError_t launch<128>(const AttnParams&, int, bool, int64_t, int, cudaStream_t);
+
+}  // namespace kv4
+}  // namespace dt

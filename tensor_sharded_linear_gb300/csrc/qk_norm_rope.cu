@@ -1,0 +1,576 @@
+// Norms of queries and keys for each head with the position rotation in the
+// same pass, and their backward pass.
+//
+// Per head of D channels and token t (all sums in fp32):
+//   r = 1 / sqrt(mean(x^2) + eps)        z = x * r * w        y = R(pos_t) z
+// and, for a gradient dy of y,
+//   dz = R(pos_t)^T dy      dw = sum over tokens and heads of dz * x * r
+//   g = dz * w              dx = r * (g - x r * mean(g * x r))
+// R(pos) turns the pairs (i, i + R/2), or (2i, 2i + 1) when interleaved, of
+// the first R channels by the angles of row pos of the cos/sin table.
+//
+// Both passes are bound by memory: the forward reads and writes each element
+// once, the backward reads x and dy and writes dx.
+//
+// Layout.  A head's channels are cut into chunks of 8.  A lane holds two
+// chunks of a head -- the two partners of a rotation, chunk l and chunk
+// l + R/16, so a pair never crosses lanes -- and D/16 lanes hold the head:
+// each access is 16 bytes (bf16), 128 contiguous bytes per 8 lanes.  A warp
+// takes heads of ONE token, so its cos/sin vectors are loaded once and stay
+// in registers, and a CTA takes one tensor (q or k), so the weights do too.
+// The heads a warp takes together (U per lane) put their loads in flight
+// before the first is used.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "heads_sm103.cuh"
+
+namespace dt {
+namespace {
+
+constexpr int NR_THREADS = 256;
+constexpr int NR_WARPS = NR_THREADS / 32;
+constexpr int NR_MAX_D = 1024;
+
+struct NormParams {
+  HeadMap x[2];         // q and k as they came
+  HeadMap y[2];         // forward: the outputs; backward: dx
+  HeadMap g[2];         // backward: dy
+  const void* w[2];     // NULL: no norm
+  void* dw[2];
+  int32_t w_dtype[2], dw_dtype[2];
+  const float* cos_sin;  // [table_rows, rotary]: cosines then sines; NULL: no rotation
+  const int32_t* pos;
+  int64_t table_rows;
+  int64_t tokens;
+  int32_t D, rotary, interleaved;
+  int32_t blocks_q;  // CTAs [0, blocks_q) work on q, the others on k
+  float eps;
+  float* part;  // backward: [CTA][D] sums of dw
+  int32_t* status;
+};
+
+__device__ __forceinline__ float load_w(const void* w, int dtype, int i) {
+  return dtype == DT_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i])
+                          : static_cast<const float*>(w)[i];
+}
+
+// Row of the cos/sin table for token t, or -1 (and the status bit) when its
+// position lies outside the table.
+__device__ __forceinline__ int64_t table_row(const NormParams& p, int64_t t, bool report) {
+  const int32_t r = __ldg(p.pos + t);
+  if (r >= 0 && r < p.table_rows) return r;
+  if (report) atomicOr(p.status, DT_DEV_ERR_INDEX);
+  return -1;
+}
+
+// Adds the CTA's sums of dw (acc: [NR_WARPS][D] in shared memory) in warp
+// order and writes them to this CTA's row of the workspace.
+__device__ __forceinline__ void write_dw_part(const NormParams& p, const float* acc) {
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.D; c += NR_THREADS) {
+    float s = acc[c];
+    for (int w = 1; w < NR_WARPS; ++w) s += acc[w * p.D + c];
+    p.part[(int64_t)blockIdx.x * p.D + c] = s;
+  }
+}
+
+template <class T>
+struct Raw8;  // 8 channels as loaded
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <>
+struct Raw8<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+};
+
+// D and rotary multiples of 16, D <= 512, 16-byte aligned heads.
+template <class T, bool BWD, int U>
+__global__ void __launch_bounds__(NR_THREADS) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ float nr_acc[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = p.D / 16;
+  int LP = 1;
+  while (LP < L) LP <<= 1;
+  const int SG = 32 / LP, sub = lane / LP, l = lane & (LP - 1);
+  const bool act = l < L;
+  const int which = blockIdx.x >= p.blocks_q;
+  const HeadMap &X = p.x[which], &Y = p.y[which], &G = p.g[which];
+  const int rl = p.cos_sin ? p.rotary / 16 : 0;  // lanes that hold rotated pairs
+  const bool rot = l < rl;
+  int ca, cb;  // first channels of the lane's two chunks
+  if (p.interleaved || !p.cos_sin) {
+    ca = 16 * l, cb = ca + 8;
+  } else if (rot) {
+    ca = 8 * l, cb = 8 * (l + rl);
+  } else {
+    ca = 16 * l, cb = ca + 8;  // 2 rl chunks are rotated, so chunk 2 l of the rest
+  }
+  const bool norm = p.w[which] != nullptr;
+  float wa[8], wb[8], da[8], db[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    wa[i] = norm && act ? load_w(p.w[which], p.w_dtype[which], ca + i) : 1.f;
+    wb[i] = norm && act ? load_w(p.w[which], p.w_dtype[which], cb + i) : 1.f;
+    da[i] = db[i] = 0.f;
+  }
+  const int nb = (X.heads + SG * U - 1) / (SG * U);
+  const int64_t units = p.tokens * nb;
+  const int64_t first = (int64_t)(which ? blockIdx.x - p.blocks_q : blockIdx.x) * NR_WARPS + warp;
+  const int64_t step = (int64_t)(which ? gridDim.x - p.blocks_q : p.blocks_q) * NR_WARPS;
+  const float inv_d = 1.f / (float)p.D;
+  for (int64_t u = first; u < units; u += step) {
+    const int64_t t = u / nb;
+    const int h0 = (int)(u - t * nb) * (SG * U) + sub;
+    Raw8<T> xa[U], xb[U], ga[BWD ? U : 1], gb[BWD ? U : 1];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (act && h0 + i * SG < X.heads) {
+        const T* x = head_ptr<T>(X, t, h0 + i * SG, p.D);
+        xa[i].load(x + ca);
+        xb[i].load(x + cb);
+        if (BWD) {
+          const T* g = head_ptr<T>(G, t, h0 + i * SG, p.D);
+          ga[i].load(g + ca);
+          gb[i].load(g + cb);
+        }
+      }
+    }
+    float c8[8], s8[8];
+    bool ok = true;
+    if (p.cos_sin) {
+      const int64_t row = table_row(p, t, lane == 0);
+      ok = row >= 0;
+      if (rot && ok) {
+        load8_keep(p.cos_sin + row * p.rotary + 8 * l, c8);
+        load8_keep(p.cos_sin + row * p.rotary + p.rotary / 2 + 8 * l, s8);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int h = h0 + i * SG;
+      const bool on = act && h < X.heads;
+      float a[8], b[8], dya[8], dyb[8];
+      if (on) {
+        xa[i].get(a);
+        xb[i].get(b);
+        if (BWD) ga[i].get(dya), gb[i].get(dyb);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = b[e] = dya[e] = dyb[e] = 0.f;
+      }
+      if (BWD && rot && ok) {  // dz = R^T dy
+        if (p.interleaved) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            rotate_pair(dya[2 * e], dya[2 * e + 1], c8[e], -s8[e]);
+            rotate_pair(dyb[2 * e], dyb[2 * e + 1], c8[4 + e], -s8[4 + e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) rotate_pair(dya[e], dyb[e], c8[e], -s8[e]);
+        }
+      }
+      float r = 1.f, gx = 0.f;
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          ss += a[e] * a[e] + b[e] * b[e];
+          if (BWD) gx += dya[e] * wa[e] * a[e] + dyb[e] * wb[e] * b[e];
+        }
+        for (int o = LP >> 1; o; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (BWD) gx += __shfl_xor_sync(0xffffffffu, gx, o);
+        }
+        r = rsqrtf(ss * inv_d + p.eps);
+      }
+      if (!on) continue;
+      T* y = head_ptr<T>(Y, t, h, p.D);
+      if (BWD) {
+        const float k = gx * r * inv_d;  // mean of g * x r
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float na = a[e] * r, nb_ = b[e] * r;
+          if (norm && ok) {
+            da[e] += dya[e] * na;
+            db[e] += dyb[e] * nb_;
+            a[e] = r * (dya[e] * wa[e] - na * k);
+            b[e] = r * (dyb[e] * wb[e] - nb_ * k);
+          } else {
+            a[e] = dya[e];
+            b[e] = dyb[e];
+          }
+        }
+      } else {
+        if (norm) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            a[e] = a[e] * r * wa[e];
+            b[e] = b[e] * r * wb[e];
+          }
+        }
+        if (rot) {
+          if (p.interleaved) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              rotate_pair(a[2 * e], a[2 * e + 1], c8[e], s8[e]);
+              rotate_pair(b[2 * e], b[2 * e + 1], c8[4 + e], s8[4 + e]);
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) rotate_pair(a[e], b[e], c8[e], s8[e]);
+          }
+        }
+      }
+      if (!ok) {  // no such position: the row is zero, as an embedding row of a bad id
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;
+      }
+      store8(y + ca, a);
+      store8(y + cb, b);
+    }
+  }
+  if (BWD && p.part) {
+    // the subgroups' sums, then the warps', in a fixed order: the same
+    // inputs give the same bits
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      for (int o = LP; o < 32; o <<= 1) {
+        da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
+        db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+      }
+    }
+    if (act && sub == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        nr_acc[warp * p.D + ca + e] = da[e];
+        nr_acc[warp * p.D + cb + e] = db[e];
+      }
+    }
+    write_dw_part(p, nr_acc);
+  }
+}
+
+// Any even rotary <= D <= NR_MAX_D and any alignment: a warp per head, a lane
+// per pair of channels, 32 pairs a step (the second look at the head comes
+// from L1).
+template <class T, bool BWD>
+__global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_constant__ NormParams p) {
+  extern __shared__ float nr_acc[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int which = blockIdx.x >= p.blocks_q;
+  const HeadMap &X = p.x[which], &Y = p.y[which], &G = p.g[which];
+  const bool norm = p.w[which] != nullptr;
+  float* acc = nr_acc + warp * p.D;
+  if (BWD && p.part)
+    for (int c = lane; c < p.D; c += 32) acc[c] = 0.f;
+  __syncwarp();
+  const int half = p.cos_sin ? p.rotary / 2 : 0;
+  const int pairs = (p.D + 1) / 2;  // rotated pairs first; of the rest, channels 2j and 2j + 1
+  const float inv_d = 1.f / (float)p.D;
+  const int64_t units = p.tokens * X.heads;
+  const int64_t first = (int64_t)(which ? blockIdx.x - p.blocks_q : blockIdx.x) * NR_WARPS + warp;
+  const int64_t step = (int64_t)(which ? gridDim.x - p.blocks_q : p.blocks_q) * NR_WARPS;
+  for (int64_t u = first; u < units; u += step) {
+    const int64_t t = u / X.heads;
+    const int h = (int)(u - t * X.heads);
+    const T* x = head_ptr<T>(X, t, h, p.D);
+    const T* g = BWD ? head_ptr<T>(G, t, h, p.D) : nullptr;
+    T* y = head_ptr<T>(Y, t, h, p.D);
+    const int64_t row = p.cos_sin ? table_row(p, t, lane == 0) : 0;
+    const bool ok = row >= 0;
+    const float* cs = p.cos_sin ? p.cos_sin + (ok ? row : 0) * p.rotary : nullptr;
+    float ss = 0.f, gx = 0.f, r = 1.f, k = 0.f;
+    for (int pass = norm ? 0 : 1; pass < 2; ++pass) {
+      for (int j = lane; j < pairs; j += 32) {
+        const bool rot = j < half;
+        const int ia = rot && !p.interleaved ? j : 2 * j, ib = rot && !p.interleaved ? j + half : 2 * j + 1;
+        const bool two = ib < p.D;
+        float a = to_f32(x[ia]), b = two ? to_f32(x[ib]) : 0.f, ya = 0.f, yb = 0.f;
+        const float wa = norm ? load_w(p.w[which], p.w_dtype[which], ia) : 1.f;
+        const float wb = norm && two ? load_w(p.w[which], p.w_dtype[which], ib) : 1.f;
+        if (BWD) {
+          ya = to_f32(g[ia]), yb = two ? to_f32(g[ib]) : 0.f;
+          if (rot && ok) rotate_pair(ya, yb, __ldg(cs + j), -__ldg(cs + half + j));
+        }
+        if (pass == 0) {
+          ss += a * a + b * b;
+          if (BWD) gx += ya * wa * a + yb * wb * b;
+          continue;
+        }
+        const float na = a * r, nb = b * r;
+        if (BWD) {
+          if (norm && ok && p.part) {
+            acc[ia] += ya * na;
+            if (two) acc[ib] += yb * nb;
+          }
+          a = norm ? r * (ya * wa - na * k) : ya;
+          b = norm ? r * (yb * wb - nb * k) : yb;
+        } else {
+          if (norm) a = na * wa, b = nb * wb;
+          if (rot && ok) rotate_pair(a, b, __ldg(cs + j), __ldg(cs + half + j));
+        }
+        from_f32(y + ia, ok ? a : 0.f);
+        if (two) from_f32(y + ib, ok ? b : 0.f);
+      }
+      if (pass == 0) {
+        for (int o = 16; o; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          if (BWD) gx += __shfl_xor_sync(0xffffffffu, gx, o);
+        }
+        r = rsqrtf(ss * inv_d + p.eps);
+        k = gx * r * inv_d;
+      }
+    }
+  }
+  if (BWD && p.part) write_dw_part(p, nr_acc);
+}
+
+// dw of q (blockIdx.y 0) and k (1): the CTAs' sums of one channel, added by
+// one warp in a fixed order.
+__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const __grid_constant__ NormParams p, int nblocks) {
+  const int which = blockIdx.y;
+  const int b0 = which ? p.blocks_q : 0, b1 = which ? nblocks : p.blocks_q;
+  const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (c >= p.D || !p.dw[which]) return;
+  float s = 0.f;
+  for (int b = b0 + lane; b < b1; b += 32) s += p.part[(int64_t)b * p.D + c];
+  for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) {
+    if (p.dw_dtype[which] == DT_BF16) static_cast<__nv_bfloat16*>(p.dw[which])[c] = __float2bfloat16_rn(s);
+    else static_cast<float*>(p.dw[which])[c] = s;
+  }
+}
+
+// ---------------------------------------------------------------- host
+
+constexpr int NR_MAX_BLOCKS = 2048;  // rows of the backward's workspace at most
+
+struct NormArgs {
+  const dt_dtensor *dy_q, *dy_k;  // backward only
+  const dt_dtensor *q, *k, *q_weight, *k_weight, *cos_sin, *positions, *q_out, *k_out;
+  const dt_dtensor *dq_weight, *dk_weight;  // backward only
+};
+
+dt_status norm_weight(const dt_dtensor* w, const char* what, const Layout& of, int D, bool output, const void** ptr,
+                      int32_t* dtype) {
+  PlainOperand o;
+  dt_status st = plain_operand(w, what, of, output, &o);
+  if (st != DT_OK) return st;
+  if (o.ndim != 1 || o.shape[0] != D) return fail(DT_ERR_SHAPE, "%s must be [head_dim]", what);
+  if (o.dtype != DT_BF16 && o.dtype != DT_FP32) return fail(DT_ERR_INVALID_ARG, "%s must be bf16 or fp32", what);
+  *ptr = o.ptr;
+  *dtype = o.dtype;
+  return DT_OK;
+}
+
+// CTAs of a launch over tokens * heads head rows: enough to fill the device,
+// fewer when there are not that many units of work.
+int norm_blocks(int64_t units) {
+  const int64_t full = std::min<int64_t>((int64_t)device_sm_count() * 8, NR_MAX_BLOCKS / 2);
+  return (int)std::max<int64_t>(1, std::min<int64_t>((units + NR_WARPS - 1) / NR_WARPS, full));
+}
+
+template <class T, bool BWD>
+void launch_norm(const NormParams& p, bool vec, int U, int grid, cudaStream_t s) {
+  const size_t smem = BWD && p.part ? (size_t)NR_WARPS * p.D * sizeof(float) : 0;
+  if (!vec) qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
+  else if (U == 1) qk_norm_vec_kernel<T, BWD, 1><<<grid, NR_THREADS, smem, s>>>(p);
+  else qk_norm_vec_kernel<T, BWD, 2><<<grid, NR_THREADS, smem, s>>>(p);
+}
+
+dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleaved, int tp, void* ws, size_t ws_bytes,
+                    int32_t* d_status, cudaStream_t stream) {
+  clear_error();
+  if (D < 2 || D > NR_MAX_D) return fail(DT_ERR_UNSUPPORTED, "head_dim %d (2 .. %d)", D, NR_MAX_D);
+  if (!(eps >= 0.f) || eps > 1.f) return fail(DT_ERR_INVALID_ARG, "eps must be in [0, 1]");
+  if (!A.q) return fail(DT_ERR_INVALID_ARG, "q is NULL");
+  if (!A.k && (A.k_weight || A.k_out || A.dy_k || A.dk_weight))
+    return fail(DT_ERR_INVALID_ARG, "k is NULL but another k operand is not");
+  if (!A.q_weight && !A.k_weight && !A.cos_sin) return fail(DT_ERR_INVALID_ARG, "neither a norm nor a rotation");
+  if ((A.cos_sin == nullptr) != (A.positions == nullptr))
+    return fail(DT_ERR_INVALID_ARG, "cos_sin and positions go together");
+  NormParams p;
+  HeadOperand x[2], y[2], g[2];
+  Layout lq, lx;
+  dt_status st;
+  const int n = A.k ? 2 : 1;
+  const dt_dtensor* xs[2] = {A.q, A.k};
+  const dt_dtensor* ys[2] = {A.q_out, A.k_out};
+  const dt_dtensor* gs[2] = {A.dy_q, A.dy_k};
+  const dt_dtensor* wts[2] = {A.q_weight, A.k_weight};
+  const dt_dtensor* dws[2] = {A.dq_weight, A.dk_weight};
+  static const char* const names[2][4] = {{"q", "dq_out", "q_weight", "dq_weight"},
+                                          {"k", "dk_out", "k_weight", "dk_weight"}};
+  const char* const ynames[2] = {bwd ? "dq" : "q_out", bwd ? "dk" : "k_out"};
+  bool vec = D % 16 == 0 && D <= 512, any_dw = false;
+  for (int i = 0; i < n; ++i) {
+    if ((st = head_operand(xs[i], names[i][0], tp, D, false, &x[i], i ? &lx : &lq)) != DT_OK) return st;
+    if (i && (st = same_mesh(lx, lq, names[i][0])) != DT_OK) return st;
+    if (x[i].tokens != x[0].tokens) return fail(DT_ERR_SHAPE, "q and k have different token counts");
+    if (x[i].dtype != x[0].dtype) return fail(DT_ERR_INVALID_ARG, "q and k must have one dtype");
+    for (int r = 0; r < (bwd ? 2 : 1); ++r) {
+      HeadOperand& o = r ? g[i] : y[i];
+      const char* nm = r ? names[i][1] : ynames[i];
+      Layout lo;
+      if ((st = head_operand(r ? gs[i] : ys[i], nm, tp, D, r == 0, &o, &lo)) != DT_OK) return st;
+      if ((st = same_mesh(lo, lq, nm)) != DT_OK) return st;
+      if (o.heads != x[i].heads || o.tokens != x[i].tokens)
+        return fail(DT_ERR_SHAPE, "%s must have the shape of %s", nm, names[i][0]);
+      if (o.dtype != x[i].dtype) return fail(DT_ERR_INVALID_ARG, "%s must have the dtype of %s", nm, names[i][0]);
+      vec = vec && o.vec16;
+    }
+    vec = vec && x[i].vec16;
+    p.x[i] = x[i].map;
+    p.y[i] = y[i].map;
+    if (bwd) p.g[i] = g[i].map;
+    p.w[i] = p.dw[i] = nullptr;
+    if (wts[i]) {
+      const void* w;
+      if ((st = norm_weight(wts[i], names[i][2], lq, D, false, &w, &p.w_dtype[i])) != DT_OK) return st;
+      p.w[i] = w;
+    }
+    if (bwd && (wts[i] == nullptr) != (dws[i] == nullptr))
+      return fail(DT_ERR_INVALID_ARG, "%s and %s go together", names[i][2], names[i][3]);
+    if (bwd && dws[i]) {
+      const void* w;
+      if ((st = norm_weight(dws[i], names[i][3], lq, D, true, &w, &p.dw_dtype[i])) != DT_OK) return st;
+      p.dw[i] = const_cast<void*>(w);
+      any_dw = true;
+    }
+  }
+  p.cos_sin = nullptr;
+  p.pos = nullptr;
+  p.table_rows = 0;
+  p.rotary = 0;
+  if (A.cos_sin) {
+    PlainOperand t, pos;
+    if ((st = plain_operand(A.cos_sin, "cos_sin", lq, false, &t)) != DT_OK) return st;
+    if ((st = plain_operand(A.positions, "positions", lq, false, &pos)) != DT_OK) return st;
+    if (t.ndim != 2 || t.shape[1] < 2 || t.shape[1] % 2 || t.shape[1] > D)
+      return fail(DT_ERR_SHAPE, "cos_sin must be [rows, rotary], rotary even and at most head_dim");
+    if (t.dtype != DT_FP32) return fail(DT_ERR_INVALID_ARG, "cos_sin must be fp32");
+    if (pos.dtype != DT_INT32) return fail(DT_ERR_INVALID_ARG, "positions must be int32");
+    if (pos.numel != x[0].tokens) return fail(DT_ERR_SHAPE, "positions must have one entry per token");
+    if (t.shape[0] == 0 && x[0].tokens > 0)
+      return fail(DT_ERR_SHAPE, "cos_sin has no rows: every position would be out of range");
+    p.cos_sin = reinterpret_cast<const float*>(t.ptr);
+    p.pos = reinterpret_cast<const int32_t*>(pos.ptr);
+    p.table_rows = t.shape[0];
+    p.rotary = (int)t.shape[1];
+    vec = vec && p.rotary % 16 == 0 && reinterpret_cast<uintptr_t>(t.ptr) % 16 == 0;
+  }
+  p.D = D;
+  p.eps = eps;
+  p.interleaved = interleaved != 0;
+  p.tokens = x[0].tokens;
+  p.part = nullptr;
+  const int heads_k = n == 2 ? x[1].heads : 0;
+  const bool nothing = p.tokens == 0 || x[0].heads + heads_k == 0;
+  if (nothing && !any_dw) return DT_OK;
+  // one warp's work: U heads per subgroup of lanes (or one head).  Two heads
+  // per lane once every warp of a full device has several units.
+  int LP = 1;
+  while (LP < D / 16) LP <<= 1;
+  const int SG = vec ? 32 / LP : 1;
+  const int64_t rows = p.tokens * ((int64_t)x[0].heads + heads_k);
+  const int64_t warps = (int64_t)device_sm_count() * 8 * NR_WARPS;
+  const int U = vec && rows / SG >= 4 * warps ? 2 : 1;
+  const int64_t uq = p.tokens * ((x[0].heads + SG * U - 1) / (SG * U));
+  const int64_t uk = p.tokens * ((heads_k + SG * U - 1) / (SG * U));
+  const int total = norm_blocks(uq + uk);
+  int bq = (int)((double)total * (double)uq / (double)std::max<int64_t>(1, uq + uk) + 0.5);
+  bq = std::max(1, std::min(bq, total));
+  int bk = uk > 0 ? std::max(1, total - bq) : 0;
+  p.blocks_q = bq;
+  const int grid = bq + bk;
+  if (any_dw) {
+    const size_t need = (size_t)grid * D * sizeof(float);
+    if (!ws || ws_bytes < need)
+      return fail(DT_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
+    if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(DT_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
+    p.part = static_cast<float*>(ws);
+  }
+  if ((st = bind_device_of(x[0].heads && p.tokens ? p.y[0].ptr[0] : any_dw ? p.dw[0] ? p.dw[0] : p.dw[1] : nullptr)) !=
+      DT_OK)
+    return st;
+  p.status = device_status_word(d_status);
+  if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
+  if (x[0].dtype == DT_BF16) {
+    if (bwd) launch_norm<__nv_bfloat16, true>(p, vec, U, grid, stream);
+    else launch_norm<__nv_bfloat16, false>(p, vec, U, grid, stream);
+  } else {
+    if (bwd) launch_norm<float, true>(p, vec, U, grid, stream);
+    else launch_norm<float, false>(p, vec, U, grid, stream);
+  }
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
+  count_launch();
+  if (any_dw) {
+    qk_norm_dw_kernel<<<dim3((D + 7) / 8, n), 256, 0, stream>>>(p, grid);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope dw launch: %s", cudaGetErrorString(e));
+    count_launch();
+  }
+  return DT_OK;
+}
+
+}  // namespace
+}  // namespace dt
+
+using namespace dt;
+
+extern "C" dt_status dt_tp_qk_norm_rope(const dt_dtensor* q, const dt_dtensor* k, const dt_dtensor* q_weight,
+                                        const dt_dtensor* k_weight, const dt_dtensor* cos_sin,
+                                        const dt_dtensor* positions, const dt_dtensor* q_out, const dt_dtensor* k_out,
+                                        int32_t head_dim, float eps, int32_t interleaved, int32_t tp_mesh_dim,
+                                        int32_t* d_status, dt_stream_t stream) {
+  return no_throw([&] {
+    NormArgs a{nullptr, nullptr, q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out, nullptr, nullptr};
+    return norm_call(false, a, head_dim, eps, interleaved, tp_mesh_dim, nullptr, 0, d_status,
+                     reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" dt_status dt_tp_qk_norm_rope_backward(const dt_dtensor* dq_out, const dt_dtensor* dk_out,
+                                                 const dt_dtensor* q, const dt_dtensor* k, const dt_dtensor* q_weight,
+                                                 const dt_dtensor* k_weight, const dt_dtensor* cos_sin,
+                                                 const dt_dtensor* positions, const dt_dtensor* dq,
+                                                 const dt_dtensor* dk, const dt_dtensor* dq_weight,
+                                                 const dt_dtensor* dk_weight, int32_t head_dim, float eps,
+                                                 int32_t interleaved, int32_t tp_mesh_dim, void* workspace,
+                                                 size_t workspace_bytes, int32_t* d_status, dt_stream_t stream) {
+  return no_throw([&] {
+    NormArgs a{dq_out, dk_out, q, k, q_weight, k_weight, cos_sin, positions, dq, dk, dq_weight, dk_weight};
+    return norm_call(true, a, head_dim, eps, interleaved, tp_mesh_dim, workspace, workspace_bytes, d_status,
+                     reinterpret_cast<cudaStream_t>(stream));
+  });
+}
+
+extern "C" dt_status dt_tp_qk_norm_rope_backward_workspace_size(int32_t head_dim, size_t* bytes) {
+  clear_error();
+  if (!bytes) return fail(DT_ERR_INVALID_ARG, "bytes is NULL");
+  if (head_dim < 2 || head_dim > NR_MAX_D) return fail(DT_ERR_UNSUPPORTED, "head_dim %d (2 .. %d)", head_dim, NR_MAX_D);
+  *bytes = (size_t)NR_MAX_BLOCKS * head_dim * sizeof(float);
+  return DT_OK;
+}
