@@ -56,7 +56,7 @@ dt_status kv4_batch(const dt_dtensor* cache, const dt_dtensor* page_table, const
   if (pt.shape[0] > (1 << 20) || pt.shape[1] >= (1ll << 31)) return fail(DT_ERR_CAPACITY, "page_table dims");
   out->batch = (int32_t)pt.shape[0];
   out->table_width = (int32_t)pt.shape[1];
-  out->capacity = (int32_t)std::min<int64_t>(pt.shape[1] * (int64_t)M.page_size, (1ll << 31) - 512);
+  out->capacity = (int32_t)std::min<int64_t>(pt.shape[1] * (int64_t)M.page_size, (1ll << 31) - (1ll << 22));
   if (M.pages == 0) out->capacity = 0;
   out->page_table = reinterpret_cast<const int32_t*>(pt.ptr);
   out->kv_lens = nullptr;

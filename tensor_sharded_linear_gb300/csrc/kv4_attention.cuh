@@ -5,18 +5,24 @@
 //   q . k  = sum over groups of  s_g (q_g . c_g) + m_g sum(q_g)
 //   O      = sum over keys of    (p s'_g) c'_g  +  p m'_g
 // so the matrix products run on the integer codes and the parameters enter
-// as one multiply-add per key, row and group.  A code becomes a bf16 number
-// by putting its nibble into the mantissa of 128 (a shift and a logic
-// operation for two codes): 128 + c.  For q . k the products see that, and
-// 128 sum(q_g) comes off in the multiply-add.  For O one subtraction per two
-// codes makes it c - 8 and the minimum m + 8 s: the products are then centred
-// like the values they stand for, where an offset of 128 (or codes of mean
-// 7.5) would cancel against the sum of all p s' and lose what a long sequence
-// averages to (measured at 131071 keys: 1.0% off with 128 + c).  fp32
-// activations enter as three bf16 parts (24 bits), with centred codes on both
-// sides; each tile's product is then added to the sums in the ordinary fp32
-// adder, which rounds to nearest where the matrix unit's own accumulation
-// truncates.
+// as a multiply-add per key, row and group, and as one small product with the
+// parameter words as they lie in memory.
+// bf16 activations: fp16 products.  An fp16 number below 2^-13 is its bit
+// pattern times 2^-24, subnormal or not, so a masked nibble IS code * 2^-24
+// (bits 0..3) or 16 * code * 2^-24 (bits 4..7): two codes cost one logic
+// operation and a quarter of a shift.  Queries are scaled per row by a power
+// of two to [2^10, 2^11), where a bf16 number fits fp16 exactly unless it is
+// 2^-25 of the row's largest.  p s' is scaled by the power of two that keeps
+// the largest step seen below 2^12: eleven bits for whatever is within 2^-26
+// of it.
+// The accumulators of a long sequence have to be centred: a code's mean of
+// 7.5 would cancel against the sum of all p m' and take the low bits along
+// (the matrix unit truncates; an offset of 128 cost 1.0% at 131071 keys in
+// runs of 2900).  So -8 times the tile's sum of p s' goes in as one more
+// product per 16 channels and tile, and m' becomes m' + 8 s'.
+// fp32 activations: three bf16 parts (24 bits) times codes - 8 made from the
+// nibble in the mantissa of 128; each tile's product is added to the sums in
+// the ordinary fp32 adder, which rounds to nearest.
 //
 // The softmax runs in one pass with a running maximum and sum in fp32.  The
 // products are S^T = K Q^T (16 keys x 8 rows x 16 channels) and
@@ -25,12 +31,12 @@
 // turn into the operand of O^T with one 8 x 8 transpose (movmatrix).
 //
 // Work.  A unit is (sequence, kv head, block of rows); its keys come in
-// blocks of 128.  The device adds up all units' blocks from kv_lens and gives
+// blocks of four tiles.  The device adds up all units' blocks from kv_lens and gives
 // every CTA an equal, contiguous share, whatever the lengths: no host
 // knowledge of them, no idle SM for one long sequence.  A share that ends
 // inside a unit leaves its sums in the workspace, and the join kernel adds
-// them.  Inside a CTA each of the four warps takes every fourth tile of 32
-// keys with its own ring of bulk copies (a page's records of a head are
+// them.  Inside a CTA each of the four warps takes every fourth tile of 64
+// keys (32 at head_dim 256) with its own ring of bulk copies (a page's records of a head are
 // contiguous: one copy per page and tile), so no warp waits for another
 // until the unit ends.
 //
@@ -39,6 +45,7 @@
 #pragma once
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 
 #include <type_traits>
 
@@ -48,9 +55,6 @@
 namespace dt {
 namespace kv4 {
 
-template <int D>
-constexpr int kStages = D <= 128 ? 4 : 3;
-
 template <int D, int G, int NT, int NP>
 struct Shape {
   static constexpr int W = kv4_words(D, G);
@@ -59,7 +63,13 @@ struct Shape {
   static constexpr int WL = D / 32;         // key code words of a lane
   static constexpr int MT = G / 16;         // 16-channel tiles of O^T in a group
   static constexpr int RB = 8 * NT;         // rows of a unit
-  static constexpr int STAGES = kStages<D>;
+    static constexpr int TILE = D <= 128 ? 64 : 32;  // keys of a warp's tile
+  static constexpr int HT = TILE / 16;
+  static constexpr int BLOCK = TILE * WARPS;       // keys of a step of the schedule
+  static constexpr int STAGES = 2;
+  // products that carry the parameters' share of q . k: 3 parts of each
+  // group's sum(q), 8 pairs (step, minimum) a product
+  static constexpr int PM = (3 * NG + 7) / 8;
   static constexpr int TILE_BYTES = TILE * W * 4;
   static constexpr int RING = WARPS * STAGES * TILE_BYTES;
   static constexpr int QF = NT * NP * WL * 32 * 16;
@@ -67,11 +77,11 @@ struct Shape {
   static constexpr int RING_OR_MERGE = RING > MERGE ? RING : MERGE;
   static constexpr int OFF_QF = RING_OR_MERGE;
   static constexpr int OFF_QS = OFF_QF + QF;
-  static constexpr int OFF_ML = OFF_QS + RB * NG * 4;
+  static constexpr int OFF_ML = OFF_QS + RB * (NG + 1) * 4;
   static constexpr int OFF_BAR = OFF_ML + WARPS * RB * 8;
   static constexpr int OFF_VM = OFF_BAR + WARPS * STAGES * 8;
-  static constexpr int OFF_SCAN = (OFF_VM + WARPS * STAGES * 4 + 15) / 16 * 16;
-  static constexpr int SMEM = OFF_SCAN + THREADS * 8 + 16;
+  static constexpr int OFF_ABORT = OFF_VM + WARPS * STAGES * 8;
+  static constexpr int SMEM = OFF_ABORT + 16;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -82,28 +92,95 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zero.
+__device__ __forceinline__ void mma16816_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// fp16 operands; accumulators d = c + a b.
+__device__ __forceinline__ void mma16816_h(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                           uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma16816_h_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
+  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
 
-// Nibble I of both halves of w as bf16 128 + code; CENTRED: code - 8.
-template <int I, bool CENTRED>
-__device__ __forceinline__ uint32_t nibbles(uint32_t w) {
-  uint32_t r = ((w >> (4 * I)) & 0x000f000fu) | 0x43004300u;
-  if (CENTRED) {
-    const __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&r);
-    const __nv_bfloat162 y = __hsub2(x, __floats2bfloat162_rn(136.f, 136.f));
-    r = *reinterpret_cast<const uint32_t*>(&y);
+// Nibbles 0..3 of both halves of w as four operand registers.
+// FULL: bf16 code - 8.  `one` is 0x43004300 in a register that the compiler
+// does not see through: mask and exponent go in with one LOP3, where two
+// immediates would take two.  Else fp16: code * 2^-24 (0 and 2) and 16 times
+// that (1 and 3).
+template <bool FULL>
+__device__ __forceinline__ void nibbles(uint32_t w, uint32_t one, uint32_t (&n)[4]) {
+  if constexpr (FULL) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      asm("lop3.b32 %0, %1, 0x000f000f, %2, 0xea;" : "=r"(n[i]) : "r"(w >> (4 * i)), "r"(one));  // (a & b) | c
+      const __nv_bfloat162 x = *reinterpret_cast<__nv_bfloat162*>(&n[i]);
+      const __nv_bfloat162 y = __hsub2(x, __floats2bfloat162_rn(136.f, 136.f));
+      n[i] = *reinterpret_cast<const uint32_t*>(&y);
+    }
+  } else {
+    const uint32_t h = w >> 8;
+    n[0] = w & 0x000f000fu, n[1] = w & 0x00f000f0u, n[2] = h & 0x000f000fu, n[3] = h & 0x00f000f0u;
   }
+}
+__device__ __forceinline__ uint32_t exponent_of_128() {
+  uint32_t r;
+  asm volatile("mov.b32 %0, 0x43004300;" : "=r"(r));
   return r;
+}
+
+// N consecutive words of shared memory, as wide as their number allows (the
+// callers' addresses are aligned to that).
+template <int N>
+__device__ __forceinline__ void load_words(const uint32_t* p, uint32_t (&w)[N]) {
+  if constexpr (N % 4 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if constexpr (N % 2 == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p + i);
+      w[i] = v.x, w[i + 1] = v.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[i] = p[i];
+  }
 }
 
 __device__ __forceinline__ float step_of(uint32_t param) { return __uint_as_float(param << 16); }
@@ -112,10 +189,14 @@ __device__ __forceinline__ float min_of(uint32_t param) { return __uint_as_float
 // x as NP bf16 parts whose sum is x (to 8 NP bits).
 template <int NP>
 __device__ __forceinline__ void parts_of(float x, float (&y)[NP]) {
+  if constexpr (NP == 1) {
+    y[0] = x;  // rounded where it is packed
+  } else {
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    y[i] = __bfloat162float(__float2bfloat16_rn(x));
-    x -= y[i];
+    for (int i = 0; i < NP; ++i) {
+      y[i] = __bfloat162float(__float2bfloat16_rn(x));
+      x -= y[i];
+    }
   }
 }
 
@@ -125,7 +206,7 @@ struct Seq {
   int nrb, nblk, klo;     // row blocks, key blocks, first key of the first block
 };
 
-template <int RB>
+template <int RB, int TILE>
 __device__ __forceinline__ Seq seq_info(const AttnParams& p, int b) {
   Seq s;
   s.q0 = p.seq.start(b);
@@ -135,7 +216,7 @@ __device__ __forceinline__ Seq seq_info(const AttnParams& p, int b) {
   s.off = s.kv - ql;
   s.nrb = (s.rows + RB - 1) / RB;
   s.klo = p.window ? max(0, s.off - p.window + 1) / TILE * TILE : 0;
-  s.nblk = max(1, (s.kv - s.klo + BLOCK - 1) / BLOCK);  // an empty sequence still writes its rows
+  s.nblk = max(1, (s.kv - s.klo + TILE * WARPS - 1) / (TILE * WARPS));  // an empty sequence still writes its rows
   return s;
 }
 
@@ -144,22 +225,26 @@ __device__ __forceinline__ int64_t cost(const AttnParams& p, const Seq& s) {
 }
 
 template <int D, int G, int NT, int NP>
-__global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
+    kv4_attention_kernel(const __grid_constant__ AttnParams p) {
   using S = Shape<D, G, NT, NP>;
   using T = typename std::conditional<NP == 1, __nv_bfloat16, float>::type;
-  constexpr int W = S::W, NG = S::NG, WPG = S::WPG, WL = S::WL, MT = S::MT, RB = S::RB, STAGES = S::STAGES;
+  constexpr int W = S::W, NG = S::NG, WPG = S::WPG, MT = S::MT, RB = S::RB, STAGES = S::STAGES;
+  constexpr int WL = S::WL, TILE = S::TILE, HT = S::HT, BLOCK = S::BLOCK, PM = S::PM;
   constexpr bool FULL = NP > 1;  // fp32 activations
-  constexpr float KOFF = FULL ? 8.f : -128.f;  // what the key products' codes are offset by, negated
+  constexpr float KOFF = FULL ? 8.f : 0.f;  // what the key products' codes are offset by, negated
   extern __shared__ __align__(128) uint8_t smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = lane >> 2, ql = lane & 3;
   uint8_t* ring = smem + warp * STAGES * S::TILE_BYTES;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + S::OFF_BAR) + warp * STAGES;
-  volatile uint32_t* vmask = reinterpret_cast<volatile uint32_t*>(smem + S::OFF_VM) + warp * STAGES;
+  volatile uint64_t* vmask = reinterpret_cast<volatile uint64_t*>(smem + S::OFF_VM) + warp * STAGES;
   float* qs = reinterpret_cast<float*>(smem + S::OFF_QS);
+  float* rsc = qs + RB * NG;
   float2* ml = reinterpret_cast<float2*>(smem + S::OFF_ML);
-  int64_t* scan = reinterpret_cast<int64_t*>(smem + S::OFF_SCAN);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(scan + THREADS);
+  int64_t* scan = reinterpret_cast<int64_t*>(smem);  // before the ring is in use
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + S::OFF_ABORT);
+  const uint32_t one = exponent_of_128();
   if (lane == 0)
     for (int i = 0; i < STAGES; ++i) mbar_init(&bars[i], 1);
   if (threadIdx.x == 0) *abort_flag = 0;
@@ -171,7 +256,7 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
     int64_t sum = 0;
     const int b0 = threadIdx.x * per;
     for (int b = b0; b < min(b0 + per, p.seq.batch); ++b) {
-      sum += cost(p, seq_info<RB>(p, b));
+      sum += cost(p, seq_info<RB, TILE>(p, b));
       if (blockIdx.x == 0 && __ldg(p.seq.kv_lens + b) != p.seq.keys(b)) atomicOr(p.status, DT_DEV_ERR_INDEX);
     }
     int64_t x = sum;
@@ -207,14 +292,16 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
     b = lo * per;
     base = lo ? scan[lo - 1] : 0;
   }
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring was written by plain stores
+  __syncthreads();
 
   uint32_t put = 0, got = 0;  // tiles issued to and taken from this warp's ring
   bool dead = false;          // a wait ran out: load and compute nothing more
   for (int64_t at = g0; at < g1;) {
-    Seq s = seq_info<RB>(p, b);
+    Seq s = seq_info<RB, TILE>(p, b);
     while (at >= base + cost(p, s)) {
       base += cost(p, s);
-      s = seq_info<RB>(p, ++b);
+      s = seq_info<RB, TILE>(p, ++b);
     }
     const int64_t rem = at - base;
     const int unit = (int)(rem / s.nblk), blk0 = (int)(rem - (int64_t)unit * s.nblk);
@@ -227,78 +314,142 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
     const int klo = p.window ? max(0, pos_a - p.window + 1) : 0;
     const int32_t* pages = p.page_table + (int64_t)b * p.table_width;
     const int key0 = s.klo + (blk0 * WARPS + warp) * TILE;
+    const int ps = p.cache.page_size;
+    const int slot = hk / p.cache.per_slot;
+    const int64_t page_stride = p.cache.page_stride[slot];
+    const int32_t* head_base = p.cache.ptr[slot] + (int64_t)(hk - slot * p.cache.per_slot) * p.cache.head_stride[slot];
 
+    // A tile's keys lie in runs of consecutive records, one per page: lane n
+    // copies run n.  Its page is looked up a tile ahead (`ready`).
+    auto first_page = [&](int j0) {
+      return (int)(__umulhi(2u * (uint32_t)j0, p.page_mul) >> p.page_shift);
+    };
+    auto look_up = [&](int i) {
+      const int j0 = key0 + i * BLOCK, pg = first_page(j0) + lane;
+      return i < nb && j0 + TILE > klo && (int64_t)pg * ps < min(j0 + TILE, khi) ? __ldg(pages + pg) : -1;
+    };
+    int32_t ready = look_up(0);
     auto issue = [&](int i) {
-      const int stage = put % STAGES, j0 = key0 + i * BLOCK, j = j0 + lane;
+      const int stage = put % STAGES, j0 = key0 + i * BLOCK;
       ++put;
-      bool ok = j < khi && j0 + TILE > klo && !dead;
-      const int pg = j / p.cache.page_size, in_pg = j - pg * p.cache.page_size;
-      int32_t page = 0;
-      if (ok) {
-        page = __ldg(pages + pg);
-        if (page < 0 || page >= p.cache.pages) {
-          ok = false;
-          atomicOr(p.status, DT_DEV_ERR_INDEX);
+      const int end = j0 + TILE > klo && !dead ? min(j0 + TILE, khi) : j0;
+      const int pg0 = first_page(j0);
+      uint64_t vm = end - j0 >= 64 ? ~0ull : end > j0 ? (1ull << (end - j0)) - 1 : 0;
+      const int nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(ring + stage * S::TILE_BYTES);
+      bool good = true;
+      for (int n0 = 0; n0 < nruns; n0 += 32) {
+        const int n = n0 + lane;
+        const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(pages + pg0 + n) : 0;
+        const bool ok = n >= nruns || (page >= 0 && page < p.cache.pages);
+        good = good && ok;
+        if (!__all_sync(0xffffffffu, ok)) {  // pages that are none: their keys are hidden
+          if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
+          uint64_t bad = 0;
+          if (!ok) {
+            const int a = max(j0, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
+            bad = (z - a >= 64 ? ~0ull : (1ull << (z - a)) - 1) << a;
+          }
+          for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+          vm &= ~bad;
         }
       }
-      const uint32_t vm = __ballot_sync(0xffffffffu, ok);
       if (lane == 0) {
         vmask[stage] = vm;
-        if (!dead) mbar_expect_tx(&bars[stage], __popc(vm) * W * 4);
+        if (!dead) mbar_expect_tx(&bars[stage], __popcll(vm) * W * 4);
       }
       __syncwarp();
-      if (ok && (lane == 0 || in_pg == 0)) {
-        const int n = min(min(p.cache.page_size - in_pg, TILE - lane), khi - j);
-        bulk_load(ring + stage * S::TILE_BYTES + lane * (W * 4),
-                  cache_page(p.cache, page, hk) + (int64_t)in_pg * W, n * W * 4, &bars[stage]);
+      for (int n = lane; n < nruns; n += 32) {
+        const int32_t page = n < 32 ? ready : __ldg(pages + pg0 + n);
+        if (page < 0 || page >= p.cache.pages) continue;
+        const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
+        bulk_load(dst + (a - j0) * W, head_base + page * page_stride + (int64_t)(a - (pg0 + n) * ps) * W,
+                  (z - a) * W * 4, &bars[stage]);
       }
+      ready = look_up(i + 1);
       __syncwarp();
     };
-    const int ahead = min(nb, STAGES - 1);
-    for (int i = 0; i < ahead; ++i) issue(i);
+    issue(0);
 
-    // ---- the queries as matrix operands, and their sums per group
-    for (int e = warp; e < NT * NG; e += WARPS) {
-      const int nt = e / NG, grp = e - nt * NG;
-      const int row = row0 + nt * 8 + r;
-      float sum = 0.f;
+    // ---- the queries as matrix operands, and their sums per group: warp nt takes 8 rows
+    if (warp < NT) {
+      const int nt = warp, row = row0 + nt * 8 + r;
+      float x[WL][8];
 #pragma unroll
-      for (int j = 0; j < WPG; ++j) {
-        float x[8];
+      for (int w = 0; w < WL; ++w)
 #pragma unroll
-        for (int c = 0; c < 8; ++c) x[c] = 0.f;
-        if (nt * 8 + r < rows) {
-          const T* q = head_ptr<T>(p.q, s.q0 + row / p.g, hk * p.g + row % p.g, D);
-          load8(q + grp * G + 8 * (ql * WPG + j), x);
-        }
-        float y[8][NP];
+        for (int c = 0; c < 8; ++c) x[w][c] = 0.f;
+      if (nt * 8 + r < rows) {
+        const T* q = head_ptr<T>(p.q, s.q0 + row / p.g, hk * p.g + row % p.g, D);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          parts_of<NP>(x[c], y[c]);
-          sum += x[c];
-        }
-#pragma unroll
-        for (int n = 0; n < NP; ++n) {
-          uint4 f;
-          f.x = pack_bf16(y[0][n], y[4][n]);
-          f.y = pack_bf16(y[1][n], y[5][n]);
-          f.z = pack_bf16(y[2][n], y[6][n]);
-          f.w = pack_bf16(y[3][n], y[7][n]);
-          reinterpret_cast<uint4*>(smem + S::OFF_QF)[((nt * NP + n) * WL + grp * WPG + j) * 32 + lane] = f;
-        }
+        for (int w = 0; w < WL; ++w) load8(q + w / WPG * G + 8 * (ql * WPG + w % WPG), x[w]);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (ql == 0) qs[(nt * 8 + r) * NG + grp] = sum;
+      float mult = 1.f;
+      if constexpr (!FULL) {
+        float top = 0.f;
+#pragma unroll
+        for (int w = 0; w < WL; ++w)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[w][c]));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int ex = __float_as_uint(top) >> 23;  // 2^10 / 2^(exponent of top), within the normal numbers
+        mult = __uint_as_float((uint32_t)max(10, min(254, 264 - ex)) << 23);
+      }
+      if (ql == 0) rsc[nt * 8 + r] = FULL ? p.scale_log2 : p.scale_log2 * 16777216.f / mult;
+#pragma unroll
+      for (int grp = 0; grp < NG; ++grp) {
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < WPG; ++j) {
+          const int w = grp * WPG + j;
+          float y[8][NP];
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            x[w][c] *= mult;
+            sum += x[w][c];
+            if (!FULL && (c & 1)) x[w][c] *= 0.0625f;  // the odd nibbles come out 16 times as large
+            parts_of<NP>(x[w][c], y[c]);
+          }
+#pragma unroll
+          for (int n = 0; n < NP; ++n) {
+            uint4 f;
+            if constexpr (FULL)
+              f = make_uint4(pack_bf16(y[0][n], y[4][n]), pack_bf16(y[1][n], y[5][n]), pack_bf16(y[2][n], y[6][n]),
+                             pack_bf16(y[3][n], y[7][n]));
+            else
+              f = make_uint4(pack_f16(y[0][n], y[4][n]), pack_f16(y[1][n], y[5][n]), pack_f16(y[2][n], y[6][n]),
+                             pack_f16(y[3][n], y[7][n]));
+            reinterpret_cast<uint4*>(smem + S::OFF_QF)[((nt * NP + n) * WL + w) * 32 + lane] = f;
+          }
+        }
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        // beside fp16 products of codes * 2^-24
+        if (ql == 0) qs[(nt * 8 + r) * NG + grp] = FULL ? sum : sum * 5.9604644775390625e-8f;
+      }
     }
     __syncthreads();
-    float qsum[NT][NG][2];
+    float sc[NT][2];  // softmax scale * log2(e) of the lane's rows, their queries' scaling undone
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) sc[nt][0] = rsc[nt * 8 + 2 * ql], sc[nt][1] = rsc[nt * 8 + 2 * ql + 1];
+    // The parameters' share of S as products: row k of the narrow operand is
+    // KOFF sum(q_g) beside a step and sum(q_g) beside a minimum, in three
+    // bf16 parts; the wide operand is the keys' parameter words as they are.
+    // Pair n of the products' 8 PM is part n / NG of group n % NG.
+    uint32_t qm[NT][PM][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int grp = 0; grp < NG; ++grp)
+      for (int mm = 0; mm < PM; ++mm)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) qsum[nt][grp][e] = qs[(nt * 8 + 2 * ql + e) * NG + grp];
+        for (int h = 0; h < 2; ++h) {
+          const int n = mm * 8 + h * 4 + ql, part = n / NG;
+          float x = qs[(nt * 8 + r) * NG + n % NG], y[3];
+          parts_of<3>(x, y);
+          x = part == 0 ? y[0] : part == 1 ? y[1] : part == 2 ? y[2] : 0.f;
+          qm[nt][mm][h] = pack_bf16(KOFF * x, x);
+        }
 
     float o[NT][NG][MT][4], om[NT][NG][2], mx[NT][2], den[NT][2];
 #pragma unroll
@@ -314,9 +465,12 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
       mx[nt][0] = mx[nt][1] = -INFINITY;
       den[nt][0] = den[nt][1] = 0.f;
     }
+    // 2^12 over the power of two above the largest value step seen
+    uint32_t step_ex = 0;  // its exponent field
+    float vmult = __uint_as_float(254u << 23);
 
     for (int i = 0; i < nb; ++i) {
-      if (i + ahead < nb) issue(i + ahead);
+      if (i + 1 < nb) issue(i + 1);
       const int stage = got % STAGES;
       if (!dead && !mbar_wait_warp(&bars[stage], (got / STAGES) & 1, abort_flag, p.wait_limit_ns)) {
         dead = true;
@@ -326,75 +480,84 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
         }
       }
       ++got;
-      const uint32_t vm = vmask[stage];
-      if (dead || vm == 0) continue;
+      const uint64_t vm = vmask[stage];
+      if (dead || vm == 0) {
+        __syncwarp();
+        continue;
+      }
       const int j0 = key0 + i * BLOCK;
       const uint32_t* tile = reinterpret_cast<const uint32_t*>(ring + stage * S::TILE_BYTES);
 
-      // ---- S^T for 32 keys: lane holds keys r, r + 8, r + 16, r + 24 and rows 2 ql, 2 ql + 1
-      float sv[NT][4][2];
+      // ---- S^T: of every 16 keys a lane holds keys r and r + 8, rows 2 ql and 2 ql + 1
+      float sv[NT][2 * HT][2];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < HT; ++h) {
         const uint32_t* ka = tile + (16 * h + r) * W;
         const uint32_t* kb = ka + 8 * W;
-        float acc[NT][NG][4];
+        float acc[NT][NG][4], base_[NT][4];
+        {
+          const uint32_t a0 = ka[D / 4 + ql % NG], a1 = kb[D / 4 + ql % NG];
+          const uint32_t a2 = NG == 8 ? ka[D / 4 + 4 + ql] : a0, a3 = NG == 8 ? kb[D / 4 + 4 + ql] : a1;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int grp = 0; grp < NG; ++grp)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) acc[nt][grp][e] = 0.f;
+            for (int mm = 0; mm < PM; ++mm) {
+              if (mm == 0) mma16816_first(base_[nt], a0, a1, a2, a3, qm[nt][mm][0], qm[nt][mm][1]);
+              else mma16816(base_[nt], a0, a1, a2, a3, qm[nt][mm][0], qm[nt][mm][1]);
+            }
+        }
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
           uint32_t wa[WPG], wb[WPG];
-          if constexpr (WPG == 2) {
-            const uint2 a2 = *reinterpret_cast<const uint2*>(ka + grp * 8 + 2 * ql);
-            const uint2 b2 = *reinterpret_cast<const uint2*>(kb + grp * 8 + 2 * ql);
-            wa[0] = a2.x, wa[1] = a2.y, wb[0] = b2.x, wb[1] = b2.y;
-          } else {
-            wa[0] = ka[grp * 4 + ql], wb[0] = kb[grp * 4 + ql];
-          }
+          load_words<WPG>(ka + grp * (G / 8) + WPG * ql, wa);
+          load_words<WPG>(kb + grp * (G / 8) + WPG * ql, wb);
 #pragma unroll
           for (int j = 0; j < WPG; ++j) {
-            const uint32_t a0 = nibbles<0, FULL>(wa[j]), a1 = nibbles<0, FULL>(wb[j]);
-            const uint32_t a2 = nibbles<1, FULL>(wa[j]), a3 = nibbles<1, FULL>(wb[j]);
-            const uint32_t a4 = nibbles<2, FULL>(wa[j]), a5 = nibbles<2, FULL>(wb[j]);
-            const uint32_t a6 = nibbles<3, FULL>(wa[j]), a7 = nibbles<3, FULL>(wb[j]);
+            uint32_t ca[4], cb[4];
+            nibbles<FULL>(wa[j], one, ca);
+            nibbles<FULL>(wb[j], one, cb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
               for (int n = 0; n < NP; ++n) {
                 const uint4 f = reinterpret_cast<const uint4*>(
                     smem + S::OFF_QF)[((nt * NP + n) * WL + grp * WPG + j) * 32 + lane];
-                mma16816(acc[nt][grp], a0, a1, a2, a3, f.x, f.y);
-                mma16816(acc[nt][grp], a4, a5, a6, a7, f.z, f.w);
+                if constexpr (FULL) {
+                  if (j == 0 && n == 0) mma16816_first(acc[nt][grp], ca[0], cb[0], ca[1], cb[1], f.x, f.y);
+                  else mma16816(acc[nt][grp], ca[0], cb[0], ca[1], cb[1], f.x, f.y);
+                  mma16816(acc[nt][grp], ca[2], cb[2], ca[3], cb[3], f.z, f.w);
+                } else {
+                  if (j == 0) mma16816_h_first(acc[nt][grp], ca[0], cb[0], ca[1], cb[1], f.x, f.y);
+                  else mma16816_h(acc[nt][grp], ca[0], cb[0], ca[1], cb[1], f.x, f.y);
+                  mma16816_h(acc[nt][grp], ca[2], cb[2], ca[3], cb[3], f.z, f.w);
+                }
               }
             }
           }
         }
+        uint32_t pa[NG], pb[NG];
+        load_words<NG>(ka + D / 4, pa);
+        load_words<NG>(kb + D / 4, pb);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) sv[nt][2 * h + k][0] = sv[nt][2 * h + k][1] = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            float x = base_[nt][e], y = base_[nt][2 + e];
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          const uint32_t pa = ka[D / 4 + grp], pb = kb[D / 4 + grp];
-          const float sa = step_of(pa), sb = step_of(pb);
-          const float ma = fmaf(KOFF, sa, min_of(pa)), mb = fmaf(KOFF, sb, min_of(pb));
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sv[nt][2 * h][e] += fmaf(sa, acc[nt][grp][e], ma * qsum[nt][grp][e]);
-              sv[nt][2 * h + 1][e] += fmaf(sb, acc[nt][grp][2 + e], mb * qsum[nt][grp][e]);
+            for (int grp = 0; grp < NG; ++grp) {
+              x = fmaf(step_of(pa[grp]), acc[nt][grp][e], x);
+              y = fmaf(step_of(pb[grp]), acc[nt][grp][2 + e], y);
             }
-        }
+            sv[nt][2 * h][e] = x, sv[nt][2 * h + 1][e] = y;
+          }
       }
 
       // ---- mask, running maximum, p = 2^(S * scale - maximum)
-      const bool masked = vm != 0xffffffffu || (p.causal && j0 + TILE - 1 > pos_a) ||
-                          (p.window && j0 <= pos_z - p.window);
-      uint32_t hidden = 0;  // bit nt * 8 + k * 2 + e: key k is not seen by row e
+      constexpr uint64_t ALL = TILE == 64 ? ~0ull : (1ull << TILE) - 1;
+      const bool masked = vm != ALL || (p.causal && j0 + TILE - 1 > pos_a) || (p.window && j0 <= pos_z - p.window);
+      uint32_t hidden[NT];  // bit 2 k + e: key 8 k + r is not seen by row 2 ql + e
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) hidden[nt] = 0;
       if (masked) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -402,10 +565,10 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
           for (int e = 0; e < 2; ++e) {
             const int pos = s.off + (row0 + nt * 8 + 2 * ql + e) / p.g;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 2 * HT; ++k) {
               const int j = j0 + 8 * k + r;
               if (!((vm >> (8 * k + r)) & 1) || (p.causal && j > pos) || (p.window && j <= pos - p.window)) {
-                hidden |= 1u << (nt * 8 + k * 2 + e);
+                hidden[nt] |= 1u << (k * 2 + e);
                 sv[nt][k][e] = -INFINITY;
               }
             }
@@ -417,7 +580,10 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float t = fmaxf(fmaxf(sv[nt][0][e], sv[nt][1][e]), fmaxf(sv[nt][2][e], sv[nt][3][e])) * p.scale_log2;
+          float t = sv[nt][0][e];
+#pragma unroll
+          for (int k = 1; k < 2 * HT; ++k) t = fmaxf(t, sv[nt][k][e]);
+          t *= sc[nt][e];
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
           t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -446,74 +612,159 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
         for (int e = 0; e < 2; ++e) {
           const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e];  // a row that has seen nothing yet
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            sv[nt][k][e] = ex2(fmaf(sv[nt][k][e], p.scale_log2, -ref));
+          for (int k = 0; k < 2 * HT; ++k) {
+            sv[nt][k][e] = ex2(fmaf(sv[nt][k][e], sc[nt][e], -ref));
             den[nt][e] += sv[nt][k][e];
           }
         }
 
       // ---- O^T += V^T P^T, 16 keys at a time
+      uint32_t vp[HT][2][NG];  // value parameters of keys r and r + 8
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const uint32_t* va = tile + (16 * h + r) * W + D / 4 + NG;  // parameters of keys r and r + 8
-        const uint32_t* vb = va + 8 * W;
-        const uint32_t* vw = tile + (16 * h + 2 * ql) * W + D / 8 + (WPG == 2 ? r : r & 3);
+      for (int h = 0; h < HT; ++h)
 #pragma unroll
-        for (int grp = 0; grp < NG; ++grp) {
-          const float st[2] = {step_of(va[grp]), step_of(vb[grp])};
-          const float mid[2] = {fmaf(8.f, st[0], min_of(va[grp])), fmaf(8.f, st[1], min_of(vb[grp]))};
-          uint32_t bf[NT][NP][2];
+        for (int k = 0; k < 2; ++k) load_words<NG>(tile + (16 * h + 8 * k + r) * W + D / 4 + NG, vp[h][k]);
+      if (masked) {  // what lies where no key is counts as zero
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float x[2][2];  // [key r / r + 8][row]
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int grp = 0; grp < NG; ++grp)
+              if (!((vm >> (16 * h + 8 * k + r)) & 1)) vp[h][k][grp] = 0;
+      }
+      if constexpr (!FULL) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int h = 0; h < HT; ++h)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int grp = 0; grp < NG; ++grp) big = max(big, vp[h][k][grp] << 16);
+        if (__any_sync(0xffffffffu, (big >> 23) > step_ex)) {
+          // steps that are not finite (a sign bit or an exponent of ones) do not count
+          big = 0;
+#pragma unroll
+          for (int h = 0; h < HT; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k)
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float pe = sv[nt][2 * h + k][e];
-                float ps = pe * st[k], pm = pe * mid[k];
-                if (masked && (hidden >> (nt * 8 + (2 * h + k) * 2 + e) & 1)) ps = pm = 0.f;  // not 0 * NaN
-                x[k][e] = ps;
-                om[nt][grp][e] += pm;
+              for (int grp = 0; grp < NG; ++grp) {
+                const uint32_t st = vp[h][k][grp] << 16;
+                if (st < 0x7f800000u) big = max(big, st);
               }
+          const uint32_t ex = max(step_ex, __reduce_max_sync(0xffffffffu, big) >> 23);
+          if (ex > step_ex) {
+            const float m2 = __uint_as_float(min(254u, 265u - ex) << 23), f = m2 / vmult;
+            vmult = m2, step_ex = ex;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[nt][grp][m][e] *= f;
+          }
+        }
+      }
+      uint32_t bsum[NT][NG][2];
+#pragma unroll
+      for (int h = 0; h < HT; ++h) {
+        const uint32_t* vw = tile + (16 * h + 2 * ql) * W + D / 8 + (WPG == 2 ? r : r & 3);
+        float x[NT][NG][2][2];  // p * step of [key r / r + 8][row]
+        if (masked) {           // a hidden key adds nothing, not 0 * NaN
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              float y0[NP], y1[NP];
-              parts_of<NP>(x[k][0], y0);
-              parts_of<NP>(x[k][1], y1);
+              float st = step_of(vp[h][k][grp]);
+              const float mid = fmaf(8.f, st, min_of(vp[h][k][grp]));
+              if (!FULL) st *= vmult;
 #pragma unroll
-              for (int n = 0; n < NP; ++n) bf[nt][n][k] = transpose8x8(pack_bf16(y0[n], y1[n]));
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  const bool hide = hidden[nt] >> ((2 * h + k) * 2 + e) & 1;
+                  x[nt][grp][k][e] = hide ? 0.f : sv[nt][2 * h + k][e] * st;
+                  om[nt][grp][e] += hide ? 0.f : sv[nt][2 * h + k][e] * mid;
+                }
             }
-          }
+        } else {
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              float st = step_of(vp[h][k][grp]);
+              const float mid = fmaf(8.f, st, min_of(vp[h][k][grp]));
+              if (!FULL) st *= vmult;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  x[nt][grp][k][e] = sv[nt][2 * h + k][e] * st;
+                  om[nt][grp][e] = fmaf(sv[nt][2 * h + k][e], mid, om[nt][grp][e]);
+                }
+            }
+        }
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          uint32_t bf[NT][NP][2];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              if constexpr (FULL) {
+                float y0[NP], y1[NP];
+                parts_of<NP>(x[nt][grp][k][0], y0);
+                parts_of<NP>(x[nt][grp][k][1], y1);
+#pragma unroll
+                for (int n = 0; n < NP; ++n) bf[nt][n][k] = transpose8x8(pack_bf16(y0[n], y1[n]));
+              } else {
+                bf[nt][0][k] = transpose8x8(pack_f16(x[nt][grp][k][0], x[nt][grp][k][1]));
+                bsum[nt][grp][k] = h == 0 ? bf[nt][0][k] : add_f16(bsum[nt][grp][k], bf[nt][0][k]);
+              }
+            }
           const uint32_t* w = vw + grp * (G / 8);
           const uint32_t w0 = w[0], w1 = w[W], w2 = w[8 * W], w3 = w[9 * W];
           const uint32_t sel = WPG == 2 || r < 4 ? 0x5410u : 0x7632u;
 #pragma unroll
           for (int half = 0; half < WPG; ++half) {
-            const uint32_t x01 = __byte_perm(w0, w1, half ? 0x7632u : sel);
-            const uint32_t x23 = __byte_perm(w2, w3, half ? 0x7632u : sel);
-            const uint32_t a0 = nibbles<0, true>(x01), a1 = nibbles<1, true>(x01);
-            const uint32_t a2 = nibbles<0, true>(x23), a3 = nibbles<1, true>(x23);
-            const uint32_t a4 = nibbles<2, true>(x01), a5 = nibbles<3, true>(x01);
-            const uint32_t a6 = nibbles<2, true>(x23), a7 = nibbles<3, true>(x23);
+            uint32_t ca[4], cb[4];  // keys 2 ql and 2 ql + 1; the same + 8
+            nibbles<FULL>(__byte_perm(w0, w1, half ? 0x7632u : sel), one, ca);
+            nibbles<FULL>(__byte_perm(w2, w3, half ? 0x7632u : sel), one, cb);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
+              float(&t0)[4] = o[nt][grp][2 * half];
+              float(&t1)[4] = o[nt][grp][2 * half + 1];
               if constexpr (FULL) {
-                float t0[4] = {0.f, 0.f, 0.f, 0.f}, t1[4] = {0.f, 0.f, 0.f, 0.f};
+                float u0[4], u1[4];
+                mma16816_first(u0, ca[0], ca[1], cb[0], cb[1], bf[nt][NP - 1][0], bf[nt][NP - 1][1]);  // small parts first
+                mma16816_first(u1, ca[2], ca[3], cb[2], cb[3], bf[nt][NP - 1][0], bf[nt][NP - 1][1]);
 #pragma unroll
-                for (int n = NP - 1; n >= 0; --n) {  // small parts first
-                  mma16816(t0, a0, a1, a2, a3, bf[nt][n][0], bf[nt][n][1]);
-                  mma16816(t1, a4, a5, a6, a7, bf[nt][n][0], bf[nt][n][1]);
+                for (int n = NP - 2; n >= 0; --n) {
+                  mma16816(u0, ca[0], ca[1], cb[0], cb[1], bf[nt][n][0], bf[nt][n][1]);
+                  mma16816(u1, ca[2], ca[3], cb[2], cb[3], bf[nt][n][0], bf[nt][n][1]);
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[nt][grp][2 * half][e] += t0[e], o[nt][grp][2 * half + 1][e] += t1[e];
+                for (int e = 0; e < 4; ++e) t0[e] += u0[e], t1[e] += u1[e];
               } else {
-                mma16816(o[nt][grp][2 * half], a0, a1, a2, a3, bf[nt][0][0], bf[nt][0][1]);
-                mma16816(o[nt][grp][2 * half + 1], a4, a5, a6, a7, bf[nt][0][0], bf[nt][0][1]);
+                mma16816_h(t0, ca[0], ca[1], cb[0], cb[1], bf[nt][0][0], bf[nt][0][1]);
+                mma16816_h(t1, ca[2], ca[3], cb[2], cb[3], bf[nt][0][0], bf[nt][0][1]);
               }
             }
           }
         }
+      }
+      if constexpr (!FULL) {  // centre: -8 (even nibbles) and -128 (odd ones, 16 times as large), times 2^-24
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int grp = 0; grp < NG; ++grp)
+#pragma unroll
+            for (int m = 0; m < MT; ++m)
+              mma16816_h(o[nt][grp][m], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, bsum[nt][grp][0],
+                         bsum[nt][grp][1]);
       }
       __syncwarp();  // the stage may be refilled
     }
@@ -541,10 +792,11 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
         for (int m = 0; m < MT; ++m)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float add = om[nt][grp][e];
+            const float add = om[nt][grp][e], inv = FULL ? 1.f : 1.f / vmult;
+            const float even = FULL ? 1.f : 16777216.f, odd = FULL ? 1.f : 1048576.f;
             const int ch = grp * G + (WPG == 2 ? 8 * r : 8 * (r & 3) + 4 * (r >> 2)) + 2 * m;
             *reinterpret_cast<float2*>(os + (nt * 8 + 2 * ql + e) * D + ch) =
-                make_float2(o[nt][grp][m][e] + add, o[nt][grp][m][2 + e] + add);
+                make_float2(fmaf(o[nt][grp][m][e] * even, inv, add), fmaf(o[nt][grp][m][2 + e] * odd, inv, add));
           }
     __syncthreads();
     const bool whole = blk0 == 0 && nb == s.nblk;
@@ -605,42 +857,62 @@ __global__ void __launch_bounds__(THREADS) kv4_attention_kernel(const __grid_con
   }
 }
 
-// Adds the pieces of the units that were split, one CTA per unit and quarter
-// of the channels, in the order of the keys.
+// Adds the pieces of the units that were split, in an order fixed by the
+// schedule.  A warp takes a row and up to 32 float4 of its channels: C lanes
+// across the channels, 32 / C lanes across the pieces, two pieces in flight
+// per lane.
+constexpr int JOIN_WARPS = 8;
+
 template <int D, int G, int NT, int NP>
-__global__ void __launch_bounds__(THREADS) kv4_join_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const __grid_constant__ AttnParams p) {
   using S = Shape<D, G, NT, NP>;
   using T = typename std::conditional<NP == 1, __nv_bfloat16, float>::type;
-  constexpr int RB = S::RB, C4 = D / 16;  // float4s of a quarter
+  constexpr int RB = S::RB, C = 8, SEG = D / 4 / C, PL = 32 / C;
   const Split sp = p.split[blockIdx.x];
   if (sp.unit < 0) return;
-  for (int x = threadIdx.x; x < sp.rows * C4; x += THREADS) {
-    const int row = x / C4, c4 = blockIdx.y * C4 + x % C4;
-    float m = -INFINITY;
-    for (int c = blockIdx.x; c <= sp.last; ++c) {
-      const int64_t piece = 2 * (int64_t)c + (c == (int)blockIdx.x ? 1 : 0);
-      m = fmaxf(m, p.part[(piece * RB + row) * (D + 4) + D]);
-    }
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
+  const int lane = threadIdx.x & 31, c4 = lane % C, pl = lane / C;
+  for (int w = blockIdx.y * JOIN_WARPS + (threadIdx.x >> 5); w < sp.rows * SEG; w += gridDim.y * JOIN_WARPS) {
+    const int row = w / SEG, col = (w % SEG) * C + c4;
+    const int n = sp.last - (int)blockIdx.x + 1;
+    auto at = [&](int i) {
+      const int64_t piece = 2 * (int64_t)(blockIdx.x + i) + (i == 0 ? 1 : 0);
+      return p.part + (piece * RB + row) * (D + 4);
+    };
+    float m = -INFINITY, l = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int c = blockIdx.x; c <= sp.last; ++c) {
-      const int64_t piece = 2 * (int64_t)c + (c == (int)blockIdx.x ? 1 : 0);
-      const float* in = p.part + (piece * RB + row) * (D + 4);
-      const float f = ex2(in[D] - ref);
-      const float4 v = reinterpret_cast<const float4*>(in)[c4];
-      l += in[D + 1] * f;
-      a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+    auto add = [&](float mi, float li, float4 v) {
+      const float top = fmaxf(m, mi), ref = top == -INFINITY ? 0.f : top;
+      const float f0 = ex2(m - ref), f1 = ex2(mi - ref);
+      m = top;
+      l = l * f0 + li * f1;
+      a.x = a.x * f0 + v.x * f1, a.y = a.y * f0 + v.y * f1, a.z = a.z * f0 + v.z * f1, a.w = a.w * f0 + v.w * f1;
+    };
+    for (int i = pl; i < n; i += 2 * PL) {
+      const float* x = at(i);
+      const float* y = at(min(i + PL, n - 1));
+      const float2 mx = *reinterpret_cast<const float2*>(x + D), my = *reinterpret_cast<const float2*>(y + D);
+      const float4 vx = reinterpret_cast<const float4*>(x)[col], vy = reinterpret_cast<const float4*>(y)[col];
+      add(mx.x, mx.y, vx);
+      if (i + PL < n) add(my.x, my.y, vy);
     }
+#pragma unroll
+    for (int o = C; o < 32; o <<= 1) {
+      const float mi = __shfl_xor_sync(0xffffffffu, m, o), li = __shfl_xor_sync(0xffffffffu, l, o);
+      float4 v;
+      v.x = __shfl_xor_sync(0xffffffffu, a.x, o), v.y = __shfl_xor_sync(0xffffffffu, a.y, o);
+      v.z = __shfl_xor_sync(0xffffffffu, a.z, o), v.w = __shfl_xor_sync(0xffffffffu, a.w, o);
+      add(mi, li, v);
+    }
+    if (pl) continue;
     const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
     const int qr = sp.q_row + row;
     const int tok = sp.q0 + qr / p.g, head = sp.head * p.g + qr % p.g;
-    T* y = head_ptr<T>(p.out, tok, head, D) + 4 * c4;
+    T* out = head_ptr<T>(p.out, tok, head, D) + 4 * col;
     if constexpr (NP == 1)
-      *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
+      *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
     else
-      *reinterpret_cast<float4*>(y) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-    if (p.want_lse && c4 == 0)
+      *reinterpret_cast<float4*>(out) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
+    if (p.want_lse && col == 0)
       *head_ptr<float>(p.lse, tok, head, 1) = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
   }
 }
@@ -673,7 +945,8 @@ cudaError_t launch_of(const AttnParams& p, int grid, cudaStream_t s) {
   kv4_attention_kernel<D, G, NT, NP><<<grid, THREADS, Shape<D, G, NT, NP>::SMEM, s>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  kv4_join_kernel<D, G, NT, NP><<<dim3(grid, 4), THREADS, 0, s>>>(p);
+  constexpr int WORK = Shape<D, G, NT, NP>::RB * (D / 32);  // warps of a split unit
+  kv4_join_kernel<D, G, NT, NP><<<dim3(grid, (WORK + 2 * JOIN_WARPS - 1) / (2 * JOIN_WARPS)), 32 * JOIN_WARPS, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -9,10 +9,8 @@
 namespace dt {
 namespace kv4 {
 
-constexpr int WARPS = 4;             // each takes every fourth tile of 32 keys
+constexpr int WARPS = 4;             // each takes every fourth tile of keys
 constexpr int THREADS = 32 * WARPS;
-constexpr int TILE = 32;             // keys of a warp's tile
-constexpr int BLOCK = TILE * WARPS;  // keys of a unit of the schedule
 
 // What a CTA left unfinished: the unit whose keys begin in its range and end
 // in CTA `last`'s (unit < 0: none).  The join kernel adds those pieces.
@@ -32,6 +30,7 @@ struct AttnParams {
   const int32_t* page_table;
   int32_t table_width;
   int32_t g;  // query heads per kv head
+  uint32_t page_mul, page_shift;  // j / page_size = umulhi(2 j, page_mul) >> page_shift for j < 2^31
   int32_t causal, window;
   int32_t want_lse;
   float scale_log2;  // softmax scale * log2(e)
