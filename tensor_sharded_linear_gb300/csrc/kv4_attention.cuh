@@ -73,9 +73,8 @@ struct Shape {
   static constexpr int TILE_BYTES = TILE * W * 4;
   static constexpr int RING = WARPS * STAGES * TILE_BYTES;
   static constexpr int QF = NT * NP * WL * 32 * 16;
-  static constexpr int MERGE = WARPS * RB * D * 4;
-  static constexpr int RING_OR_MERGE = RING > MERGE ? RING : MERGE;
-  static constexpr int OFF_QF = RING_OR_MERGE;
+  static_assert(RB * D * 4 <= TILE_BYTES, "a warp's sums fit one stage of its ring");
+  static constexpr int OFF_QF = RING;
   static constexpr int OFF_QS = OFF_QF + QF;
   static constexpr int OFF_ML = OFF_QS + RB * (NG + 1) * 4;
   static constexpr int OFF_BAR = OFF_ML + WARPS * RB * 8;
@@ -206,6 +205,11 @@ struct Seq {
   int nrb, nblk, klo;     // row blocks, key blocks, first key of the first block
 };
 
+// Besides its blocks of keys a unit counts one more in the schedule, after
+// them, for its start and end (measured at 48 sequences of 800 to 8192 keys:
+// without it the busiest SM worked 22% longer than the average).
+constexpr int UNIT_EXTRA = 1;
+
 template <int RB, int TILE>
 __device__ __forceinline__ Seq seq_info(const AttnParams& p, int b) {
   Seq s;
@@ -221,7 +225,7 @@ __device__ __forceinline__ Seq seq_info(const AttnParams& p, int b) {
 }
 
 __device__ __forceinline__ int64_t cost(const AttnParams& p, const Seq& s) {
-  return (int64_t)s.nrb * s.nblk * p.cache.heads;
+  return (int64_t)s.nrb * (s.nblk + UNIT_EXTRA) * p.cache.heads;
 }
 
 template <int D, int G, int NT, int NP>
@@ -278,7 +282,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
   // CTAs that share the work: with fewer blocks than CTAs, one block each (so
   // that every CTA between a split unit's first and last holds a piece)
   const int64_t ncta = min((int64_t)gridDim.x, total);
-  if (blockIdx.x >= ncta) return;
+  if (blockIdx.x >= ncta) return;  // (a CTA that leaves allows the next kernel too)
   const int64_t g0 = total * blockIdx.x / ncta, g1 = total * (blockIdx.x + 1) / ncta;
   int b = 0;
   int64_t base = 0;
@@ -297,93 +301,133 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
 
   uint32_t put = 0, got = 0;  // tiles issued to and taken from this warp's ring
   bool dead = false;          // a wait ran out: load and compute nothing more
-  for (int64_t at = g0; at < g1;) {
-    Seq s = seq_info<RB, TILE>(p, b);
-    while (at >= base + cost(p, s)) {
-      base += cost(p, s);
-      s = seq_info<RB, TILE>(p, ++b);
-    }
-    const int64_t rem = at - base;
-    const int unit = (int)(rem / s.nblk), blk0 = (int)(rem - (int64_t)unit * s.nblk);
-    const int nb = (int)min((int64_t)(s.nblk - blk0), g1 - at);
-    const int hk = unit / s.nrb, row0 = (unit - hk * s.nrb) * RB;
-    const int rows = min(RB, s.rows - row0);
-    // positions of the block's first and last query, and the keys any of them sees
-    const int pos_a = s.off + row0 / p.g, pos_z = s.off + (row0 + rows - 1) / p.g;
-    const int khi = p.causal ? min(s.kv, pos_z + 1) : s.kv;
-    const int klo = p.window ? max(0, pos_a - p.window + 1) : 0;
-    const int32_t* pages = p.page_table + (int64_t)b * p.table_width;
-    const int key0 = s.klo + (blk0 * WARPS + warp) * TILE;
-    const int ps = p.cache.page_size;
-    const int slot = hk / p.cache.per_slot;
-    const int64_t page_stride = p.cache.page_stride[slot];
-    const int32_t* head_base = p.cache.ptr[slot] + (int64_t)(hk - slot * p.cache.per_slot) * p.cache.head_stride[slot];
+  const int ps = p.cache.page_size;
 
-    // A tile's keys lie in runs of consecutive records, one per page: lane n
-    // copies run n.  Its page is looked up a tile ahead (`ready`).
-    auto first_page = [&](int j0) {
-      return (int)(__umulhi(2u * (uint32_t)j0, p.page_mul) >> p.page_shift);
-    };
-    auto look_up = [&](int i) {
-      const int j0 = key0 + i * BLOCK, pg = first_page(j0) + lane;
-      return i < nb && j0 + TILE > klo && (int64_t)pg * ps < min(j0 + TILE, khi) ? __ldg(pages + pg) : -1;
-    };
-    int32_t ready = look_up(0);
-    auto issue = [&](int i) {
-      const int stage = put % STAGES, j0 = key0 + i * BLOCK;
-      ++put;
-      const int end = j0 + TILE > klo && !dead ? min(j0 + TILE, khi) : j0;
-      const int pg0 = first_page(j0);
-      uint64_t vm = end - j0 >= 64 ? ~0ull : end > j0 ? (1ull << (end - j0)) - 1 : 0;
-      const int nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(ring + stage * S::TILE_BYTES);
-      bool good = true;
-      for (int n0 = 0; n0 < nruns; n0 += 32) {
-        const int n = n0 + lane;
-        const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(pages + pg0 + n) : 0;
-        const bool ok = n >= nruns || (page >= 0 && page < p.cache.pages);
-        good = good && ok;
-        if (!__all_sync(0xffffffffu, ok)) {  // pages that are none: their keys are hidden
-          if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
-          uint64_t bad = 0;
-          if (!ok) {
-            const int a = max(j0, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
-            bad = (z - a >= 64 ? ~0ull : (1ull << (z - a)) - 1) << a;
-          }
-          for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-          vm &= ~bad;
+  // A unit's part within this CTA's share.
+  struct Segment {
+    int q0, off, row0, rows;   // first token of the sequence, its first query's position; rows of the unit
+    int hk, unit, nb;          // kv head; the unit's number within the sequence; key blocks here
+    int key0, klo, khi;        // this warp's first key; the keys any row sees
+    int pos_a, pos_z;          // positions of the first and last query
+    bool first, whole;         // holds the unit's first block; all of them
+    int last;                  // CTA with the unit's last block (set where first)
+    const int32_t *pages, *base;  // the sequence's page table row; the head's records in page 0
+    int64_t page_stride;
+  };
+  int64_t at = g0;
+  // The next segment of the share and true, or false at its end.
+  auto advance = [&](Segment& x) {
+    while (at < g1) {
+      Seq s = seq_info<RB, TILE>(p, b);
+      while (at >= base + cost(p, s)) {
+        base += cost(p, s);
+        s = seq_info<RB, TILE>(p, ++b);
+      }
+      const int64_t rem = at - base;
+      const int width = s.nblk + UNIT_EXTRA;
+      x.unit = (int)(rem / width);
+      const int blk0 = (int)(rem - (int64_t)x.unit * width);
+      at = min(g1, base + (int64_t)(x.unit + 1) * width);
+      if (blk0 >= s.nblk) continue;  // only the unit's extra
+      x.nb = (int)min((int64_t)(s.nblk - blk0), at - rem - base);
+      x.hk = x.unit / s.nrb;
+      x.row0 = (x.unit - x.hk * s.nrb) * RB;
+      x.rows = min(RB, s.rows - x.row0);
+      x.q0 = s.q0;
+      x.off = s.off;
+      x.pos_a = s.off + x.row0 / p.g;
+      x.pos_z = s.off + (x.row0 + x.rows - 1) / p.g;
+      x.khi = p.causal ? min(s.kv, x.pos_z + 1) : s.kv;
+      x.klo = p.window ? max(0, x.pos_a - p.window + 1) : 0;
+      x.key0 = s.klo + (blk0 * WARPS + warp) * TILE;
+      x.first = blk0 == 0;
+      x.whole = x.first && x.nb == s.nblk;
+      x.last = (int)(((base + (int64_t)x.unit * width + s.nblk) * ncta - 1) / total);
+      x.pages = p.page_table + (int64_t)b * p.table_width;
+      const int slot = x.hk / p.cache.per_slot;
+      x.page_stride = p.cache.page_stride[slot];
+      x.base = p.cache.ptr[slot] + (int64_t)(x.hk - slot * p.cache.per_slot) * p.cache.head_stride[slot];
+      return true;
+    }
+    return false;
+  };
+
+  // A tile's keys lie in runs of consecutive records, one per page: lane n
+  // copies run n.  Its page is looked up a tile ahead (`ready`).
+  auto first_page = [&](int j0) { return (int)(__umulhi(2u * (uint32_t)j0, p.page_mul) >> p.page_shift); };
+  auto look_up = [&](const Segment& x, int i) {
+    const int j0 = x.key0 + i * BLOCK, pg = first_page(j0) + lane;
+    return i < x.nb && j0 + TILE > x.klo && (int64_t)pg * ps < min(j0 + TILE, x.khi) ? __ldg(x.pages + pg) : -1;
+  };
+  int32_t ready;
+  auto issue = [&](const Segment& x, int i) {
+    const int stage = put % STAGES, j0 = x.key0 + i * BLOCK;
+    ++put;
+    const int end = j0 + TILE > x.klo && !dead ? min(j0 + TILE, x.khi) : j0;
+    const int pg0 = first_page(j0);
+    uint64_t vm = end - j0 >= 64 ? ~0ull : end > j0 ? (1ull << (end - j0)) - 1 : 0;
+    const int nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(ring + stage * S::TILE_BYTES);
+    for (int n0 = 0; n0 < nruns; n0 += 32) {
+      const int n = n0 + lane;
+      const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(x.pages + pg0 + n) : 0;
+      const bool ok = n >= nruns || (page >= 0 && page < p.cache.pages);
+      if (!__all_sync(0xffffffffu, ok)) {  // pages that are none: their keys are hidden
+        if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
+        uint64_t bad = 0;
+        if (!ok) {
+          const int a = max(j0, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
+          bad = (z - a >= 64 ? ~0ull : (1ull << (z - a)) - 1) << a;
         }
+        for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+        vm &= ~bad;
       }
-      if (lane == 0) {
-        vmask[stage] = vm;
-        if (!dead) mbar_expect_tx(&bars[stage], __popcll(vm) * W * 4);
-      }
-      __syncwarp();
-      for (int n = lane; n < nruns; n += 32) {
-        const int32_t page = n < 32 ? ready : __ldg(pages + pg0 + n);
-        if (page < 0 || page >= p.cache.pages) continue;
-        const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
-        bulk_load(dst + (a - j0) * W, head_base + page * page_stride + (int64_t)(a - (pg0 + n) * ps) * W,
-                  (z - a) * W * 4, &bars[stage]);
-      }
-      ready = look_up(i + 1);
-      __syncwarp();
-    };
-    issue(0);
+    }
+    if (lane == 0) {
+      vmask[stage] = vm;
+      if (!dead) mbar_expect_tx(&bars[stage], __popcll(vm) * W * 4);
+    }
+    __syncwarp();
+    for (int n = lane; n < nruns; n += 32) {
+      const int32_t page = n < 32 ? ready : __ldg(x.pages + pg0 + n);
+      if (page < 0 || page >= p.cache.pages) continue;
+      const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
+      bulk_load(dst + (a - j0) * W, x.base + page * x.page_stride + (int64_t)(a - (pg0 + n) * ps) * W,
+                (z - a) * W * 4, &bars[stage]);
+    }
+    ready = look_up(x, i + 1);
+    __syncwarp();
+  };
+  // The queries of a segment as loaded (warp nt holds 8 rows).
+  Raw8<T> qraw[WL];
+  auto load_queries = [&](const Segment& x) {
+    const int row = x.row0 + warp * 8 + r;
+    if (warp < NT && warp * 8 + r < x.rows) {
+      const T* q = head_ptr<T>(p.q, x.q0 + row / p.g, x.hk * p.g + row % p.g, D);
+#pragma unroll
+      for (int w = 0; w < WL; ++w) qraw[w].load(q + w / WPG * G + 8 * (ql * WPG + w % WPG));
+    } else {
+#pragma unroll
+      for (int w = 0; w < WL; ++w) qraw[w].zero();
+    }
+  };
+
+  allow_next_kernel();  // the join's CTAs find room as this kernel's leave
+  Segment next;
+  if (!advance(next)) return;
+  ready = look_up(next, 0);
+  load_queries(next);
+  issue(next, 0);
+  while (true) {
+    const Segment s = next;
+    const int nb = s.nb, hk = s.hk, row0 = s.row0, rows = s.rows, pos_a = s.pos_a, pos_z = s.pos_z, key0 = s.key0;
 
     // ---- the queries as matrix operands, and their sums per group: warp nt takes 8 rows
     if (warp < NT) {
-      const int nt = warp, row = row0 + nt * 8 + r;
+      const int nt = warp;
       float x[WL][8];
 #pragma unroll
-      for (int w = 0; w < WL; ++w)
-#pragma unroll
-        for (int c = 0; c < 8; ++c) x[w][c] = 0.f;
-      if (nt * 8 + r < rows) {
-        const T* q = head_ptr<T>(p.q, s.q0 + row / p.g, hk * p.g + row % p.g, D);
-#pragma unroll
-        for (int w = 0; w < WL; ++w) load8(q + w / WPG * G + 8 * (ql * WPG + w % WPG), x[w]);
-      }
+      for (int w = 0; w < WL; ++w) qraw[w].get(x[w]);
       float mult = 1.f;
       if constexpr (!FULL) {
         float top = 0.f;
@@ -470,7 +514,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     float vmult = __uint_as_float(254u << 23);
 
     for (int i = 0; i < nb; ++i) {
-      if (i + 1 < nb) issue(i + 1);
+      if (i + 1 < nb) issue(s, i + 1);
       const int stage = got % STAGES;
       if (!dead && !mbar_wait_warp(&bars[stage], (got / STAGES) & 1, abort_flag, p.wait_limit_ns)) {
         dead = true;
@@ -769,7 +813,14 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
       __syncwarp();  // the stage may be refilled
     }
 
-    // ---- the four warps' sums meet in shared memory
+    // ---- the next segment's first tile and queries are under way before this one is finished
+    const bool more = advance(next);
+    if (more) {
+      ready = look_up(next, 0);
+      issue(next, 0);
+    }
+
+    // ---- the four warps' sums meet in shared memory, each in the stage of its ring that no copy is on its way to
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -782,8 +833,8 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
         }
         if (r == 0) ml[warp * RB + nt * 8 + 2 * ql + e] = make_float2(mx[nt][e], den[nt][e]);
       }
-    __syncthreads();  // every warp is done with its ring
-    float* os = reinterpret_cast<float*>(smem) + warp * RB * D;
+    const int spare = put % STAGES * S::TILE_BYTES;
+    float* os = reinterpret_cast<float*>(ring + spare);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -798,10 +849,9 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
             *reinterpret_cast<float2*>(os + (nt * 8 + 2 * ql + e) * D + ch) =
                 make_float2(fmaf(o[nt][grp][m][e] * even, inv, add), fmaf(o[nt][grp][m][2 + e] * odd, inv, add));
           }
+    if (more) load_queries(next);
     __syncthreads();
-    const bool whole = blk0 == 0 && nb == s.nblk;
-    const bool first = blk0 == 0;  // of the pieces of a split unit
-    const int64_t piece = 2 * (int64_t)blockIdx.x + (first ? 1 : 0);
+    const int64_t piece = 2 * (int64_t)blockIdx.x + (s.first ? 1 : 0);
     for (int x = threadIdx.x; x < rows * (D / 4); x += THREADS) {
       const int row = x / (D / 4), c4 = x - row * (D / 4);
       float m = -INFINITY;
@@ -814,11 +864,11 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
       for (int w = 0; w < WARPS; ++w) {
         const float2 mlw = ml[w * RB + row];
         const float f = ex2(mlw.x - ref);
-        const float4 v = reinterpret_cast<const float4*>(smem)[(w * RB + row) * (D / 4) + c4];
+        const float4 v = reinterpret_cast<const float4*>(smem + w * STAGES * S::TILE_BYTES + spare)[x];
         l += mlw.y * f;
         a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
       }
-      if (whole) {
+      if (s.whole) {
         const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // nothing seen: zeros; NaN stays
         const int qr = row0 + row;
         const int tok = s.q0 + qr / p.g, head = hk * p.g + qr % p.g;
@@ -827,28 +877,19 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
           *reinterpret_cast<uint2*>(y) = make_uint2(pack_bf16(a.x * inv, a.y * inv), pack_bf16(a.z * inv, a.w * inv));
         else
           *reinterpret_cast<float4*>(y) = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        if (p.want_lse && c4 == 0) *head_ptr<float>(p.lse, tok, head, 1) = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+        if (p.want_lse && c4 == 0)
+          *head_ptr<float>(p.lse, tok, head, 1) = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
       } else {
         float* out = p.part + (piece * RB + row) * (D + 4);
         reinterpret_cast<float4*>(out)[c4] = a;
         if (c4 == 0) out[D] = m, out[D + 1] = l;
       }
     }
-    if (threadIdx.x == 0 && first && !whole) {
-      // the CTA whose share holds the unit's last block
-      const int64_t end = base + (int64_t)(unit + 1) * s.nblk - 1;
-      Split sp;
-      sp.unit = unit;
-      sp.q_row = row0;
-      sp.rows = rows;
-      sp.q0 = s.q0;
-      sp.head = hk;
-      sp.last = (int32_t)(((end + 1) * ncta - 1) / total);
-      p.split[blockIdx.x] = sp;
-    }
+    if (threadIdx.x == 0 && s.first && !s.whole)
+      p.split[blockIdx.x] = Split{s.unit, row0, rows, s.q0, hk, s.last};
+    if (!more) break;
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring was written by plain stores
     __syncthreads();
-    at += nb;
   }
   if (dead) {  // copies issued before a wait gave up: a bounded time to land
     const uint64_t t0 = globaltimer();
@@ -868,6 +909,7 @@ __global__ void __launch_bounds__(32 * JOIN_WARPS) kv4_join_kernel(const __grid_
   using S = Shape<D, G, NT, NP>;
   using T = typename std::conditional<NP == 1, __nv_bfloat16, float>::type;
   constexpr int RB = S::RB, C = 8, SEG = D / 4 / C, PL = 32 / C;
+  wait_for_previous_kernel();
   const Split sp = p.split[blockIdx.x];
   if (sp.unit < 0) return;
   const int lane = threadIdx.x & 31, c4 = lane % C, pl = lane / C;
@@ -946,8 +988,8 @@ cudaError_t launch_of(const AttnParams& p, int grid, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   constexpr int WORK = Shape<D, G, NT, NP>::RB * (D / 32);  // warps of a split unit
-  kv4_join_kernel<D, G, NT, NP><<<dim3(grid, (WORK + 2 * JOIN_WARPS - 1) / (2 * JOIN_WARPS)), 32 * JOIN_WARPS, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(kv4_join_kernel<D, G, NT, NP>, dim3(grid, (WORK + 2 * JOIN_WARPS - 1) / (2 * JOIN_WARPS)),
+                          32 * JOIN_WARPS, s, p);
 }
 
 // Rows of a unit: 8 for fp32 (three parts per operand) and for up to 8 rows

@@ -77,32 +77,6 @@ __device__ __forceinline__ void write_dw_part(const NormParams& p, const float* 
   }
 }
 
-template <class T>
-struct Raw8;  // 8 channels as loaded
-template <>
-struct Raw8<__nv_bfloat16> {
-  uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(w[i] << 16);
-      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-  }
-};
-template <>
-struct Raw8<float> {
-  float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  }
-};
-
 // D and rotary multiples of 16, D <= 512, 16-byte aligned heads.
 template <class T, bool BWD, int U>
 __global__ void __launch_bounds__(NR_THREADS) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
@@ -349,6 +323,7 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_co
 // dw of q (blockIdx.y 0) and k (1): the CTAs' sums of one channel, added by
 // one warp in a fixed order.
 __global__ void __launch_bounds__(256) qk_norm_dw_kernel(const __grid_constant__ NormParams p, int nblocks) {
+  wait_for_previous_kernel();
   const int which = blockIdx.y;
   const int b0 = which ? p.blocks_q : 0, b1 = which ? nblocks : p.blocks_q;
   const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
@@ -527,8 +502,7 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
   count_launch();
   if (any_dw) {
-    qk_norm_dw_kernel<<<dim3((D + 7) / 8, n), 256, 0, stream>>>(p, grid);
-    e = cudaGetLastError();
+    e = launch_dependent(qk_norm_dw_kernel, dim3((D + 7) / 8, n), 256, stream, p, grid);
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope dw launch: %s", cudaGetErrorString(e));
     count_launch();
   }
