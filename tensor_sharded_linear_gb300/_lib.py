@@ -76,6 +76,8 @@ class DtError(RuntimeError):
 def load(path: str = LIB_PATH) -> C.CDLL:
     """Load libdt.so; raises if it has not been built (there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

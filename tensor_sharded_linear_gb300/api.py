@@ -118,7 +118,9 @@ def _layout(mesh: DeviceMesh, placements, gshape, dtype, materialize) -> L.Layou
 
 
 def _stream_handle() -> int:
-    return torch.cuda.current_stream().cuda_stream
+    """The current torch stream's cudaStream_t (the raw handle alone: building
+    a torch.cuda.Stream object for it costs several microseconds a call)."""
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 # ---------------------------------------------------------------- DTensor
@@ -145,6 +147,7 @@ class DTensor:
                 raise ValueError("slot dtype")
         self.slots = list(slots)
         self._layout_key = bytes(self._layout)
+        self._desc_cache = None
 
     # -- layout queries (host only)
     @property
@@ -262,10 +265,24 @@ class DTensor:
     def _desc(self):
         """The C descriptor (dt_dtensor) of this tensor.  Built once and kept
         while the slots' addresses and strides stay the same."""
+        return self._described()[0]
+
+    def _arg(self):
+        """The descriptor as an argument of a library call."""
+        return self._described()[1]
+
+    def _described(self):
+        cached = self._desc_cache
+        if cached is not None:
+            seen = cached[2]
+            slots = self.slots
+            if len(slots) == len(seen):
+                for t, (ptr, stride) in zip(slots, seen):
+                    if t.data_ptr() != ptr or t.stride() != stride:
+                        break
+                else:
+                    return cached
         key = self._key()
-        cached = getattr(self, "_desc_cache", None)
-        if cached is not None and cached[0] == key:
-            return cached[1]
         n = max(1, self.nslots)
         ptrs = (C.c_void_p * n)(*[p or None for p, _ in key])
         strides = (C.c_int64 * max(1, self.nslots * len(self.gshape)))(*[d for _, st in key for d in st])
@@ -275,8 +292,8 @@ class DTensor:
         desc.slots = C.cast(ptrs, C.POINTER(C.c_void_p))
         desc.strides = C.cast(strides, C.POINTER(C.c_int64))
         desc._keep = (ptrs, strides)  # keep the arrays alive with the descriptor
-        self._desc_cache = (key, desc)
-        return desc
+        self._desc_cache = (desc, C.byref(desc), [(t.data_ptr(), t.stride()) for t in self.slots])
+        return self._desc_cache
 
     def __repr__(self):
         return f"DTensor(gshape={self.gshape}, placements={self.placements}, mesh={self.mesh.shape}, slots={self.nslots})"
@@ -531,7 +548,7 @@ def tp_attention_projections(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, 
 
 def _ref(t: Optional[DTensor]):
     """A descriptor argument (NULL for None); the DTensor keeps the descriptor alive."""
-    return None if t is None else C.byref(t._desc())
+    return None if t is None else t._arg()
 
 
 def _like(t: DTensor, dtype=None) -> DTensor:

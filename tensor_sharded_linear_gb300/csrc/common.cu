@@ -51,11 +51,21 @@ void count_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
 
 int32_t* device_status_word(int32_t* user) {
   if (user) return user;
+  // the word's address on each device, looked up once
+  static std::atomic<int32_t*> known[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  if (dev >= 0 && dev < 64)
+    if (int32_t* w = known[dev].load(std::memory_order_relaxed)) return w;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_dt_status_word) != cudaSuccess) {
     cudaGetLastError();
     return nullptr;
   }
+  if (dev >= 0 && dev < 64) known[dev].store(static_cast<int32_t*>(p), std::memory_order_relaxed);
   return static_cast<int32_t*>(p);
 }
 
