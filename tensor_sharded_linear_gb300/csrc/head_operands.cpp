@@ -30,7 +30,7 @@ dt_status head_operand(const dt_dtensor* in, const char* what, int tp, int head_
   const int64_t width = L.gshape[last];
   if (width % head_dim != 0)
     return fail(DT_ERR_SHAPE, "%s: last dim %lld is not a multiple of head_dim %d", what, (long long)width, head_dim);
-  if (width / head_dim > (1 << 20)) return fail(DT_ERR_CAPACITY, "%s: more than 2^20 heads", what);
+  if (width / head_dim > MAX_HEADS) return fail(DT_ERR_CAPACITY, "%s: more than %d heads", what, MAX_HEADS);
   const bool sharded = tp >= 0 && L.is_shard(tp, last);
   for (int m = 0; m < L.mesh_ndim; ++m) {
     if (m == tp && sharded) continue;
@@ -52,13 +52,14 @@ dt_status head_operand(const dt_dtensor* in, const char* what, int tp, int head_
   HeadMap& M = out->map;
   M.heads = out->heads;
   M.per_slot = chunk > 0 ? (int32_t)(chunk / head_dim) : 1;
+  M.mul = (uint32_t)(((1ull << 31) + M.per_slot - 1) / M.per_slot);
   out->vec16 = true;
   for (int j = 0; j < parts; ++j) {
     int c[DT_MAX_MESH_DIMS] = {0, 0, 0, 0};
     if (sharded) c[tp] = j;
     const SlotView& v = X.slots[L.slot_of_coords(c)];
-    M.ptr[j] = v.ptr;
-    M.stride[j] = 0;
+    M.slot[j].ptr = v.ptr;
+    M.slot[j].stride = 0;
     if (v.numel == 0) continue;  // an empty slot's strides are arbitrary
     if (v.shape[last] > 1 && v.stride[last] != 1)
       return fail(DT_ERR_UNSUPPORTED, "%s must have unit inner stride", what);
@@ -78,7 +79,7 @@ dt_status head_operand(const dt_dtensor* in, const char* what, int tp, int head_
     }
     if (output && out->tokens > 1 && rs < v.shape[last])
       return fail(DT_ERR_UNSUPPORTED, "%s: rows of an output overlap", what);
-    M.stride[j] = rs;
+    M.slot[j].stride = rs;
     out->vec16 = out->vec16 && reinterpret_cast<uintptr_t>(v.ptr) % 16 == 0 && (rs * L.esize) % 16 == 0;
   }
   out->vec16 = out->vec16 && (head_dim * L.esize) % 16 == 0;

@@ -11,20 +11,25 @@
 namespace dt {
 
 // Where head h of token t lives: slot h / per_slot, at
-// ptr[slot] + (t * stride[slot] + (h % per_slot) * D) * element size.
+// ptr + (t * stride + (h % per_slot) * D) * element size.
 struct HeadMap {
-  char* ptr[DT_MAX_SLOTS];
-  int64_t stride[DT_MAX_SLOTS];  // elements between consecutive tokens
-  int32_t per_slot;              // heads of a full slot
-  int32_t heads;                 // heads in all
+  struct Slot {
+    char* ptr;
+    int64_t stride;  // elements between consecutive tokens
+  } slot[DT_MAX_SLOTS];
+  int32_t per_slot;  // heads of a full slot
+  uint32_t mul;      // ceil(2^31 / per_slot): h / per_slot = umulhi(2 h + 1, mul) for h < 2^15
+  int32_t heads;     // heads in all
 };
+constexpr int MAX_HEADS = 1 << 15;
 
 #ifdef __CUDACC__
-// Element offset-free address of head h of token t.
+// Address of head h of token t.
 template <class T>
 __device__ __forceinline__ T* head_ptr(const HeadMap& m, int64_t t, int h, int d) {
-  const int s = static_cast<unsigned>(h) / static_cast<unsigned>(m.per_slot);
-  return reinterpret_cast<T*>(m.ptr[s]) + t * m.stride[s] + static_cast<int64_t>(h - s * m.per_slot) * d;
+  const int s = __umulhi(2u * (uint32_t)h + 1u, m.mul);
+  const HeadMap::Slot& v = m.slot[s];
+  return reinterpret_cast<T*>(v.ptr) + (t * v.stride + (h - s * m.per_slot) * d);
 }
 #endif
 

@@ -11,6 +11,38 @@
 
 namespace dt {
 
+// Two fp32 numbers in a register pair, and the arithmetic that takes both in
+// one instruction.
+struct f2 {
+  float x, y;
+};
+__device__ __forceinline__ uint64_t f2_bits(f2 a) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a.x), "f"(a.y));
+  return r;
+}
+__device__ __forceinline__ f2 f2_of(uint64_t r) {
+  f2 a;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a.x), "=f"(a.y) : "l"(r));
+  return a;
+}
+__device__ __forceinline__ f2 operator*(f2 a, f2 b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ f2 operator+(f2 a, f2 b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)));
+  return f2_of(r);
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(f2_bits(a)), "l"(f2_bits(b)), "l"(f2_bits(c)));
+  return f2_of(r);
+}
+__device__ __forceinline__ f2 both(float a) { return f2{a, a}; }
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -33,6 +65,11 @@ struct Raw8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void get2(f2 (&v)[4]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
@@ -48,11 +85,26 @@ struct Raw8<float> {
   __device__ __forceinline__ void load(const float* p) {
     a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
   }
+  __device__ __forceinline__ void load_keep(const float* p) {  // what other warps re-read
+    a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void get2(f2 (&v)[4]) const {
+    v[0] = f2{a.x, a.y}, v[1] = f2{a.z, a.w}, v[2] = f2{b.x, b.y}, v[3] = f2{b.z, b.w};
+  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
 };
+
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const f2 (&v)[4]) {
+  __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                                                 pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y)));
+}
+__device__ __forceinline__ void store8(float* p, const f2 (&v)[4]) {
+  __stcs(reinterpret_cast<float4*>(p), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+  __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+}
 
 template <class T>
 __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {

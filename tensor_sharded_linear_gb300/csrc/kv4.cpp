@@ -18,7 +18,7 @@ dt_status kv4_batch(const dt_dtensor* cache, const dt_dtensor* page_table, const
   const int W = kv4_words(D, G);
   if (L.ndim != 4 || L.gshape[3] != W)
     return fail(DT_ERR_SHAPE, "cache must be [pages, heads, page_size, %d] for head_dim %d in groups of %d", W, D, G);
-  if (L.gshape[0] >= (1ll << 31) || L.gshape[1] > (1 << 20) || L.gshape[2] > (1 << 20))
+  if (L.gshape[0] >= (1ll << 31) || L.gshape[1] > MAX_HEADS || L.gshape[2] > (1 << 20))
     return fail(DT_ERR_CAPACITY, "cache dims");
   if (L.gshape[2] < 1) return fail(DT_ERR_SHAPE, "cache: page_size must be at least 1");
   const bool sharded = tp >= 0 && L.is_shard(tp, 1);

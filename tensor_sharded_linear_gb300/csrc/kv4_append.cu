@@ -247,6 +247,7 @@ dt_status append_call(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor
   for (auto& r : rest) {
     r.map->heads = 0;
     r.map->per_slot = 1;
+    r.map->mul = 1u << 31;
     if (!r.d && r.map != &p.v) continue;
     HeadOperand o;
     Layout lo;

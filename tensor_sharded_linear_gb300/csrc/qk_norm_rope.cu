@@ -16,10 +16,12 @@
 // chunks of a head -- the two partners of a rotation, chunk l and chunk
 // l + R/16, so a pair never crosses lanes -- and D/16 lanes hold the head:
 // each access is 16 bytes (bf16), 128 contiguous bytes per 8 lanes.  A warp
-// takes heads of ONE token, so its cos/sin vectors are loaded once and stay
-// in registers, and a CTA takes one tensor (q or k), so the weights do too.
-// The heads a warp takes together (U per lane) put their loads in flight
-// before the first is used.
+// takes heads of ONE token, so its cos/sin vectors are loaded once, with the
+// weight folded in (forward: y = r (P x + Q partner)), and a CTA takes one
+// tensor (q or k), so the weights stay in registers.  The next heads' loads
+// are in flight while the present ones are worked on.  The arithmetic runs on
+// register pairs (fp32x2): with one channel per instruction the forward
+// needs more instructions a byte than an SM issues.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,7 +32,7 @@
 namespace dt {
 namespace {
 
-constexpr int NR_THREADS = 256;
+constexpr int NR_THREADS = 128;
 constexpr int NR_WARPS = NR_THREADS / 32;
 constexpr int NR_MAX_D = 1024;
 
@@ -47,6 +49,7 @@ struct NormParams {
   int64_t tokens;
   int32_t D, rotary, interleaved;
   int32_t blocks_q;  // CTAs [0, blocks_q) work on q, the others on k
+  int32_t inner[2];  // blocks of heads of a warp's unit
   float eps;
   float* part;  // backward: [CTA][D] sums of dw
   int32_t* status;
@@ -77,10 +80,17 @@ __device__ __forceinline__ void write_dw_part(const NormParams& p, const float* 
   }
 }
 
-// D and rotary multiples of 16, D <= 512, 16-byte aligned heads.
-template <class T, bool BWD, int U>
-__global__ void __launch_bounds__(NR_THREADS) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
-  extern __shared__ float nr_acc[];
+// D and rotary multiples of 16, D <= 512, 16-byte aligned heads.  A unit of
+// work is `inner` blocks of heads (SG * U heads each) of one token.
+template <class T, bool BWD>
+struct NormVec {
+  static constexpr int U = sizeof(T) == 2 && !BWD ? 2 : 1;  // heads per lane and step
+};
+
+template <class T, bool BWD, bool INTER>
+__global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
+  constexpr int U = NormVec<T, BWD>::U;
+  extern __shared__ __align__(16) float nr_acc[];  // backward: [NR_WARPS][D] sums; forward: [D] weights
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int L = p.D / 16;
   int LP = 1;
@@ -91,154 +101,192 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_vec_kernel(const __grid_co
   const HeadMap &X = p.x[which], &Y = p.y[which], &G = p.g[which];
   const int rl = p.cos_sin ? p.rotary / 16 : 0;  // lanes that hold rotated pairs
   const bool rot = l < rl;
-  int ca, cb;  // first channels of the lane's two chunks
-  if (p.interleaved || !p.cos_sin) {
-    ca = 16 * l, cb = ca + 8;
-  } else if (rot) {
-    ca = 8 * l, cb = 8 * (l + rl);
-  } else {
-    ca = 16 * l, cb = ca + 8;  // 2 rl chunks are rotated, so chunk 2 l of the rest
-  }
+  // first channels of the lane's two chunks; a pair's partner is in the other
+  // chunk, or (INTER) the neighbour channel.  2 rl chunks are rotated, so the
+  // rest starts at chunk 2 l.
+  const int ca = rot && !INTER ? 8 * l : 16 * l;
+  const int cb = rot && !INTER ? 8 * (l + rl) : ca + 8;
   const bool norm = p.w[which] != nullptr;
-  float wa[8], wb[8], da[8], db[8];
+  f2 wa[4], wb[4], da[4], db[4];
+  if (BWD) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    wa[i] = norm && act ? load_w(p.w[which], p.w_dtype[which], ca + i) : 1.f;
-    wb[i] = norm && act ? load_w(p.w[which], p.w_dtype[which], cb + i) : 1.f;
-    da[i] = db[i] = 0.f;
+    for (int i = 0; i < 4; ++i) {
+      wa[i] = wb[i] = both(1.f), da[i] = db[i] = both(0.f);
+      if (norm && act) {
+        wa[i] = f2{load_w(p.w[which], p.w_dtype[which], ca + 2 * i), load_w(p.w[which], p.w_dtype[which], ca + 2 * i + 1)};
+        wb[i] = f2{load_w(p.w[which], p.w_dtype[which], cb + 2 * i), load_w(p.w[which], p.w_dtype[which], cb + 2 * i + 1)};
+      }
+    }
+  } else {
+    for (int c = threadIdx.x; c < p.D; c += NR_THREADS) nr_acc[c] = norm ? load_w(p.w[which], p.w_dtype[which], c) : 1.f;
+    __syncthreads();
   }
-  const int nb = (X.heads + SG * U - 1) / (SG * U);
-  const int64_t units = p.tokens * nb;
-  const int64_t first = (int64_t)(which ? blockIdx.x - p.blocks_q : blockIdx.x) * NR_WARPS + warp;
-  const int64_t step = (int64_t)(which ? gridDim.x - p.blocks_q : p.blocks_q) * NR_WARPS;
+  const int inner = p.inner[which];
+  const int per_tok = ((X.heads + SG * U - 1) / (SG * U) + inner - 1) / inner;  // units of a token
+  const int step = (which ? gridDim.x - p.blocks_q : p.blocks_q) * NR_WARPS;
+  const int step_tok = step / per_tok, step_blk = step - step_tok * per_tok;  // a stride of units, without a division
   const float inv_d = 1.f / (float)p.D;
-  for (int64_t u = first; u < units; u += step) {
-    const int64_t t = u / nb;
-    const int h0 = (int)(u - t * nb) * (SG * U) + sub;
-    Raw8<T> xa[U], xb[U], ga[BWD ? U : 1], gb[BWD ? U : 1];
+
+  Raw8<T> xa[U], xb[U], ga[U], gb[U];
+  auto load = [&](int64_t t, int block, Raw8<T>(&a)[U], Raw8<T>(&b)[U], Raw8<T>(&c)[U], Raw8<T>(&d)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      if (act && h0 + i * SG < X.heads) {
-        const T* x = head_ptr<T>(X, t, h0 + i * SG, p.D);
-        xa[i].load(x + ca);
-        xb[i].load(x + cb);
+      const int h = (block * U + i) * SG + sub;
+      if (act && h < X.heads) {
+        const T* x = head_ptr<T>(X, t, h, p.D);
+        a[i].load(x + ca);
+        b[i].load(x + cb);
         if (BWD) {
-          const T* g = head_ptr<T>(G, t, h0 + i * SG, p.D);
-          ga[i].load(g + ca);
-          gb[i].load(g + cb);
+          const T* g = head_ptr<T>(G, t, h, p.D);
+          c[i].load(g + ca);
+          d[i].load(g + cb);
         }
-      }
-    }
-    float c8[8], s8[8];
-    bool ok = true;
-    if (p.cos_sin) {
-      const int64_t row = table_row(p, t, lane == 0);
-      ok = row >= 0;
-      if (rot && ok) {
-        load8_keep(p.cos_sin + row * p.rotary + 8 * l, c8);
-        load8_keep(p.cos_sin + row * p.rotary + p.rotary / 2 + 8 * l, s8);
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int h = h0 + i * SG;
-      const bool on = act && h < X.heads;
-      float a[8], b[8], dya[8], dyb[8];
-      if (on) {
-        xa[i].get(a);
-        xb[i].get(b);
-        if (BWD) ga[i].get(dya), gb[i].get(dyb);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = b[e] = dya[e] = dyb[e] = 0.f;
+        a[i].zero(), b[i].zero();
+        if (BWD) c[i].zero(), d[i].zero();
       }
-      if (BWD && rot && ok) {  // dz = R^T dy
-        if (p.interleaved) {
+    }
+  };
+  const int u0 = (which ? blockIdx.x - p.blocks_q : blockIdx.x) * NR_WARPS + warp;
+  int64_t t = u0 / per_tok;
+  int blk = u0 - (int)t * per_tok;  // unit blk of token t
+  int64_t row_next = 0;
+  if (t < p.tokens) {
+    load(t, blk * inner, xa, xb, ga, gb);
+    if (p.cos_sin) row_next = table_row(p, t, lane == 0);
+  }
+  while (t < p.tokens) {
+    const int64_t row = row_next;
+    const bool ok = row >= 0;
+    f2 c2[4], s2[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c2[i] = both(1.f), s2[i] = both(0.f);
+    if (rot && ok) {
+      Raw8<float> c, s;
+      c.load_keep(p.cos_sin + row * p.rotary + 8 * l);
+      s.load_keep(p.cos_sin + row * p.rotary + p.rotary / 2 + 8 * l);
+      c.get2(c2);
+      s.get2(s2);
+    }
+    int64_t tn = t + step_tok;
+    int bn = blk + step_blk;
+    if (bn >= per_tok) bn -= per_tok, ++tn;
+    if (tn < p.tokens && p.cos_sin) row_next = table_row(p, tn, lane == 0);
+    // pair e of chunk a has the cosines cosa(e), of chunk b cosb(e)
+    auto at = [](const f2(&v)[4], int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; };
+    auto cosa = [&](int e) { return INTER ? both(at(c2, e)) : c2[e]; };
+    auto cosb = [&](int e) { return INTER ? both(at(c2, 4 + e)) : c2[e]; };
+    auto sina = [&](int e) { return INTER ? both(at(s2, e)) : s2[e]; };
+    auto sinb = [&](int e) { return INTER ? both(at(s2, 4 + e)) : s2[e]; };
+    auto swap = [](f2 v) { return f2{v.y, v.x}; };
+    // forward: y = P x + Q partner with the weights in P and Q
+    f2 pa[4], pb[4], qa[4], qb[4];
+    if (!BWD) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f2 va = act ? *reinterpret_cast<const f2*>(nr_acc + ca + 2 * e) : both(0.f);
+        const f2 vb = act ? *reinterpret_cast<const f2*>(nr_acc + cb + 2 * e) : both(0.f);
+        pa[e] = cosa(e) * va, pb[e] = cosb(e) * vb;
+        qa[e] = INTER ? sina(e) * f2{-va.y, va.x} : sina(e) * vb * both(-1.f);
+        qb[e] = INTER ? sinb(e) * f2{-vb.y, vb.x} : sinb(e) * va;
+      }
+    }
+    for (int in = 0; in < inner; ++in) {
+      const int block = blk * inner + in;
+      Raw8<T> nxa[U], nxb[U], nga[U], ngb[U];
+      if (in + 1 < inner) load(t, block + 1, nxa, nxb, nga, ngb);
+      else if (tn < p.tokens) load(tn, bn * inner, nxa, nxb, nga, ngb);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int h = (block * U + i) * SG + sub;
+        f2 a[4], b[4], ya[4], yb[4];
+        xa[i].get2(a);
+        xb[i].get2(b);
+        float r = 1.f;
+        if (norm) {
+          f2 ss = a[0] * a[0];
+#pragma unroll
+          for (int e = 1; e < 4; ++e) ss = fma2(a[e], a[e], ss);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) ss = fma2(b[e], b[e], ss);
+          float s = ss.x + ss.y;
+          for (int o = LP >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+          r = rsqrtf(s * inv_d + p.eps);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a[e] = a[e] * both(r), b[e] = b[e] * both(r);
+        }
+        if (!BWD) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            rotate_pair(dya[2 * e], dya[2 * e + 1], c8[e], -s8[e]);
-            rotate_pair(dyb[2 * e], dyb[2 * e + 1], c8[4 + e], -s8[4 + e]);
+            ya[e] = fma2(INTER ? swap(a[e]) : b[e], qa[e], a[e] * pa[e]);
+            yb[e] = fma2(INTER ? swap(b[e]) : a[e], qb[e], b[e] * pb[e]);
           }
         } else {
+          f2 dya[4], dyb[4];  // dz = R^T dy
+          ga[i].get2(dya);
+          gb[i].get2(dyb);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) rotate_pair(dya[e], dyb[e], c8[e], -s8[e]);
-        }
-      }
-      float r = 1.f, gx = 0.f;
-      if (norm) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          ss += a[e] * a[e] + b[e] * b[e];
-          if (BWD) gx += dya[e] * wa[e] * a[e] + dyb[e] * wb[e] * b[e];
-        }
-        for (int o = LP >> 1; o; o >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          if (BWD) gx += __shfl_xor_sync(0xffffffffu, gx, o);
-        }
-        r = rsqrtf(ss * inv_d + p.eps);
-      }
-      if (!on) continue;
-      T* y = head_ptr<T>(Y, t, h, p.D);
-      if (BWD) {
-        const float k = gx * r * inv_d;  // mean of g * x r
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float na = a[e] * r, nb_ = b[e] * r;
-          if (norm && ok) {
-            da[e] += dya[e] * na;
-            db[e] += dyb[e] * nb_;
-            a[e] = r * (dya[e] * wa[e] - na * k);
-            b[e] = r * (dyb[e] * wb[e] - nb_ * k);
-          } else {
-            a[e] = dya[e];
-            b[e] = dyb[e];
+          for (int e = 0; e < 4; ++e) {
+            if (INTER) {
+              ya[e] = fma2(f2{dya[e].y, -dya[e].x}, sina(e), dya[e] * cosa(e));
+              yb[e] = fma2(f2{dyb[e].y, -dyb[e].x}, sinb(e), dyb[e] * cosb(e));
+            } else {
+              ya[e] = fma2(dyb[e], s2[e], dya[e] * c2[e]);
+              yb[e] = fma2(dya[e] * both(-1.f), s2[e], dyb[e] * c2[e]);
+            }
           }
-        }
-      } else {
-        if (norm) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = a[e] * r * wa[e];
-            b[e] = b[e] * r * wb[e];
-          }
-        }
-        if (rot) {
-          if (p.interleaved) {
+          if (norm) {
+            const f2 on = both(ok ? 1.f : 0.f);
+            f2 gx = both(0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              rotate_pair(a[2 * e], a[2 * e + 1], c8[e], s8[e]);
-              rotate_pair(b[2 * e], b[2 * e + 1], c8[4 + e], s8[4 + e]);
+              const f2 ta = ya[e] * a[e], tb = yb[e] * b[e];
+              da[e] = fma2(ta, on, da[e]), db[e] = fma2(tb, on, db[e]);
+              gx = fma2(ta, wa[e], gx), gx = fma2(tb, wb[e], gx);
             }
-          } else {
+            float k = gx.x + gx.y;
+            for (int o = LP >> 1; o; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
+            k *= -r * inv_d;  // - r * mean(g * x r)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) rotate_pair(a[e], b[e], c8[e], s8[e]);
+            for (int e = 0; e < 4; ++e) {
+              ya[e] = fma2(a[e], both(k), ya[e] * (wa[e] * both(r)));
+              yb[e] = fma2(b[e], both(k), yb[e] * (wb[e] * both(r)));
+            }
           }
         }
-      }
-      if (!ok) {  // no such position: the row is zero, as an embedding row of a bad id
+        if (!act || h >= X.heads) continue;
+        if (!ok) {  // no such position: the row is zero, as an embedding row of a bad id
 #pragma unroll
-        for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;
+          for (int e = 0; e < 4; ++e) ya[e] = yb[e] = both(0.f);
+        }
+        T* y = head_ptr<T>(Y, t, h, p.D);
+        store8(y + ca, ya);
+        store8(y + cb, yb);
       }
-      store8(y + ca, a);
-      store8(y + cb, b);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        xa[i] = nxa[i], xb[i] = nxb[i];
+        if (BWD) ga[i] = nga[i], gb[i] = ngb[i];
+      }
     }
+    t = tn;
+    blk = bn;
   }
   if (BWD && p.part) {
     // the subgroups' sums, then the warps', in a fixed order: the same
     // inputs give the same bits
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int e = 0; e < 4; ++e) {
       for (int o = LP; o < 32; o <<= 1) {
-        da[e] += __shfl_xor_sync(0xffffffffu, da[e], o);
-        db[e] += __shfl_xor_sync(0xffffffffu, db[e], o);
+        da[e].x += __shfl_xor_sync(0xffffffffu, da[e].x, o), da[e].y += __shfl_xor_sync(0xffffffffu, da[e].y, o);
+        db[e].x += __shfl_xor_sync(0xffffffffu, db[e].x, o), db[e].y += __shfl_xor_sync(0xffffffffu, db[e].y, o);
       }
     }
     if (act && sub == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        nr_acc[warp * p.D + ca + e] = da[e];
-        nr_acc[warp * p.D + cb + e] = db[e];
+      for (int e = 0; e < 4; ++e) {
+        *reinterpret_cast<f2*>(nr_acc + warp * p.D + ca + 2 * e) = da[e];
+        *reinterpret_cast<f2*>(nr_acc + warp * p.D + cb + 2 * e) = db[e];
       }
     }
     write_dw_part(p, nr_acc);
@@ -362,16 +410,16 @@ dt_status norm_weight(const dt_dtensor* w, const char* what, const Layout& of, i
 // CTAs of a launch over tokens * heads head rows: enough to fill the device,
 // fewer when there are not that many units of work.
 int norm_blocks(int64_t units) {
-  const int64_t full = std::min<int64_t>((int64_t)device_sm_count() * 8, NR_MAX_BLOCKS / 2);
+  const int64_t full = std::min<int64_t>((int64_t)device_sm_count() * 4, NR_MAX_BLOCKS / 2);
   return (int)std::max<int64_t>(1, std::min<int64_t>((units + NR_WARPS - 1) / NR_WARPS, full));
 }
 
 template <class T, bool BWD>
-void launch_norm(const NormParams& p, bool vec, int U, int grid, cudaStream_t s) {
-  const size_t smem = BWD && p.part ? (size_t)NR_WARPS * p.D * sizeof(float) : 0;
-  if (!vec) qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
-  else if (U == 1) qk_norm_vec_kernel<T, BWD, 1><<<grid, NR_THREADS, smem, s>>>(p);
-  else qk_norm_vec_kernel<T, BWD, 2><<<grid, NR_THREADS, smem, s>>>(p);
+void launch_norm(const NormParams& p, bool vec, int grid, cudaStream_t s) {
+  const size_t smem = (size_t)p.D * sizeof(float) * (!BWD ? 1 : p.part ? NR_WARPS : 0);
+  if (vec && p.interleaved) qk_norm_vec_kernel<T, BWD, true><<<grid, NR_THREADS, smem, s>>>(p);
+  else if (vec) qk_norm_vec_kernel<T, BWD, false><<<grid, NR_THREADS, smem, s>>>(p);
+  else qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
 }
 
 dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleaved, int tp, void* ws, size_t ws_bytes,
@@ -463,20 +511,29 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
   const int heads_k = n == 2 ? x[1].heads : 0;
   const bool nothing = p.tokens == 0 || x[0].heads + heads_k == 0;
   if (nothing && !any_dw) return DT_OK;
-  // one warp's work: U heads per subgroup of lanes (or one head).  Two heads
-  // per lane once every warp of a full device has several units.
+  // A warp's unit is as many blocks of heads of one token as leave eight
+  // units for every warp of a full device: the token's angles are fetched
+  // once for them (measured at 8192 tokens x 64 heads, backward: 139.8 us
+  // with one block a unit).
   int LP = 1;
   while (LP < D / 16) LP <<= 1;
-  const int SG = vec ? 32 / LP : 1;
-  const int64_t rows = p.tokens * ((int64_t)x[0].heads + heads_k);
-  const int64_t warps = (int64_t)device_sm_count() * 8 * NR_WARPS;
-  const int U = vec && rows / SG >= 4 * warps ? 2 : 1;
-  const int64_t uq = p.tokens * ((x[0].heads + SG * U - 1) / (SG * U));
-  const int64_t uk = p.tokens * ((heads_k + SG * U - 1) / (SG * U));
-  const int total = norm_blocks(uq + uk);
-  int bq = (int)((double)total * (double)uq / (double)std::max<int64_t>(1, uq + uk) + 0.5);
+  const int U = x[0].dtype == DT_BF16 && !bwd ? NormVec<__nv_bfloat16, false>::U : NormVec<float, true>::U;
+  const int per_block = vec ? 32 / LP * U : 1;
+  const int64_t all = std::max<int64_t>(1, (int64_t)x[0].heads + heads_k);
+  int64_t units[2];
+  for (int i = 0; i < 2; ++i) {
+    const int heads = i ? heads_k : x[0].heads, blocks = std::max(1, (heads + per_block - 1) / per_block);
+    const int64_t warps = (int64_t)device_sm_count() * 4 * NR_WARPS * heads / all;
+    p.inner[i] = 1;
+    while (vec && p.inner[i] < blocks && p.tokens * ((blocks + 2 * p.inner[i] - 1) / (2 * p.inner[i])) >= 8 * warps)
+      p.inner[i] *= 2;
+    units[i] = heads ? p.tokens * ((blocks + p.inner[i] - 1) / p.inner[i]) : 0;
+  }
+  // CTAs in proportion to the heads
+  const int total = norm_blocks(units[0] + units[1]);
+  int bq = (int)((double)total * (double)x[0].heads / (double)all + 0.5);
   bq = std::max(1, std::min(bq, total));
-  int bk = uk > 0 ? std::max(1, total - bq) : 0;
+  const int bk = units[1] > 0 ? std::max(1, total - bq) : 0;
   p.blocks_q = bq;
   const int grid = bq + bk;
   if (any_dw) {
@@ -486,17 +543,17 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
     if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(DT_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
     p.part = static_cast<float*>(ws);
   }
-  if ((st = bind_device_of(x[0].heads && p.tokens ? p.y[0].ptr[0] : any_dw ? p.dw[0] ? p.dw[0] : p.dw[1] : nullptr)) !=
+  if ((st = bind_device_of(x[0].heads && p.tokens ? p.y[0].slot[0].ptr : any_dw ? p.dw[0] ? p.dw[0] : p.dw[1] : nullptr)) !=
       DT_OK)
     return st;
   p.status = device_status_word(d_status);
   if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
   if (x[0].dtype == DT_BF16) {
-    if (bwd) launch_norm<__nv_bfloat16, true>(p, vec, U, grid, stream);
-    else launch_norm<__nv_bfloat16, false>(p, vec, U, grid, stream);
+    if (bwd) launch_norm<__nv_bfloat16, true>(p, vec, grid, stream);
+    else launch_norm<__nv_bfloat16, false>(p, vec, grid, stream);
   } else {
-    if (bwd) launch_norm<float, true>(p, vec, U, grid, stream);
-    else launch_norm<float, false>(p, vec, U, grid, stream);
+    if (bwd) launch_norm<float, true>(p, vec, grid, stream);
+    else launch_norm<float, false>(p, vec, grid, stream);
   }
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
