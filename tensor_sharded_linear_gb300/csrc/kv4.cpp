@@ -49,6 +49,10 @@ dt_status kv4_batch(const dt_dtensor* cache, const dt_dtensor* page_table, const
         (v.shape[1] > 1 && v.stride[1] % 4))
       return fail(DT_ERR_ALIGNMENT, "cache: records must start on 16-byte boundaries");
   }
+  // m = ceil(2^(31 + s) / d) with 2^s >= d: j m / 2^(31 + s) has the floor of j / d for every j < 2^31
+  out->page_shift = 0;
+  while ((1 << out->page_shift) < M.page_size) ++out->page_shift;
+  out->page_mul = (uint32_t)(((1ull << (31 + out->page_shift)) + M.page_size - 1) / M.page_size);
   PlainOperand pt, kl, qs;
   if ((st = plain_operand(page_table, "page_table", mesh_of, false, &pt)) != DT_OK) return st;
   if (pt.dtype != DT_INT32) return fail(DT_ERR_INVALID_ARG, "page_table must be int32");

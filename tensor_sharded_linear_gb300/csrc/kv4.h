@@ -48,6 +48,7 @@ struct Kv4Batch {
   const int32_t* q_starts;
   int32_t batch, table_width, q_len;
   int32_t capacity;  // keys a row of the page table can address
+  uint32_t page_mul, page_shift;  // j / page_size = umulhi(2 j, page_mul) >> page_shift for j < 2^31
 };
 dt_status kv4_batch(const dt_dtensor* cache, const dt_dtensor* page_table, const dt_dtensor* kv_lens,
                     const dt_dtensor* q_starts, int tp, int D, int G, int64_t tokens, const Layout& mesh_of,

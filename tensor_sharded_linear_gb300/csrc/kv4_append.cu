@@ -19,8 +19,11 @@
 // Layout.  D/16 lanes hold a head row, two chunks of 8 channels each: chunk
 // l and chunk l + D/16, the partners of a full rotation.  The codes of a
 // chunk are one word of the record, and a group's minimum and maximum are a
-// few shuffles (a group of 64 is 8 neighbouring lanes' chunk).  A warp takes
-// rows of one token: sequence, position and page are looked up once per warp.
+// few shuffles (a group of 64 is 8 neighbouring lanes' chunk).  A block is
+// the rows of one kind (q, k or v) that a warp holds at a time; a warp takes
+// `inner` blocks of one token, so its sequence, position, page and angles
+// are looked up once for them, and the next block's loads are in flight while
+// the present one is worked on.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -33,7 +36,8 @@
 namespace dt {
 namespace {
 
-constexpr int AP_THREADS = 256;
+constexpr int AP_THREADS = 128;
+constexpr int AP_CTAS = 5;  // per SM
 constexpr int AP_WARPS = AP_THREADS / 32;
 
 struct AppendParams {
@@ -42,10 +46,12 @@ struct AppendParams {
   SeqTable seq;
   const int32_t* page_table;
   int32_t table_width;
+  uint32_t page_mul, page_shift;  // division by the page size (Kv4Batch)
   const float* cos_sin;  // NULL: no rotation
   int64_t table_rows;
   int32_t rotary, interleaved;
   int32_t has_stored;
+  int32_t inner;  // blocks of a warp's unit
   int32_t* status;
 };
 
@@ -102,8 +108,10 @@ __device__ __forceinline__ void rotate_row(const AppendParams& p, const T* x, co
   }
 }
 
-// Codes and parameters of one chunk whose group spans `lanes` neighbouring
-// lanes and `both` chunks; y becomes the values as the cache holds them.
+// Codes and parameters of one chunk of a group with minimum lo and maximum
+// hi; y becomes the values as the cache holds them.  A number in [0, 15] is
+// rounded to nearest even by adding 1.5 * 2^23, whose sum has it in its low
+// bits.
 __device__ __forceinline__ void quantise(float lo, float hi, float (&y)[8], uint32_t* word, uint32_t* param) {
   float m = __bfloat162float(__float2bfloat16_rn(lo));
   float s = __bfloat162float(__float2bfloat16_rn(__fmul_rn(__fsub_rn(hi, lo), 0.06666667014360428f)));
@@ -112,104 +120,162 @@ __device__ __forceinline__ void quantise(float lo, float hi, float (&y)[8], uint
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float c = fminf(fmaxf(rintf(__fmul_rn(__fsub_rn(y[e], m), inv)), 0.f), 15.f);  // NaN -> 0
-    w |= static_cast<uint32_t>(c) << (4 * e);
-    y[e] = __fadd_rn(__fmul_rn(c, s), m);
+    const float x = fminf(fmaxf(__fmul_rn(__fsub_rn(y[e], m), inv), 0.f), 15.f);  // NaN -> 0
+    const float c = __fadd_rn(x, 12582912.f);
+    w |= (__float_as_uint(c) & 15u) << (4 * e);
+    y[e] = __fadd_rn(__fmul_rn(__fsub_rn(c, 12582912.f), s), m);
   }
   *word = w;
   *param = (__float_as_uint(s) >> 16) | (__float_as_uint(m) & 0xffff0000u);
 }
 
 template <class T, int D, int G>
-__global__ void __launch_bounds__(AP_THREADS) kv4_append_kernel(const __grid_constant__ AppendParams p, int units) {
+__global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int L = D / 16, SG = 32 / L, W = kv4_words(D, G), NG = D / G;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / L, l = lane % L;
-  const int rows = p.q.heads + 2 * p.cache.heads;  // q heads, key heads, value heads
-  const int64_t total = (int64_t)p.seq.tokens * units;
-  for (int64_t w = (int64_t)blockIdx.x * AP_WARPS + warp; w < total; w += (int64_t)gridDim.x * AP_WARPS) {
-    const int t = (int)(w / units);
-    const int row = (int)(w - (int64_t)t * units) * SG + sub;
-    const int hk = p.cache.heads, hq = p.q.heads;
-    const int kind = row < hq ? 0 : row < hq + hk ? 1 : row < rows ? 2 : 3;
-    const int h = kind == 0 ? row : kind == 1 ? row - hq : row - hq - hk;
-    // the row's loads go out before its token is looked up
-    const T* x = nullptr;
-    float a[8], b[8];
-    if (kind < 3) {
-      x = kind == 0 ? head_ptr<T>(p.q, t, h, D) : kind == 1 ? head_ptr<T>(p.k, t, h, D) : head_ptr<T>(p.v, t, h, D);
-      load8(x + 8 * l, a);
-      load8(x + 8 * (l + L), b);
-    }
+  const int hk = p.cache.heads, hq = p.q.heads;
+  const int nq = (hq + SG - 1) / SG, nk = (hk + SG - 1) / SG;  // blocks of q, of k and of v
+  const int blocks = nq + 2 * nk;
+  const int per_tok = (blocks + p.inner - 1) / p.inner;  // units of a token
+  const int step = gridDim.x * AP_WARPS;
+  const int step_tok = step / per_tok, step_blk = step - step_tok * per_tok;
+  const bool full_rot = p.cos_sin && !p.interleaved && p.rotary == D;
+
+  // block n: its kind (0 q, 1 k, 2 v) and this lane's head, the last one again where there is none
+  auto kind_of = [&](int n) { return n < nq ? 0 : n < nq + nk ? 1 : 2; };
+  auto head_of = [&](int n, int kind) { return (n - (kind == 0 ? 0 : kind == 1 ? nq : nq + nk)) * SG + sub; };
+  auto row_of = [&](int64_t t, int n) {
+    const int kind = kind_of(n), h = head_of(n, kind);
+    return kind == 0 ? head_ptr<T>(p.q, t, min(h, hq - 1), D)
+                     : head_ptr<T>(kind == 1 ? p.k : p.v, t, min(h, hk - 1), D);
+  };
+
+  const int u0 = blockIdx.x * AP_WARPS + warp;
+  int t = u0 / per_tok, unit = u0 - t * per_tok;
+  Raw8<T> xa, xb;
+  if (t < p.seq.tokens) {
+    const T* x = row_of(t, unit * p.inner);
+    xa.load(x + 8 * l);
+    xb.load(x + 8 * (l + L));
+  }
+  while (t < p.seq.tokens) {
+    int tn = t + step_tok, un = unit + step_blk;
+    if (un >= per_tok) un -= per_tok, ++tn;
+    // the token's sequence, position, page and angles
     const int sq = warp_seq_of_token(p.seq, t, lane);
-    if (sq < 0) continue;  // a row of no sequence: nothing is written for it
-    const int s0 = p.seq.start(sq);
-    const int pos = p.seq.keys(sq) - (p.seq.start(sq + 1) - s0) + (t - s0);
-    const bool in_table = !p.cos_sin || (pos >= 0 && pos < p.table_rows);
-    const int32_t page = pos >= 0 && pos < p.seq.capacity ? __ldg(p.page_table + (int64_t)sq * p.table_width + pos / p.cache.page_size) : -1;
-    const bool in_cache = page >= 0 && page < p.cache.pages;
-    if (lane == 0 && (!in_table || !in_cache || __ldg(p.seq.kv_lens + sq) != p.seq.keys(sq)))
-      atomicOr(p.status, DT_DEV_ERR_INDEX);
-    if (kind < 2 && p.cos_sin && in_table) rotate_row<T, D>(p, x, p.cos_sin + (int64_t)pos * p.rotary, l, a, b);
-    if (!in_table) {
+    int pos = -1;
+    int32_t page = -1;
+    bool in_table = false;
+    f2 c2[4], s2[4];
+    if (sq >= 0) {
+      const int s0 = p.seq.start(sq);
+      pos = p.seq.keys(sq) - (p.seq.start(sq + 1) - s0) + (t - s0);
+      in_table = !p.cos_sin || (pos >= 0 && pos < p.table_rows);
+      if (pos >= 0 && pos < p.seq.capacity) {
+        const int pg = __umulhi(2u * (uint32_t)pos, p.page_mul) >> p.page_shift;
+        page = __ldg(p.page_table + (int64_t)sq * p.table_width + pg);
+      }
+      if (full_rot && in_table) {
+        Raw8<float> c, s;
+        c.load_keep(p.cos_sin + (int64_t)pos * D + 8 * l);
+        s.load_keep(p.cos_sin + (int64_t)pos * D + D / 2 + 8 * l);
+        c.get2(c2);
+        s.get2(s2);
+      }
+      if (lane == 0 && (!in_table || page < 0 || page >= p.cache.pages || __ldg(p.seq.kv_lens + sq) != p.seq.keys(sq)))
+        atomicOr(p.status, DT_DEV_ERR_INDEX);
+    }
+    const bool to_cache = in_table && page >= 0 && page < p.cache.pages;
+    const int last = min((unit + 1) * p.inner, blocks);
+    for (int n = unit * p.inner; n < last; ++n) {
+      const int kind = kind_of(n), h = head_of(n, kind);
+      const bool on = h < (kind == 0 ? hq : hk) && sq >= 0;  // (a row of no sequence: nothing is written for it)
+      f2 a2[4], b2[4];
+      xa.get2(a2);
+      xb.get2(b2);
+      if (n + 1 < last || tn < p.seq.tokens) {
+        const T* x = n + 1 < last ? row_of(t, n + 1) : row_of(tn, un * p.inner);
+        xa.load(x + 8 * l);
+        xb.load(x + 8 * (l + L));
+      }
+      if (kind < 2 && full_rot) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;
-    }
-    if (kind == 0) {
-      T* y = head_ptr<T>(p.q_out, t, h, D);
-      store8(y + 8 * l, a);
-      store8(y + 8 * (l + L), b);
-    }
-    // every lane takes part in the shuffles below
-    float la = INFINITY, ha = -INFINITY, lb = INFINITY, hb = -INFINITY;
-    if (kind == 1 || kind == 2) {
-      la = ha = a[0], lb = hb = b[0];
+        for (int e = 0; e < 4; ++e) {
+          rotate_pair(a2[e].x, b2[e].x, c2[e].x, s2[e].x);
+          rotate_pair(a2[e].y, b2[e].y, c2[e].y, s2[e].y);
+        }
+      }
+      float a[8], b[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) a[2 * e] = a2[e].x, a[2 * e + 1] = a2[e].y, b[2 * e] = b2[e].x, b[2 * e + 1] = b2[e].y;
+      if (kind < 2 && p.cos_sin && !full_rot && in_table)
+        rotate_row<T, D>(p, row_of(t, n), p.cos_sin + (int64_t)pos * p.rotary, l, a, b);
+      if (!in_table) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = b[e] = 0.f;
+      }
+      if (kind == 0) {
+        if (on) {
+          T* y = head_ptr<T>(p.q_out, t, h, D);
+          store8(y + 8 * l, a);
+          store8(y + 8 * (l + L), b);
+        }
+        continue;
+      }
+      float la = a[0], ha = a[0], lb = b[0], hb = b[0];
 #pragma unroll
       for (int e = 1; e < 8; ++e) {
         la = min_nan(la, a[e]), ha = max_nan(ha, a[e]);
         lb = min_nan(lb, b[e]), hb = max_nan(hb, b[e]);
       }
-    }
-    if constexpr (D == 64 && G == 64) {  // both chunks are in the one group
-      la = lb = min_nan(la, lb);
-      ha = hb = max_nan(ha, hb);
-    }
-    constexpr int SPAN = (D == 64 && G == 64) ? L : (G / 8 < L ? G / 8 : L);  // lanes of a group
+      if constexpr (D == 64 && G == 64) {  // both chunks are in the one group
+        la = lb = min_nan(la, lb);
+        ha = hb = max_nan(ha, hb);
+      }
+      constexpr int SPAN = G / 8 < L ? G / 8 : L;  // lanes of a group
 #pragma unroll
-    for (int o = SPAN >> 1; o; o >>= 1) {
-      la = min_nan(la, __shfl_xor_sync(0xffffffffu, la, o)), ha = max_nan(ha, __shfl_xor_sync(0xffffffffu, ha, o));
-      lb = min_nan(lb, __shfl_xor_sync(0xffffffffu, lb, o)), hb = max_nan(hb, __shfl_xor_sync(0xffffffffu, hb, o));
+      for (int o = SPAN >> 1; o; o >>= 1) {
+        la = min_nan(la, __shfl_xor_sync(0xffffffffu, la, o)), ha = max_nan(ha, __shfl_xor_sync(0xffffffffu, ha, o));
+        lb = min_nan(lb, __shfl_xor_sync(0xffffffffu, lb, o)), hb = max_nan(hb, __shfl_xor_sync(0xffffffffu, hb, o));
+      }
+      if (!on) continue;
+      uint32_t wa, wb, pa, pb;
+      quantise(la, ha, a, &wa, &pa);
+      quantise(lb, hb, b, &wb, &pb);
+      if (p.has_stored) {
+        T* y = head_ptr<T>(kind == 1 ? p.k_st : p.v_st, t, h, D);
+        store8(y + 8 * l, a);
+        store8(y + 8 * (l + L), b);
+      }
+      if (!to_cache) continue;
+      const int in_page = pos - (int)(__umulhi(2u * (uint32_t)pos, p.page_mul) >> p.page_shift) * p.cache.page_size;
+      uint32_t* rec = reinterpret_cast<uint32_t*>(cache_page(p.cache, page, h)) + (int64_t)in_page * W;
+      uint32_t* codes = rec + (kind == 2 ? D / 8 : 0);
+      uint32_t* params = rec + D / 4 + (kind == 2 ? NG : 0);
+      codes[l] = wa;
+      codes[l + L] = wb;
+      if (8 * l % G == 0) params[8 * l / G] = pa;
+      if (8 * (l + L) % G == 0) params[8 * (l + L) / G] = pb;
+      if (kind == 2 && l < W - D / 4 - 2 * NG) rec[D / 4 + 2 * NG + l] = 0;  // padding
     }
-    if (kind != 1 && kind != 2) continue;
-    uint32_t wa, wb, pa, pb;
-    quantise(la, ha, a, &wa, &pa);
-    quantise(lb, hb, b, &wb, &pb);
-    if (p.has_stored) {
-      T* y = kind == 1 ? head_ptr<T>(p.k_st, t, h, D) : head_ptr<T>(p.v_st, t, h, D);
-      store8(y + 8 * l, a);
-      store8(y + 8 * (l + L), b);
-    }
-    if (!in_cache || !in_table) continue;
-    uint32_t* rec = reinterpret_cast<uint32_t*>(cache_page(p.cache, page, h)) +
-                    (int64_t)(pos % p.cache.page_size) * W;
-    uint32_t* codes = rec + (kind == 2 ? D / 8 : 0);
-    uint32_t* params = rec + D / 4 + (kind == 2 ? NG : 0);
-    codes[l] = wa;
-    codes[l + L] = wb;
-    if (8 * l % G == 0) params[8 * l / G] = pa;
-    if (8 * (l + L) % G == 0) params[8 * (l + L) / G] = pb;
-    if (kind == 2 && l < W - D / 4 - 2 * NG) rec[D / 4 + 2 * NG + l] = 0;  // padding
+    t = tn;
+    unit = un;
   }
 }
 
 template <class T>
-void launch_append(const AppendParams& p, int D, int G, cudaStream_t s) {
+void launch_append(AppendParams& p, int D, int G, cudaStream_t s) {
   const int SG = 32 / (D / 16);
-  const int units = (p.q.heads + 2 * p.cache.heads + SG - 1) / SG;
-  const int64_t warps = (int64_t)p.seq.tokens * units;
-  const int grid = (int)std::min<int64_t>((warps + AP_WARPS - 1) / AP_WARPS, (int64_t)device_sm_count() * 32);
+  const int blocks = (p.q.heads + SG - 1) / SG + 2 * ((p.cache.heads + SG - 1) / SG);
+  // as many blocks of a token to a unit as leave four units for every warp of a full device
+  const int64_t warps = (int64_t)device_sm_count() * AP_CTAS * AP_WARPS;
+  p.inner = 1;
+  while (p.inner < blocks && p.seq.tokens * (int64_t)((blocks + 2 * p.inner - 1) / (2 * p.inner)) >= 4 * warps) p.inner *= 2;
+  const int64_t units = (int64_t)p.seq.tokens * ((blocks + p.inner - 1) / p.inner);
+  const int grid = (int)std::min<int64_t>((units + AP_WARPS - 1) / AP_WARPS, (int64_t)device_sm_count() * AP_CTAS);
 #define DT_AP(d, g) \
-  if (D == d && G == g) kv4_append_kernel<T, d, g><<<grid, AP_THREADS, 0, s>>>(p, units)
+  if (D == d && G == g) kv4_append_kernel<T, d, g><<<grid, AP_THREADS, 0, s>>>(p)
   DT_AP(64, 32);
   DT_AP(64, 64);
   DT_AP(128, 32);
@@ -285,6 +351,8 @@ dt_status append_call(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor
   p.cache = B.cache;
   p.page_table = B.page_table;
   p.table_width = B.table_width;
+  p.page_mul = B.page_mul;
+  p.page_shift = B.page_shift;
   p.seq = SeqTable{B.q_starts, B.kv_lens, B.batch, B.q_len, (int32_t)K.tokens, B.capacity};
   p.interleaved = interleaved != 0;
   p.has_stored = k_stored != nullptr;

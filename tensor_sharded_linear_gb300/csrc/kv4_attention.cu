@@ -94,11 +94,8 @@ dt_status attention_call(const dt_dtensor* q, const dt_dtensor* cache, const dt_
   p.page_table = c.B.page_table;
   p.table_width = c.B.table_width;
   p.g = c.Q.heads / c.B.cache.heads;
-  // division by the page size (exact for every key number below 2^31)
-  uint32_t shift = 0;
-  while ((1u << shift) < (uint32_t)p.cache.page_size) ++shift;
-  p.page_shift = shift;
-  p.page_mul = (uint32_t)((((uint64_t)1 << (31 + shift)) + p.cache.page_size - 1) / p.cache.page_size);
+  p.page_mul = c.B.page_mul;
+  p.page_shift = c.B.page_shift;
   p.causal = causal != 0;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;

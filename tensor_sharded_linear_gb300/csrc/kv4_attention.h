@@ -30,7 +30,7 @@ struct AttnParams {
   const int32_t* page_table;
   int32_t table_width;
   int32_t g;  // query heads per kv head
-  uint32_t page_mul, page_shift;  // j / page_size = umulhi(2 j, page_mul) >> page_shift for j < 2^31
+  uint32_t page_mul, page_shift;  // division by the page size (Kv4Batch)
   int32_t causal, window;
   int32_t want_lse;
   float scale_log2;  // softmax scale * log2(e)

@@ -82,21 +82,42 @@ __device__ __forceinline__ void write_dw_part(const NormParams& p, const float* 
 
 // D and rotary multiples of 16, D <= 512, 16-byte aligned heads.  A unit of
 // work is `inner` blocks of heads (SG * U heads each) of one token.
+// CTAs per SM: 5 forward, 4 backward (128 registers for its sums of dw), the
+// loop over blocks unrolled twice backward; measured at 8192 tokens x 64
+// heads against 3..5 CTAs and both unrollings.
+__host__ __device__ constexpr int norm_ctas(bool bwd) { return bwd ? 4 : 5; }
+
 template <class T, bool BWD>
 struct NormVec {
   static constexpr int U = sizeof(T) == 2 && !BWD ? 2 : 1;  // heads per lane and step
 };
 
-template <class T, bool BWD, bool INTER>
-__global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
+// LANES: D / 16 where that is 4, 8 or 16 (all lanes hold channels and the
+// sums' steps are known), else 0.
+template <class T, bool BWD, bool INTER, int LANES>
+__global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
   constexpr int U = NormVec<T, BWD>::U;
   extern __shared__ __align__(16) float nr_acc[];  // backward: [NR_WARPS][D] sums; forward: [D] weights
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int L = p.D / 16;
-  int LP = 1;
-  while (LP < L) LP <<= 1;
+  const int D = LANES ? 16 * LANES : p.D, L = D / 16;
+  int LP = LANES;
+  if (!LANES) {
+    LP = 1;
+    while (LP < L) LP <<= 1;
+  }
   const int SG = 32 / LP, sub = lane / LP, l = lane & (LP - 1);
-  const bool act = l < L;
+  const bool act = LANES || l < L;
+  // the sum over a head's lanes
+  auto head_sum = [&](float v) {
+    if constexpr (LANES) {
+#pragma unroll
+      for (int o = LANES >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    } else {
+      v = act ? v : 0.f;
+      for (int o = LP >> 1; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    }
+    return v;
+  };
   const int which = blockIdx.x >= p.blocks_q;
   const HeadMap &X = p.x[which], &Y = p.y[which], &G = p.g[which];
   const int rl = p.cos_sin ? p.rotary / 16 : 0;  // lanes that hold rotated pairs
@@ -104,7 +125,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
   // first channels of the lane's two chunks; a pair's partner is in the other
   // chunk, or (INTER) the neighbour channel.  2 rl chunks are rotated, so the
   // rest starts at chunk 2 l.
-  const int ca = rot && !INTER ? 8 * l : 16 * l;
+  const int ca = !act ? 0 : rot && !INTER ? 8 * l : 16 * l;
   const int cb = rot && !INTER ? 8 * (l + rl) : ca + 8;
   const bool norm = p.w[which] != nullptr;
   f2 wa[4], wb[4], da[4], db[4];
@@ -122,28 +143,24 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
     __syncthreads();
   }
   const int inner = p.inner[which];
-  const int per_tok = ((X.heads + SG * U - 1) / (SG * U) + inner - 1) / inner;  // units of a token
+  const int64_t tokens = X.heads ? p.tokens : 0;
+  const int per_tok = max(1, ((X.heads + SG * U - 1) / (SG * U) + inner - 1) / inner);  // units of a token
   const int step = (which ? gridDim.x - p.blocks_q : p.blocks_q) * NR_WARPS;
   const int step_tok = step / per_tok, step_blk = step - step_tok * per_tok;  // a stride of units, without a division
-  const float inv_d = 1.f / (float)p.D;
+  const float inv_d = 1.f / (float)D;
 
   Raw8<T> xa[U], xb[U], ga[U], gb[U];
   auto load = [&](int64_t t, int block, Raw8<T>(&a)[U], Raw8<T>(&b)[U], Raw8<T>(&c)[U], Raw8<T>(&d)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int h = (block * U + i) * SG + sub;
-      if (act && h < X.heads) {
-        const T* x = head_ptr<T>(X, t, h, p.D);
-        a[i].load(x + ca);
-        b[i].load(x + cb);
-        if (BWD) {
-          const T* g = head_ptr<T>(G, t, h, p.D);
-          c[i].load(g + ca);
-          d[i].load(g + cb);
-        }
-      } else {
-        a[i].zero(), b[i].zero();
-        if (BWD) c[i].zero(), d[i].zero();
+      const int h = min((block * U + i) * SG + sub, X.heads - 1);  // past the last head: that one again, not stored
+      const T* x = head_ptr<T>(X, t, h, D);
+      a[i].load(x + ca);
+      b[i].load(x + cb);
+      if (BWD) {
+        const T* g = head_ptr<T>(G, t, h, D);
+        c[i].load(g + ca);
+        d[i].load(g + cb);
       }
     }
   };
@@ -151,11 +168,11 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
   int64_t t = u0 / per_tok;
   int blk = u0 - (int)t * per_tok;  // unit blk of token t
   int64_t row_next = 0;
-  if (t < p.tokens) {
+  if (t < tokens) {
     load(t, blk * inner, xa, xb, ga, gb);
     if (p.cos_sin) row_next = table_row(p, t, lane == 0);
   }
-  while (t < p.tokens) {
+  while (t < tokens) {
     const int64_t row = row_next;
     const bool ok = row >= 0;
     f2 c2[4], s2[4];
@@ -171,7 +188,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
     int64_t tn = t + step_tok;
     int bn = blk + step_blk;
     if (bn >= per_tok) bn -= per_tok, ++tn;
-    if (tn < p.tokens && p.cos_sin) row_next = table_row(p, tn, lane == 0);
+    if (tn < tokens && p.cos_sin) row_next = table_row(p, tn, lane == 0);
     // pair e of chunk a has the cosines cosa(e), of chunk b cosb(e)
     auto at = [](const f2(&v)[4], int e) { return e & 1 ? v[e >> 1].y : v[e >> 1].x; };
     auto cosa = [&](int e) { return INTER ? both(at(c2, e)) : c2[e]; };
@@ -191,11 +208,12 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
         qb[e] = INTER ? sinb(e) * f2{-vb.y, vb.x} : sinb(e) * va;
       }
     }
+#pragma unroll(BWD ? 2 : 1)
     for (int in = 0; in < inner; ++in) {
       const int block = blk * inner + in;
       Raw8<T> nxa[U], nxb[U], nga[U], ngb[U];
       if (in + 1 < inner) load(t, block + 1, nxa, nxb, nga, ngb);
-      else if (tn < p.tokens) load(tn, bn * inner, nxa, nxb, nga, ngb);
+      else if (tn < tokens) load(tn, bn * inner, nxa, nxb, nga, ngb);
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int h = (block * U + i) * SG + sub;
@@ -209,9 +227,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
           for (int e = 1; e < 4; ++e) ss = fma2(a[e], a[e], ss);
 #pragma unroll
           for (int e = 0; e < 4; ++e) ss = fma2(b[e], b[e], ss);
-          float s = ss.x + ss.y;
-          for (int o = LP >> 1; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-          r = rsqrtf(s * inv_d + p.eps);
+          r = rsqrtf(head_sum(ss.x + ss.y) * inv_d + p.eps);
 #pragma unroll
           for (int e = 0; e < 4; ++e) a[e] = a[e] * both(r), b[e] = b[e] * both(r);
         }
@@ -236,7 +252,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
             }
           }
           if (norm) {
-            const f2 on = both(ok ? 1.f : 0.f);
+            const f2 on = both(ok && h < X.heads ? 1.f : 0.f);
             f2 gx = both(0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -244,9 +260,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
               da[e] = fma2(ta, on, da[e]), db[e] = fma2(tb, on, db[e]);
               gx = fma2(ta, wa[e], gx), gx = fma2(tb, wb[e], gx);
             }
-            float k = gx.x + gx.y;
-            for (int o = LP >> 1; o; o >>= 1) k += __shfl_xor_sync(0xffffffffu, k, o);
-            k *= -r * inv_d;  // - r * mean(g * x r)
+            const float k = head_sum(gx.x + gx.y) * -r * inv_d;  // - r * mean(g * x r)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               ya[e] = fma2(a[e], both(k), ya[e] * (wa[e] * both(r)));
@@ -259,7 +273,7 @@ __global__ void __launch_bounds__(NR_THREADS, 4) qk_norm_vec_kernel(const __grid
 #pragma unroll
           for (int e = 0; e < 4; ++e) ya[e] = yb[e] = both(0.f);
         }
-        T* y = head_ptr<T>(Y, t, h, p.D);
+        T* y = head_ptr<T>(Y, t, h, D);
         store8(y + ca, ya);
         store8(y + cb, yb);
       }
@@ -409,17 +423,25 @@ dt_status norm_weight(const dt_dtensor* w, const char* what, const Layout& of, i
 
 // CTAs of a launch over tokens * heads head rows: enough to fill the device,
 // fewer when there are not that many units of work.
-int norm_blocks(int64_t units) {
-  const int64_t full = std::min<int64_t>((int64_t)device_sm_count() * 4, NR_MAX_BLOCKS / 2);
+int norm_blocks(int64_t units, bool bwd) {
+  const int64_t full = std::min<int64_t>((int64_t)device_sm_count() * norm_ctas(bwd), NR_MAX_BLOCKS / 2);
   return (int)std::max<int64_t>(1, std::min<int64_t>((units + NR_WARPS - 1) / NR_WARPS, full));
 }
+
+int vec_lanes(int D) { return D == 64 || D == 128 || D == 256 ? D / 16 : 0; }
 
 template <class T, bool BWD>
 void launch_norm(const NormParams& p, bool vec, int grid, cudaStream_t s) {
   const size_t smem = (size_t)p.D * sizeof(float) * (!BWD ? 1 : p.part ? NR_WARPS : 0);
-  if (vec && p.interleaved) qk_norm_vec_kernel<T, BWD, true><<<grid, NR_THREADS, smem, s>>>(p);
-  else if (vec) qk_norm_vec_kernel<T, BWD, false><<<grid, NR_THREADS, smem, s>>>(p);
-  else qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
+#define DT_NR(inter, lanes)                                                                  \
+  if (vec && (p.interleaved != 0) == inter && vec_lanes(p.D) == lanes) {                     \
+    qk_norm_vec_kernel<T, BWD, inter, lanes><<<grid, NR_THREADS, smem, s>>>(p);              \
+    return;                                                                                  \
+  }
+  DT_NR(false, 4) DT_NR(false, 8) DT_NR(false, 16) DT_NR(false, 0)
+  DT_NR(true, 4) DT_NR(true, 8) DT_NR(true, 16) DT_NR(true, 0)
+#undef DT_NR
+  qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
 }
 
 dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleaved, int tp, void* ws, size_t ws_bytes,
@@ -511,10 +533,10 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
   const int heads_k = n == 2 ? x[1].heads : 0;
   const bool nothing = p.tokens == 0 || x[0].heads + heads_k == 0;
   if (nothing && !any_dw) return DT_OK;
-  // A warp's unit is as many blocks of heads of one token as leave eight
+  // A warp's unit is as many blocks of heads of one token as leave four
   // units for every warp of a full device: the token's angles are fetched
   // once for them (measured at 8192 tokens x 64 heads, backward: 139.8 us
-  // with one block a unit).
+  // with one block a unit where four took 90.8 us).
   int LP = 1;
   while (LP < D / 16) LP <<= 1;
   const int U = x[0].dtype == DT_BF16 && !bwd ? NormVec<__nv_bfloat16, false>::U : NormVec<float, true>::U;
@@ -523,14 +545,14 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
   int64_t units[2];
   for (int i = 0; i < 2; ++i) {
     const int heads = i ? heads_k : x[0].heads, blocks = std::max(1, (heads + per_block - 1) / per_block);
-    const int64_t warps = (int64_t)device_sm_count() * 4 * NR_WARPS * heads / all;
+    const int64_t warps = (int64_t)device_sm_count() * norm_ctas(bwd) * NR_WARPS * heads / all;
     p.inner[i] = 1;
-    while (vec && p.inner[i] < blocks && p.tokens * ((blocks + 2 * p.inner[i] - 1) / (2 * p.inner[i])) >= 8 * warps)
+    while (vec && p.inner[i] < blocks && p.tokens * ((blocks + 2 * p.inner[i] - 1) / (2 * p.inner[i])) >= 4 * warps)
       p.inner[i] *= 2;
     units[i] = heads ? p.tokens * ((blocks + p.inner[i] - 1) / p.inner[i]) : 0;
   }
   // CTAs in proportion to the heads
-  const int total = norm_blocks(units[0] + units[1]);
+  const int total = norm_blocks(units[0] + units[1], bwd);
   int bq = (int)((double)total * (double)x[0].heads / (double)all + 0.5);
   bq = std::max(1, std::min(bq, total));
   const int bk = units[1] > 0 ? std::max(1, total - bq) : 0;
