@@ -165,3 +165,21 @@ def attention(q, k, v, scale, causal, window, k_step=None, v_step=None):
                 b32[i] = (2 * e * (mag + np.abs(s).max()) + e) * (vmax + 15 * smax)
                 b16[i] = 2 * e * mag16 * vmax + 2.0 ** -9 * 1.02 * 15 * smax + e * 288 * smax
     return out, lse, b32, b16
+
+
+def prompt_bound(q, k, v, scale, causal, window):
+    """What fp16 operands may add to ``attention``'s error, per query: keys and
+    values rounded to 11 bits (2^-12 of each, K's through the logits, whose
+    error counts twice), probabilities to 11 bits, the row's smallest queries
+    to 2^-25 of its largest."""
+    see = visible(q.shape[0], k.shape[0], causal, window)
+    out = np.zeros(q.shape[0])
+    for i in range(q.shape[0]):
+        j = np.nonzero(see[i])[0]
+        if j.size == 0:
+            continue
+        with np.errstate(all="ignore"):
+            logit = scale * 2.0 ** -12 * (np.abs(k[j]) @ np.abs(q[i])).max()
+            logit += scale * 2.0 ** -25 * np.abs(q[i]).max() * np.abs(k[j]).sum(-1).max()
+            out[i] = (2 * logit * 1.01 + 2.0 ** -10) * np.abs(v[j]).max()
+    return out

@@ -24,7 +24,13 @@ namespace {
 
 using namespace kv4;
 
+// The kernel for prompts from this many (query, head) rows per sequence and
+// kv head.
+constexpr int64_t PROMPT_FROM = 64;
+bool prompt_kernel(int D, bool fp32, int64_t rows) { return !fp32 && D <= 128 && rows >= PROMPT_FROM; }
+
 cudaError_t variant_any(int D, int G, bool fp32, int64_t rows, Variant* v) {
+  if (prompt_kernel(D, fp32, rows)) return prompt_variant(D, G, v);
   return D == 64 ? variant<64>(G, fp32, rows, v) : D == 128 ? variant<128>(G, fp32, rows, v)
                                                             : variant<256>(G, fp32, rows, v);
 }
@@ -115,7 +121,9 @@ dt_status attention_call(const dt_dtensor* q, const dt_dtensor* cache, const dt_
                                     ((size_t)v.grid * sizeof(Split) + 255) / 256 * 256);
   p.status = device_status_word(d_status);
   if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
-  e = D == 64 ? launch<64>(p, G, fp32, c.rows_per_seq, v.grid, stream)
+  p.rb = v.rows;
+  e = prompt_kernel(D, fp32, c.rows_per_seq) ? prompt_launch(p, D, G, v.grid, stream)
+      : D == 64 ? launch<64>(p, G, fp32, c.rows_per_seq, v.grid, stream)
               : D == 128 ? launch<128>(p, G, fp32, c.rows_per_seq, v.grid, stream)
                          : launch<256>(p, G, fp32, c.rows_per_seq, v.grid, stream);
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "kv4_attention launch: %s", cudaGetErrorString(e));

@@ -33,6 +33,7 @@ struct AttnParams {
   uint32_t page_mul, page_shift;  // division by the page size (Kv4Batch)
   int32_t causal, window;
   int32_t want_lse;
+  int32_t rb;        // rows of a unit (for the join)
   float scale_log2;  // softmax scale * log2(e)
   float* part;       // [2 CTAs][rows][D + 2]: sums, then maximum (log2 units) and denominator
   Split* split;      // [CTA]
@@ -51,6 +52,11 @@ template <int D>
 cudaError_t variant(int G, bool fp32, int64_t rows_per_seq, Variant* out);
 template <int D>
 cudaError_t launch(const AttnParams& p, int G, bool fp32, int64_t rows_per_seq, int grid, cudaStream_t s);
+
+// Rows of a sequence and kv head from which the tensor-core kernel for
+// prompts runs, and that kernel (bf16, head_dim 64 and 128).
+cudaError_t prompt_variant(int D, int G, Variant* out);
+cudaError_t prompt_launch(const AttnParams& p, int D, int G, int grid, cudaStream_t s);
 
 }  // namespace kv4
 }  // namespace dt

@@ -14,8 +14,9 @@ pytestmark = pytest.mark.gpu
 HALF_ULP = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -23}
 
 
-def check(b, q, hq, dtype, out, lse, scale, causal, window):
-    """Every query of every sequence; returns the largest error over its bound."""
+def check(b, q, hq, dtype, out, lse, scale, causal, window, prompt=False):
+    """Every query of every sequence; returns the largest error over its bound.
+    ``prompt``: the tensor-core kernel's fp16 operands add theirs."""
     t, d, g = b.tokens, b.d, hq // b.hk
     got = full(out).reshape(t, hq, d)
     got_lse = full(lse) if lse is not None else None
@@ -27,6 +28,9 @@ def check(b, q, hq, dtype, out, lse, scale, causal, window):
             e, el, b32, b16 = heads.attention(q[at:at + n].reshape(n, hq, d)[:, h], k[:, kh], v[:, kh], scale, causal,
                                               window, ks[:, kh], vs[:, kh])
             tol = b32 + (b16 if dtype == "bf16" else 0)
+            if prompt:
+                tol = tol + heads.prompt_bound(q[at:at + n].reshape(n, hq, d)[:, h], k[:, kh], v[:, kh], scale, causal,
+                                               window)
             y = got[at:at + n, h]
             np.testing.assert_array_equal(np.isnan(y), np.isnan(e))
             err = np.abs(y - e)
@@ -46,7 +50,7 @@ def check(b, q, hq, dtype, out, lse, scale, causal, window):
 
 
 def run(rng, q_lens, kv_lens, hq, hk, d, group, page, p, dtype, causal=True, window=0, scale=None, with_lse=True,
-        starts=True, replicate=False, q_scale=1.0, **kw):
+        starts=True, replicate=False, q_scale=1.0, prompt=False, **kw):
     mesh = tsl.DeviceMesh((p,), ("tp",))
     b = Batch(rng, mesh, q_lens, kv_lens, hk, d, group, page, replicate=replicate, **kw)
     q = draw(rng, (b.tokens, hq * d), dtype, q_scale)
@@ -57,7 +61,7 @@ def run(rng, q_lens, kv_lens, hq, hk, d, group, page, p, dtype, causal=True, win
     y = tsl.tp_kv4_attention(qd, b.cache(), pt, kl, qs if starts else None, head_dim=d, group=group, scale=scale,
                              causal=causal, window=window, lse=lse, out=out)
     assert tsl.read_device_status() == 0
-    return check(b, q, hq, dtype, y, lse, d ** -0.5 if scale is None else scale, causal, window)
+    return check(b, q, hq, dtype, y, lse, d ** -0.5 if scale is None else scale, causal, window, prompt)
 
 
 FORMATS = [(64, 32), (64, 64), (128, 32), (128, 64), (256, 32), (256, 64)]
@@ -97,7 +101,119 @@ def test_masks(lib, causal, window, dtype):
 @pytest.mark.parametrize("d", [64, 128, 256])
 def test_prompt_chunks(lib, d):
     """Many queries per sequence: whole prompts, and a chunk behind a context."""
-    run(np.random.default_rng(36), [130, 64, 1], [130, 200, 70], 4, 1, d, 64, 16, 1, "bf16")
+    run(np.random.default_rng(36), [130, 64, 1], [130, 200, 70], 4, 1, d, 64, 16, 1, "bf16", prompt=d <= 128)
+
+
+# What follows has 64 (query, head) rows per sequence and kv head or more: the tensor-core kernel.
+
+@pytest.mark.parametrize("d,group", FORMATS[:4])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hk", [
+    ([64], [64], 1, 1),                               # one tile, one step
+    ([65, 64, 63], [65, 300, 129], 2, 1),             # at and around the tiles' ends
+    ([256, 300], [256, 1000], 1, 1),                  # two tiles, several row blocks
+    ([100, 1, 0, 37, 200], [100, 500, 0, 37, 900], 6, 2),  # prompts, a decode step, no queries, odd group of 3
+    ([90, 40], [60, 40], 2, 2),                       # more queries than keys
+])
+def test_prompt_lengths(lib, d, group, q_lens, kv_lens, hq, hk):
+    run(np.random.default_rng(50), q_lens, kv_lens, hq, hk, d, group, 16, hk, "bf16", prompt=True)
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (True, 1), (True, 60), (True, 128), (True, 250), (True, 10 ** 6)])
+def test_prompt_masks(lib, causal, window):
+    run(np.random.default_rng(51), [150, 70], [400, 70], 4, 2, 64, 64, 16, 2, "bf16", causal, window, prompt=True)
+
+
+@pytest.mark.parametrize("page", [1, 7, 8, 33, 64, 128, 500])
+def test_prompt_page_sizes(lib, page):
+    run(np.random.default_rng(52), [80, 90], [300, 129], 2, 1, 128, 64, page, 1, "bf16", prompt=True)
+
+
+def test_prompt_split_over_ctas(lib):
+    """One row block on a long context: every CTA holds a piece of it."""
+    run(np.random.default_rng(53), [70, 64], [9000, 64], 4, 2, 128, 64, 64, 2, "bf16", prompt=True)
+
+
+@pytest.mark.parametrize("kv_scale,q_scale", [(1e5, 1e-4), (1e-5, 1.0), (1.0, 30.0), (1e-30, 1e20)])
+def test_prompt_magnitudes(lib, kv_scale, q_scale):
+    """Keys and values beyond and far below fp16's range; large logits."""
+    run(np.random.default_rng(54), [70, 80], [300, 200], 2, 1, 64, 64, 16, 1, "bf16", kv_scale=kv_scale,
+        q_scale=q_scale, prompt=True)
+
+
+def test_prompt_values_that_grow(lib):
+    """Steps of 128 keys whose values grow by powers of two, and shrink again: what O is scaled by follows."""
+    rng = np.random.default_rng(55)
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    b = Batch(rng, mesh, [70], [900], 1, 64, 64, 16)
+    k, _, _, _ = heads.unpack(b.kv[0], 64, 64)
+    v = rng.standard_normal((900, 1, 64)) * 2.0 ** np.array([0, 9, -5, 20, 30, 3, -20, 0])[np.arange(900) // 128][:, None, None]
+    b.kv[0] = heads.pack(np.float32(k), np.float32(v), 64)
+    for j in range(900):
+        b.records[b.table[0, j // 16], :, j % 16] = b.kv[0][j]
+    q = draw(rng, (70, 64), "bf16")
+    pt, kl, qs = b.operands()
+    y = tsl.tp_kv4_attention(sharded(q, mesh, "bf16"), b.cache(), pt, kl, qs, head_dim=64)
+    check(b, q, 1, "bf16", y, None, 0.125, True, 0, True)
+
+
+@pytest.mark.parametrize("poison", [0x7F807F80, 0xFF80FF80, 0x7FC07FC0, 0xFFFFFFFF])
+def test_prompt_hidden_keys(lib, poison):
+    """NaN and infinities in hidden keys and beyond the lengths; a visible one reaches the queries that see it."""
+    rng = np.random.default_rng(56)
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    b = Batch(rng, mesh, [100], [300], 1, 128, 64, 16, poison=poison)
+    q = draw(rng, (100, 2 * 128), "bf16")
+    rec = b.kv[0][250].copy()
+    rec[..., 32:] = poison  # key 250: seen by queries at positions 250 to 289 of 200 to 299
+    b.records[b.table[0, 250 // 16], :, 250 % 16] = rec
+    pt, kl, qs = b.operands()
+    y = full(tsl.tp_kv4_attention(sharded(q, mesh, "bf16"), b.cache(), pt, kl, qs, head_dim=128, window=40))
+    bad = np.zeros(100, bool)
+    bad[50:90] = True
+    assert np.isnan(y[bad]).all() and np.isfinite(y[~bad]).all()
+    k, v, ks, vs = heads.unpack(b.kv[0], 128, 64)
+    for h in range(2):
+        qh = q.reshape(100, 2, 128)[:, h]
+        e, _, b32, b16 = heads.attention(qh, k[:, 0], v[:, 0], 128 ** -0.5, True, 40, ks[:, 0], vs[:, 0])
+        tol = b32 + b16 + heads.prompt_bound(qh, k[:, 0], v[:, 0], 128 ** -0.5, True, 40)
+        err = np.abs(y.reshape(100, 2, 128)[:, h] - e)
+        assert (err <= tol[:, None] + 2.0 ** -8 * np.abs(e))[~bad].all()
+
+
+def test_prompt_bad_pages(lib):
+    rng = np.random.default_rng(57)
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    q = draw(rng, (80, 2 * 64), "bf16")
+    b = Batch(rng, mesh, [80], [240], 1, 64, 64, 16)
+    tab = b.table.copy()
+    tab[0, 1], tab[0, 8] = -1, 10 ** 6
+    y = tsl.tp_kv4_attention(sharded(q, mesh, "bf16"), b.cache(), ints(tab, mesh), b.operands()[1], head_dim=64,
+                             causal=False)
+    assert tsl.read_device_status() == tsl._lib.DEV_ERR_INDEX
+    b.kv[0] = np.concatenate([b.kv[0][:16], b.kv[0][32:128], b.kv[0][144:]])
+    b.kv_lens = [208]
+    check(b, q, 2, "bf16", y, None, 0.125, False, 0, True)
+
+
+def test_prompt_repeats_and_graph(lib):
+    rng = np.random.default_rng(58)
+    mesh = tsl.DeviceMesh((2,), ("tp",))
+    b = Batch(rng, mesh, [100, 64], [700, 64], 2, 128, 64, 16)
+    q = draw(rng, (164, 8 * 128), "bf16")
+    qd, cache, (pt, kl, qs) = sharded(q, mesh, "bf16"), b.cache(), b.operands()
+    n = tsl.tp_kv4_attention_workspace_bytes(qd, cache, pt, head_dim=128)
+    buf = torch.full((n + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    a = tsl.tp_kv4_attention(qd, cache, pt, kl, qs, head_dim=128, workspace=buf[:n])
+    assert (buf[n:] == 0xA5).all()
+    check(b, q, 8, "bf16", a, None, 128 ** -0.5, True, 0, True)
+    out = sharded(np.zeros_like(q), mesh, "bf16")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        tsl.tp_kv4_attention(qd, cache, pt, kl, qs, head_dim=128, workspace=buf[:n], out=out)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, u) for s, u in zip(a.slots, out.slots))
 
 
 def test_long_sequence_is_split(lib):
