@@ -15,17 +15,21 @@
 // softmax's multiplier), and for V the largest so far, with O rescaled where
 // it grows.
 //
-// Roles, 14 warps: two softmax groups of four warps (one row of one tile per
-// thread), four unpacking warps (one key per thread), one warp that issues
-// the bulk copies of the packed records, one that issues the matrix products.
-// While one tile's softmax runs, the tensor core works on the other's
-// products.  A row's reference for the exponential follows its maximum only
-// when that has grown by more than 2^8, so O, which stays in tensor memory,
-// is rescaled rarely.
+// Roles, 15 warps: two softmax groups of four warps (one row of one tile per
+// thread), four unpacking warps (two for K, two for V, one key per thread), one
+// warp that issues the bulk copies of the packed records, one per tile that
+// issues its matrix products.  Everything goes in steps of 64 keys through rings: four
+// packed, three unpacked, two S per tile.  While the softmax of a step runs,
+// the tensor core forms P V of the step before and S of the step after, for
+// both tiles in turn, and the records of the next steps are on their way.
+// (With steps of 128 keys and one packed buffer the wait for the records
+// alone took 3090 cycles a step, measured with everything else taken out.)
+// A row's reference for the exponential follows its maximum only when that
+// has grown by more than 2^8, so O, which stays in tensor memory, is rescaled
+// rarely.
 //
 // Bound: the tensor core (4 D flops a pair of row and key) for contexts of
-// any length; per step of 256 rows x 128 keys the products take about 2050
-// cycles, the softmax 3400 and the unpacking 2200 of 8200 issue slots.
+// any length.
 //
 // The schedule, the pieces of units that a CTA's share cuts and the join are
 // those of kv4_attention.cuh, with each row block's own number of key blocks.
@@ -42,52 +46,106 @@ namespace dt {
 namespace kv4 {
 
 constexpr int PROMPT_ROWS = 256;
-constexpr int PROMPT_KEYS = 128;
-constexpr int PROMPT_WARPS = 14;
-constexpr int PROMPT_EXTRA = 1;  // key blocks a unit counts for its start and end
+constexpr int PROMPT_KEYS = 64;  // of a step
+constexpr int PROMPT_WARPS = 15;
+constexpr int PROMPT_EXTRA = 4;  // steps a unit counts for its start and end
+constexpr int PROMPT_PACKED = 4, PROMPT_STAGES = 3, PROMPT_INFO = 8;  // rings: packed, unpacked, scales
 
 template <int D, int G>
 struct PromptShape {
   static constexpr int W = kv4_words(D, G);
   static constexpr int NG = D / G;
-  static constexpr int PANELS = D / 64;                   // 64 channels: one 128-byte row
-  static constexpr int TILE_BYTES = 128 * D * 2;          // 128 rows or keys, fp16
+  static constexpr int PANELS = D / 64;                    // 64 channels: one 128-byte row
+  static constexpr int Q_BYTES = 128 * D * 2;              // a tile of 128 rows, fp16
+  static constexpr int KV_BYTES = PROMPT_KEYS * D * 2;     // a step's keys or values, fp16
+  static constexpr int KV_PANEL = PROMPT_KEYS * 128;
   static constexpr int PACKED_BYTES = PROMPT_KEYS * W * 4;
-  static constexpr int OFF_K = 2 * TILE_BYTES, OFF_V = 4 * TILE_BYTES, OFF_PACKED = 6 * TILE_BYTES;
-  static constexpr int OFF_BAR = OFF_PACKED + PACKED_BYTES;  // barriers, flags
-  static constexpr int SMEM = OFF_BAR + 512 + 1024;          // and alignment to 1024
-  static constexpr int TMEM_S = 0, TMEM_O = 256;             // columns: S (and P) of tile t at t * 128; O at 256 + t * D
+  static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + PROMPT_STAGES * KV_BYTES;
+  static constexpr int OFF_PACKED = OFF_V + PROMPT_STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_PACKED + PROMPT_PACKED * PACKED_BYTES;  // barriers, flags
+  static constexpr int SMEM = OFF_BAR + 1024 + 1024;                         // and alignment to 1024
+  static constexpr int TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of tile t, step n at t * 128 + (n & 1) * 64; O
+};
+
+// What the softmax has to know of a step.  A slot is written again eight
+// steps later; no role is more than five steps ahead of another.
+struct alignas(16) StepInfo {
+  float kmul;         // S is to be multiplied by this
+  float vgrow;        // O is to be multiplied by this before the step's product
+  float vscale;       // O is to be multiplied by this in the end
+  uint32_t all;       // all 64 keys exist
+  uint32_t valid[2];  // which do
 };
 
 struct PromptBars {
-  uint64_t packed_full, packed_empty;
-  uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
-  uint64_t sfull[2], pready[2], qready[2], ofull[2];
-  uint32_t valid[4];      // keys of the packed step that exist
-  uint32_t svalid[2][4];  // the same of the step in a V stage
-  float kmul[2];       // what S of a K stage is to be multiplied by
-  float vgrow[2];      // what O is to be multiplied by before a V stage's product
-  float vscale[2];     // what O is to be multiplied by in the end
-  uint32_t top[2][2][4];  // the unpacking warps' largest magnitudes (step parity; K, V)
+  uint64_t packed_full[PROMPT_PACKED], packed_empty[PROMPT_PACKED];
+  uint64_t kfull[PROMPT_STAGES], kempty[PROMPT_STAGES], vfull[PROMPT_STAGES], vempty[PROMPT_STAGES];
+  uint64_t sfull[2][2], pready[2][2];  // [tile][step & 1]
+  uint64_t pdone[2], ofull[2], qready[2];  // [tile]
+  StepInfo info[PROMPT_INFO];
+  uint32_t valid[PROMPT_PACKED][2];    // keys of a packed step that exist
+  uint32_t top[2][2][2];               // [step & 1][K, V][warp]: largest magnitudes
+  uint32_t there[2][2];                // [step & 1][warp]: keys that exist
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(PromptBars) <= 512, "barriers and flags");
+static_assert(sizeof(PromptBars) <= 1024, "barriers and flags");
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// Bounded wait of a whole warp that sleeps in the barrier unit (up to the
+// hint per try) instead of spinning.
+__device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_sleep_warp(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                unsigned long long limit_ns) {
+  if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, 20000))) return true;
+  const uint64_t t0 = globaltimer();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait_hint(bar, parity, 20000))) return true;
+    const int give_up = (*abort_flag != 0) || (globaltimer() - t0 > limit_ns);
+    if (__any_sync(0xffffffffu, give_up)) return false;
+  }
+}
+
+// Four products of 16 deep each: operands advance by fixed steps of their
+// descriptors (16-byte units) and tensor-memory columns, so that a product
+// costs the issuing warp a few instructions.
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t"
+      "add.u64 a, %1, 2;\n\tadd.u64 b, %2, 2;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+      "add.u64 a, %1, 4;\n\tadd.u64 b, %2, 4;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t"
+      "add.u64 a, %1, 6;\n\tadd.u64 b, %2, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, q;\n\t}" ::"r"(d),
       "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "{\n\t.reg .pred p, q;\n\t.reg .b32 a;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 q, 0, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t"
+      "add.u32 a, %1, 8;\n\tadd.u64 b, %2, 128;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.u32 a, %1, 16;\n\tadd.u64 b, %2, 256;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t"
+      "add.u32 a, %1, 24;\n\tadd.u64 b, %2, 384;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, q;\n\t}" ::"r"(d),
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -136,28 +194,29 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
   using S = PromptShape<D, G>;
   constexpr int W = S::W, NG = S::NG, RB = PROMPT_ROWS, KB = PROMPT_KEYS;
   extern __shared__ uint8_t prompt_smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(prompt_smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = prompt_smem_raw + ((1024 - (smem_u32(prompt_smem_raw) & 1023)) & 1023);
   PromptBars& B = *reinterpret_cast<PromptBars*>(smem + S::OFF_BAR);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   volatile int* abort_flag = &B.abort;
 
   if (threadIdx.x == 0) {
-    mbar_init(&B.packed_full, 1);
-    mbar_init(&B.packed_empty, 1);
+    for (int i = 0; i < PROMPT_PACKED; ++i) mbar_init(&B.packed_full[i], 1), mbar_init(&B.packed_empty[i], 4);
+    for (int i = 0; i < PROMPT_STAGES; ++i) {
+      mbar_init(&B.kfull[i], 2);
+      mbar_init(&B.kempty[i], 2);
+      mbar_init(&B.vfull[i], 2);
+      mbar_init(&B.vempty[i], 2);
+    }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&B.kfull[i], 4);
-      mbar_init(&B.kempty[i], 1);
-      mbar_init(&B.vfull[i], 4);
-      mbar_init(&B.vempty[i], 1);
-      mbar_init(&B.sfull[i], 1);
-      mbar_init(&B.pready[i], 4);
-      mbar_init(&B.qready[i], 4);
+      for (int j = 0; j < 2; ++j) mbar_init(&B.sfull[i][j], 1), mbar_init(&B.pready[i][j], 4);
+      mbar_init(&B.pdone[i], 1);
       mbar_init(&B.ofull[i], 1);
+      mbar_init(&B.qready[i], 4);
     }
     B.abort = 0;
     fence_mbar_init();
   }
-  if (warp == PROMPT_WARPS - 1) {
+  if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -292,7 +351,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
   };
   // Bounded wait of a whole warp; false: give up everywhere.
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait_warp(bar, parity, abort_flag, p.wait_limit_ns)) return true;
+    if (mbar_sleep_warp(bar, parity, abort_flag, p.wait_limit_ns)) return true;
     if (lane == 0) {
       atomicExch(&B.abort, 1);
       atomicOr(p.status, DT_DEV_ERR_TIMEOUT);
@@ -305,25 +364,28 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     const int t = warp >> 2, row_in = t * 128 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + S::TMEM_S + t * 128, to = tmem + lanes + S::TMEM_O + t * D;
-    uint8_t* qtile = smem + t * S::TILE_BYTES;
-    uint32_t steps = 0, vsteps = 0;  // S tiles taken so far (this tile's; all of the share's steps)
+    uint8_t* qtile = smem + t * S::Q_BYTES;
+    uint32_t mine = 0, all = 0, nseg = 0;  // steps so far in which this tile has rows; of the whole share; units
+    uint32_t vstage = 0, vphase = 0;       // ring position of step `all`
+    auto skip = [&](uint32_t n) {
+      all += n, vstage += n;
+      while (vstage >= PROMPT_STAGES) vstage -= PROMPT_STAGES, vphase ^= 1;
+    };
     Segment s;
-    uint32_t nseg = 0;
     bool ok = true;
     while (ok && advance(s)) {
-      const bool tile_on = t == 0 || s.rows > 128;  // else this tile has no rows
-      if (!tile_on) {
-        vsteps += s.nb;
+      if (t == 1 && s.rows <= 128) {  // no rows in this tile
+        skip(s.nb);
         continue;
       }
       const bool on = row_in < s.rows;
       const int qr = s.row0 + row_in, tok = s.q0 + qr / p.g, head = s.hk * p.g + qr % p.g;
       const int pos = s.off + qr / p.g;
-      // ---- the row's query: fp16, scaled to [2^10, 2^11) at its largest
-      float mult = 1.f;
+      // ---- the row's query: fp16, scaled to [2^10, 2^11) at its largest.  (The last S of the unit before
+      // has been taken, so its queries are done with.)
+      float row_scale;
       {
         Raw8<__nv_bfloat16> raw[D / 8];
-        float top = 0.f;
         if (on) {
           const __nv_bfloat16* q = head_ptr<__nv_bfloat16>(p.q, tok, head, D);
 #pragma unroll
@@ -332,6 +394,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
 #pragma unroll
           for (int w = 0; w < D / 8; ++w) raw[w].zero();
         }
+        float top = 0.f;
 #pragma unroll
         for (int w = 0; w < D / 8; ++w) {
           float x[8];
@@ -339,16 +402,15 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
 #pragma unroll
           for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[c]));
         }
-        mult = __uint_as_float((uint32_t)max(10, min(254, 264 - (int)(__float_as_uint(top) >> 23))) << 23);
+        const float mult = __uint_as_float((uint32_t)max(10, min(254, 264 - (int)(__float_as_uint(top) >> 23))) << 23);
+        row_scale = p.scale_log2 / mult;
 #pragma unroll
         for (int w = 0; w < D / 8; ++w) {
           float x[8];
           raw[w].get(x);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) x[c] *= mult;
           // the order of channels in which a word's nibble pairs come apart
-          auto pk = [](float lo, float hi) {
-            const __half2 h = __floats2half2_rn(lo, hi);
+          auto pk = [&](float lo, float hi) {
+            const __half2 h = __floats2half2_rn(lo * mult, hi * mult);
             return *reinterpret_cast<const uint32_t*>(&h);
           };
           const int r = row_in & 127;
@@ -359,105 +421,105 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.qready[t]);
-      const float row_scale = p.scale_log2 / mult;
       float ref = -INFINITY, den = 0.f, vs = 1.f;  // P = 2^(S - ref + 6)
-      for (int i = 0; i < s.nb; ++i, ++steps, ++vsteps) {
-        if (!(ok = wait(&B.sfull[t], steps & 1))) break;
+      // (The loop stays a loop: unrolled, the roles' code misses the instruction cache all the time.)
+#pragma unroll 1
+      for (int i = 0; i < s.nb; ++i) {
+        const uint32_t place = mine & 1, tb = ts + 64 * place;
+        // (V's barrier second: its phase is told by its parity, so the step before has to have come, as it has
+        // when there is an S)
+        if (!(ok = wait(&B.sfull[t][place], (mine >> 1) & 1) && wait(&B.vfull[vstage], vphase))) break;
         gemm::tc_fence_after();
-        const int stage = vsteps & 1;
-        const float sc = row_scale * B.kmul[stage], vgrow = B.vgrow[stage];
-        vs = B.vscale[stage];
+        uint32_t u[32], v[32];
+        gemm::tmem_ld32(tb, u);
+        gemm::tmem_ld32(tb + 32, v);
+        const StepInfo& I = B.info[all % PROMPT_INFO];
+        const float sc = row_scale * I.kmul;
+        vs = I.vscale;
         const int j0 = s.key0 + i * KB;
         // columns [lo, hi) of the step are seen by this row
         int lo = 0, hi = min(KB, s.khi - j0);
         if (p.causal) hi = min(hi, pos + 1 - j0);
         if (p.window) lo = max(0, pos - p.window + 1 - j0);
-        uint32_t see[4];
-        bool masked = false;
+        const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < KB || !I.all);
+        gemm::tmem_ld_wait();
+        if (masked) {
+          auto see = [&](int c) {  // bit e: column 32 c + e
+            const int a = max(lo - 32 * c, 0), z = min(hi - 32 * c, 32);
+            return (z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u) & I.valid[c];
+          };
+          const uint32_t su = see(0), sv = see(1);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int a = max(lo - 32 * c, 0), z = min(hi - 32 * c, 32);  // bits [a, z)
-          see[c] = z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0;
-          see[c] &= B.svalid[stage][c];
-          masked = masked || see[c] != 0xffffffffu;
-        }
-        masked = __any_sync(0xffffffffu, masked);
-        float top = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32];
-          gemm::tmem_ld32(ts + 32 * c, v);
-          gemm::tmem_ld_wait();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) v[e] = 0xff800000u;
+          for (int e = 0; e < 32; ++e) {
+            if (!(su >> e & 1)) u[e] = 0xff800000u;
+            if (!(sv >> e & 1)) v[e] = 0xff800000u;
           }
-#pragma unroll
-          for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(v[e]));
         }
-        top *= sc;
-        float f = 1.f;
+        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four short chains)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          t4[e & 2] = fmaxf(t4[e & 2], fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
+          t4[1 + (e & 2)] = fmaxf(t4[1 + (e & 2)], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+        }
+        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+        float f = I.vgrow;  // what O is to be multiplied by
         if (i == 0) {
           ref = top;
-        } else if (top > ref + 8.f) {
-          f = ex2(ref - top);
-          ref = top;
-        }
-        den *= f;
-        f *= vgrow;
-        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+        } else {
+          if (top > ref + 8.f) {
+            const float g = ex2(ref - top);
+            ref = top;
+            den *= g;
+            f *= g;
+          }
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            // every product before is in O (S of this step followed all but the last)
+            if (!(ok = wait(&B.pdone[t], (mine - 1) & 1))) break;
+            gemm::tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t v[16], w[16];
-            tmem_ld16(to + 32 * c, v);
-            tmem_ld16(to + 32 * c + 16, w);
-            gemm::tmem_ld_wait();
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t w[16];
+              tmem_ld16(to + 16 * c, w);
+              gemm::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-              w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+              tmem_st16(to + 16 * c, w);
             }
-            tmem_st16(to + 32 * c, v);
-            tmem_st16(to + 32 * c + 16, w);
           }
         }
         const float add = ref == -INFINITY ? 0.f : 6.f - ref;  // a row that has seen nothing yet
-        f2 sum = both(0.f);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t v[32], w[16];
-          gemm::tmem_ld32(ts + 32 * c, v);
-          gemm::tmem_ld_wait();
-          if (masked) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see[c] >> e & 1)) v[e] = 0xff800000u;
-          }
+        float d0 = 0.f, d1 = 0.f;
+        auto half = [&](uint32_t(&x)[32], int col) {
+          uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            f2 x = fma2(f2{__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])}, both(sc), both(add));
-            x = f2{ex2(x.x), ex2(x.y)};
-            sum = sum + x;
-            const __half2 h = __floats2half2_rn(x.x, x.y);
+            const float y0 = ex2(fmaf(__uint_as_float(x[2 * e]), sc, add));
+            const float y1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sc, add));
+            d0 += y0, d1 += y1;
+            const __half2 h = __floats2half2_rn(y0, y1);
             w[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
-          tmem_st16(ts + 16 * c, w);  // over columns that have been read
-        }
-        den += sum.x + sum.y;
+          tmem_st16(tb + col, w);  // over columns that have been read
+        };
+        half(u, 0);
+        half(v, 16);
+        den += d0 + d1;
         tmem_st_wait();
         gemm::tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.pready[t]);
+        if (lane == 0) mbar_arrive(&B.pready[t][place]);
+        ++mine;
+        skip(1);
       }
-      if (!ok || !(ok = wait(&B.ofull[t], nseg & 1))) break;
-      ++nseg;
+      if (!ok || !(ok = wait(&B.ofull[t], nseg & 1))) break;  // the unit's last product (a barrier of its own: of
+      ++nseg;                                                 // pdone's two may be outstanding here)
       gemm::tc_fence_after();
       // ---- the row's result (channels back in order), or this share's piece of it
       const float inv = den > 0.f ? vs / den : den == 0.f ? 0.f : den;
       const int64_t piece = 2 * (int64_t)blockIdx.x + (s.first ? 1 : 0);
       __nv_bfloat16* y = on && s.whole ? head_ptr<__nv_bfloat16>(p.out, tok, head, D) : nullptr;
       float* out = p.part + (piece * RB + row_in) * (D + 4);
+      const float mul = s.whole ? inv : vs;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t v[32];
@@ -467,7 +529,6 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           float x[8];
-          const float mul = s.whole ? inv : vs;
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[(e >> 1) + 4 * (e & 1)] = __uint_as_float(v[8 * w + e]) * mul;
           if (s.whole) {
@@ -490,89 +551,94 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         p.split[blockIdx.x] = Split{s.unit, s.row0, s.rows, s.q0, s.hk, s.last};
     }
   } else if (warp < 12) {
-    // ================================================= unpacking: one key per thread
-    const int key = threadIdx.x - 256, w4 = warp - 8;
+    // ================================================= unpacking: warps 8, 9 keys, 10, 11 values; one key per thread
+    const int kv = (warp - 8) >> 1, half = warp & 1, key = half * 32 + lane;
     uint32_t magic;
     asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic));
-    uint32_t steps = 0;
+    uint32_t n = 0, stage = 0, phase = 0;  // step of the share, its place in the rings
     Segment s;
     bool ok = true;
     while (ok && advance(s)) {
       int vex = 0;  // exponent field that V's scaling is made for
-      for (int i = 0; i < s.nb; ++i, ++steps) {
-        const int stage = steps & 1;
-        if (!(ok = wait(&B.packed_full, steps & 1))) break;
-        uint32_t rec[W];
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(smem + S::OFF_PACKED) + key * W;
+      for (int i = 0; i < s.nb; ++i, ++n) {
+        const uint32_t slot = n % PROMPT_PACKED, par = n & 1;
+        if (!(ok = wait(&B.packed_full[slot], n / PROMPT_PACKED & 1))) break;
+        const uint32_t* rec = reinterpret_cast<const uint32_t*>(smem + S::OFF_PACKED + slot * S::PACKED_BYTES) + key * W;
+        uint32_t word[D / 8], prm[2 * NG];
 #pragma unroll
-        for (int x = 0; x < W; x += 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(src + x);
-          rec[x] = v.x, rec[x + 1] = v.y, rec[x + 2] = v.z, rec[x + 3] = v.w;
+        for (int x = 0; x < D / 8; x += 4) {
+          const uint4 q = *reinterpret_cast<const uint4*>(rec + kv * (D / 8) + x);
+          word[x] = q.x, word[x + 1] = q.y, word[x + 2] = q.z, word[x + 3] = q.w;
         }
-        const bool have = B.valid[key >> 5] >> (key & 31) & 1;
-        // the largest magnitudes of the step's keys and values
-        uint32_t top[2] = {0, 0};
 #pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp) {
-            uint32_t& w = rec[D / 4 + kv * NG + grp];
-            if (!have) w = 0;
-            const float st = __uint_as_float(w << 16), m = __uint_as_float(w & 0xffff0000u);
-            const uint32_t a = __float_as_uint(fmaxf(fabsf(m), fabsf(fmaf(15.f, st, m))));
-            if (a < 0x7f800000u) top[kv] = max(top[kv], a);
-          }
-          top[kv] = __reduce_max_sync(0xffffffffu, top[kv]);
+        for (int x = 0; x < 2 * NG; x += 2) {
+          const uint2 q = *reinterpret_cast<const uint2*>(rec + D / 4 + x);
+          prm[x] = q.x, prm[x + 1] = q.y;
         }
-        uint32_t(&tops)[2][4] = B.top[stage];  // (the other step's may still be read)
-        if (lane == 0) tops[0][w4] = top[0], tops[1][w4] = top[1];
-        asm volatile("bar.sync 1, 128;" ::: "memory");
-        if (key == 0) mbar_arrive(&B.packed_empty);  // every record is in registers
-        const uint32_t kt = max(max(tops[0][0], tops[0][1]), max(tops[0][2], tops[0][3])) >> 23;
-        const uint32_t vt = max(max(tops[1][0], tops[1][1]), max(tops[1][2], tops[1][3])) >> 23;
-        // K: below 2^15; V: the largest so far in [2^12, 2^13)
-        const float kmul = kt > 141 ? __uint_as_float((268u - kt) << 23) : 1.f;  // 2^(14 - (kt - 127))
-        const int vex2 = max(max(vex, (int)vt), 13);
-        const float vmul = __uint_as_float((uint32_t)min(254, 266 - vex2) << 23);  // 2^(12 - (vex2 - 127))
-        if (!(ok = wait(&B.vempty[stage], ((steps >> 1) & 1) ^ 1))) break;  // (its scales are still in use until then)
+        const bool have = B.valid[slot][half] >> lane & 1;
+        // the largest magnitude of the step's keys (values), and where NaN is
+        uint32_t top = 0, nan = 0, mine[NG];
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          mine[grp] = !have ? 0 : kv ? prm[NG + grp] : prm[grp];
+          const float st = __uint_as_float(mine[grp] << 16), m = __uint_as_float(mine[grp] & 0xffff0000u);
+          const uint32_t a = __float_as_uint(fmaxf(fabsf(m), fabsf(fmaf(15.f, st, m))));
+          if (a < 0x7f800000u) top = max(top, a);
+          const uint32_t vw = prm[NG + grp];
+          if (have && ((vw & 0x7f80u) == 0x7f80u || (vw & 0x7f800000u) == 0x7f800000u)) nan |= 1u << grp;
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
         const uint32_t there = __ballot_sync(0xffffffffu, have);
-        if (lane == 0) B.svalid[stage][w4] = there;
-        if (key == 0) {
-          B.kmul[stage] = 1.f / kmul;
-          const int d = i == 0 ? 0 : vex - vex2;  // by which power of two O shrinks
-          B.vgrow[stage] = d > -126 ? __uint_as_float((uint32_t)(127 + d) << 23) : 0.f;
-          B.vscale[stage] = 1.f / vmul;
+        if (lane == 0) {
+          mbar_arrive(&B.packed_empty[slot]);  // (the warp's records are in its registers)
+          B.top[par][kv][half] = top;
+          if (kv == 0) B.there[par][half] = there;
         }
-        vex = vex2;
-        if (!(ok = wait(&B.kempty[stage], ((steps >> 1) & 1) ^ 1))) break;
-#pragma unroll
-        for (int kv = 0; kv < 2; ++kv) {
-          uint8_t* dst = smem + (kv ? S::OFF_V : S::OFF_K) + stage * S::TILE_BYTES + key * 128;
-          const float mul = kv ? vmul : kmul;
-#pragma unroll
-          for (int grp = 0; grp < NG; ++grp) {
-            const uint32_t pw = rec[D / 4 + kv * NG + grp];
-            const __half2 st = __float2half2_rn(__uint_as_float(pw << 16) * mul);
-            __half2 m = __float2half2_rn(__uint_as_float(pw & 0xffff0000u) * mul);
-            if (kv == 0) {  // a value that is NaN reaches the queries that see its key, through S
-              const uint32_t vw = rec[D / 4 + NG + grp];
-              if ((vw & 0x7f80u) == 0x7f80u || (vw & 0x7f800000u) == 0x7f800000u) m = __float2half2_rn(__int_as_float(0x7fc00000));
-            }
-            const bool bad = kv && ((pw & 0x7f80u) == 0x7f80u || (pw & 0x7f800000u) == 0x7f800000u);
-#pragma unroll
-            for (int x = 0; x < G / 8; ++x) {
-              const int word = grp * (G / 8) + x;
-              const uint32_t cw = rec[kv * (D / 8) + word], ch = cw >> 8;
-              uint4 o = make_uint4(unpack2<0>(cw, magic, st, m), unpack2<1>(cw, magic, st, m),
-                                   unpack2<0>(ch, magic, st, m), unpack2<1>(ch, magic, st, m));
-              if (kv && bad) o = make_uint4(0, 0, 0, 0);  // 0 * NaN must not reach the others
-              *reinterpret_cast<uint4*>(dst + (word >> 3) * 16384 + (((word & 7) ^ (key & 7)) << 4)) = o;
-            }
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + kv) : "memory");
+        const int ex = (int)(max(B.top[par][kv][0], B.top[par][kv][1]) >> 23);
+        StepInfo& I = B.info[n % PROMPT_INFO];
+        float mul;
+        if (kv == 0) {  // below 2^15
+          mul = ex > 141 ? __uint_as_float((268u - ex) << 23) : 1.f;  // 2^(14 - (ex - 127))
+          if (key == 0) {
+            I.kmul = 1.f / mul;
+            I.valid[0] = B.there[par][0], I.valid[1] = B.there[par][1];
+            I.all = (B.there[par][0] & B.there[par][1]) == 0xffffffffu;
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(kv ? &B.vfull[stage] : &B.kfull[stage]);
+        } else {  // the largest so far in [2^12, 2^13)
+          const int vex2 = max(max(vex, ex), 13);
+          mul = __uint_as_float((uint32_t)min(254, 266 - vex2) << 23);  // 2^(12 - (vex2 - 127))
+          if (key == 0) {
+            const int d = i == 0 ? 0 : vex - vex2;  // by which power of two O shrinks
+            I.vgrow = d > -126 ? __uint_as_float((uint32_t)(127 + d) << 23) : 0.f;
+            I.vscale = 1.f / mul;
+          }
+          vex = vex2;
         }
+        if (!(ok = wait(kv ? &B.vempty[stage] : &B.kempty[stage], phase ^ 1))) break;
+        uint8_t* dst = smem + (kv ? S::OFF_V : S::OFF_K) + stage * S::KV_BYTES + key * 128;
+#pragma unroll
+        for (int grp = 0; grp < NG; ++grp) {
+          __half2 st = __float2half2_rn(__uint_as_float(mine[grp] << 16) * mul);
+          __half2 m = __float2half2_rn(__uint_as_float(mine[grp] & 0xffff0000u) * mul);
+          if (nan) {  // a value that is NaN reaches the queries that see its key through S; its group of V is
+                      // zeros, as 0 * NaN must not reach the others
+            if (kv == 0) m = __float2half2_rn(__int_as_float(0x7fc00000));
+            else if (nan >> grp & 1) st = m = __float2half2_rn(0.f);
+          }
+#pragma unroll
+          for (int x = 0; x < G / 8; ++x) {
+            const int c = grp * (G / 8) + x;
+            const uint32_t cw = word[c], ch = cw >> 8;
+            *reinterpret_cast<uint4*>(dst + (c >> 3) * S::KV_PANEL + (((c & 7) ^ (key & 7)) << 4)) =
+                make_uint4(unpack2<0>(cw, magic, st, m), unpack2<1>(cw, magic, st, m), unpack2<0>(ch, magic, st, m),
+                           unpack2<1>(ch, magic, st, m));
+          }
+        }
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(kv ? &B.vfull[stage] : &B.kfull[stage]);
+        if (++stage == PROMPT_STAGES) stage = 0, phase ^= 1;
       }
     }
   } else if (warp == 12) {
@@ -587,109 +653,117 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       const int slot = s.hk / p.cache.per_slot;
       const int64_t page_stride = p.cache.page_stride[slot];
       const int32_t* head_base = p.cache.ptr[slot] + (int64_t)(s.hk - slot * p.cache.per_slot) * p.cache.head_stride[slot];
+      // lane n copies the step's run n of records, one per page, looked up a step ahead
+      auto look_up = [&](int i) {
+        const int j0 = s.key0 + i * KB, pg = first_page(j0) + lane;
+        return i < s.nb && (int64_t)pg * ps < min(j0 + KB, s.khi) ? __ldg(pages + pg) : -1;
+      };
+      int32_t ready = look_up(0);
       for (int i = 0; i < s.nb; ++i, ++steps) {
+        const uint32_t ring = steps % PROMPT_PACKED;
         const int j0 = s.key0 + i * KB, end = max(j0, min(j0 + KB, s.khi));
         const int pg0 = first_page(j0), nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
-        if (!(ok = wait(&B.packed_empty, (steps & 1) ^ 1))) break;
         // keys that exist: those before `end` whose page is one
-        uint32_t vm[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int n = end - j0 - 32 * c;
-          vm[c] = n >= 32 ? 0xffffffffu : n > 0 ? (1u << n) - 1 : 0;
-        }
-        int bytes = (end - j0) * W * 4;
+        uint64_t vm = end - j0 >= 64 ? ~0ull : (1ull << (end - j0)) - 1;
         for (int n0 = 0; n0 < nruns; n0 += 32) {
           const int n = n0 + lane;
-          const int32_t page = n < nruns ? __ldg(pages + pg0 + n) : 0;
-          const bool good = page >= 0 && page < p.cache.pages;
-          unsigned badm = __ballot_sync(0xffffffffu, !good);
-          if (badm) {
+          const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(pages + pg0 + n) : 0;
+          const bool good = n >= nruns || (page >= 0 && page < p.cache.pages);
+          if (!__all_sync(0xffffffffu, good)) {
             if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
-            while (badm) {
-              const int m = n0 + __ffs(badm) - 1;
-              badm &= badm - 1;
-              const int a = max(j0, (pg0 + m) * ps) - j0, z = min(end, (pg0 + m + 1) * ps) - j0;
-              for (int k = a; k < z; ++k) vm[k >> 5] &= ~(1u << (k & 31));
-              bytes -= (z - a) * W * 4;
+            uint64_t bad = 0;
+            if (!good) {
+              const int a = max(j0, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
+              bad = (z - a >= 64 ? ~0ull : (1ull << (z - a)) - 1) << a;
             }
+            for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+            vm &= ~bad;
           }
         }
+        if (!(ok = wait(&B.packed_empty[ring], (steps / PROMPT_PACKED & 1) ^ 1))) break;
         if (lane == 0) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c) B.valid[c] = vm[c];
-          mbar_expect_tx(&B.packed_full, bytes);
+          B.valid[ring][0] = (uint32_t)vm, B.valid[ring][1] = (uint32_t)(vm >> 32);
+          mbar_expect_tx(&B.packed_full[ring], __popcll(vm) * W * 4);
         }
         __syncwarp();
         for (int n = lane; n < nruns; n += 32) {
-          const int32_t page = __ldg(pages + pg0 + n);
+          const int32_t page = n < 32 ? ready : __ldg(pages + pg0 + n);
           if (page < 0 || page >= p.cache.pages) continue;
           const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
-          bulk_load(smem + S::OFF_PACKED + (a - j0) * (W * 4),
-                    head_base + page * page_stride + (int64_t)(a - (pg0 + n) * ps) * W, (z - a) * W * 4, &B.packed_full);
+          bulk_load(smem + S::OFF_PACKED + ring * S::PACKED_BYTES + (a - j0) * (W * 4),
+                    head_base + page * page_stride + (int64_t)(a - (pg0 + n) * ps) * W, (z - a) * W * 4,
+                    &B.packed_full[ring]);
         }
+        ready = look_up(i + 1);
         __syncwarp();
       }
     }
   } else {
-    // ================================================= matrix products
+    // ================================================= matrix products of tile t
+    const int t = warp - 13;
     const bool leader = elect_one();
-    const uint32_t qa = smem_u32(smem), ka = qa + S::OFF_K, va = qa + S::OFF_V;
+    const uint32_t qa = smem_u32(smem) + t * S::Q_BYTES, ka = smem_u32(smem) + S::OFF_K, va = smem_u32(smem) + S::OFF_V;
+    const uint32_t ds = tmem + S::TMEM_S + t * 128, dout = tmem + S::TMEM_O + t * D;
     constexpr uint32_t idesc_s = prompt_idesc(KB, false), idesc_o = prompt_idesc(D, true);
-    auto product_s = [&](int t, int stage) {
+    uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // ring positions of the next K and V
+    uint32_t done = 0, units = 0;                 // this tile's steps and units so far
+    auto next_k = [&]() {
+      if (++kst == PROMPT_STAGES) kst = 0, kph ^= 1;
+    };
+    auto next_v = [&]() {
+      if (++vst == PROMPT_STAGES) vst = 0, vph ^= 1;
+    };
+    auto product_s = [&](uint32_t place) {
       if (leader) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_ss(tmem + S::TMEM_S + t * 128,
-                     gemm::smem_desc(qa + t * S::TILE_BYTES + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024),
-                     gemm::smem_desc(ka + stage * S::TILE_BYTES + (k >> 2) * 16384 + (k & 3) * 32, 16, 1024), idesc_s,
-                     k > 0);
-        mma_commit(&B.sfull[t]);
+        for (int pn = 0; pn < S::PANELS; ++pn)
+          mma4_ss(ds + 64 * place, gemm::smem_desc(qa + pn * 16384, 16, 1024),
+                  gemm::smem_desc(ka + kst * S::KV_BYTES + pn * S::KV_PANEL, 16, 1024), idesc_s, pn > 0);
+        mma_commit(&B.sfull[t][place]);
+        mma_commit(&B.kempty[kst]);
       }
       __syncwarp();
+      next_k();
     };
-    uint32_t steps = 0, nseg = 0, pcount[2] = {0, 0}, qcount[2] = {0, 0};
     Segment s;
     bool ok = true;
     while (ok && advance(s)) {
-      const int tiles = s.rows > 128 ? 2 : 1;
-      if (!(ok = wait(&B.kfull[steps & 1], (steps >> 1) & 1))) break;
-      for (int t = 0; t < tiles && ok; ++t) {
-        if (!(ok = wait(&B.qready[t], qcount[t]++ & 1))) break;
-        gemm::tc_fence_after();
-        product_s(t, steps & 1);
+      if (t == 1 && s.rows <= 128) {  // no rows in this tile: its share in the rings' barriers all the same
+        for (int i = 0; i < s.nb && ok; ++i) {
+          if (!(ok = wait(&B.kfull[kst], kph))) break;
+          if (lane == 0) mbar_arrive(&B.kempty[kst]);
+          next_k();
+          if (!(ok = wait(&B.vfull[vst], vph))) break;
+          if (lane == 0) mbar_arrive(&B.vempty[vst]);
+          next_v();
+        }
+        continue;
       }
-      if (!ok) break;
-      if (leader) mma_commit(&B.kempty[steps & 1]);
-      __syncwarp();
-      for (int i = 0; i < s.nb && ok; ++i, ++steps) {
-        const int stage = steps & 1, next = stage ^ 1;
-        if (!(ok = wait(&B.vfull[stage], (steps >> 1) & 1))) break;
-        for (int t = 0; t < tiles; ++t) {
-          if (!(ok = wait(&B.pready[t], pcount[t]++ & 1))) break;
+      ok = wait(&B.qready[t], units++ & 1);
+      for (int i = 0; i < min(2, s.nb) && ok; ++i) {  // S of the first two steps
+        if (!(ok = wait(&B.kfull[kst], kph))) break;
+        gemm::tc_fence_after();
+        product_s((done + i) & 1);
+      }
+      for (int i = 0; i < s.nb && ok; ++i) {
+        const uint32_t place = done & 1;
+        if (!(ok = wait(&B.vfull[vst], vph) && wait(&B.pready[t][place], (done >> 1) & 1))) break;
+        gemm::tc_fence_after();
+        if (leader) {
+          mma4_ts(dout, ds + 64 * place, gemm::smem_desc(va + vst * S::KV_BYTES, S::KV_PANEL, 1024), idesc_o, i > 0);
+          mma_commit(&B.pdone[t]);
+          if (i + 1 == s.nb) mma_commit(&B.ofull[t]);
+          mma_commit(&B.vempty[vst]);
+        }
+        __syncwarp();
+        next_v();
+        ++done;
+        if (i + 2 < s.nb) {  // S two steps on, where this step's P was
+          if (!(ok = wait(&B.kfull[kst], kph))) break;
           gemm::tc_fence_after();
-          if (leader) {
-#pragma unroll
-            for (int k = 0; k < KB / 16; ++k)
-              mma_f16_ts(tmem + S::TMEM_O + t * D, tmem + S::TMEM_S + t * 128 + 8 * k,
-                         gemm::smem_desc(va + stage * S::TILE_BYTES + k * 2048, 16384, 1024), idesc_o,
-                         i > 0 || k > 0);
-            if (i + 1 == s.nb) mma_commit(&B.ofull[t]);
-            if (t + 1 == tiles) mma_commit(&B.vempty[stage]);
-          }
-          __syncwarp();
-          if (i + 1 < s.nb) {
-            if (t == 0 && !(ok = wait(&B.kfull[next], ((steps + 1) >> 1) & 1))) break;
-            gemm::tc_fence_after();
-            product_s(t, next);
-            if (t + 1 == tiles) {
-              if (leader) mma_commit(&B.kempty[next]);
-              __syncwarp();
-            }
-          }
+          product_s(place);
         }
       }
-      ++nseg;
     }
   }
   // ---- everything issued is done (or, given up, has had its time); free tensor memory
@@ -702,7 +776,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
   gemm::tc_fence_before();
   __syncthreads();
   gemm::tc_fence_after();
-  if (warp == PROMPT_WARPS - 1)
+  if (warp == 13)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
 }
 
