@@ -489,9 +489,13 @@ DT_API dt_status dt_tp_kv4_append(const dt_dtensor* k, const dt_dtensor* v, cons
  * A query that sees no key gets out = 0 and lse = -inf.  Whatever the hidden
  * keys, or places of the pages beyond a sequence's length, hold (infinities
  * and NaN too) does not reach the result.
- * The softmax and all sums are fp32; for bf16 activations the probabilities
- * times the value steps are rounded to bf16 before their product (fp32
- * activations: three bf16 parts, 24 bits).
+ * The softmax and all sums are fp32.  For bf16 activations the products take
+ * fp16 operands (11 bits), scaled by powers of two into fp16's range: queries,
+ * probabilities times value steps, and with many rows the cache's numbers.
+ * For fp32 activations each is three bf16 parts (24 bits).
+ * A value group held as NaN makes the results that see it NaN: its channels,
+ * and with 64 (query, head) rows per sequence and kv head or more the whole
+ * head's.  At most 32768 query heads.
  * workspace: 256-byte aligned device memory of the queried size, which
  * depends on the current device; its contents between calls are the
  * caller's.  Waits for copies are bounded (DT_DEV_ERR_TIMEOUT).

@@ -677,6 +677,40 @@ def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: D
     return y
 
 
+def tp_cached_attention(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, wo: DTensor, cache: DTensor,
+                        page_table: DTensor, kv_lens: DTensor, q_starts: Optional[DTensor] = None, *, head_dim: int,
+                        group: int = 64, q_weight: Optional[DTensor] = None, k_weight: Optional[DTensor] = None,
+                        cos_sin: Optional[DTensor] = None, positions: Optional[DTensor] = None, eps: float = 1e-6,
+                        interleaved: bool = False, scale: Optional[float] = None, causal: bool = True,
+                        window: int = 0, mode: str = ALL_REDUCE, tp_dim="tp", out_dtype=None,
+                        out: Optional[DTensor] = None) -> DTensor:
+    """One attention block over a paged 4-bit cache, for prompts, chunks of them and decode steps alike.
+
+    x [tokens, hidden] holds the new tokens of each sequence, one after the
+    other (``q_starts`` [batch + 1], or None: the same number each), and
+    ``kv_lens`` the lengths with them.  q/k/v column-parallel in one launch;
+    with ``q_weight`` / ``k_weight`` the head norms and, if ``positions`` (one
+    per token) are given, the rotation in the same pass; the new keys and
+    values go into ``cache`` (rotated on the way, queries too, when
+    ``positions`` are not given); attention; o row-parallel on its Shard(-1)
+    output.  Nothing waits for the device, so a decode step can be captured
+    into a graph and replayed with new contents of x, kv_lens and positions."""
+    q, k, v = column_parallel_linear_multi(x, [wq, wk, wv], tp_dim=tp_dim)
+    kw = dict(head_dim=head_dim, tp_dim=tp_dim)
+    in_norm = positions is not None
+    if q_weight is not None or k_weight is not None or in_norm:
+        q, k = tp_qk_norm_rope(q, k, q_weight, k_weight, cos_sin if in_norm else None, positions, eps=eps,
+                               interleaved=interleaved, **kw)
+    kw["group"] = group
+    if cos_sin is None or in_norm:
+        tp_kv4_append(k, v, cache, page_table, kv_lens, q_starts, **kw)
+    else:
+        q = tp_kv4_append(k, v, cache, page_table, kv_lens, q_starts, q=q, cos_sin=cos_sin, interleaved=interleaved,
+                          **kw)
+    a = tp_kv4_attention(q, cache, page_table, kv_lens, q_starts, scale=scale, causal=causal, window=window, **kw)
+    return row_parallel_linear(a, wo, mode=mode, tp_dim=tp_dim, out_dtype=out_dtype, out=out)
+
+
 # ---------------------------------------------------------------- DTorch-style layers
 
 class Linear:

@@ -49,7 +49,7 @@ constexpr int PROMPT_ROWS = 256;
 constexpr int PROMPT_KEYS = 64;  // of a step
 constexpr int PROMPT_WARPS = 15;
 // Steps that a unit counts for its start and end when the work is shared out
-// (4: 281 us, 12: 267 us for three prompt chunks of 2048, 1500 and 777 tokens).
+// (4: 281 us, 12: 267 us for three chunks of up to 1024 tokens on up to 8000 keys).
 constexpr int PROMPT_EXTRA = 12;
 constexpr int PROMPT_PACKED = 4, PROMPT_STAGES = 3, PROMPT_INFO = 8;  // rings: packed, unpacked, scales
 

@@ -252,12 +252,12 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
             }
           }
           if (norm) {
-            const f2 on = both(ok && h < X.heads ? 1.f : 0.f);
+            const bool on = ok && h < X.heads;  // (a choice, not a factor: what is left out may be NaN)
             f2 gx = both(0.f);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const f2 ta = ya[e] * a[e], tb = yb[e] * b[e];
-              da[e] = fma2(ta, on, da[e]), db[e] = fma2(tb, on, db[e]);
+              if (on) da[e] = fma2(ya[e], a[e], da[e]), db[e] = fma2(yb[e], b[e], db[e]);
               gx = fma2(ta, wa[e], gx), gx = fma2(tb, wb[e], gx);
             }
             const float k = head_sum(gx.x + gx.y) * -r * inv_d;  // - r * mean(g * x r)

@@ -177,6 +177,28 @@ def test_positions_outside_the_table(lib, d):
     check_backward(case, got, dys, xs, ws, cs, pos)
 
 
+@pytest.mark.parametrize("d", [128, 40])
+def test_left_out_tokens_may_hold_nan(lib, d):
+    """Tokens without a position add nothing to the weights' gradients, whatever they hold."""
+    case = (6, 5, 3, d, d, 1, "bf16", False)
+    mesh, rng, xs, ws, cs, pos, ops = make(case, 21)
+    pos = pos.copy()
+    pos[1], pos[4] = -1, cs.shape[0]
+    ops["positions"] = ints(pos, mesh)
+    dys = [draw(rng, x.shape, "bf16") for x in xs]
+    dyd = [sharded(y, mesh, "bf16") for y in dys]
+    for n in "qk":
+        ops[n].slots[0][1] = float("nan")
+        ops[n].slots[0][4] = float("inf")
+    for y in dyd:
+        y.slots[0][4] = float("nan")
+    for x in xs + tuple(dys):
+        x[[1, 4]] = 0
+    got = tsl.tp_qk_norm_rope_backward(*dyd, **ops, head_dim=d, eps=EPS)
+    assert tsl.read_device_status() == tsl._lib.DEV_ERR_INDEX
+    check_backward(case, got, dys, xs, ws, cs, pos)
+
+
 def test_gradient_against_differences(lib):
     """fp32, a small head: central differences of the kernel's own forward."""
     case = (2, 2, 1, 16, 8, 1, "fp32", False)
