@@ -18,8 +18,9 @@
 // The accumulators of a long sequence have to be centred: a code's mean of
 // 7.5 would cancel against the sum of all p m' and take the low bits along
 // (the matrix unit truncates; an offset of 128 cost 1.0% at 131071 keys in
-// runs of 2900).  So -8 times the tile's sum of p s' goes in as one more
-// product per 16 channels and tile, and m' becomes m' + 8 s'.
+// runs of 2900).  So each tile adds -8 times its sum of p s' as rounded, which
+// one more product per 16 keys and group forms in fp32 (a sum taken in fp16
+// instead cost an error of 2^-10 of the result), and m' becomes m' + 8 s'.
 // fp32 activations: three bf16 parts (24 bits) times codes - 8 made from the
 // nibble in the mantissa of 128; each tile's product is added to the sums in
 // the ordinary fp32 adder, which rounds to nearest.
@@ -31,17 +32,22 @@
 // turn into the operand of O^T with one 8 x 8 transpose (movmatrix).
 //
 // Work.  A unit is (sequence, kv head, block of rows); its keys come in
-// blocks of four tiles.  The device adds up all units' blocks from kv_lens and gives
-// every CTA an equal, contiguous share, whatever the lengths: no host
-// knowledge of them, no idle SM for one long sequence.  A share that ends
+// blocks of four tiles.  The device adds up all units' blocks from kv_lens
+// and gives every CTA an equal, contiguous share, whatever the lengths: no
+// host knowledge of them, no idle SM for one long sequence.  A share that ends
 // inside a unit leaves its sums in the workspace, and the join kernel adds
 // them.  Inside a CTA each of the four warps takes every fourth tile of 64
-// keys (32 at head_dim 256) with its own ring of bulk copies (a page's records of a head are
-// contiguous: one copy per page and tile), so no warp waits for another
-// until the unit ends.
+// keys (32 at head_dim 256) with its own ring of bulk copies (a page's records
+// of a head are contiguous: one copy per page and tile), so no warp waits for
+// another until the unit ends.
 //
-// Bound: HBM for 1 to 8 rows (every record is read once), instruction issue
-// close behind it.
+// Bound: the instructions and their latency at the 12 warps an SM has room for
+// (168 registers each), HBM next.  48 sequences of up to 8192 keys, 32/8 heads
+// of 128: 67.9 us for 252 MB of records, 3.7 TB/s; the same loads without the
+// arithmetic 48.6, the arithmetic without the loads 69.  Five sequences of
+// 131071: 93.6 us for 436 MB, 4.7 TB/s (73.7 and 97).  One sequence of 4097:
+// 11.9 us, all of it launches and latency.  Tiles of 32 keys with up to five
+// CTAs an SM: 81 to 153 us where these take 68.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -64,7 +70,7 @@ struct Shape {
   static constexpr int WL = D / 32;         // key code words of a lane
   static constexpr int MT = G / 16;         // 16-channel tiles of O^T in a group
   static constexpr int RB = 8 * NT;         // rows of a unit
-    static constexpr int TILE = D <= 128 ? 64 : 32;  // keys of a warp's tile
+  static constexpr int TILE = D <= 128 ? 64 : 32;  // keys of a warp's tile
   static constexpr int HT = TILE / 16;
   static constexpr int BLOCK = TILE * WARPS;       // keys of a step of the schedule
   static constexpr int STAGES = 2;
@@ -116,10 +122,6 @@ __device__ __forceinline__ void mma16816_h_first(float (&d)[4], uint32_t a0, uin
 }
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ uint32_t add_f16(uint32_t a, uint32_t b) {
-  const __half2 h = __hadd2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
@@ -658,6 +660,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
         }
 
       // ---- O^T += V^T P^T, 16 keys at a time
+      float csum[NT][NG][4];  // -8 (even nibbles) and -128 (odd ones, 16 times as large) times 2^-24 times the sums of p s'
       uint32_t vp[HT][2][NG];  // value parameters of keys r and r + 8
 #pragma unroll
       for (int h = 0; h < HT; ++h)
@@ -707,7 +710,6 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
           }
         }
       }
-      uint32_t bsum[NT][NG][2];
 #pragma unroll
       for (int h = 0; h < HT; ++h) {
         const uint32_t* vw = tile + (16 * h + 2 * ql) * W + D / 8 + (WPG == 2 ? r : r & 3);
@@ -761,9 +763,17 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
                 for (int n = 0; n < NP; ++n) bf[nt][n][k] = transpose8x8(pack_bf16(y0[n], y1[n]));
               } else {
                 bf[nt][0][k] = transpose8x8(pack_f16(x[nt][grp][k][0], x[nt][grp][k][1]));
-                bsum[nt][grp][k] = h == 0 ? bf[nt][0][k] : add_f16(bsum[nt][grp][k], bf[nt][0][k]);
               }
             }
+          if constexpr (!FULL) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              if (h == 0)
+                mma16816_h_first(csum[nt][grp], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, bf[nt][0][0], bf[nt][0][1]);
+              else
+                mma16816_h(csum[nt][grp], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, bf[nt][0][0], bf[nt][0][1]);
+            }
+          }
           const uint32_t* w = vw + grp * (G / 8);
           const uint32_t w0 = w[0], w1 = w[W], w2 = w[8 * W], w3 = w[9 * W];
           const uint32_t sel = WPG == 2 || r < 4 ? 0x5410u : 0x7632u;
@@ -795,15 +805,15 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
           }
         }
       }
-      if constexpr (!FULL) {  // centre: -8 (even nibbles) and -128 (odd ones, 16 times as large), times 2^-24
+      if constexpr (!FULL) {  // centre
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int grp = 0; grp < NG; ++grp)
 #pragma unroll
             for (int m = 0; m < MT; ++m)
-              mma16816_h(o[nt][grp][m], 0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u, bsum[nt][grp][0],
-                         bsum[nt][grp][1]);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) o[nt][grp][m][e] += csum[nt][grp][e];
       }
       __syncwarp();  // the stage may be refilled
     }

@@ -35,7 +35,7 @@ struct AttnParams {
   int32_t want_lse;
   int32_t rb;        // rows of a unit (for the join)
   float scale_log2;  // softmax scale * log2(e)
-  float* part;       // [2 CTAs][rows][D + 2]: sums, then maximum (log2 units) and denominator
+  float* part;       // [2 CTAs][rows][D + 4]: sums, then maximum (log2 units), denominator, padding
   Split* split;      // [CTA]
   int32_t* status;
   unsigned long long wait_limit_ns;

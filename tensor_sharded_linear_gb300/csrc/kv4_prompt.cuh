@@ -490,22 +490,22 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           }
         }
         const float add = ref == -INFINITY ? 0.f : 6.f - ref;  // a row that has seen nothing yet
-        float d0 = 0.f, d1 = 0.f;
+        f2 sum = both(0.f);
         auto half = [&](uint32_t(&x)[32], int col) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float y0 = ex2(fmaf(__uint_as_float(x[2 * e]), sc, add));
-            const float y1 = ex2(fmaf(__uint_as_float(x[2 * e + 1]), sc, add));
-            d0 += y0, d1 += y1;
-            const __half2 h = __floats2half2_rn(y0, y1);
+            f2 y = fma2(f2{__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])}, both(sc), both(add));
+            y = f2{ex2(y.x), ex2(y.y)};
+            sum = sum + y;
+            const __half2 h = __floats2half2_rn(y.x, y.y);
             w[e] = *reinterpret_cast<const uint32_t*>(&h);
           }
           tmem_st16(tb + col, w);  // over columns that have been read
         };
         half(u, 0);
         half(v, 16);
-        den += d0 + d1;
+        den += sum.x + sum.y;
         tmem_st_wait();
         gemm::tc_fence_before();
         __syncwarp();
