@@ -11,7 +11,7 @@
 // minimum + step * code is one fp16 multiply-add, correctly rounded to 11
 // bits (with bf16's 8, keys, values and probabilities would each add as much
 // error as the output's own rounding).  fp16's range is met by powers of
-// two: per row for the queries, per step of 128 keys for K (undone in the
+// two: per row for the queries, per step of 64 keys for K (undone in the
 // softmax's multiplier), and for V the largest so far, with O rescaled where
 // it grows.
 //
@@ -22,14 +22,20 @@
 // packed, three unpacked, two S per tile.  While the softmax of a step runs,
 // the tensor core forms P V of the step before and S of the step after, for
 // both tiles in turn, and the records of the next steps are on their way.
-// (With steps of 128 keys and one packed buffer the wait for the records
-// alone took 3090 cycles a step, measured with everything else taken out.)
-// A row's reference for the exponential follows its maximum only when that
-// has grown by more than 2^8, so O, which stays in tensor memory, is rescaled
-// rarely.
+// A row's reference for the exponential follows its maximum only when a step's
+// sum passes 2^14, so ordinary steps take no maximum, and O, which stays in
+// tensor memory, is rescaled rarely.
 //
-// Bound: the tensor core (4 D flops a pair of row and key) for contexts of
-// any length.
+// Bound: three chunks of up to 1024 tokens on up to 8000 keys, 32/8 heads of
+// 128, take 241 us for 239 GFLOP, 0.99 PFLOP/s; 256 rows against 128 keys take
+// 3710 cycles, of which the products need 2050 at the tensor core's rate.  An S
+// of 64 keys takes 372 cycles instead of 256, since it reads the queries' tile
+// from shared memory each time; without exponentials, tensor-memory loads and
+// unpacking's stores 3395 are left, with half of each S 2650, without products
+// 2300, the round trips between the roles.  Tensor memory is full (two O, four
+// S), so an S of 128 keys has one buffer a tile: 5370 cycles, the softmax then
+// waits for every product.  A second loader warp, four unpacked stages and
+// longer or shorter sleeps in the waits changed nothing.
 //
 // The schedule, the pieces of units that a CTA's share cuts and the join are
 // those of kv4_attention.cuh, with each row block's own number of key blocks.
@@ -49,8 +55,9 @@ constexpr int PROMPT_ROWS = 256;
 constexpr int PROMPT_KEYS = 64;  // of a step
 constexpr int PROMPT_WARPS = 15;
 // Steps that a unit counts for its start and end when the work is shared out
-// (4: 281 us, 12: 267 us for three chunks of up to 1024 tokens on up to 8000 keys).
-constexpr int PROMPT_EXTRA = 12;
+// (4: 281 us, 12: 267 us for three chunks of up to 1024 tokens on up to 8000
+// keys; with shorter steps since, 12: 244, 16: 241, 22: 244).
+constexpr int PROMPT_EXTRA = 16;
 constexpr int PROMPT_PACKED = 4, PROMPT_STAGES = 3, PROMPT_INFO = 8;  // rings: packed, unpacked, scales
 
 template <int D, int G>
@@ -106,6 +113,17 @@ __device__ __forceinline__ bool mbar_try_wait_hint(uint64_t* bar, uint32_t parit
       "selp.u32 %0, 1, 0, p;\n\t}"
       : "=r"(ok)
       : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
       : "memory");
   return ok != 0;
 }
@@ -429,12 +447,12 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       for (int i = 0; i < s.nb; ++i) {
         const uint32_t place = mine & 1, tb = ts + 64 * place;
         // (V's barrier second: its phase is told by its parity, so the step before has to have come, as it has
-        // when there is an S)
-        if (!(ok = wait(&B.sfull[t][place], (mine >> 1) & 1) && wait(&B.vfull[vstage], vphase))) break;
+        // when there is an S.  Both in one look: a wait that need not wait costs 150 cycles.)
+        const bool s_there = mbar_test(&B.sfull[t][place], (mine >> 1) & 1), v_there = mbar_test(&B.vfull[vstage], vphase);
+        if (!__all_sync(0xffffffffu, s_there && v_there) &&
+            !(ok = wait(&B.sfull[t][place], (mine >> 1) & 1) && wait(&B.vfull[vstage], vphase)))
+          break;
         gemm::tc_fence_after();
-        uint32_t u[32], v[32];
-        gemm::tmem_ld32(tb, u);
-        gemm::tmem_ld32(tb + 32, v);
         const StepInfo& I = B.info[all % PROMPT_INFO];
         const float sc = row_scale * I.kmul;
         vs = I.vscale;
@@ -444,67 +462,78 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         if (p.causal) hi = min(hi, pos + 1 - j0);
         if (p.window) lo = max(0, pos - p.window + 1 - j0);
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < KB || !I.all);
-        gemm::tmem_ld_wait();
-        if (masked) {
-          auto see = [&](int c) {  // bit e: column 32 c + e
-            const int a = max(lo - 32 * c, 0), z = min(hi - 32 * c, 32);
-            return (z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u) & I.valid[c];
-          };
-          const uint32_t su = see(0), sv = see(1);
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            if (!(su >> e & 1)) u[e] = 0xff800000u;
-            if (!(sv >> e & 1)) v[e] = 0xff800000u;
-          }
-        }
-        float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four short chains)
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          t4[e & 2] = fmaxf(t4[e & 2], fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
-          t4[1 + (e & 2)] = fmaxf(t4[1 + (e & 2)], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
-        }
-        const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
         float f = I.vgrow;  // what O is to be multiplied by
-        if (i == 0) {
-          ref = top;
-        } else {
-          if (top > ref + 8.f) {
-            const float g = ex2(ref - top);
-            ref = top;
-            den *= g;
-            f *= g;
-          }
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-            // every product before is in O (S of this step followed all but the last)
-            if (!(ok = wait(&B.pdone[t], (mine - 1) & 1))) break;
-            gemm::tc_fence_after();
+        // The reference stays while the row's sum of this step is at most 2^14, so no maximum is taken; else (and
+        // where there is none yet) the step is taken once more with its maximum.
+        bool look = __any_sync(0xffffffffu, ref == -INFINITY);
+        uint32_t w[32];
+        f2 sum;
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t w[16];
-              tmem_ld16(to + 16 * c, w);
-              gemm::tmem_ld_wait();
+        while (true) {
+          uint32_t u[32], v[32];
+          gemm::tmem_ld32(tb, u);
+          gemm::tmem_ld32(tb + 32, v);
+          gemm::tmem_ld_wait();
+          if (masked) {
+            auto see = [&](int c) {  // bit e: column 32 c + e
+              const int a = max(lo - 32 * c, 0), z = min(hi - 32 * c, 32);
+              return (z > a ? (0xffffffffu >> (32 - (z - a))) << a : 0u) & I.valid[c];
+            };
+            const uint32_t su = see(0), sv = see(1);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-              tmem_st16(to + 16 * c, w);
+            for (int e = 0; e < 32; ++e) {
+              if (!(su >> e & 1)) u[e] = 0xff800000u;
+              if (!(sv >> e & 1)) v[e] = 0xff800000u;
             }
           }
-        }
-        const float add = ref == -INFINITY ? 0.f : 6.f - ref;  // a row that has seen nothing yet
-        f2 sum = both(0.f);
-        auto half = [&](uint32_t(&x)[32], int col) {
-          uint32_t w[16];
+          if (look) {
+            float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};  // (four short chains)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            f2 y = fma2(f2{__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])}, both(sc), both(add));
-            y = f2{ex2(y.x), ex2(y.y)};
-            sum = sum + y;
-            const __half2 h = __floats2half2_rn(y.x, y.y);
-            w[e] = *reinterpret_cast<const uint32_t*>(&h);
+            for (int e = 0; e < 32; e += 2) {
+              t4[e & 2] = fmaxf(t4[e & 2], fmaxf(__uint_as_float(u[e]), __uint_as_float(u[e + 1])));
+              t4[1 + (e & 2)] = fmaxf(t4[1 + (e & 2)], fmaxf(__uint_as_float(v[e]), __uint_as_float(v[e + 1])));
+            }
+            const float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3])) * sc;
+            if (top > ref) {
+              const float g = ex2(ref - top);  // (0 from no reference: O and the sum are zero there, or not yet begun)
+              ref = top;
+              den *= g;
+              f *= g;
+            }
           }
-          tmem_st16(tb + col, w);  // over columns that have been read
-        };
-        half(u, 0);
-        half(v, 16);
+          const float add = ref == -INFINITY ? 0.f : 6.f - ref;  // a row that has seen nothing yet
+          sum = both(0.f);
+          auto half = [&](const uint32_t(&x)[32], int at) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              f2 y = fma2(f2{__uint_as_float(x[2 * e]), __uint_as_float(x[2 * e + 1])}, both(sc), both(add));
+              y = f2{ex2(y.x), ex2(y.y)};
+              sum = sum + y;
+              const __half2 h = __floats2half2_rn(y.x, y.y);
+              w[at + e] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+          };
+          half(u, 0);
+          half(v, 16);
+          if (look || __all_sync(0xffffffffu, sum.x + sum.y <= 16384.f)) break;
+          look = true;
+        }
+        if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          // every product before is in O (S of this step followed all but the last)
+          if (!(ok = wait(&B.pdone[t], (mine - 1) & 1))) break;
+          gemm::tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld16(to + 16 * c, x);
+            gemm::tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f);
+            tmem_st16(to + 16 * c, x);
+          }
+        }
+        tmem_st16(tb, *reinterpret_cast<uint32_t(*)[16]>(w));  // over columns that have been read
+        tmem_st16(tb + 16, *reinterpret_cast<uint32_t(*)[16]>(w + 16));
         den += sum.x + sum.y;
         tmem_st_wait();
         gemm::tc_fence_before();
@@ -603,7 +632,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         if (kv == 0) {  // below 2^15
           mul = ex > 141 ? __uint_as_float((268u - ex) << 23) : 1.f;  // 2^(14 - (ex - 127))
           if (key == 0) {
-            I.kmul = 1.f / mul;
+            I.kmul = ex > 141 ? __uint_as_float((ex - 14u) << 23) : 1.f;  // 1 / mul
             I.valid[0] = B.there[par][0], I.valid[1] = B.there[par][1];
             I.all = (B.there[par][0] & B.there[par][1]) == 0xffffffffu;
           }
@@ -613,7 +642,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           if (key == 0) {
             const int d = i == 0 ? 0 : vex - vex2;  // by which power of two O shrinks
             I.vgrow = d > -126 ? __uint_as_float((uint32_t)(127 + d) << 23) : 0.f;
-            I.vscale = 1.f / mul;
+            I.vscale = __uint_as_float((uint32_t)max(0, vex2 - 12) << 23);  // 1 / mul
           }
           vex = vex2;
         }
