@@ -25,17 +25,18 @@ namespace {
 using namespace kv4;
 
 // The kernel for prompts from this many (query, head) rows per sequence and
-// kv head.  It works on blocks of 256 rows whatever their number, the other in
-// passes of 16.  16 sequences of 4096 keys, 32/8 heads of 128: 48 rows 85 us
-// there against 86 here, 64 rows 111 against 86, 256 rows 405 against 104;
-// 16/16 heads of 64: 48 rows 95 against 103, 64 rows 125 against 104.  With two
-// sequences of 2048 keys, too little for the whole device, the two meet at
-// about 96 to 128 rows (64 rows: 17.6 against 22.1 us).
+// kv head.  It works on blocks of 256 rows (128 at head_dim 256) whatever
+// their number, the other in passes of 16.  16 sequences of 4096 keys, the
+// other kernel's time first: 32/8 heads of 128, 64 rows 111 and 76 us, 256
+// rows 405 and 98, and 48 rows 87 where 64 take 76 here; 16/16 heads of 64, 64
+// rows 125 and 100; 16/2 heads of 256, 48 rows 60 where 64 take 45 here.  With
+// two sequences of 2048 keys, too little for the whole device, the two meet
+// at about 96 to 128 rows (64 rows: 17.6 and 21.9 us).
 constexpr int64_t PROMPT_FROM = 64;
-bool prompt_kernel(int D, bool fp32, int64_t rows) { return !fp32 && D <= 128 && rows >= PROMPT_FROM; }
+bool prompt_kernel(bool fp32, int64_t rows) { return !fp32 && rows >= PROMPT_FROM; }
 
 cudaError_t variant_any(int D, int G, bool fp32, int64_t rows, Variant* v) {
-  if (prompt_kernel(D, fp32, rows)) return prompt_variant(D, G, v);
+  if (prompt_kernel(fp32, rows)) return prompt_variant(D, G, v);
   return D == 64 ? variant<64>(G, fp32, rows, v) : D == 128 ? variant<128>(G, fp32, rows, v)
                                                             : variant<256>(G, fp32, rows, v);
 }
@@ -127,7 +128,7 @@ dt_status attention_call(const dt_dtensor* q, const dt_dtensor* cache, const dt_
   p.status = device_status_word(d_status);
   if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
   p.rb = v.rows;
-  e = prompt_kernel(D, fp32, c.rows_per_seq) ? prompt_launch(p, D, G, v.grid, stream)
+  e = prompt_kernel(fp32, c.rows_per_seq) ? prompt_launch(p, D, G, v.grid, stream)
       : D == 64 ? launch<64>(p, G, fp32, c.rows_per_seq, v.grid, stream)
               : D == 128 ? launch<128>(p, G, fp32, c.rows_per_seq, v.grid, stream)
                          : launch<256>(p, G, fp32, c.rows_per_seq, v.grid, stream);

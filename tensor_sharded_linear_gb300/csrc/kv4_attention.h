@@ -53,8 +53,7 @@ cudaError_t variant(int G, bool fp32, int64_t rows_per_seq, Variant* out);
 template <int D>
 cudaError_t launch(const AttnParams& p, int G, bool fp32, int64_t rows_per_seq, int grid, cudaStream_t s);
 
-// Rows of a sequence and kv head from which the tensor-core kernel for
-// prompts runs, and that kernel (bf16, head_dim 64 and 128).
+// The tensor-core kernel for prompts (bf16).
 cudaError_t prompt_variant(int D, int G, Variant* out);
 cudaError_t prompt_launch(const AttnParams& p, int D, int G, int grid, cudaStream_t s);
 

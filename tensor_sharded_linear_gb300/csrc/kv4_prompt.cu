@@ -35,19 +35,21 @@ cudaError_t launch_one(const AttnParams& p, int grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t prompt_variant(int D, int G, Variant* out) {
-  cudaError_t e = D == 64 ? (G == 32 ? prepare<64, 32>() : prepare<64, 64>())
-                          : (G == 32 ? prepare<128, 32>() : prepare<128, 64>());
+  cudaError_t e = D == 64    ? (G == 32 ? prepare<64, 32>() : prepare<64, 64>())
+                  : D == 128 ? (G == 32 ? prepare<128, 32>() : prepare<128, 64>())
+                             : (G == 32 ? prepare<256, 32>() : prepare<256, 64>());
   if (e != cudaSuccess) return e;
   out->grid = device_sm_count();
-  out->rows = PROMPT_ROWS;
+  out->rows = D == 64 ? PromptShape<64, 64>::ROWS : D == 128 ? PromptShape<128, 64>::ROWS : PromptShape<256, 64>::ROWS;
   const size_t splits = ((size_t)out->grid * sizeof(Split) + 255) / 256 * 256;
-  out->bytes = splits + (size_t)2 * out->grid * PROMPT_ROWS * (D + 4) * sizeof(float);
+  out->bytes = splits + (size_t)2 * out->grid * out->rows * (D + 4) * sizeof(float);
   return cudaSuccess;
 }
 
 cudaError_t prompt_launch(const AttnParams& p, int D, int G, int grid, cudaStream_t s) {
   if (D == 64) return G == 32 ? launch_one<64, 32>(p, grid, s) : launch_one<64, 64>(p, grid, s);
-  return G == 32 ? launch_one<128, 32>(p, grid, s) : launch_one<128, 64>(p, grid, s);
+  if (D == 128) return G == 32 ? launch_one<128, 32>(p, grid, s) : launch_one<128, 64>(p, grid, s);
+  return G == 32 ? launch_one<256, 32>(p, grid, s) : launch_one<256, 64>(p, grid, s);
 }
 
 }  // namespace kv4

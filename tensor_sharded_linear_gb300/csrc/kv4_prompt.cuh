@@ -1,9 +1,10 @@
 // Attention of many queries per sequence over the paged 4-bit cache: prompts
-// and chunks of prompts (bf16 activations, head_dim 64 or 128).
+// and chunks of prompts (bf16 activations).
 //
 // The same mathematics as kv4_attention.cuh, in the form that feeds
 // tcgen05: a CTA takes 256 (query, head) rows of one sequence and kv head as
-// two tiles of 128, and steps through the keys 128 at a time.
+// two tiles of 128 (head_dim 256: one tile), and steps through the keys 64 at
+// a time.
 //   S = Q K^T   both operands in shared memory, S in tensor memory
 //   P = 2^(S * scale - reference), fp16, over S's columns in tensor memory
 //   O += P V    P from tensor memory, V from shared memory
@@ -18,10 +19,11 @@
 // Roles, 15 warps: two softmax groups of four warps (one row of one tile per
 // thread), four unpacking warps (two for K, two for V, one key per thread), one
 // warp that issues the bulk copies of the packed records, one per tile that
-// issues its matrix products.  Everything goes in steps of 64 keys through rings: four
-// packed, three unpacked, two S per tile.  While the softmax of a step runs,
-// the tensor core forms P V of the step before and S of the step after, for
-// both tiles in turn, and the records of the next steps are on their way.
+// issues its matrix products.  Everything goes in steps of 64 keys through
+// rings: four packed, three unpacked, two S per tile.  While the softmax of a
+// step runs, the tensor core forms P V of the step before and S of the step
+// after, for both tiles in turn, and the records of the next steps are on
+// their way.
 // A row's reference for the exponential follows its maximum only when a step's
 // sum passes 2^14, so ordinary steps take no maximum, and O, which stays in
 // tensor memory, is rescaled rarely.
@@ -35,7 +37,10 @@
 // 2300, the round trips between the roles.  Tensor memory is full (two O, four
 // S), so an S of 128 keys has one buffer a tile: 5370 cycles, the softmax then
 // waits for every product.  A second loader warp, four unpacked stages and
-// longer or shorter sleeps in the waits changed nothing.
+// longer or shorter sleeps in the waits changed nothing.  Heads of 256 have room
+// for one tile, two unpacked stages and one packed: 212 us for three chunks of
+// up to 512 tokens on up to 8000 keys, 16/2 heads, 0.58 PFLOP/s (958 us in
+// passes of 16 rows).
 //
 // The schedule, the pieces of units that a CTA's share cuts and the join are
 // those of kv4_attention.cuh, with each row block's own number of key blocks.
@@ -51,27 +56,29 @@
 namespace dt {
 namespace kv4 {
 
-constexpr int PROMPT_ROWS = 256;
 constexpr int PROMPT_KEYS = 64;  // of a step
 constexpr int PROMPT_WARPS = 15;
 // Steps that a unit counts for its start and end when the work is shared out
 // (4: 281 us, 12: 267 us for three chunks of up to 1024 tokens on up to 8000
 // keys; with shorter steps since, 12: 244, 16: 241, 22: 244).
 constexpr int PROMPT_EXTRA = 16;
-constexpr int PROMPT_PACKED = 4, PROMPT_STAGES = 3, PROMPT_INFO = 8;  // rings: packed, unpacked, scales
+constexpr int PROMPT_PACKED = 4, PROMPT_STAGES = 3, PROMPT_INFO = 8;  // rings at most: packed, unpacked, scales
 
 template <int D, int G>
 struct PromptShape {
   static constexpr int W = kv4_words(D, G);
   static constexpr int NG = D / G;
+  static constexpr int TILES = D <= 128 ? 2 : 1, ROWS = 128 * TILES;  // (a tile's O of 256 channels fills half of
+                                                                      // tensor memory, its queries 64 KB)
+  static constexpr int PACKED = D <= 128 ? PROMPT_PACKED : 1, STAGES = D <= 128 ? PROMPT_STAGES : 2;  // what fits
   static constexpr int PANELS = D / 64;                    // 64 channels: one 128-byte row
   static constexpr int Q_BYTES = 128 * D * 2;              // a tile of 128 rows, fp16
   static constexpr int KV_BYTES = PROMPT_KEYS * D * 2;     // a step's keys or values, fp16
   static constexpr int KV_PANEL = PROMPT_KEYS * 128;
   static constexpr int PACKED_BYTES = PROMPT_KEYS * W * 4;
-  static constexpr int OFF_K = 2 * Q_BYTES, OFF_V = OFF_K + PROMPT_STAGES * KV_BYTES;
-  static constexpr int OFF_PACKED = OFF_V + PROMPT_STAGES * KV_BYTES;
-  static constexpr int OFF_BAR = OFF_PACKED + PROMPT_PACKED * PACKED_BYTES;  // barriers, flags
+  static constexpr int OFF_K = TILES * Q_BYTES, OFF_V = OFF_K + STAGES * KV_BYTES;
+  static constexpr int OFF_PACKED = OFF_V + STAGES * KV_BYTES;
+  static constexpr int OFF_BAR = OFF_PACKED + PACKED * PACKED_BYTES;  // barriers, flags
   static constexpr int SMEM = OFF_BAR + 1024 + 1024;                         // and alignment to 1024
   static constexpr int TMEM_S = 0, TMEM_O = 256;  // columns: S (and P) of tile t, step n at t * 128 + (n & 1) * 64; O
 };
@@ -212,7 +219,7 @@ __device__ __forceinline__ uint32_t unpack2(uint32_t w, uint32_t magic, __half2 
 template <int D, int G>
 __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const __grid_constant__ AttnParams p) {
   using S = PromptShape<D, G>;
-  constexpr int W = S::W, NG = S::NG, RB = PROMPT_ROWS, KB = PROMPT_KEYS;
+  constexpr int W = S::W, NG = S::NG, RB = S::ROWS, KB = PROMPT_KEYS;
   extern __shared__ uint8_t prompt_smem_raw[];
   uint8_t* smem = prompt_smem_raw + ((1024 - (smem_u32(prompt_smem_raw) & 1023)) & 1023);
   PromptBars& B = *reinterpret_cast<PromptBars*>(smem + S::OFF_BAR);
@@ -223,9 +230,9 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     for (int i = 0; i < PROMPT_PACKED; ++i) mbar_init(&B.packed_full[i], 1), mbar_init(&B.packed_empty[i], 4);
     for (int i = 0; i < PROMPT_STAGES; ++i) {
       mbar_init(&B.kfull[i], 2);
-      mbar_init(&B.kempty[i], 2);
+      mbar_init(&B.kempty[i], S::TILES);
       mbar_init(&B.vfull[i], 2);
-      mbar_init(&B.vempty[i], 2);
+      mbar_init(&B.vempty[i], S::TILES);
     }
     for (int i = 0; i < 2; ++i) {
       for (int j = 0; j < 2; ++j) mbar_init(&B.sfull[i][j], 1), mbar_init(&B.pready[i][j], 4);
@@ -379,7 +386,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     return false;
   };
 
-  if (warp < 8) {
+  if (warp < 4 * S::TILES) {
     // ================================================= softmax: tile t, one row per thread
     const int t = warp >> 2, row_in = t * 128 + (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -389,7 +396,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     uint32_t vstage = 0, vphase = 0;       // ring position of step `all`
     auto skip = [&](uint32_t n) {
       all += n, vstage += n;
-      while (vstage >= PROMPT_STAGES) vstage -= PROMPT_STAGES, vphase ^= 1;
+      while (vstage >= S::STAGES) vstage -= S::STAGES, vphase ^= 1;
     };
     Segment s;
     bool ok = true;
@@ -405,29 +412,32 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       // has been taken, so its queries are done with.)
       float row_scale;
       {
-        Raw8<__nv_bfloat16> raw[D / 8];
-        if (on) {
-          const __nv_bfloat16* q = head_ptr<__nv_bfloat16>(p.q, tok, head, D);
+        // (256 channels would not stay in registers: they are read twice)
+        constexpr int HELD = D <= 128 ? D / 8 : 0;
+        const __nv_bfloat16* q = on ? head_ptr<__nv_bfloat16>(p.q, tok, head, D) : nullptr;
+        Raw8<__nv_bfloat16> raw[HELD ? HELD : 1];
+        auto fetch = [&](int w) {
+          Raw8<__nv_bfloat16> x;
+          if (on) x.load(q + 8 * w);
+          else x.zero();
+          return x;
+        };
 #pragma unroll
-          for (int w = 0; w < D / 8; ++w) raw[w].load(q + 8 * w);
-        } else {
-#pragma unroll
-          for (int w = 0; w < D / 8; ++w) raw[w].zero();
-        }
+        for (int w = 0; w < HELD; ++w) raw[w] = fetch(w);
         float top = 0.f;
-#pragma unroll
+#pragma unroll(HELD ? HELD : 8)
         for (int w = 0; w < D / 8; ++w) {
           float x[8];
-          raw[w].get(x);
+          (HELD ? raw[HELD ? w : 0] : fetch(w)).get(x);
 #pragma unroll
           for (int c = 0; c < 8; ++c) top = fmaxf(top, fabsf(x[c]));
         }
         const float mult = __uint_as_float((uint32_t)max(10, min(254, 264 - (int)(__float_as_uint(top) >> 23))) << 23);
         row_scale = p.scale_log2 / mult;
-#pragma unroll
+#pragma unroll(HELD ? HELD : 8)
         for (int w = 0; w < D / 8; ++w) {
           float x[8];
-          raw[w].get(x);
+          (HELD ? raw[HELD ? w : 0] : fetch(w)).get(x);
           // the order of channels in which a word's nibble pairs come apart
           auto pk = [&](float lo, float hi) {
             const __half2 h = __floats2half2_rn(lo * mult, hi * mult);
@@ -581,7 +591,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       if (threadIdx.x == 0 && s.first && !s.whole)
         p.split[blockIdx.x] = Split{s.unit, s.row0, s.rows, s.q0, s.hk, s.last};
     }
-  } else if (warp < 12) {
+  } else if (warp >= 8 && warp < 12) {
     // ================================================= unpacking: warps 8, 9 keys, 10, 11 values; one key per thread
     const int kv = (warp - 8) >> 1, half = warp & 1, key = half * 32 + lane;
     uint32_t magic;
@@ -592,8 +602,8 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     while (ok && advance(s)) {
       int vex = 0;  // exponent field that V's scaling is made for
       for (int i = 0; i < s.nb; ++i, ++n) {
-        const uint32_t slot = n % PROMPT_PACKED, par = n & 1;
-        if (!(ok = wait(&B.packed_full[slot], n / PROMPT_PACKED & 1))) break;
+        const uint32_t slot = n % S::PACKED, par = n & 1;
+        if (!(ok = wait(&B.packed_full[slot], n / S::PACKED & 1))) break;
         const uint32_t* rec = reinterpret_cast<const uint32_t*>(smem + S::OFF_PACKED + slot * S::PACKED_BYTES) + key * W;
         uint32_t word[D / 8], prm[2 * NG];
 #pragma unroll
@@ -669,7 +679,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(kv ? &B.vfull[stage] : &B.kfull[stage]);
-        if (++stage == PROMPT_STAGES) stage = 0, phase ^= 1;
+        if (++stage == S::STAGES) stage = 0, phase ^= 1;
       }
     }
   } else if (warp == 12) {
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       };
       int32_t ready = look_up(0);
       for (int i = 0; i < s.nb; ++i, ++steps) {
-        const uint32_t ring = steps % PROMPT_PACKED;
+        const uint32_t ring = steps % S::PACKED;
         const int j0 = s.key0 + i * KB, end = max(j0, min(j0 + KB, s.khi));
         const int pg0 = first_page(j0), nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
         // keys that exist: those before `end` whose page is one
@@ -711,7 +721,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
             vm &= ~bad;
           }
         }
-        if (!(ok = wait(&B.packed_empty[ring], (steps / PROMPT_PACKED & 1) ^ 1))) break;
+        if (!(ok = wait(&B.packed_empty[ring], (steps / S::PACKED & 1) ^ 1))) break;
         if (lane == 0) {
           B.valid[ring][0] = (uint32_t)vm, B.valid[ring][1] = (uint32_t)(vm >> 32);
           mbar_expect_tx(&B.packed_full[ring], __popcll(vm) * W * 4);
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         __syncwarp();
       }
     }
-  } else {
+  } else if (warp >= 13 && warp < 13 + S::TILES) {
     // ================================================= matrix products of tile t
     const int t = warp - 13;
     const bool leader = elect_one();
@@ -739,10 +749,10 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     uint32_t kst = 0, kph = 0, vst = 0, vph = 0;  // ring positions of the next K and V
     uint32_t done = 0, units = 0;                 // this tile's steps and units so far
     auto next_k = [&]() {
-      if (++kst == PROMPT_STAGES) kst = 0, kph ^= 1;
+      if (++kst == S::STAGES) kst = 0, kph ^= 1;
     };
     auto next_v = [&]() {
-      if (++vst == PROMPT_STAGES) vst = 0, vph ^= 1;
+      if (++vst == S::STAGES) vst = 0, vph ^= 1;
     };
     auto product_s = [&](uint32_t place) {
       if (leader) {

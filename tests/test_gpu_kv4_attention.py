@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import tensor_sharded_linear_gb300 as tsl
-from oracle import heads
+from oracle import bf16, heads
 
 from heads_helpers import Batch, draw, full, ints, sharded
 
@@ -193,6 +193,41 @@ def test_prompt_bad_pages(lib):
     b.kv[0] = np.concatenate([b.kv[0][:16], b.kv[0][32:128], b.kv[0][144:]])
     b.kv_lens = [208]
     check(b, q, 2, "bf16", y, None, 0.125, False, 0, True)
+
+
+@pytest.mark.parametrize("group", [32, 64])
+@pytest.mark.parametrize("q_lens,kv_lens,hq,hk,causal,window", [
+    ([64], [64], 1, 1, True, 0),
+    ([65, 64, 63], [65, 300, 129], 2, 1, True, 0),
+    ([300], [1000], 1, 1, True, 0),                              # several row blocks of 128
+    ([100, 1, 0, 37, 200], [100, 500, 0, 37, 700], 6, 2, True, 0),
+    ([90, 40], [60, 40], 2, 2, True, 60),
+    ([80], [400], 4, 2, False, 0),
+    ([70, 64], [5000, 64], 4, 2, True, 0),                       # split over CTAs
+])
+def test_prompt_wide_heads(lib, group, q_lens, kv_lens, hq, hk, causal, window):
+    run(np.random.default_rng(59), q_lens, kv_lens, hq, hk, 256, group, 24, hk, "bf16", causal, window, prompt=True)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+@pytest.mark.parametrize("rise", [0.02, 0.2, 3.0, -0.2])
+def test_prompt_rising_logits(lib, d, rise):
+    """Logits that rise (fall) by `rise` (log2 units, about) from key to key: references that follow late or each
+    step."""
+    rng = np.random.default_rng(60)
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    b = Batch(rng, mesh, [96], [500], 1, d, 64, 16)
+    _, v, _, _ = heads.unpack(b.kv[0], d, 64)
+    k = np.ones((500, 1, d)) * (rise * np.log(2) * (np.arange(500) - 250)[:, None, None] / d ** 0.5) \
+        + 0.1 * rng.standard_normal((500, 1, d))
+    b.kv[0] = heads.pack(np.float32(k), np.float32(v), 64)
+    for j in range(500):
+        b.records[b.table[0, j // 16], :, j % 16] = b.kv[0][j]
+    q = draw(rng, (96, d), "bf16", 0.05) + 1
+    q = bf16.widen64(bf16.round_rne(q))
+    pt, kl, qs = b.operands()
+    y = tsl.tp_kv4_attention(sharded(q, mesh, "bf16"), b.cache(), pt, kl, qs, head_dim=d)
+    check(b, q, 1, "bf16", y, None, d ** -0.5, True, 0, True)
 
 
 def test_prompt_repeats_and_graph(lib):
