@@ -33,6 +33,8 @@ placement   Mesh coordinates, torch.chunk-style block split, slots and boxes.
 redistribute  Global assembly (in-order fp32 Partial sums) and slicing.
 linear      fp64 column/row parallel linears, TP MLP, attention projections.
 embedding   EmbeddingWithReplicateOutput gather.
+heads       Head norms with rotation and their gradients, the 4-bit cache's
+            record, attention over it and the kernels' error bounds.
 
 Parity status: every function here is pinned by a ``-m "not gpu"`` test in
 ``tests/test_oracle_*.py``; the readings the pages leave open are listed in

@@ -13,8 +13,12 @@
 // Each operation rounds on its own (no fused multiply-adds), so the codes
 // are a function of these formulas alone.
 //
-// Bound by memory: q, k and v are read once, q and one record per token and
-// kv head written once.
+// Memory's floor: q, k and v are read once, q and one record per token and kv
+// head written once.  Bound: the instructions of the exact quantisation and
+// their latency, 20 warps an SM at 94 registers.  Prompts of 9150 tokens
+// together, 32/8 heads of 128 in bf16, the stored values returned too: 54.9 us
+// for 240 MB, 4.4 TB/s, 0.65 of a copy's rate; a decode step of 32 tokens
+// 3.1 us, a launch.
 //
 // Layout.  D/16 lanes hold a head row, two chunks of 8 channels each: chunk
 // l and chunk l + D/16, the partners of a full rotation.  The codes of a
