@@ -267,32 +267,24 @@ class DTensor:
         while the slots' addresses and strides stay the same."""
         return self._described()[0]
 
-    def _arg(self):
-        """The descriptor as an argument of a library call."""
-        return self._described()[1]
-
     def _described(self):
+        """(descriptor, the descriptor as an argument, the slots' addresses, their strides)."""
+        slots = self.slots
+        ptrs, strides = [t.data_ptr() for t in slots], [t.stride() for t in slots]
         cached = self._desc_cache
-        if cached is not None:
-            seen = cached[2]
-            slots = self.slots
-            if len(slots) == len(seen):
-                for t, (ptr, stride) in zip(slots, seen):
-                    if t.data_ptr() != ptr or t.stride() != stride:
-                        break
-                else:
-                    return cached
+        if cached is not None and ptrs == cached[2] and strides == cached[3]:
+            return cached
         key = self._key()
         n = max(1, self.nslots)
-        ptrs = (C.c_void_p * n)(*[p or None for p, _ in key])
-        strides = (C.c_int64 * max(1, self.nslots * len(self.gshape)))(*[d for _, st in key for d in st])
+        cptrs = (C.c_void_p * n)(*[p or None for p, _ in key])
+        cstrides = (C.c_int64 * max(1, self.nslots * len(self.gshape)))(*[d for _, st in key for d in st])
         desc = L.DTensorDesc()
         desc.layout = self._layout
         desc.nslots = self.nslots
-        desc.slots = C.cast(ptrs, C.POINTER(C.c_void_p))
-        desc.strides = C.cast(strides, C.POINTER(C.c_int64))
-        desc._keep = (ptrs, strides)  # keep the arrays alive with the descriptor
-        self._desc_cache = (desc, C.byref(desc), [(t.data_ptr(), t.stride()) for t in self.slots])
+        desc.slots = C.cast(cptrs, C.POINTER(C.c_void_p))
+        desc.strides = C.cast(cstrides, C.POINTER(C.c_int64))
+        desc._keep = (cptrs, cstrides)  # keep the arrays alive with the descriptor
+        self._desc_cache = (desc, C.byref(desc), ptrs, strides)
         return self._desc_cache
 
     def __repr__(self):
@@ -547,8 +539,16 @@ def tp_attention_projections(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, 
 # ---------------------------------------------------------------- between q/k/v and o
 
 def _ref(t: Optional[DTensor]):
-    """A descriptor argument (NULL for None); the DTensor keeps the descriptor alive."""
-    return None if t is None else t._arg()
+    """A descriptor argument (NULL for None); the DTensor keeps the descriptor
+    alive.  Written out, since a call makes up to thirteen of them."""
+    if t is None:
+        return None
+    cached = t._desc_cache
+    if cached is not None:
+        slots = t.slots
+        if [x.data_ptr() for x in slots] == cached[2] and [x.stride() for x in slots] == cached[3]:
+            return cached[1]
+    return t._described()[1]
 
 
 def _like(t: DTensor, dtype=None) -> DTensor:

@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include "head_operands.h"
+#include "ptx_sm103.cuh"
 
 namespace dt {
 
@@ -43,6 +44,16 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
 }
 __device__ __forceinline__ f2 both(float a) { return f2{a, a}; }
 
+// Asynchronous copies of 16 bytes, and waits for all but a thread's last N groups.
+__device__ __forceinline__ void copy16_async(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -64,6 +75,7 @@ template <>
 struct Raw8<__nv_bfloat16> {
   uint4 u;
   __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void set(const uint4* p, int) { u = p[0]; }  // from 16-byte pieces, `step` apart
   __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void get2(f2 (&v)[4]) const {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -84,6 +96,9 @@ struct Raw8<float> {
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
     a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+  }
+  __device__ __forceinline__ void set(const uint4* p, int step) {
+    a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + step);
   }
   __device__ __forceinline__ void load_keep(const float* p) {  // what other warps re-read
     a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);

@@ -15,10 +15,11 @@
 //
 // Memory's floor: q, k and v are read once, q and one record per token and kv
 // head written once.  Bound: the instructions of the exact quantisation and
-// their latency, 20 warps an SM at 94 registers.  Prompts of 9150 tokens
-// together, 32/8 heads of 128 in bf16, the stored values returned too: 54.9 us
-// for 240 MB, 4.4 TB/s, 0.65 of a copy's rate; a decode step of 32 tokens
-// 3.1 us, a launch.
+// their latency.  Prompts of 9150 tokens together, 32/8 heads of 128 in bf16,
+// the stored values returned too: 47.1 us for 240 MB, 5.1 TB/s, 0.75 of a
+// copy's rate (with the next row's loads in registers, one block ahead, 54.9;
+// with 4 and 5 CTAs an SM 49.3 and 48.3); a decode step of 32 tokens 2.9 us, a
+// launch.
 //
 // Layout.  D/16 lanes hold a head row, two chunks of 8 channels each: chunk
 // l and chunk l + D/16, the partners of a full rotation.  The codes of a
@@ -26,8 +27,8 @@
 // few shuffles (a group of 64 is 8 neighbouring lanes' chunk).  A block is
 // the rows of one kind (q, k or v) that a warp holds at a time; a warp takes
 // `inner` blocks of one token, so its sequence, position, page and angles
-// are looked up once for them, and the next block's loads are in flight while
-// the present one is worked on.
+// are looked up once for them.  Rows come through a ring of asynchronous
+// copies, each lane its own chunks, three blocks ahead.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -41,8 +42,9 @@ namespace dt {
 namespace {
 
 constexpr int AP_THREADS = 128;
-constexpr int AP_CTAS = 5;  // per SM
+constexpr int AP_CTAS = 6;  // per SM
 constexpr int AP_WARPS = AP_THREADS / 32;
+constexpr int AP_STAGES = 4;
 
 struct AppendParams {
   HeadMap k, v, q, q_out, k_st, v_st;  // q*: heads 0 without queries; *_st: per_slot 0 when not wanted
@@ -157,12 +159,31 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const _
 
   const int u0 = blockIdx.x * AP_WARPS + warp;
   int t = u0 / per_tok, unit = u0 - t * per_tok;
-  Raw8<T> xa, xb;
-  if (t < p.seq.tokens) {
-    const T* x = row_of(t, unit * p.inner);
-    xa.load(x + 8 * l);
-    xb.load(x + 8 * (l + L));
-  }
+  // rows come through a ring of asynchronous copies, each lane its own two
+  // chunks; (ft, funit, fn) is the block to be fetched next
+  constexpr int PIECES = 8 * sizeof(T) / 16, E = 16 / sizeof(T);  // 16-byte pieces of a chunk, elements of a piece
+  __shared__ uint4 ring_smem[AP_STAGES * 2 * PIECES * AP_THREADS];
+  uint4* ring = ring_smem + threadIdx.x;
+  int ft = t, funit = unit, fn = unit * p.inner, fput = 0, fget = 0;
+  auto fetch = [&]() {
+    if (ft < p.seq.tokens) {
+      const T* x = row_of(ft, fn);
+      uint4* to = ring + fput * (2 * PIECES * AP_THREADS);
+#pragma unroll
+      for (int i = 0; i < PIECES; ++i) {
+        copy16_async(to + i * AP_THREADS, x + 8 * l + i * E);
+        copy16_async(to + (PIECES + i) * AP_THREADS, x + 8 * (l + L) + i * E);
+      }
+      if (++fn == min((funit + 1) * p.inner, blocks)) {
+        ft += step_tok, funit += step_blk;
+        if (funit >= per_tok) funit -= per_tok, ++ft;
+        fn = funit * p.inner;
+      }
+    }
+    copies_commit();
+    if (++fput == AP_STAGES) fput = 0;
+  };
+  for (int i = 0; i + 1 < AP_STAGES; ++i) fetch();
   while (t < p.seq.tokens) {
     int tn = t + step_tok, un = unit + step_blk;
     if (un >= per_tok) un -= per_tok, ++tn;
@@ -196,13 +217,14 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const _
       const int kind = kind_of(n), h = head_of(n, kind);
       const bool on = h < (kind == 0 ? hq : hk) && sq >= 0;  // (a row of no sequence: nothing is written for it)
       f2 a2[4], b2[4];
+      fetch();
+      copies_wait<AP_STAGES - 1>();
+      Raw8<T> xa, xb;
+      xa.set(ring + fget * (2 * PIECES * AP_THREADS), AP_THREADS);
+      xb.set(ring + fget * (2 * PIECES * AP_THREADS) + PIECES * AP_THREADS, AP_THREADS);
+      if (++fget == AP_STAGES) fget = 0;
       xa.get2(a2);
       xb.get2(b2);
-      if (n + 1 < last || tn < p.seq.tokens) {
-        const T* x = n + 1 < last ? row_of(t, n + 1) : row_of(tn, un * p.inner);
-        xa.load(x + 8 * l);
-        xb.load(x + 8 * (l + L));
-      }
       if (kind < 2 && full_rot) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {

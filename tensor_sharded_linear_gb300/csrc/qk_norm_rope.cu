@@ -12,8 +12,7 @@
 // Both passes are bound by memory: the forward reads and writes each element
 // once, the backward reads x and dy and writes dx.  8192 tokens, 32 + 32 heads
 // of 128 in bf16: forward 44.8 us for 273 MB, 6.1 TB/s, 0.90 of a copy's rate;
-// backward 79.3 us for 407 MB, 5.1 TB/s, 0.76: its 128 registers leave 16 warps
-// an SM to cover the loads.  8 tokens take 2.8 us, a launch.
+// backward 64.8 us for 407 MB, 6.3 TB/s, 0.93.  8 tokens take 2.8 us, a launch.
 //
 // Layout.  A head's channels are cut into chunks of 8.  A lane holds two
 // chunks of a head -- the two partners of a rotation, chunk l and chunk
@@ -85,14 +84,23 @@ __device__ __forceinline__ void write_dw_part(const NormParams& p, const float* 
 
 // D and rotary multiples of 16, D <= 512, 16-byte aligned heads.  A unit of
 // work is `inner` blocks of heads (SG * U heads each) of one token.
-// CTAs per SM: 5 forward, 4 backward (128 registers for its sums of dw), the
-// loop over blocks unrolled twice backward; measured at 8192 tokens x 64
-// heads against 3..5 CTAs and both unrollings.
+// CTAs per SM: 5 forward, 4 backward (128 registers for its sums of dw);
+// measured at 8192 tokens x 64 heads against 3..5 CTAs (backward with 5: 97.7
+// us, with 4: 64.8).
 __host__ __device__ constexpr int norm_ctas(bool bwd) { return bwd ? 4 : 5; }
 
 template <class T, bool BWD>
 struct NormVec {
   static constexpr int U = sizeof(T) == 2 && !BWD ? 2 : 1;  // heads per lane and step
+  // bf16 backward: x and dy come through a ring of asynchronous copies, each
+  // lane its own four chunks, so three steps are on their way without taking
+  // registers: 64.8 us where the next step's loads in registers, one step
+  // ahead, took 79.3 (8192 tokens x 64 heads); the forward is the other way
+  // round, 46.3 and 44.8.  In fp32 two stages are what
+  // 48 KB hold, and loads in registers are the faster ones (11.4 and 13.0 us
+  // for 1531 tokens x 16 heads of 64).
+  static constexpr int STAGES = BWD && sizeof(T) == 2 ? 4 : 0;
+  static constexpr int RING = STAGES * 64 * NR_THREADS;
 };
 
 // LANES: D / 16 where that is 4, 8 or 16 (all lanes hold channels and the
@@ -153,6 +161,8 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
   const float inv_d = 1.f / (float)D;
 
   Raw8<T> xa[U], xb[U], ga[U], gb[U];
+  using V = NormVec<T, BWD>;
+  constexpr bool RING = V::STAGES > 0;
   auto load = [&](int64_t t, int block, Raw8<T>(&a)[U], Raw8<T>(&b)[U], Raw8<T>(&c)[U], Raw8<T>(&d)[U]) {
 #pragma unroll
     for (int i = 0; i < U; ++i) {
@@ -171,8 +181,42 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
   int64_t t = u0 / per_tok;
   int blk = u0 - (int)t * per_tok;  // unit blk of token t
   int64_t row_next = 0;
+  // the ring, and the step to be fetched into it next
+  uint4* ring = reinterpret_cast<uint4*>(nr_acc + NR_WARPS * D) + threadIdx.x;
+  int64_t ft = t;
+  int fblk = blk, fin = 0, fput = 0, fget = 0;
+  auto fetch = [&]() {
+    if constexpr (RING) {
+      if (ft < tokens) {
+        const int h = min((fblk * inner + fin) * SG + sub, X.heads - 1);
+        const T *x = head_ptr<T>(X, ft, h, D), *g = head_ptr<T>(G, ft, h, D);
+        uint4* to = ring + fput * (4 * NR_THREADS);
+        copy16_async(to, x + ca);
+        copy16_async(to + NR_THREADS, x + cb);
+        copy16_async(to + 2 * NR_THREADS, g + ca);
+        copy16_async(to + 3 * NR_THREADS, g + cb);
+        if (++fin == inner) {
+          fin = 0;
+          ft += step_tok, fblk += step_blk;
+          if (fblk >= per_tok) fblk -= per_tok, ++ft;
+        }
+      }
+      copies_commit();
+      if (++fput == V::STAGES) fput = 0;
+    }
+  };
+  auto take = [&]() {
+    if constexpr (RING) {
+      copies_wait<V::STAGES - 1>();
+      const uint4* from = ring + fget * (4 * NR_THREADS);
+      xa[0].u = from[0], xb[0].u = from[NR_THREADS], ga[0].u = from[2 * NR_THREADS], gb[0].u = from[3 * NR_THREADS];
+      if (++fget == V::STAGES) fget = 0;
+    }
+  };
+  if constexpr (RING)
+    for (int i = 0; i + 1 < V::STAGES; ++i) fetch();
   if (t < tokens) {
-    load(t, blk * inner, xa, xb, ga, gb);
+    if (!RING) load(t, blk * inner, xa, xb, ga, gb);
     if (p.cos_sin) row_next = table_row(p, t, lane == 0);
   }
   while (t < tokens) {
@@ -211,12 +255,17 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
         qb[e] = INTER ? sinb(e) * f2{-vb.y, vb.x} : sinb(e) * va;
       }
     }
-#pragma unroll(BWD ? 2 : 1)
+#pragma unroll(BWD && !RING ? 2 : 1)
     for (int in = 0; in < inner; ++in) {
       const int block = blk * inner + in;
       Raw8<T> nxa[U], nxb[U], nga[U], ngb[U];
-      if (in + 1 < inner) load(t, block + 1, nxa, nxb, nga, ngb);
-      else if (tn < tokens) load(tn, bn * inner, nxa, nxb, nga, ngb);
+      if constexpr (RING) {
+        fetch();
+        take();
+      } else {
+        if (in + 1 < inner) load(t, block + 1, nxa, nxb, nga, ngb);
+        else if (tn < tokens) load(tn, bn * inner, nxa, nxb, nga, ngb);
+      }
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         const int h = (block * U + i) * SG + sub;
@@ -281,7 +330,7 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
         store8(y + cb, yb);
       }
 #pragma unroll
-      for (int i = 0; i < U; ++i) {
+      for (int i = 0; i < U && !RING; ++i) {
         xa[i] = nxa[i], xb[i] = nxb[i];
         if (BWD) ga[i] = nga[i], gb[i] = ngb[i];
       }
@@ -385,18 +434,27 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_co
   if (BWD && p.part) write_dw_part(p, nr_acc);
 }
 
-// dw of q (blockIdx.y 0) and k (1): the CTAs' sums of one channel, added by
-// one warp in a fixed order.
-__global__ void __launch_bounds__(256) qk_norm_dw_kernel(const __grid_constant__ NormParams p, int nblocks) {
+// dw of q (blockIdx.y 0) and k (1): the CTAs' sums of 32 channels, each warp
+// every 32nd row of them, then the warps' sums; a fixed order.
+constexpr int DW_THREADS = 1024;
+__global__ void __launch_bounds__(DW_THREADS) qk_norm_dw_kernel(const __grid_constant__ NormParams p, int nblocks) {
+  __shared__ float acc[32][33];
   wait_for_previous_kernel();
-  const int which = blockIdx.y;
+  const int which = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (!p.dw[which]) return;
   const int b0 = which ? p.blocks_q : 0, b1 = which ? nblocks : p.blocks_q;
-  const int c = blockIdx.x * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (c >= p.D || !p.dw[which]) return;
+  int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  for (int b = b0 + lane; b < b1; b += 32) s += p.part[(int64_t)b * p.D + c];
+  if (c < p.D) {
+#pragma unroll 8
+    for (int b = b0 + warp; b < b1; b += 32) s += p.part[(int64_t)b * p.D + c];
+  }
+  acc[warp][lane] = s;
+  __syncthreads();
+  s = acc[lane][warp];
   for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) {
+  c = blockIdx.x * 32 + warp;
+  if (lane == 0 && c < p.D) {
     if (p.dw_dtype[which] == DT_BF16) static_cast<__nv_bfloat16*>(p.dw[which])[c] = __float2bfloat16_rn(s);
     else static_cast<float*>(p.dw[which])[c] = s;
   }
@@ -435,7 +493,9 @@ int vec_lanes(int D) { return D == 64 || D == 128 || D == 256 ? D / 16 : 0; }
 
 template <class T, bool BWD>
 void launch_norm(const NormParams& p, bool vec, int grid, cudaStream_t s) {
-  const size_t smem = (size_t)p.D * sizeof(float) * (!BWD ? 1 : p.part ? NR_WARPS : 0);
+  constexpr int RING = NormVec<T, BWD>::RING;
+  size_t smem = (size_t)p.D * sizeof(float) * (!BWD ? 1 : p.part || (vec && RING) ? NR_WARPS : 0);
+  if (vec) smem += RING;  // (at most 40 KB)
 #define DT_NR(inter, lanes)                                                                  \
   if (vec && (p.interleaved != 0) == inter && vec_lanes(p.D) == lanes) {                     \
     qk_norm_vec_kernel<T, BWD, inter, lanes><<<grid, NR_THREADS, smem, s>>>(p);              \
@@ -584,7 +644,7 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
   count_launch();
   if (any_dw) {
-    e = launch_dependent(qk_norm_dw_kernel, dim3((D + 7) / 8, n), 256, stream, p, grid);
+    e = launch_dependent(qk_norm_dw_kernel, dim3((D + 31) / 32, n), DW_THREADS, stream, p, grid);
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope dw launch: %s", cudaGetErrorString(e));
     count_launch();
   }
