@@ -64,6 +64,7 @@ EXPORTS = [
 ]
 
 _lib = None
+_untyped: dict = {}
 _lock = threading.Lock()
 
 
@@ -129,8 +130,20 @@ def load(path: str = LIB_PATH) -> C.CDLL:
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
+        for name in ("dt_tp_qk_norm_rope", "dt_tp_qk_norm_rope_backward", "dt_tp_kv4_append", "dt_tp_kv4_attention"):
+            _untyped[name] = lib[name]  # an object of its own beside the typed one; the result is an int
         _lib = lib
         return lib
+
+
+def untyped(name: str):
+    """An entry without declared argument types, for the calls of a decode
+    step: checking twenty arguments against their types takes ctypes two
+    microseconds.  The caller passes descriptors by reference, None, 32-bit
+    ints, and C.c_float, C.c_size_t or C.c_void_p objects for all else."""
+    if _lib is None:
+        load()
+    return _untyped[name]
 
 
 def check(status: int, what: str) -> None:

@@ -551,6 +551,17 @@ def _ref(t: Optional[DTensor]):
     return t._described()[1]
 
 
+def _stream_arg() -> C.c_void_p:
+    return C.c_void_p(_stream_handle())
+
+
+def _ws_untyped(workspace: Optional[torch.Tensor]):
+    """(pointer, bytes) of a workspace tensor for an untyped call."""
+    if workspace is None:
+        return None, C.c_size_t(0)
+    return C.c_void_p(workspace.data_ptr()), C.c_size_t(workspace.numel() * workspace.element_size())
+
+
 def _like(t: DTensor, dtype=None) -> DTensor:
     return DTensor.empty(t.mesh, t.placements, t.gshape, dtype or t.dtype, device=t.slots[0].device)
 
@@ -566,9 +577,10 @@ def tp_qk_norm_rope(q: DTensor, k: Optional[DTensor] = None, q_weight: Optional[
     sines, with int32 ``positions`` per token (both None: no rotation).
     Returns (q_out, k_out); ``out`` = (q_out, k_out) to write into."""
     qo, ko = out if out is not None else (_like(q), None if k is None else _like(k))
-    L.check(L.load().dt_tp_qk_norm_rope(_ref(q), _ref(k), _ref(q_weight), _ref(k_weight), _ref(cos_sin),
-                                        _ref(positions), _ref(qo), _ref(ko), head_dim, eps, int(interleaved),
-                                        _tp_index(q.mesh, tp_dim), None, _stream_handle()), "tp_qk_norm_rope")
+    L.check(L.untyped("dt_tp_qk_norm_rope")(_ref(q), _ref(k), _ref(q_weight), _ref(k_weight), _ref(cos_sin),
+                                            _ref(positions), _ref(qo), _ref(ko), int(head_dim), C.c_float(eps),
+                                            int(interleaved), _tp_index(q.mesh, tp_dim), None, _stream_arg()),
+            "tp_qk_norm_rope")
     return qo, ko
 
 
@@ -595,10 +607,10 @@ def tp_qk_norm_rope_backward(dq_out: DTensor, dk_out: Optional[DTensor], q: DTen
                None if k_weight is None else _like(k_weight))
     if workspace is None and (q_weight is not None or k_weight is not None):
         workspace = _workspace(tp_qk_norm_rope_backward_workspace_bytes(q, k, head_dim=head_dim), q.slots[0].device)
-    L.check(L.load().dt_tp_qk_norm_rope_backward(
+    L.check(L.untyped("dt_tp_qk_norm_rope_backward")(
         _ref(dq_out), _ref(dk_out), _ref(q), _ref(k), _ref(q_weight), _ref(k_weight), _ref(cos_sin), _ref(positions),
-        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), head_dim, eps, int(interleaved),
-        _tp_index(q.mesh, tp_dim), *_ws_args(workspace), None, _stream_handle()), "tp_qk_norm_rope_backward")
+        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), int(head_dim), C.c_float(eps), int(interleaved),
+        _tp_index(q.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()), "tp_qk_norm_rope_backward")
     return tuple(out)
 
 
@@ -634,10 +646,10 @@ def tp_kv4_append(k: DTensor, v: DTensor, cache: DTensor, page_table: DTensor, k
     if q is not None and q_out is None:
         q_out = _like(q)
     ks, vs = stored if stored is not None else (None, None)
-    L.check(L.load().dt_tp_kv4_append(_ref(k), _ref(v), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
-                                      _ref(cos_sin), _ref(q), _ref(q_out), _ref(ks), _ref(vs), head_dim, group,
-                                      int(interleaved), _tp_index(k.mesh, tp_dim), None, _stream_handle()),
-            "tp_kv4_append")
+    L.check(L.untyped("dt_tp_kv4_append")(_ref(k), _ref(v), _ref(cache), _ref(page_table), _ref(kv_lens),
+                                          _ref(q_starts), _ref(cos_sin), _ref(q), _ref(q_out), _ref(ks), _ref(vs),
+                                          int(head_dim), int(group), int(interleaved), _tp_index(k.mesh, tp_dim), None,
+                                          _stream_arg()), "tp_kv4_append")
     return q_out
 
 
@@ -669,11 +681,11 @@ def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: D
     if workspace is None:
         workspace = _workspace(tp_kv4_attention_workspace_bytes(q, cache, page_table, head_dim=head_dim, group=group,
                                                                 tp_dim=tp_dim), q.slots[0].device)
-    L.check(L.load().dt_tp_kv4_attention(_ref(q), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
-                                         _ref(y), _ref(lse), head_dim, group,
-                                         head_dim ** -0.5 if scale is None else scale, int(causal), window,
-                                         _tp_index(q.mesh, tp_dim), *_ws_args(workspace), None, _stream_handle()),
-            "tp_kv4_attention")
+    L.check(L.untyped("dt_tp_kv4_attention")(_ref(q), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
+                                             _ref(y), _ref(lse), int(head_dim), int(group),
+                                             C.c_float(head_dim ** -0.5 if scale is None else scale), int(causal),
+                                             int(window), _tp_index(q.mesh, tp_dim), *_ws_untyped(workspace), None,
+                                             _stream_arg()), "tp_kv4_attention")
     return y
 
 

@@ -648,16 +648,18 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
           }
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        f2 less, sum = both(0.f);  // (0 for a row that has seen nothing yet)
+        less.x = mx[nt][0] == -INFINITY ? 0.f : -mx[nt][0];
+        less.y = mx[nt][1] == -INFINITY ? 0.f : -mx[nt][1];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e];  // a row that has seen nothing yet
-#pragma unroll
-          for (int k = 0; k < 2 * HT; ++k) {
-            sv[nt][k][e] = ex2(fmaf(sv[nt][k][e], sc[nt][e], -ref));
-            den[nt][e] += sv[nt][k][e];
-          }
+        for (int k = 0; k < 2 * HT; ++k) {
+          const f2 y = fma2(f2{sv[nt][k][0], sv[nt][k][1]}, f2{sc[nt][0], sc[nt][1]}, less);
+          sv[nt][k][0] = ex2(y.x), sv[nt][k][1] = ex2(y.y);
+          sum = sum + f2{sv[nt][k][0], sv[nt][k][1]};
         }
+        den[nt][0] += sum.x, den[nt][1] += sum.y;
+      }
 
       // ---- O^T += V^T P^T, 16 keys at a time
       float csum[NT][NG][4];  // -8 (even nibbles) and -128 (odd ones, 16 times as large) times 2^-24 times the sums of p s'
