@@ -58,6 +58,10 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
+template <class T>
+__device__ __forceinline__ T load_plain(const T* p) {
+  return *p;
+}
 // 8 consecutive channels (16-byte aligned) as fp32, and back with one
 // rounding.  Activations are read once and outputs written once, so both
 // use the streaming cache hint.
@@ -101,7 +105,7 @@ struct Raw8<float> {
     a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + step);
   }
   __device__ __forceinline__ void load_keep(const float* p) {  // what other warps re-read
-    a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = load_plain(reinterpret_cast<const float4*>(p)), b = load_plain(reinterpret_cast<const float4*>(p) + 1);
   }
   __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get2(f2 (&v)[4]) const {
@@ -129,7 +133,7 @@ __device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
 }
 // 8 fp32 values of a table that many warps re-read.
 __device__ __forceinline__ void load8_keep(const float* p, float (&v)[8]) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(p)), b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+  const float4 a = load_plain(reinterpret_cast<const float4*>(p)), b = load_plain(reinterpret_cast<const float4*>(p) + 1);
   v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
 }
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -147,17 +151,22 @@ __device__ __forceinline__ void rotate_pair(float& a, float& b, float c, float s
   a = x;
 }
 
-// A second kernel that reads what the first wrote, launched early: its CTAs
-// are set up while the first kernel's last ones run, and wait for its end
-// (and its writes) before they read.
+// Kernels here are launched early: their CTAs are set up while the last ones of
+// the stream's kernel before run (once each of those has left, or allowed it),
+// and wait for its end, and its writes, before they touch memory.  Every
+// thread waits, first thing, so that a kernel's end implies that of all before
+// it.  Loads are plain ones: what the kernel before may have written is not
+// read-only for this one's duration.
 __device__ __forceinline__ void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <class... P, class... A>
-cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, cudaStream_t stream, const A&... args) {
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                         const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -180,9 +189,9 @@ struct SeqTable {
 
   __device__ __forceinline__ int start(int b) const {
     if (!q_starts) return b * q_len;
-    return min(max(__ldg(q_starts + b), 0), tokens);
+    return min(max(load_plain(q_starts + b), 0), tokens);
   }
-  __device__ __forceinline__ int keys(int b) const { return min(max(__ldg(kv_lens + b), 0), capacity); }
+  __device__ __forceinline__ int keys(int b) const { return min(max(load_plain(kv_lens + b), 0), capacity); }
 };
 
 // Sequence of token t (all lanes of a converged warp call this with one t):

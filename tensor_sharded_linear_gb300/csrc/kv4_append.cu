@@ -95,7 +95,7 @@ __device__ __forceinline__ void rotate_row(const AppendParams& p, const T* x, co
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int i = 4 * c + e;
-        rotate_pair(y[2 * e], y[2 * e + 1], __ldg(cs + i), __ldg(cs + R / 2 + i));
+        rotate_pair(y[2 * e], y[2 * e + 1], load_plain(cs + i), load_plain(cs + R / 2 + i));
       }
     } else {  // R a multiple of 16: the partner is another chunk of the row
       const int hc = R / 16;
@@ -138,6 +138,7 @@ __device__ __forceinline__ void quantise(float lo, float hi, float (&y)[8], uint
 template <class T, int D, int G>
 __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int L = D / 16, SG = 32 / L, W = kv4_words(D, G), NG = D / G;
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane / L, l = lane % L;
   const int hk = p.cache.heads, hq = p.q.heads;
@@ -199,7 +200,7 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const _
       in_table = !p.cos_sin || (pos >= 0 && pos < p.table_rows);
       if (pos >= 0 && pos < p.seq.capacity) {
         const int pg = __umulhi(2u * (uint32_t)pos, p.page_mul) >> p.page_shift;
-        page = __ldg(p.page_table + (int64_t)sq * p.table_width + pg);
+        page = load_plain(p.page_table + (int64_t)sq * p.table_width + pg);
       }
       if (full_rot && in_table) {
         Raw8<float> c, s;
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const _
         c.get2(c2);
         s.get2(s2);
       }
-      if (lane == 0 && (!in_table || page < 0 || page >= p.cache.pages || __ldg(p.seq.kv_lens + sq) != p.seq.keys(sq)))
+      if (lane == 0 && (!in_table || page < 0 || page >= p.cache.pages || load_plain(p.seq.kv_lens + sq) != p.seq.keys(sq)))
         atomicOr(p.status, DT_DEV_ERR_INDEX);
     }
     const bool to_cache = in_table && page >= 0 && page < p.cache.pages;
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(AP_THREADS, AP_CTAS) kv4_append_kernel(const _
 }
 
 template <class T>
-void launch_append(AppendParams& p, int D, int G, cudaStream_t s) {
+cudaError_t launch_append(AppendParams& p, int D, int G, cudaStream_t s) {
   const int SG = 32 / (D / 16);
   const int blocks = (p.q.heads + SG - 1) / SG + 2 * ((p.cache.heads + SG - 1) / SG);
   // as many blocks of a token to a unit as leave four units for every warp of a full device
@@ -301,7 +302,7 @@ void launch_append(AppendParams& p, int D, int G, cudaStream_t s) {
   const int64_t units = (int64_t)p.seq.tokens * ((blocks + p.inner - 1) / p.inner);
   const int grid = (int)std::min<int64_t>((units + AP_WARPS - 1) / AP_WARPS, (int64_t)device_sm_count() * AP_CTAS);
 #define DT_AP(d, g) \
-  if (D == d && G == g) kv4_append_kernel<T, d, g><<<grid, AP_THREADS, 0, s>>>(p)
+  if (D == d && G == g) return launch_early(kv4_append_kernel<T, d, g>, dim3(grid), AP_THREADS, 0, s, p)
   DT_AP(64, 32);
   DT_AP(64, 64);
   DT_AP(128, 32);
@@ -309,6 +310,7 @@ void launch_append(AppendParams& p, int D, int G, cudaStream_t s) {
   DT_AP(256, 32);
   DT_AP(256, 64);
 #undef DT_AP
+  return cudaErrorInvalidValue;
 }
 
 dt_status append_call(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor* cache, const dt_dtensor* page_table,
@@ -385,9 +387,8 @@ dt_status append_call(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor
   if ((st = bind_device_of(B.kv_lens)) != DT_OK) return st;
   p.status = device_status_word(d_status);
   if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
-  if (K.dtype == DT_BF16) launch_append<__nv_bfloat16>(p, D, G, stream);
-  else launch_append<float>(p, D, G, stream);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = K.dtype == DT_BF16 ? launch_append<__nv_bfloat16>(p, D, G, stream)
+                                           : launch_append<float>(p, D, G, stream);
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "kv4_append launch: %s", cudaGetErrorString(e));
   count_launch();
   return DT_OK;

@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     for (int i = 0; i < STAGES; ++i) mbar_init(&bars[i], 1);
   if (threadIdx.x == 0) *abort_flag = 0;
   fence_mbar_init();
+  wait_for_previous_kernel();
 
   // ---- the schedule: this CTA's share [g0, g1) of all units' key blocks
   const int per = (p.seq.batch + THREADS - 1) / THREADS;
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     const int b0 = threadIdx.x * per;
     for (int b = b0; b < min(b0 + per, p.seq.batch); ++b) {
       sum += cost(p, seq_info<RB, TILE>(p, b));
-      if (blockIdx.x == 0 && __ldg(p.seq.kv_lens + b) != p.seq.keys(b)) atomicOr(p.status, DT_DEV_ERR_INDEX);
+      if (blockIdx.x == 0 && load_plain(p.seq.kv_lens + b) != p.seq.keys(b)) atomicOr(p.status, DT_DEV_ERR_INDEX);
     }
     int64_t x = sum;
 #pragma unroll
@@ -354,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
   auto first_page = [&](int j0) { return (int)(__umulhi(2u * (uint32_t)j0, p.page_mul) >> p.page_shift); };
   auto look_up = [&](const Segment& x, int i) {
     const int j0 = x.key0 + i * BLOCK, pg = first_page(j0) + lane;
-    return i < x.nb && j0 + TILE > x.klo && (int64_t)pg * ps < min(j0 + TILE, x.khi) ? __ldg(x.pages + pg) : -1;
+    return i < x.nb && j0 + TILE > x.klo && (int64_t)pg * ps < min(j0 + TILE, x.khi) ? load_plain(x.pages + pg) : -1;
   };
   int32_t ready;
   auto issue = [&](const Segment& x, int i) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     uint32_t* dst = reinterpret_cast<uint32_t*>(ring + stage * S::TILE_BYTES);
     for (int n0 = 0; n0 < nruns; n0 += 32) {
       const int n = n0 + lane;
-      const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(x.pages + pg0 + n) : 0;
+      const int32_t page = n0 == 0 ? ready : n < nruns ? load_plain(x.pages + pg0 + n) : 0;
       const bool ok = n >= nruns || (page >= 0 && page < p.cache.pages);
       if (!__all_sync(0xffffffffu, ok)) {  // pages that are none: their keys are hidden
         if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     }
     __syncwarp();
     for (int n = lane; n < nruns; n += 32) {
-      const int32_t page = n < 32 ? ready : __ldg(x.pages + pg0 + n);
+      const int32_t page = n < 32 ? ready : load_plain(x.pages + pg0 + n);
       if (page < 0 || page >= p.cache.pages) continue;
       const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
       bulk_load(dst + (a - j0) * W, x.base + page * x.page_stride + (int64_t)(a - (pg0 + n) * ps) * W,
@@ -930,11 +931,10 @@ cudaError_t variant_of(Variant* out) {
 
 template <int D, int G, int NT, int NP>
 cudaError_t launch_of(const AttnParams& p, int grid, cudaStream_t s) {
-  kv4_attention_kernel<D, G, NT, NP><<<grid, THREADS, Shape<D, G, NT, NP>::SMEM, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_early(kv4_attention_kernel<D, G, NT, NP>, dim3(grid), THREADS, Shape<D, G, NT, NP>::SMEM, s, p);
   if (e != cudaSuccess) return e;
   using T = typename std::conditional<NP == 1, __nv_bfloat16, float>::type;
-  return launch_dependent(kv4_join_kernel<T, D>, join_grid(grid, p.rb, D), 32 * JOIN_WARPS, s, p);
+  return launch_early(kv4_join_kernel<T, D>, join_grid(grid, p.rb, D), 32 * JOIN_WARPS, 0, s, p);
 }
 
 // Rows of a unit: 8 for fp32 (three parts per operand) and for up to 8 rows

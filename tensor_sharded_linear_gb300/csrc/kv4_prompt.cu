@@ -26,10 +26,10 @@ cudaError_t prepare() {
 
 template <int D, int G>
 cudaError_t launch_one(const AttnParams& p, int grid, cudaStream_t s) {
-  kv4_prompt_kernel<D, G><<<grid, 32 * PROMPT_WARPS, PromptShape<D, G>::SMEM, s>>>(p);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e =
+      launch_early(kv4_prompt_kernel<D, G>, dim3(grid), 32 * PROMPT_WARPS, PromptShape<D, G>::SMEM, s, p);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kv4_join_kernel<__nv_bfloat16, D>, join_grid(grid, p.rb, D), 32 * JOIN_WARPS, s, p);
+  return launch_early(kv4_join_kernel<__nv_bfloat16, D>, join_grid(grid, p.rb, D), 32 * JOIN_WARPS, 0, s, p);
 }
 
 }  // namespace

@@ -249,6 +249,8 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
 
+  wait_for_previous_kernel();
+
   // ---- the schedule: this CTA's share [g0, g1) of all units' key blocks
   struct Part {
     int q0, rows, kv, off, nrb;
@@ -283,7 +285,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     int64_t sum = 0;
     for (int b = threadIdx.x * per; b < min((int)(threadIdx.x + 1) * per, p.seq.batch); ++b) {
       sum += head_cost(seq_at(b)) * p.cache.heads;
-      if (blockIdx.x == 0 && __ldg(p.seq.kv_lens + b) != p.seq.keys(b)) atomicOr(p.status, DT_DEV_ERR_INDEX);
+      if (blockIdx.x == 0 && load_plain(p.seq.kv_lens + b) != p.seq.keys(b)) atomicOr(p.status, DT_DEV_ERR_INDEX);
     }
     scan[threadIdx.x] = sum;
   }
@@ -697,7 +699,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
       // lane n copies the step's run n of records, one per page, looked up a step ahead
       auto look_up = [&](int i) {
         const int j0 = s.key0 + i * KB, pg = first_page(j0) + lane;
-        return i < s.nb && (int64_t)pg * ps < min(j0 + KB, s.khi) ? __ldg(pages + pg) : -1;
+        return i < s.nb && (int64_t)pg * ps < min(j0 + KB, s.khi) ? load_plain(pages + pg) : -1;
       };
       int32_t ready = look_up(0);
       for (int i = 0; i < s.nb; ++i, ++steps) {
@@ -708,7 +710,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         uint64_t vm = end - j0 >= 64 ? ~0ull : (1ull << (end - j0)) - 1;
         for (int n0 = 0; n0 < nruns; n0 += 32) {
           const int n = n0 + lane;
-          const int32_t page = n0 == 0 ? ready : n < nruns ? __ldg(pages + pg0 + n) : 0;
+          const int32_t page = n0 == 0 ? ready : n < nruns ? load_plain(pages + pg0 + n) : 0;
           const bool good = n >= nruns || (page >= 0 && page < p.cache.pages);
           if (!__all_sync(0xffffffffu, good)) {
             if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
@@ -728,7 +730,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         }
         __syncwarp();
         for (int n = lane; n < nruns; n += 32) {
-          const int32_t page = n < 32 ? ready : __ldg(pages + pg0 + n);
+          const int32_t page = n < 32 ? ready : load_plain(pages + pg0 + n);
           if (page < 0 || page >= p.cache.pages) continue;
           const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
           bulk_load(smem + S::OFF_PACKED + ring * S::PACKED_BYTES + (a - j0) * (W * 4),

@@ -65,7 +65,7 @@ __device__ __forceinline__ float load_w(const void* w, int dtype, int i) {
 // Row of the cos/sin table for token t, or -1 (and the status bit) when its
 // position lies outside the table.
 __device__ __forceinline__ int64_t table_row(const NormParams& p, int64_t t, bool report) {
-  const int32_t r = __ldg(p.pos + t);
+  const int32_t r = load_plain(p.pos + t);
   if (r >= 0 && r < p.table_rows) return r;
   if (report) atomicOr(p.status, DT_DEV_ERR_INDEX);
   return -1;
@@ -107,6 +107,7 @@ struct NormVec {
 // sums' steps are known), else 0.
 template <class T, bool BWD, bool INTER, int LANES>
 __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel(const __grid_constant__ NormParams p) {
+  wait_for_previous_kernel();
   constexpr int U = NormVec<T, BWD>::U;
   extern __shared__ __align__(16) float nr_acc[];  // backward: [NR_WARPS][D] sums; forward: [D] weights
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -365,6 +366,7 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
 template <class T, bool BWD>
 __global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_constant__ NormParams p) {
   extern __shared__ float nr_acc[];
+  wait_for_previous_kernel();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int which = blockIdx.x >= p.blocks_q;
   const HeadMap &X = p.x[which], &Y = p.y[which], &G = p.g[which];
@@ -399,7 +401,7 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_co
         const float wb = norm && two ? load_w(p.w[which], p.w_dtype[which], ib) : 1.f;
         if (BWD) {
           ya = to_f32(g[ia]), yb = two ? to_f32(g[ib]) : 0.f;
-          if (rot && ok) rotate_pair(ya, yb, __ldg(cs + j), -__ldg(cs + half + j));
+          if (rot && ok) rotate_pair(ya, yb, load_plain(cs + j), -load_plain(cs + half + j));
         }
         if (pass == 0) {
           ss += a * a + b * b;
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(NR_THREADS) qk_norm_any_kernel(const __grid_co
           b = norm ? r * (yb * wb - nb * k) : yb;
         } else {
           if (norm) a = na * wa, b = nb * wb;
-          if (rot && ok) rotate_pair(a, b, __ldg(cs + j), __ldg(cs + half + j));
+          if (rot && ok) rotate_pair(a, b, load_plain(cs + j), load_plain(cs + half + j));
         }
         from_f32(y + ia, ok ? a : 0.f);
         if (two) from_f32(y + ib, ok ? b : 0.f);
@@ -492,19 +494,17 @@ int norm_blocks(int64_t units, bool bwd) {
 int vec_lanes(int D) { return D == 64 || D == 128 || D == 256 ? D / 16 : 0; }
 
 template <class T, bool BWD>
-void launch_norm(const NormParams& p, bool vec, int grid, cudaStream_t s) {
+cudaError_t launch_norm(const NormParams& p, bool vec, int grid, cudaStream_t s) {
   constexpr int RING = NormVec<T, BWD>::RING;
   size_t smem = (size_t)p.D * sizeof(float) * (!BWD ? 1 : p.part || (vec && RING) ? NR_WARPS : 0);
   if (vec) smem += RING;  // (at most 40 KB)
-#define DT_NR(inter, lanes)                                                                  \
-  if (vec && (p.interleaved != 0) == inter && vec_lanes(p.D) == lanes) {                     \
-    qk_norm_vec_kernel<T, BWD, inter, lanes><<<grid, NR_THREADS, smem, s>>>(p);              \
-    return;                                                                                  \
-  }
+#define DT_NR(inter, lanes)                                              \
+  if (vec && (p.interleaved != 0) == inter && vec_lanes(p.D) == lanes) \
+    return launch_early(qk_norm_vec_kernel<T, BWD, inter, lanes>, dim3(grid), NR_THREADS, smem, s, p);
   DT_NR(false, 4) DT_NR(false, 8) DT_NR(false, 16) DT_NR(false, 0)
   DT_NR(true, 4) DT_NR(true, 8) DT_NR(true, 16) DT_NR(true, 0)
 #undef DT_NR
-  qk_norm_any_kernel<T, BWD><<<grid, NR_THREADS, smem, s>>>(p);
+  return launch_early(qk_norm_any_kernel<T, BWD>, dim3(grid), NR_THREADS, smem, s, p);
 }
 
 dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleaved, int tp, void* ws, size_t ws_bytes,
@@ -633,18 +633,14 @@ dt_status norm_call(bool bwd, const NormArgs& A, int D, float eps, int interleav
     return st;
   p.status = device_status_word(d_status);
   if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
-  if (x[0].dtype == DT_BF16) {
-    if (bwd) launch_norm<__nv_bfloat16, true>(p, vec, grid, stream);
-    else launch_norm<__nv_bfloat16, false>(p, vec, grid, stream);
-  } else {
-    if (bwd) launch_norm<float, true>(p, vec, grid, stream);
-    else launch_norm<float, false>(p, vec, grid, stream);
-  }
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = x[0].dtype == DT_BF16 ? (bwd ? launch_norm<__nv_bfloat16, true>(p, vec, grid, stream)
+                                               : launch_norm<__nv_bfloat16, false>(p, vec, grid, stream))
+                                        : (bwd ? launch_norm<float, true>(p, vec, grid, stream)
+                                               : launch_norm<float, false>(p, vec, grid, stream));
   if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope launch: %s", cudaGetErrorString(e));
   count_launch();
   if (any_dw) {
-    e = launch_dependent(qk_norm_dw_kernel, dim3((D + 31) / 32, n), DW_THREADS, stream, p, grid);
+    e = launch_early(qk_norm_dw_kernel, dim3((D + 31) / 32, n), DW_THREADS, 0, stream, p, grid);
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "qk_norm_rope dw launch: %s", cudaGetErrorString(e));
     count_launch();
   }
