@@ -268,7 +268,8 @@ class DTensor:
         return self._described()[0]
 
     def _described(self):
-        """(descriptor, the descriptor as an argument, the slots' addresses, their strides)."""
+        """(descriptor, the descriptor as an argument, the slots' addresses, their strides, the addresses of
+        contiguous slots and -1 for others)."""
         slots = self.slots
         ptrs, strides = [t.data_ptr() for t in slots], [t.stride() for t in slots]
         cached = self._desc_cache
@@ -284,7 +285,8 @@ class DTensor:
         desc.slots = C.cast(cptrs, C.POINTER(C.c_void_p))
         desc.strides = C.cast(cstrides, C.POINTER(C.c_int64))
         desc._keep = (cptrs, cstrides)  # keep the arrays alive with the descriptor
-        self._desc_cache = (desc, C.byref(desc), ptrs, strides)
+        self._desc_cache = (desc, C.byref(desc), ptrs, strides,
+                            [t.data_ptr() if t.is_contiguous() else -1 for t in slots])
         return self._desc_cache
 
     def __repr__(self):
@@ -540,14 +542,14 @@ def tp_attention_projections(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, 
 
 def _ref(t: Optional[DTensor]):
     """A descriptor argument (NULL for None); the DTensor keeps the descriptor
-    alive.  Written out, since a call makes up to thirteen of them."""
+    alive.  Written out and with one look at each slot, since a call makes up
+    to twelve of them."""
     if t is None:
         return None
     cached = t._desc_cache
-    if cached is not None:
-        slots = t.slots
-        if [x.data_ptr() for x in slots] == cached[2] and [x.stride() for x in slots] == cached[3]:
-            return cached[1]
+    # contiguous slots where they were have the strides they had (0: none that is kept)
+    if cached is not None and [x.data_ptr() if x.is_contiguous() else 0 for x in t.slots] == cached[4]:
+        return cached[1]
     return t._described()[1]
 
 

@@ -230,3 +230,32 @@ def test_python_layer_raises(lib):
         assert np.isfinite(lse.slots[0].numpy()).all()
         tsl.api.L.check(attention(lib, scale=-1.0, lse=lse), "tp_kv4_attention")
     assert e.value.status == L.ERR_INVALID_ARG and "scale" in str(e.value)
+
+
+def test_descriptor_arguments_follow_the_slots(lib):
+    """The argument is kept while every slot lies where it did with the strides it had."""
+    from tensor_sharded_linear_gb300 import api
+    mesh = tsl.DeviceMesh((2,), ("tp",), device="cpu")
+    t = tsl.DTensor([torch.zeros(6, 64) for _ in range(2)], mesh, [tsl.Shard(1)], (6, 128), torch.float32)
+
+    def seen():
+        d = api._ref(t)._obj
+        return [(d.slots[i], d.strides[2 * i], d.strides[2 * i + 1]) for i in range(2)]
+
+    def held():
+        return [(s.data_ptr(), *s.stride()) for s in t.slots]
+
+    assert api._ref(None) is None
+    first = api._ref(t)
+    assert api._ref(t) is first and seen() == held()
+    t.slots[1] = torch.zeros(6, 64)
+    assert api._ref(t) is not first and seen() == held()
+    wide = torch.zeros(6, 80)
+    t.slots[0] = wide[:, :64]  # a pitch
+    assert seen() == held()
+    pitched = api._ref(t)
+    assert api._ref(t) is pitched
+    t.slots[0] = wide.view(-1)[:384].view(6, 64)  # the same address, contiguous
+    assert seen() == held()
+    t.slots[0] = wide[:, :64]
+    assert seen() == held()
