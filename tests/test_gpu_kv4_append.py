@@ -82,6 +82,16 @@ def test_append(lib, case, stored):
         np.testing.assert_array_equal(full(st[1]), ev)
 
 
+@pytest.mark.parametrize("case", [
+    ([5000, 1, 0, 4100], [5003, 200, 9, 4100], 4, 2, 64, 64, 64, 1, "bf16", 64, False),
+    ([5000, 1, 0, 4100], [5003, 200, 9, 4100], 3, 1, 64, 32, 24, 1, "fp32", 32, True),
+    ([3001, 1200], [3001, 1300], 16, 3, 128, 64, 16, 1, "bf16", 128, False),
+])
+def test_long_prompts(lib, case):
+    """More units than warps: every warp takes several, of several blocks each."""
+    test_append(lib, case, True)
+
+
 def test_without_rotation_queries_or_starts(lib):
     rng = np.random.default_rng(22)
     mesh = tsl.DeviceMesh((2,), ("tp",))
