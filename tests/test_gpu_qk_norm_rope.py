@@ -177,6 +177,18 @@ def test_positions_outside_the_table(lib, d):
     check_backward(case, got, dys, xs, ws, cs, pos)
 
 
+@pytest.mark.parametrize("case", [
+    (6001, 13, 3, 64, 64, 1, "bf16", False),
+    (5000, 5, 3, 80, 80, 1, "bf16", False),
+    (3000, 9, 9, 256, 64, 1, "bf16", True),
+    (2001, 11, 2, 128, 96, 1, "fp32", False),
+])
+def test_many_tokens(lib, case):
+    """Several units a warp, with heads that do not fill the last block."""
+    test_forward(lib, case)
+    test_backward(lib, case)
+
+
 @pytest.mark.parametrize("d", [128, 40])
 def test_left_out_tokens_may_hold_nan(lib, d):
     """Tokens without a position add nothing to the weights' gradients, whatever they hold."""
