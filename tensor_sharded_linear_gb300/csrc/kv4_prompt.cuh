@@ -243,13 +243,15 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     B.abort = 0;
     fence_mbar_init();
   }
+
+  wait_for_previous_kernel();
+  // Tensor memory is taken after that: a CTA that held it while it waits could keep one of the kernel before, set up
+  // on the same SM but not yet at its own allocation, from ending.
   if (warp == 13) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&B.tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-
-  wait_for_previous_kernel();
 
   // ---- the schedule: this CTA's share [g0, g1) of all units' key blocks
   struct Part {
