@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <exception>
 
 #include "kv4_attention.h"
@@ -39,6 +40,28 @@ cudaError_t variant_any(int D, int G, bool fp32, int64_t rows, Variant* v) {
   if (prompt_kernel(fp32, rows)) return prompt_variant(D, G, v);
   return D == 64 ? variant<64>(G, fp32, rows, v) : D == 128 ? variant<128>(G, fp32, rows, v)
                                                             : variant<256>(G, fp32, rows, v);
+}
+
+// Test hooks, read once from the environment: DT_KV4_WAIT_LIMIT_MS bounds the
+// kernels' waits for copies (default 2000 ms); DT_KV4_STARVE=n makes the
+// barriers of each CTA's n-th step and those after it await more bytes than
+// are copied, so the waits run out and the kernel reports DT_DEV_ERR_TIMEOUT.
+struct Hooks {
+  unsigned long long wait_limit_ns = WAIT_LIMIT_NS;
+  uint32_t starve = ~0u;  // a step's number; no share has that many
+};
+const Hooks& hooks() {
+  static const Hooks h = [] {
+    Hooks x;
+    const char* e = getenv("DT_KV4_WAIT_LIMIT_MS");
+    const long ms = e ? atol(e) : 0;
+    if (ms > 0 && ms <= 10000) x.wait_limit_ns = (unsigned long long)ms * 1000000ull;
+    e = getenv("DT_KV4_STARVE");
+    const long n = e ? atol(e) : 0;
+    if (n > 0 && n <= 1000000) x.starve = (uint32_t)n - 1;
+    return x;
+  }();
+  return h;
 }
 
 // The operands that decide the variant, checked.
@@ -111,7 +134,8 @@ dt_status attention_call(const dt_dtensor* q, const dt_dtensor* cache, const dt_
   p.causal = causal != 0;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.wait_limit_ns = WAIT_LIMIT_NS;
+  p.wait_limit_ns = hooks().wait_limit_ns;
+  p.starve = hooks().starve;
   if ((st = bind_device_of(c.B.kv_lens)) != DT_OK) return st;
   const bool fp32 = c.Q.dtype == DT_FP32;
   Variant v;

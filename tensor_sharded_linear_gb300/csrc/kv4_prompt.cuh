@@ -603,11 +603,15 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
     uint32_t n = 0, stage = 0, phase = 0;  // step of the share, its place in the rings
     Segment s;
     bool ok = true;
+    int left = 0;  // of the unit's meetings, where a wait gave up
     while (ok && advance(s)) {
       int vex = 0;  // exponent field that V's scaling is made for
       for (int i = 0; i < s.nb; ++i, ++n) {
         const uint32_t slot = n % S::PACKED, par = n & 1;
-        if (!(ok = wait(&B.packed_full[slot], n / S::PACKED & 1))) break;
+        if (!(ok = wait(&B.packed_full[slot], n / S::PACKED & 1))) {
+          left = s.nb - i;
+          break;
+        }
         const uint32_t* rec = reinterpret_cast<const uint32_t*>(smem + S::OFF_PACKED + slot * S::PACKED_BYTES) + key * W;
         uint32_t word[D / 8], prm[2 * NG];
 #pragma unroll
@@ -660,7 +664,10 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           }
           vex = vex2;
         }
-        if (!(ok = wait(kv ? &B.vempty[stage] : &B.kempty[stage], phase ^ 1))) break;
+        if (!(ok = wait(kv ? &B.vempty[stage] : &B.kempty[stage], phase ^ 1))) {
+          left = s.nb - i - 1;
+          break;
+        }
         uint8_t* dst = smem + (kv ? S::OFF_V : S::OFF_K) + stage * S::KV_BYTES + key * 128;
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
@@ -685,6 +692,13 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         if (lane == 0) mbar_arrive(kv ? &B.vfull[stage] : &B.kfull[stage]);
         if (++stage == S::STAGES) stage = 0, phase ^= 1;
       }
+    }
+    // A warp that gave up still comes to every meeting of the share, so that its partner, which may see the same
+    // barrier complete or learn of the end a step later, never waits there for good.
+    while (!ok) {
+      for (; left > 0; --left) asm volatile("bar.sync %0, 64;" ::"r"(1 + kv) : "memory");
+      if (!advance(s)) break;
+      left = s.nb;
     }
   } else if (warp == 12) {
     // ================================================= bulk copies of the packed records
@@ -728,7 +742,8 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         if (!(ok = wait(&B.packed_empty[ring], (steps / S::PACKED & 1) ^ 1))) break;
         if (lane == 0) {
           B.valid[ring][0] = (uint32_t)vm, B.valid[ring][1] = (uint32_t)(vm >> 32);
-          mbar_expect_tx(&B.packed_full[ring], __popcll(vm) * W * 4);
+          const uint32_t starve = steps >= p.starve ? 16 : 0;  // (more bytes than will come)
+          mbar_expect_tx(&B.packed_full[ring], __popcll(vm) * W * 4 + starve);
         }
         __syncwarp();
         for (int n = lane; n < nruns; n += 32) {
