@@ -43,9 +43,10 @@ cudaError_t variant_any(int D, int G, bool fp32, int64_t rows, Variant* v) {
 }
 
 // Test hooks, read once from the environment: DT_KV4_WAIT_LIMIT_MS bounds the
-// kernels' waits for copies (default 2000 ms); DT_KV4_STARVE=n makes the
-// barriers of each CTA's n-th step and those after it await more bytes than
-// are copied, so the waits run out and the kernel reports DT_DEV_ERR_TIMEOUT.
+// kernels' waits (default 2000 ms); DT_KV4_STARVE=n makes the barriers of the
+// n-th step of each CTA (tile of each warp) and of those after it await more
+// bytes than are copied, so the waits run out and the kernel reports
+// DT_DEV_ERR_TIMEOUT.
 struct Hooks {
   unsigned long long wait_limit_ns = WAIT_LIMIT_NS;
   uint32_t starve = ~0u;  // a step's number; no share has that many

@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     }
     if (lane == 0) {
       vmask[stage] = vm;
-      if (!dead) mbar_expect_tx(&bars[stage], __popcll(vm) * W * 4);
+      if (!dead) mbar_expect_tx(&bars[stage], __popcll(vm) * W * 4 + (put > p.starve ? 16 : 0));
     }
     __syncwarp();
     for (int n = lane; n < nruns; n += 32) {

@@ -39,7 +39,7 @@ struct AttnParams {
   Split* split;      // [CTA]
   int32_t* status;
   unsigned long long wait_limit_ns;
-  uint32_t starve;  // test hook: from this step on a prompt's copies stay short of what their barrier awaits
+  uint32_t starve;  // test hook: from this step (tile) on copies stay short of what their barrier awaits
 };
 
 // Grid of the device-filling launch, rows of a unit and workspace of one

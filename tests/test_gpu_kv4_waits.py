@@ -1,7 +1,7 @@
 """The waits of the attention kernels over the 4-bit cache: behind other kernels, and for copies that do not come.
 
-The second kind makes the waits run out without a fault: DT_KV4_STARVE=n lets the barriers of each CTA's n-th step and
-of those after it await more bytes than are copied (the copies themselves are those of any call), and
+The second kind makes the waits run out without a fault: DT_KV4_STARVE=n lets the barriers of each CTA's n-th step
+(each warp's n-th tile, with few rows) and of those after it await more bytes than are copied (the copies themselves are those of any call), and
 DT_KV4_WAIT_LIMIT_MS shortens the limit.  The kernel has to report DT_DEV_ERR_TIMEOUT and to end, and the context has
 to be usable after it.  A process each, since the hooks are read once."""
 import os
@@ -89,3 +89,8 @@ def starved(cases, dtype, step):
 @pytest.mark.parametrize("step", [1, 2, 5])
 def test_prompt_waits_run_out_and_report(lib, step):
     starved([(64, 32, 300, 6000), (128, 64, 300, 6000), (256, 64, 200, 6000)], "bf16", step)
+
+
+@pytest.mark.parametrize("step,dtype", [(1, "bf16"), (2, "bf16"), (3, "fp32")])
+def test_waits_of_few_rows_run_out_and_report(lib, step, dtype):
+    starved([(64, 32, 1, 90000), (128, 64, 7, 60000), (256, 64, 2, 60000)], dtype, step)
