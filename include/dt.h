@@ -372,7 +372,8 @@ DT_API dt_status dt_tp_mlp_static_workspace(const dt_dtensor* x, const dt_dtenso
  * everywhere), Replicate on the other mesh dims, leading dims collapsible to
  * one token dim, unit inner stride.  bf16 or fp32; all arithmetic is fp32 and
  * each result is rounded once.  All heads of all shards run in one launch.
- * Outputs must not have materialised replicas.
+ * Outputs must not have materialised replicas.  Tokens (in attention times
+ * query heads per kv head) number less than 2^31 - 2^16 (DT_ERR_CAPACITY).
  */
 
 /*

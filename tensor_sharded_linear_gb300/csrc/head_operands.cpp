@@ -48,7 +48,7 @@ dt_status head_operand(const dt_dtensor* in, const char* what, int tp, int head_
   out->dtype = L.dtype;
   out->tokens = 1;
   for (int d = 0; d < last; ++d) out->tokens *= L.gshape[d];
-  if (out->tokens >= (1ll << 31) - 512) return fail(DT_ERR_CAPACITY, "%s: more than 2^31 - 512 tokens", what);
+  if (out->tokens >= MAX_ROWS) return fail(DT_ERR_CAPACITY, "%s: 2^31 - 2^16 tokens or more", what);
   HeadMap& M = out->map;
   M.heads = out->heads;
   M.per_slot = chunk > 0 ? (int32_t)(chunk / head_dim) : 1;

@@ -22,6 +22,9 @@ struct HeadMap {
   int32_t heads;     // heads in all
 };
 constexpr int MAX_HEADS = 1 << 15;
+// Tokens, and (query, head) rows of a kv head, stay below this: kernels count
+// them in 32 bits and add a grid's stride of them (a few thousand).
+constexpr int64_t MAX_ROWS = (1ll << 31) - (1ll << 16);
 
 #ifdef __CUDACC__
 // Address of head h of token t.

@@ -89,7 +89,7 @@ dt_status check(const dt_dtensor* q, const dt_dtensor* cache, const dt_dtensor* 
   if (!c->nothing && c->B.batch > 0) {
     const int64_t g = c->Q.heads / c->B.cache.heads;
     c->rows_per_seq = (c->Q.tokens + c->B.batch - 1) / c->B.batch * g;
-    if (c->Q.tokens * g >= (1ll << 31)) return fail(DT_ERR_CAPACITY, "q: more than 2^31 rows per kv head");
+    if (c->Q.tokens * g >= MAX_ROWS) return fail(DT_ERR_CAPACITY, "q: 2^31 - 2^16 rows per kv head or more");
   }
   return DT_OK;
 }
