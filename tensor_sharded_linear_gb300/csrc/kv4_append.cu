@@ -369,6 +369,8 @@ dt_status append_call(const dt_dtensor* k, const dt_dtensor* v, const dt_dtensor
     if (t.ndim != 2 || t.shape[1] < 16 || t.shape[1] % 16 || t.shape[1] > D)
       return fail(DT_ERR_SHAPE, "cos_sin must be [rows, rotary], rotary a multiple of 16 and at most head_dim");
     if (reinterpret_cast<uintptr_t>(t.ptr) % 16) return fail(DT_ERR_ALIGNMENT, "cos_sin must be 16-byte aligned");
+    if (t.shape[0] == 0 && K.tokens > 0)  // (its pointer may be NULL, which stands for no rotation below)
+      return fail(DT_ERR_SHAPE, "cos_sin has no rows: every position would be out of range");
     p.cos_sin = reinterpret_cast<const float*>(t.ptr);
     p.table_rows = t.shape[0];
     p.rotary = (int)t.shape[1];

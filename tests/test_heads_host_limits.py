@@ -33,3 +33,14 @@ def test_rows_per_kv_head_near_32_bits(lib, n, want):
     """8 query heads on each kv head; below the limit the call goes on to its next check, the output's shape."""
     one = dict(page_table=dt((1, 2), R, I32), kv_lens=dt((1,), R, I32), q_starts=dt((2,), R, I32))
     assert attention(lib, q=rows(n, 16 * 64), **one) == want
+
+
+def test_append_with_an_empty_table(lib):
+    """No rows of cosines and sines: refused, as the norms do, and not taken for "no rotation"."""
+    n0 = lib.dt_launch_count()
+    for rotary in (64, 32):
+        assert append(lib, cos_sin=dt((0, rotary), R, F32)) == L.ERR_SHAPE
+        assert b"no rows" in lib.dt_last_error()
+    assert lib.dt_launch_count() == n0
+    empty = dict(k=dt((0, 128)), v=dt((0, 128)), q=dt((0, 256)), q_out=dt((0, 256)))
+    assert append(lib, cos_sin=dt((0, 64), R, F32), **empty) == L.OK
