@@ -438,7 +438,8 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
         const int ex = __float_as_uint(top) >> 23;  // 2^10 / 2^(exponent of top), within the normal numbers
         mult = __uint_as_float((uint32_t)max(10, min(254, 264 - ex)) << 23);
       }
-      if (ql == 0) rsc[nt * 8 + r] = FULL ? p.scale_log2 : p.scale_log2 * 16777216.f / mult;
+      // (never 0: a hidden key's -inf times it has to stay -inf)
+      if (ql == 0) rsc[nt * 8 + r] = FULL ? p.scale_log2 : fmaxf(p.scale_log2 * 16777216.f / mult, LEAST_SCALE);
 #pragma unroll
       for (int grp = 0; grp < NG; ++grp) {
         float sum = 0.f;

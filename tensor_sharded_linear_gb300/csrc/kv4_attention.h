@@ -11,6 +11,10 @@ namespace kv4 {
 
 constexpr int WARPS = 4;             // each takes every fourth tile of keys
 constexpr int THREADS = 32 * WARPS;
+// Least multiplier of S, the least positive fp32 number: |S| stays below
+// 2^123, so what is smaller makes logits of 0 as this does; but 0 itself would
+// make NaN of the -inf that hidden keys have.
+constexpr float LEAST_SCALE = 1.401298464324817e-45f;
 
 // What a CTA left unfinished: the unit whose keys begin in its range and end
 // in CTA `last`'s (unit < 0: none).  The join kernel adds those pieces.

@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           break;
         gemm::tc_fence_after();
         const StepInfo& I = B.info[all % PROMPT_INFO];
-        const float sc = row_scale * I.kmul;
+        const float sc = fmaxf(row_scale * I.kmul, LEAST_SCALE);
         vs = I.vscale;
         const int j0 = s.key0 + i * KB;
         // columns [lo, hi) of the step are seen by this row

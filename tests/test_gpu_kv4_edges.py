@@ -1,0 +1,86 @@
+"""Attention over the 4-bit cache at the edges of its range, against the fp64 oracle.
+
+Tolerance: relative to the norm of each (sequence, head)'s result.  Rounding to bf16 is at most 2^-8 of an element.
+Operands in fp16 add 2^-11 of a probability and of a value, and 2^-11 of a key through a logit: with logits whose
+terms sum to less than 3 in magnitude on average that is under 2^-9 of the result, altogether less than 2^-7.
+"""
+import numpy as np
+import pytest
+import torch
+
+import tensor_sharded_linear_gb300 as tsl
+from oracle import bf16, heads
+
+from heads_helpers import Batch, draw, full, ints, sharded
+
+pytestmark = pytest.mark.gpu
+CLOSE = 2.0 ** -7
+
+
+def put(b, s, j, rec):
+    """Record `rec` [kv heads, words] as key j of sequence s, in the pages and for the oracle."""
+    b.kv[s][j] = rec
+    b.records[b.table[s, j // b.page], :, j % b.page] = rec
+
+
+def put_all(b, s, k, v):
+    """fp32 keys and values [n, kv heads, d] as sequence s's."""
+    rec = heads.pack(np.float32(k), np.float32(v), b.group)
+    for j in range(len(rec)):
+        put(b, s, j, rec[j])
+
+
+def expected(b, q, hq, scale, causal=True, window=0):
+    """fp64 results [tokens, hq, d] and logs [tokens, hq]."""
+    out, logs, at, g = [], [], 0, hq // b.hk
+    for s, n in enumerate(b.q_lens):
+        k, v, _, _ = heads.unpack(b.kv[s][:b.kv_lens[s]], b.d, b.group)
+        qs = q[at:at + n].reshape(n, hq, b.d)
+        r = [heads.attention(qs[:, h], k[:, h // g], v[:, h // g], scale, causal, window) for h in range(hq)]
+        out.append(np.stack([x[0] for x in r], 1))
+        logs.append(np.stack([x[1] for x in r], 1))
+        at += n
+    return np.concatenate(out), np.concatenate(logs)
+
+
+def call(b, q, hq, dtype="bf16", table=None, kv_lens=None, status=0, **kw):
+    """Results [tokens, hq, d] and logs [tokens, hq] of one call."""
+    pt, kl, qs = b.operands()
+    if table is not None:
+        pt = ints(table, b.mesh)
+    if kv_lens is not None:
+        kl = ints(kv_lens, b.mesh)
+    tsl.read_device_status(clear=True)
+    lse = tsl.DTensor.empty(b.mesh, [tsl.Shard(1)], (b.tokens, hq), torch.float32)
+    y = tsl.tp_kv4_attention(sharded(q, b.mesh, dtype), b.cache(), pt, kl, qs, head_dim=b.d, group=b.group, lse=lse, **kw)
+    assert tsl.read_device_status() == status
+    return full(y).reshape(b.tokens, hq, b.d), full(lse)
+
+
+def assert_close(got, want, b, limit=CLOSE):
+    at = 0
+    for s, n in enumerate(b.q_lens):
+        for h in range(want.shape[1]):
+            y, e = got[at:at + n, h], want[at:at + n, h]
+            assert np.isfinite(y).all(), (s, h)
+            err = np.linalg.norm(y - e)
+            assert err <= limit * np.linalg.norm(e), (s, h, err / np.linalg.norm(e))
+        at += n
+
+
+MESH1 = tsl.DeviceMesh((1,), ("tp",))
+
+
+@pytest.mark.parametrize("n", [4, 80])
+@pytest.mark.parametrize("scale", [1e-9, 1e-20, 1e-37])
+def test_tiny_scales_and_queries_of_zero(lib, n, scale):
+    """A row of zeros, or logits that are all but zero, weigh all visible keys alike; the hidden ones stay hidden."""
+    rng = np.random.default_rng(70)
+    b = Batch(rng, MESH1, [n, n], [n, 150], 1, 64, 64, 16)
+    q = draw(rng, (2 * n, 2 * 64), "bf16")
+    q[1::2] = 0
+    q[2::4] *= 2.0 ** -100
+    got, logs = call(b, q, 2, scale=scale)
+    want, want_logs = expected(b, q, 2, scale)
+    assert_close(got, want, b)
+    assert (np.abs(logs - want_logs) <= 1e-4).all()
