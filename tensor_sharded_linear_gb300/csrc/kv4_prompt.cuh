@@ -647,10 +647,11 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         const int ex = (int)(max(B.top[par][kv][0], B.top[par][kv][1]) >> 23);
         StepInfo& I = B.info[n % PROMPT_INFO];
         float mul;
-        if (kv == 0) {  // below 2^15
-          mul = ex > 141 ? __uint_as_float((268u - ex) << 23) : 1.f;  // 2^(14 - (ex - 127))
+        if (kv == 0) {  // the step's largest in [2^14, 2^15), however small it is
+          const int kex = max(ex, 15);
+          mul = __uint_as_float((268u - kex) << 23);  // 2^(14 - (kex - 127))
           if (key == 0) {
-            I.kmul = ex > 141 ? __uint_as_float((ex - 14u) << 23) : 1.f;  // 1 / mul
+            I.kmul = __uint_as_float((kex - 14u) << 23);  // 1 / mul
             I.valid[0] = B.there[par][0], I.valid[1] = B.there[par][1];
             I.all = (B.there[par][0] & B.there[par][1]) == 0xffffffffu;
           }

@@ -84,3 +84,43 @@ def test_tiny_scales_and_queries_of_zero(lib, n, scale):
     want, want_logs = expected(b, q, 2, scale)
     assert_close(got, want, b)
     assert (np.abs(logs - want_logs) <= 1e-4).all()
+
+
+@pytest.mark.parametrize("d,group", [(64, 32), (64, 64), (128, 64), (256, 32)])
+@pytest.mark.parametrize("n", [6, 90])
+@pytest.mark.parametrize("small", [1e-4, 1e-6, 1e-8, 1e-20, 1e-30])
+def test_small_keys_and_large_queries(lib, n, small, d, group):
+    """Keys far below fp16's range with queries as far above it: ordinary logits."""
+    rng = np.random.default_rng(71)
+    b = Batch(rng, MESH1, [n, n], [300, n], 1, d, group, 16)
+    for s, m in enumerate(b.kv_lens):
+        put_all(b, s, rng.standard_normal((m, 1, d)) * small, rng.standard_normal((m, 1, d)))
+    q = draw(rng, (2 * n, 2 * d), "bf16", 1 / small)
+    got, _ = call(b, q, 2)
+    assert_close(got, expected(b, q, 2, d ** -0.5)[0], b)
+
+
+@pytest.mark.parametrize("n", [6, 90])
+@pytest.mark.parametrize("small,large", [(1e-6, 10.0), (1e-3, 1e4), (1e-12, 1e-6)])
+def test_small_group_of_channels_beside_a_large_one(lib, n, small, large):
+    """Both halves of the channels make up half of each logit, their keys 10^6 and more apart."""
+    rng = np.random.default_rng(72)
+    b = Batch(rng, MESH1, [n], [300], 1, 128, 64, 16)
+    size = np.repeat([small, large], 64)
+    put_all(b, 0, rng.standard_normal((300, 1, 128)) * size, rng.standard_normal((300, 1, 128)))
+    q = draw(rng, (n, 128), "bf16") / size
+    q = bf16.widen64(bf16.round_rne(q))
+    got, _ = call(b, q, 1)
+    assert_close(got, expected(b, q, 1, 128 ** -0.5)[0], b)
+
+
+@pytest.mark.parametrize("n", [6, 90])
+def test_steps_of_keys_of_very_different_size(lib, n):
+    """Each 64 keys have a scale of their own, from 1e-12 to 1e3; the logits stay ordinary."""
+    rng = np.random.default_rng(73)
+    b = Batch(rng, MESH1, [n], [512], 1, 64, 64, 16)
+    size = 10.0 ** np.array([3, -12, 0, -6, 2, -9, -3, 1])[np.arange(512) // 64]
+    put_all(b, 0, rng.standard_normal((512, 1, 64)) * size[:, None, None], rng.standard_normal((512, 1, 64)))
+    q = draw(rng, (n, 64), "bf16", 1e-3)
+    got, _ = call(b, q, 1)
+    assert_close(got, expected(b, q, 1, 0.125)[0], b)
