@@ -287,8 +287,11 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
         if (!BWD) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            ya[e] = fma2(INTER ? swap(a[e]) : b[e], qa[e], a[e] * pa[e]);
-            yb[e] = fma2(INTER ? swap(b[e]) : a[e], qb[e], b[e] * pb[e]);
+            ya[e] = a[e] * pa[e], yb[e] = b[e] * pb[e];
+            if (rot) {  // (a choice, not a sine of 0: the other channel may be infinite)
+              ya[e] = fma2(INTER ? swap(a[e]) : b[e], qa[e], ya[e]);
+              yb[e] = fma2(INTER ? swap(b[e]) : a[e], qb[e], yb[e]);
+            }
           }
         } else {
           f2 dya[4], dyb[4];  // dz = R^T dy
@@ -296,12 +299,10 @@ __global__ void __launch_bounds__(NR_THREADS, norm_ctas(BWD)) qk_norm_vec_kernel
           gb[i].get2(dyb);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            if (INTER) {
-              ya[e] = fma2(f2{dya[e].y, -dya[e].x}, sina(e), dya[e] * cosa(e));
-              yb[e] = fma2(f2{dyb[e].y, -dyb[e].x}, sinb(e), dyb[e] * cosb(e));
-            } else {
-              ya[e] = fma2(dyb[e], s2[e], dya[e] * c2[e]);
-              yb[e] = fma2(dya[e] * both(-1.f), s2[e], dyb[e] * c2[e]);
+            ya[e] = dya[e] * cosa(e), yb[e] = dyb[e] * cosb(e);
+            if (rot) {
+              ya[e] = fma2(INTER ? f2{dya[e].y, -dya[e].x} : dyb[e], sina(e), ya[e]);
+              yb[e] = fma2(INTER ? f2{dyb[e].y, -dyb[e].x} : dya[e] * both(-1.f), sinb(e), yb[e]);
             }
           }
           if (norm) {
