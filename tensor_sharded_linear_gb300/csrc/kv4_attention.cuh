@@ -351,20 +351,22 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
   };
 
   // A tile's keys lie in runs of consecutive records, one per page: lane n
-  // copies run n.  Its page is looked up a tile ahead (`ready`).
+  // copies run n.  Its page is looked up a tile ahead (`ready`).  Keys of the
+  // first tile that no row sees (behind the window) are left out: their pages
+  // need not exist.
   auto first_page = [&](int j0) { return (int)(__umulhi(2u * (uint32_t)j0, p.page_mul) >> p.page_shift); };
   auto look_up = [&](const Segment& x, int i) {
-    const int j0 = x.key0 + i * BLOCK, pg = first_page(j0) + lane;
-    return i < x.nb && j0 + TILE > x.klo && (int64_t)pg * ps < min(j0 + TILE, x.khi) ? load_plain(x.pages + pg) : -1;
+    const int j0 = x.key0 + i * BLOCK, pg = first_page(max(j0, x.klo)) + lane;
+    return i < x.nb && (int64_t)pg * ps < min(j0 + TILE, x.khi) ? load_plain(x.pages + pg) : -1;
   };
   int32_t ready;
   auto issue = [&](const Segment& x, int i) {
     const int stage = put % STAGES, j0 = x.key0 + i * BLOCK;
     ++put;
-    const int end = j0 + TILE > x.klo && !dead ? min(j0 + TILE, x.khi) : j0;
-    const int pg0 = first_page(j0);
-    uint64_t vm = end - j0 >= 64 ? ~0ull : end > j0 ? (1ull << (end - j0)) - 1 : 0;
-    const int nruns = end > j0 ? first_page(end - 1) - pg0 + 1 : 0;
+    const int begin = max(j0, x.klo), end = dead ? begin : min(j0 + TILE, x.khi);
+    const int pg0 = first_page(begin), n_keys = max(0, end - begin);
+    uint64_t vm = n_keys >= 64 ? ~0ull : ((1ull << n_keys) - 1) << ((begin - j0) & 63);
+    const int nruns = n_keys ? first_page(end - 1) - pg0 + 1 : 0;
     uint32_t* dst = reinterpret_cast<uint32_t*>(ring + stage * S::TILE_BYTES);
     for (int n0 = 0; n0 < nruns; n0 += 32) {
       const int n = n0 + lane;
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
         if (lane == 0) atomicOr(p.status, DT_DEV_ERR_INDEX);
         uint64_t bad = 0;
         if (!ok) {
-          const int a = max(j0, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
+          const int a = max(begin, (pg0 + n) * ps) - j0, z = min(end, (pg0 + n + 1) * ps) - j0;
           bad = (z - a >= 64 ? ~0ull : (1ull << (z - a)) - 1) << a;
         }
         for (int o = 16; o; o >>= 1) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
     for (int n = lane; n < nruns; n += 32) {
       const int32_t page = n < 32 ? ready : load_plain(x.pages + pg0 + n);
       if (page < 0 || page >= p.cache.pages) continue;
-      const int a = max(j0, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
+      const int a = max(begin, (pg0 + n) * ps), z = min(end, (pg0 + n + 1) * ps);
       bulk_load(dst + (a - j0) * W, x.base + page * x.page_stride + (int64_t)(a - (pg0 + n) * ps) * W,
                 (z - a) * W * 4, &bars[stage]);
     }

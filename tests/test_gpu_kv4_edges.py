@@ -124,3 +124,36 @@ def test_steps_of_keys_of_very_different_size(lib, n):
     q = draw(rng, (n, 64), "bf16", 1e-3)
     got, _ = call(b, q, 1)
     assert_close(got, expected(b, q, 1, 0.125)[0], b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_lens,kv_lens,window", [
+    ([1, 1], [1000, 500], 128), ([1, 1], [1000, 333], 1), ([3, 5], [700, 200], 37), ([40, 1], [700, 1000], 200),
+    ([90, 70], [700, 1000], 100)])
+def test_pages_behind_the_window_need_not_exist(lib, q_lens, kv_lens, window, d, dtype):
+    """Entries of pages that lie wholly before the first query's window are no pages: nothing is reported, and the
+    results are those of the whole table."""
+    rng = np.random.default_rng(74)
+    b = Batch(rng, MESH1, q_lens, kv_lens, 1, d, 64, 16)
+    q = draw(rng, (b.tokens, 2 * d), dtype)
+    table = b.table.copy()
+    for s, (n, kv) in enumerate(zip(q_lens, kv_lens)):
+        first = max(0, kv - n - window + 1)
+        table[s, :first // 16] = -1
+    got, logs = call(b, q, 2, dtype, table=table, window=window)
+    whole, whole_logs = call(b, q, 2, dtype, window=window)
+    np.testing.assert_array_equal(got, whole)
+    np.testing.assert_array_equal(logs, whole_logs)
+    assert_close(got, expected(b, q, 2, d ** -0.5, True, window)[0], b)
+
+
+def test_pages_of_the_window_are_still_looked_at(lib):
+    """The page with the window's first key is used: an entry that is none is reported."""
+    rng = np.random.default_rng(75)
+    for n in (1, 70):
+        b = Batch(rng, MESH1, [n], [500], 1, 64, 64, 16)
+        q = draw(rng, (n, 64), "bf16")
+        table = b.table.copy()
+        table[0, (500 - n - 100 + 1) // 16] = -1
+        call(b, q, 1, table=table, window=100, status=tsl._lib.DEV_ERR_INDEX)
