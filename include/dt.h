@@ -489,7 +489,11 @@ DT_API dt_status dt_tp_kv4_append(const dt_dtensor* k, const dt_dtensor* v, cons
  *         position; window > 0 (causal only): of those the last `window`
  * A query that sees no key gets out = 0 and lse = -inf.  Whatever the hidden
  * keys, or places of the pages beyond a sequence's length, hold (infinities
- * and NaN too) does not reach the result.
+ * and NaN too) does not reach the result.  One limit: what fits numbers into
+ * fp16 is a power of two for a block of queries (with few rows 8 or 16 of
+ * them; with 64 rows or more per sequence and kv head 256).  A key that some
+ * queries of a block see and others do not, with finite numbers more than
+ * 2^16 times those of the others' keys, takes bits from the others.
  * The softmax and all sums are fp32.  For bf16 activations the products take
  * fp16 operands (11 bits), scaled by powers of two into fp16's range: queries,
  * probabilities times value steps, and with many rows the cache's numbers.

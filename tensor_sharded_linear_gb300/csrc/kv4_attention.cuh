@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
       mx[nt][0] = mx[nt][1] = -INFINITY;
       den[nt][0] = den[nt][1] = 0.f;
     }
-    // 2^12 over the power of two above the largest value step seen
+    // 2^12 over the power of two above the largest value step that some row has seen (one for all rows: a row's own
+    // takes 73.1 and 96.6 us where this takes 67.9 and 93.9)
     uint32_t step_ex = 0;  // its exponent field
     float vmult = __uint_as_float(254u << 23);
 

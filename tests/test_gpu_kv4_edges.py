@@ -157,3 +157,38 @@ def test_pages_of_the_window_are_still_looked_at(lib):
         table = b.table.copy()
         table[0, (500 - n - 100 + 1) // 16] = -1
         call(b, q, 1, table=table, window=100, status=tsl._lib.DEV_ERR_INDEX)
+
+
+@pytest.mark.parametrize("n", [1, 4, 80])
+@pytest.mark.parametrize("e", [40, 100, 120])
+def test_finite_numbers_in_hidden_keys(lib, n, e):
+    """Steps and minima of 2^e in places that no query sees: before the window, beyond the length, in spare pages."""
+    rng = np.random.default_rng(76)
+    word = int((127 + e) << 7) * 0x10001  # step and minimum 2^e
+    b = Batch(rng, MESH1, [n, n], [400, 333], 1, 128, 64, 16, poison=word)
+    q = draw(rng, (2 * n, 2 * 128), "bf16")
+    for s, kv in enumerate(b.kv_lens):
+        for j in range(max(0, kv - n - 100 - 70), kv - n - 100 + 1):  # the first query sees keys from kv - n - 99
+            rec = b.kv[s][j].copy()
+            rec[..., 32:36] = word
+            put(b, s, j, rec)
+    got, _ = call(b, q, 2, window=100)
+    assert_close(got, expected(b, q, 2, 128 ** -0.5, True, 100)[0], b)
+
+
+@pytest.mark.parametrize("n,hq,e", [(5, 1, 10), (5, 1, 16), (5, 2, 16), (12, 4, 16), (80, 4, 16)])
+def test_finite_numbers_in_keys_that_some_queries_see(lib, n, hq, e):
+    """The last key holds steps and minima of 2^e and only the last query sees it: the others, which share a power of
+    two with it, resolve their values to 2^-36 of the largest and do not notice."""
+    rng = np.random.default_rng(79)
+    b = Batch(rng, MESH1, [n, n], [n, 200], 1, 128, 64, 16)
+    q = draw(rng, (2 * n, hq * 128), "bf16")
+    want = expected(b, q, hq, 128 ** -0.5)[0]
+    for s, kv in enumerate(b.kv_lens):
+        rec = b.kv[s][kv - 1].copy()
+        rec[..., 32:36] = ((127 + e) << 7) * 0x10001
+        put(b, s, kv - 1, rec)
+    got, _ = call(b, q, hq)
+    keep = np.arange(2 * n) % n < n - 1
+    b.q_lens = [n - 1, n - 1]
+    assert_close(got[keep], want[keep], b)
