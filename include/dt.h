@@ -500,7 +500,8 @@ DT_API dt_status dt_tp_kv4_append(const dt_dtensor* k, const dt_dtensor* v, cons
  * For fp32 activations each is three bf16 parts (24 bits).
  * A value group held as NaN makes the results that see it NaN: its channels,
  * and with 64 (query, head) rows per sequence and kv head or more the whole
- * head's.  At most 32768 query heads.
+ * head's (there also for a group whose minimum + 15 steps is beyond fp32).
+ * At most 32768 query heads.
  * workspace: 256-byte aligned device memory of the queried size, which
  * depends on the current device; its contents between calls are the
  * caller's.  Waits for copies are bounded (DT_DEV_ERR_TIMEOUT).

@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           prm[x] = q.x, prm[x + 1] = q.y;
         }
         const bool have = B.valid[slot][half] >> lane & 1;
-        // the largest magnitude of the step's keys (values), and where NaN is
+        // the largest magnitude of the step's keys (values), and where values are not finite
         uint32_t top = 0, nan = 0, mine[NG];
 #pragma unroll
         for (int grp = 0; grp < NG; ++grp) {
@@ -633,8 +633,10 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
           const float st = __uint_as_float(mine[grp] << 16), m = __uint_as_float(mine[grp] & 0xffff0000u);
           const uint32_t a = __float_as_uint(fmaxf(fabsf(m), fabsf(fmaf(15.f, st, m))));
           if (a < 0x7f800000u) top = max(top, a);
+          // (not finite: minimum, step or the largest value that they make)
           const uint32_t vw = prm[NG + grp];
-          if (have && ((vw & 0x7f80u) == 0x7f80u || (vw & 0x7f800000u) == 0x7f800000u)) nan |= 1u << grp;
+          const float vt = fmaf(15.f, __uint_as_float(vw << 16), __uint_as_float(vw & 0xffff0000u));
+          if (have && !(fabsf(vt) < INFINITY)) nan |= 1u << grp;
         }
         top = __reduce_max_sync(0xffffffffu, top);
         const uint32_t there = __ballot_sync(0xffffffffu, have);
@@ -674,8 +676,8 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         for (int grp = 0; grp < NG; ++grp) {
           __half2 st = __float2half2_rn(__uint_as_float(mine[grp] << 16) * mul);
           __half2 m = __float2half2_rn(__uint_as_float(mine[grp] & 0xffff0000u) * mul);
-          if (nan) {  // a value that is NaN reaches the queries that see its key through S; its group of V is
-                      // zeros, as 0 * NaN must not reach the others
+          if (nan) {  // a value that is not finite makes NaN of the queries that see its key, through S; its group
+                      // of V is zeros, as 0 * NaN must not reach the others
             if (kv == 0) m = __float2half2_rn(__int_as_float(0x7fc00000));
             else if (nan >> grp & 1) st = m = __float2half2_rn(0.f);
           }

@@ -192,3 +192,23 @@ def test_finite_numbers_in_keys_that_some_queries_see(lib, n, hq, e):
     keep = np.arange(2 * n) % n < n - 1
     b.q_lens = [n - 1, n - 1]
     assert_close(got[keep], want[keep], b)
+
+
+@pytest.mark.parametrize("d,value_words", [(64, slice(17, 18)), (256, slice(68, 72))])
+@pytest.mark.parametrize("word", [0x7F007F00, 0x00007F00, 0x7F803F80, 0x3F807F80])
+def test_values_whose_sum_is_infinite_stay_with_their_key(lib, word, d, value_words):
+    """The last key's value steps and minima are finite, minimum + 15 steps is not (or one of them is not): queries
+    that do not see it do not notice."""
+    rng = np.random.default_rng(77)
+    for n in (5, 80):
+        if n == 5 and word & 0x7F80 == 0x7F00:
+            continue  # few rows share the scale of all finite steps, however large
+        b = Batch(rng, MESH1, [n], [200], 1, d, 64, 16)
+        q = draw(rng, (n, 2 * d), "bf16")
+        want = expected(b, q, 2, d ** -0.5)[0]
+        rec = b.kv[0][199].copy()
+        rec[..., value_words] = word
+        put(b, 0, 199, rec)
+        got, _ = call(b, q, 2)
+        b.q_lens = [n - 1]
+        assert_close(got[:-1], want[:-1], b)
