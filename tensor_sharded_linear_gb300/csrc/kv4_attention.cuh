@@ -216,7 +216,7 @@ __device__ __forceinline__ Seq seq_info(const AttnParams& p, int b) {
   s.rows = ql * p.g;
   s.off = s.kv - ql;
   s.nrb = (s.rows + RB - 1) / RB;
-  s.klo = p.window ? max(0, s.off - p.window + 1) / TILE * TILE : 0;
+  s.klo = window_begin(s.off, p.window) / TILE * TILE;
   s.nblk = max(1, (s.kv - s.klo + TILE * WARPS - 1) / (TILE * WARPS));  // an empty sequence still writes its rows
   return s;
 }
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
       x.pos_a = s.off + x.row0 / p.g;
       x.pos_z = s.off + (x.row0 + x.rows - 1) / p.g;
       x.khi = p.causal ? min(s.kv, x.pos_z + 1) : s.kv;
-      x.klo = p.window ? max(0, x.pos_a - p.window + 1) : 0;
+      x.klo = window_begin(x.pos_a, p.window);
       x.key0 = s.klo + (blk0 * WARPS + warp) * TILE;
       x.first = blk0 == 0;
       x.whole = x.first && x.nb == s.nblk;
@@ -600,7 +600,7 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
 
       // ---- mask, running maximum, p = 2^(S * scale - maximum)
       constexpr uint64_t ALL = TILE == 64 ? ~0ull : (1ull << TILE) - 1;
-      const bool masked = vm != ALL || (p.causal && j0 + TILE - 1 > pos_a) || (p.window && j0 <= pos_z - p.window);
+      const bool masked = vm != ALL || (p.causal && j0 + TILE - 1 > pos_a) || j0 < window_begin(pos_z, p.window);
       uint32_t hidden[NT];  // bit 2 k + e: key 8 k + r is not seen by row 2 ql + e
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) hidden[nt] = 0;
@@ -609,11 +609,11 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int pos = s.off + (row0 + nt * 8 + 2 * ql + e) / p.g;
+            const int pos = s.off + (row0 + nt * 8 + 2 * ql + e) / p.g, lo = window_begin(pos, p.window);
 #pragma unroll
             for (int k = 0; k < 2 * HT; ++k) {
               const int j = j0 + 8 * k + r;
-              if (!((vm >> (8 * k + r)) & 1) || (p.causal && j > pos) || (p.window && j <= pos - p.window)) {
+              if (!((vm >> (8 * k + r)) & 1) || (p.causal && j > pos) || j < lo) {
                 hidden[nt] |= 1u << (k * 2 + e);
                 sv[nt][k][e] = -INFINITY;
               }

@@ -46,6 +46,15 @@ struct AttnParams {
   uint32_t starve;  // test hook: from this step (tile) on copies stay short of what their barrier awaits
 };
 
+#ifdef __CUDACC__
+// First key that a query at position pos sees through the window (0: none).
+// Positions are negative where a sequence has more queries than keys, and
+// windows may be any size: pos - window itself can leave 32 bits.
+__device__ __forceinline__ int window_begin(int pos, int window) {
+  return window && pos >= window ? pos - window + 1 : 0;
+}
+#endif
+
 // Grid of the device-filling launch, rows of a unit and workspace of one
 // variant; and its launch (defined per head_dim).
 struct Variant {

@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
   // keys [lo, hi) that row block rb sees, and its number of key blocks
   auto span = [&](const Part& s, int rb, int* lo, int* hi) {
     const int row0 = rb * RB, row1 = min(s.rows, row0 + RB) - 1;
-    *lo = p.window ? max(0, s.off + row0 / p.g - p.window + 1) : 0;
+    *lo = window_begin(s.off + row0 / p.g, p.window);
     *hi = p.causal ? min(s.kv, s.off + row1 / p.g + 1) : s.kv;
     return max(1, (*hi - *lo + KB - 1) / KB);
   };
@@ -474,7 +474,7 @@ __global__ void __launch_bounds__(32 * PROMPT_WARPS, 1) kv4_prompt_kernel(const 
         // columns [lo, hi) of the step are seen by this row
         int lo = 0, hi = min(KB, s.khi - j0);
         if (p.causal) hi = min(hi, pos + 1 - j0);
-        if (p.window) lo = max(0, pos - p.window + 1 - j0);
+        if (p.window) lo = max(0, window_begin(pos, p.window) - j0);
         const bool masked = __any_sync(0xffffffffu, lo > 0 || hi < KB || !I.all);
         float f = I.vgrow;  // what O is to be multiplied by
         // The reference stays while the row's sum of this step is at most 2^14, so no maximum is taken; else (and

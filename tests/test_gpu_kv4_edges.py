@@ -212,3 +212,30 @@ def test_values_whose_sum_is_infinite_stay_with_their_key(lib, word, d, value_wo
         got, _ = call(b, q, 2)
         b.q_lens = [n - 1]
         assert_close(got[:-1], want[:-1], b)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,kv", [(10, 5), (90, 40), (70, 0), (3, 1)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 2, 2 ** 30, 2 ** 31, 2 ** 40 + 5])
+def test_windows_beyond_every_key(lib, window, n, kv, dtype):
+    """More queries than keys, so the first positions are negative, and windows near the end of 32 bits or beyond it:
+    the results without a window."""
+    rng = np.random.default_rng(85)
+    b = Batch(rng, MESH1, [n, 2], [kv, 300], 1, 64, 64, 16)
+    q = draw(rng, (n + 2, 2 * 64), dtype)
+    got, logs = call(b, q, 2, dtype, window=window)
+    whole, whole_logs = call(b, q, 2, dtype)
+    np.testing.assert_array_equal(got, whole)
+    np.testing.assert_array_equal(logs, whole_logs)
+    if kv:
+        assert_close(got, expected(b, q, 2, 0.125)[0], b)
+
+
+@pytest.mark.parametrize("n,kv", [(10, 5), (90, 40)])
+@pytest.mark.parametrize("window", [1, 3, 2 ** 20])
+def test_windows_with_more_queries_than_keys(lib, window, n, kv):
+    rng = np.random.default_rng(86)
+    b = Batch(rng, MESH1, [n, 2], [kv, 300], 1, 64, 64, 16)
+    q = draw(rng, (n + 2, 2 * 64), "bf16")
+    got, _ = call(b, q, 2, window=window)
+    assert_close(got, expected(b, q, 2, 0.125, True, window)[0], b)
