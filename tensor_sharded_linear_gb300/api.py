@@ -677,7 +677,8 @@ def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: D
     """Attention of each sequence's new tokens (its last keys' queries) over its
     keys in the 4-bit cache; ``scale`` defaults to head_dim ** -0.5.
 
-    ``window`` > 0 keeps the last ``window`` keys of each query; ``lse`` (fp32
+    ``window`` > 0 keeps the last ``window`` keys of each query under the causal
+    mask (without that every key is seen, whatever the window); ``lse`` (fp32
     [..., heads]) receives the log of the softmax's denominator."""
     y = out if out is not None else _like(q)
     if workspace is None:
@@ -686,9 +687,9 @@ def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: D
     L.check(L.untyped("dt_tp_kv4_attention")(_ref(q), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
                                              _ref(y), _ref(lse), int(head_dim), int(group),
                                              C.c_float(head_dim ** -0.5 if scale is None else scale), int(causal),
-                                             max(-1, min(int(window), 0x7FFFFFFF)), _tp_index(q.mesh, tp_dim),
-                                             *_ws_untyped(workspace), None,
-                                             _stream_arg()), "tp_kv4_attention")
+                                             max(-1, min(int(window), 0x7FFFFFFF)) if causal else 0,
+                                             _tp_index(q.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()),
+            "tp_kv4_attention")
     return y
 
 

@@ -239,3 +239,15 @@ def test_windows_with_more_queries_than_keys(lib, window, n, kv):
     q = draw(rng, (n + 2, 2 * 64), "bf16")
     got, _ = call(b, q, 2, window=window)
     assert_close(got, expected(b, q, 2, 0.125, True, window)[0], b)
+
+
+@pytest.mark.parametrize("n", [1, 80])
+def test_a_window_without_the_causal_mask(lib, n):
+    """The window belongs to the causal mask: without that every key is seen."""
+    rng = np.random.default_rng(78)
+    b = Batch(rng, MESH1, [n], [200], 1, 64, 64, 16)
+    q = draw(rng, (n, 64), "bf16")
+    a = call(b, q, 1, causal=False, window=64)
+    c = call(b, q, 1, causal=False)
+    np.testing.assert_array_equal(a[0], c[0])
+    assert_close(a[0], expected(b, q, 1, 0.125, False)[0], b)
