@@ -53,6 +53,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "kv4_attention.h"
@@ -913,20 +914,22 @@ __global__ void __launch_bounds__(THREADS, NP == 1 && NT * D <= 128 ? 3 : 2)
 template <int D, int G, int NT, int NP>
 cudaError_t variant_of(Variant* out) {
   using S = Shape<D, G, NT, NP>;
-  static int per_sm[64] = {};
+  static std::atomic<int> per_sm[64];  // by device; calls come from any thread
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!per_sm[dev]) {
+  int resident = per_sm[dev].load(std::memory_order_acquire);
+  if (!resident) {
     e = cudaFuncSetAttribute(kv4_attention_kernel<D, G, NT, NP>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM);
     if (e != cudaSuccess) return e;
     int n = 0;
     e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv4_attention_kernel<D, G, NT, NP>, THREADS, S::SMEM);
     if (e != cudaSuccess) return e;
-    per_sm[dev] = n > 0 ? n : 1;
+    resident = n > 0 ? n : 1;
+    per_sm[dev].store(resident, std::memory_order_release);
   }
-  out->grid = device_sm_count() * per_sm[dev];
+  out->grid = device_sm_count() * resident;
   out->rows = S::RB;
   const size_t splits = ((size_t)out->grid * sizeof(Split) + 255) / 256 * 256;
   out->bytes = splits + (size_t)2 * out->grid * S::RB * (D + 4) * sizeof(float);

@@ -1,4 +1,5 @@
 // The tensor-core attention kernel for prompts: instantiations and launch.
+#include <atomic>
 #include <exception>
 
 #include "kv4_prompt.cuh"
@@ -10,16 +11,16 @@ namespace {
 
 template <int D, int G>
 cudaError_t prepare() {
-  static bool done[64] = {};
+  static std::atomic<bool> done[64];  // by device; calls come from any thread
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!done[dev]) {
+  if (!done[dev].load(std::memory_order_acquire)) {
     e = cudaFuncSetAttribute(kv4_prompt_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              PromptShape<D, G>::SMEM);
     if (e != cudaSuccess) return e;
-    done[dev] = true;
+    done[dev].store(true, std::memory_order_release);
   }
   return cudaSuccess;
 }
