@@ -143,8 +143,11 @@ def attention(q, k, v, scale, causal, window, k_step=None, v_step=None):
     """One kv head: q [n, d], k and v [m, d] fp64 -> (out, lse, bounds).
 
     bounds = (fp32 bound, additional bound for bf16 activations) on |out|'s
-    error per query, for sums of products taken in fp32 (relative error 2^-18
-    of the sum of magnitudes: up to 64 roundings) on codes offset by 128."""
+    error per query, one for all channels: sums of products in fp32 (relative
+    error 2^-18 of the sum of magnitudes: up to 64 roundings) on codes offset
+    by up to 128, probability times step in 8 bits.  They hold for the kernels,
+    which offset codes by 8 and keep 11 bits, but leave room: ``attention_error``
+    bounds what the kernels compute."""
     n, m = q.shape[0], k.shape[0]
     see = visible(n, m, causal, window)
     out, lse, b32, b16 = np.zeros((n, q.shape[1])), np.full(n, -np.inf), np.zeros(n), np.zeros(n)
@@ -165,6 +168,42 @@ def attention(q, k, v, scale, causal, window, k_step=None, v_step=None):
                 b32[i] = (2 * e * (mag + np.abs(s).max()) + e) * (vmax + 15 * smax)
                 b16[i] = 2 * e * mag16 * vmax + 2.0 ** -9 * 1.02 * 15 * smax + e * 288 * smax
     return out, lse, b32, b16
+
+
+def attention_error(q, k, v, scale, causal, window, k_step, v_step, dtype, many=False):
+    """One kv head: (bound on |out|'s error [n, d], bound on lse's [n]) of the kernels' arithmetic, before the output's
+    rounding.  Every term is weighted by the probabilities, so it shrinks with the result where many keys share it.
+
+    Logit j is off by delta_j: 2^-18 of the magnitudes it is summed from (with |minimum| <= |k| + 15 steps), for bf16
+    activations 2^-31 of the row's largest query per step (queries in fp16, the odd codes' 16 times smaller), and with
+    many rows 2^-11 of each |q k| (keys in fp16) and 2^-25 of the largest query per |k|.  To first order that moves out
+    by sum p delta |v - out|; 1 % more covers the rest, as delta stays far below 0.01.
+    Products with V: fp32 sums, 2^-18 of p (|v| + 15 steps).  bf16, few rows: p times step to 11 bits (2^-11), on codes
+    centred by 8, or to 2^-36 of the largest step.  Many rows: p and v to 11 bits, or to 2^-31 of 1 and 2^-37 of the
+    largest |v|."""
+    see = visible(q.shape[0], k.shape[0], causal, window)
+    out, log = np.zeros((q.shape[0], q.shape[1])), np.zeros(q.shape[0])
+    for i in range(q.shape[0]):
+        j = np.nonzero(see[i])[0]
+        if j.size == 0:
+            continue
+        aq, ak, av = np.abs(q[i]), np.abs(k[j]), np.abs(v[j])
+        s = scale * (k[j] @ q[i])
+        u = np.exp(s - s.max())
+        p = u / u.sum()
+        delta = 2.0 ** -18 * (scale * ((ak + 30 * k_step[j]) @ aq) + np.abs(s) + 1)
+        if many:
+            delta += scale * (2.0 ** -11 * (ak @ aq) + 2.0 ** -25 * aq.max() * ak.sum(-1))
+        elif dtype == "bf16":
+            delta += 2.0 ** -31 * scale * aq.max() * 15 * k_step[j].sum(-1)
+        mean = p @ v[j]
+        out[i] = 1.01 * ((p * delta) @ np.abs(v[j] - mean)) + 2.0 ** -18 * (p @ (av + 15 * v_step[j]))
+        if many:
+            out[i] += 2.0 ** -10 * (p @ av) + (2.0 ** -31 * av.sum(0) + 2.0 ** -37 * av.max() * u.sum()) / u.sum()
+        elif dtype == "bf16":
+            out[i] += 2.0 ** -11 * 8 * (p @ v_step[j]) + 2.0 ** -36 * 8 * v_step[j].max() * j.size / u.sum()
+        log[i] = 1.01 * (p @ delta) + 2.0 ** -18 * (1 + abs(s.max() + np.log(u.sum())))
+    return out, log
 
 
 def prompt_bound(q, k, v, scale, causal, window):
