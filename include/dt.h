@@ -47,14 +47,17 @@
  *      DT_GEMM_BANDS=m,n   fixes the GEMM tile order's band height and block
  *                          width (in 256 x 256 tiles) instead of the host's
  *                          choice, to compare orders.
- *    Two test hooks exercise the bounded-wait exit without a fault:
+ *    Test hooks exercise the bounded-wait exit without a fault:
  *      DT_GEMM_WAIT_LIMIT_MS=n  bounds every GEMM barrier wait at n ms
  *                               (1..10000; default 2000);
  *      DT_GEMM_STARVE=1         makes the GEMM producers issue no copies,
  *                               so every wait runs out and the launch
  *                               reports DT_DEV_ERR_TIMEOUT.
  *      DT_RD_WAIT_LIMIT_MS=n,   the same two hooks for the bulk (TMA) copy
- *      DT_RD_STARVE=1           kernel of dt_redistribute.
+ *      DT_RD_STARVE=1           kernel of dt_redistribute;
+ *      DT_KV4_WAIT_LIMIT_MS=n,  and for dt_tp_kv4_attention, whose copies
+ *      DT_KV4_STARVE=m          stay short of what is awaited from the m-th
+ *                               step of each CTA (tile of each warp) on.
  *  - Compute calls are asynchronous on the given stream (a cudaStream_t;
  *    NULL = the legacy default stream).  Their return value covers the checks
  *    done on the host before any launch; on any error nothing is launched.

@@ -687,7 +687,7 @@ def tp_kv4_attention(q: DTensor, cache: DTensor, page_table: DTensor, kv_lens: D
     L.check(L.untyped("dt_tp_kv4_attention")(_ref(q), _ref(cache), _ref(page_table), _ref(kv_lens), _ref(q_starts),
                                              _ref(y), _ref(lse), int(head_dim), int(group),
                                              C.c_float(head_dim ** -0.5 if scale is None else scale), int(causal),
-                                             max(-1, min(int(window), 0x7FFFFFFF)) if causal else 0,
+                                             max(-1, min(int(window), 0x7FFFFFFF)) if window and causal else 0,
                                              _tp_index(q.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()),
             "tp_kv4_attention")
     return y

@@ -16,9 +16,9 @@
 // Memory's floor: q, k and v are read once, q and one record per token and kv
 // head written once.  Bound: the instructions of the exact quantisation and
 // their latency.  Prompts of 9150 tokens together, 32/8 heads of 128 in bf16,
-// the stored values returned too: 47.1 us for 240 MB, 5.1 TB/s, 0.75 of a
+// the stored values returned too: 47.4 us for 240 MB, 5.1 TB/s, 0.75 of a
 // copy's rate (with the next row's loads in registers, one block ahead, 54.9;
-// with 4 and 5 CTAs an SM 49.3 and 48.3); a decode step of 32 tokens 2.9 us, a
+// with 4 and 5 CTAs an SM 49.3 and 48.3); a decode step of 32 tokens 2.7 us, a
 // launch.
 //
 // Layout.  D/16 lanes hold a head row, two chunks of 8 channels each: chunk

@@ -43,11 +43,11 @@
 //
 // Bound: the instructions and their latency at the 12 warps an SM has room for
 // (168 registers each), HBM next.  48 sequences of up to 8192 keys, 32/8 heads
-// of 128: 67.9 us for 252 MB of records, 3.7 TB/s; the same loads without the
-// arithmetic 48.6, the arithmetic without the loads 69.  Five sequences of
-// 131071: 93.6 us for 436 MB, 4.7 TB/s (73.7 and 97).  One sequence of 4097:
-// 11.9 us, all of it launches and latency.  Tiles of 32 keys with up to five
-// CTAs an SM: 81 to 153 us where these take 68.
+// of 128: 68.2 us for 252 MB of records, 3.7 TB/s; the same loads without the
+// arithmetic 48.3, the arithmetic without the loads 63.8.  Five sequences of
+// 131071: 94.2 us for 436 MB, 4.6 TB/s (73.6 and 91.5).  One sequence of 4097:
+// 11.9 us (9.5 and 11.5), launches and latency.  Tiles of 32 keys with up to
+// five CTAs an SM: 81 to 153 us where these take 68.
 #pragma once
 
 #include <cuda_bf16.h>

@@ -12,9 +12,10 @@
 // minimum + step * code is one fp16 multiply-add, correctly rounded to 11
 // bits (with bf16's 8, keys, values and probabilities would each add as much
 // error as the output's own rounding).  fp16's range is met by powers of
-// two: per row for the queries, per step of 64 keys for K (undone in the
-// softmax's multiplier), and for V the largest so far, with O rescaled where
-// it grows.
+// two: per row for the queries, per step of 64 keys for K (the largest to
+// [2^14, 2^15), undone in the softmax's multiplier), and for V the largest so
+// far, with O rescaled where it grows.  The error of the chunks below against
+// 64 bits is that of the output's rounding, 0.0017 of the norm.
 //
 // Roles, 15 warps: two softmax groups of four warps (one row of one tile per
 // thread), four unpacking warps (two for K, two for V, one key per thread), one
@@ -29,7 +30,7 @@
 // tensor memory, is rescaled rarely.
 //
 // Bound: three chunks of up to 1024 tokens on up to 8000 keys, 32/8 heads of
-// 128, take 241 us for 239 GFLOP, 0.99 PFLOP/s; 256 rows against 128 keys take
+// 128, take 240 us for 239 GFLOP, 1.00 PFLOP/s; 256 rows against 128 keys take
 // 3710 cycles, of which the products need 2050 at the tensor core's rate.  An S
 // of 64 keys takes 372 cycles instead of 256, since it reads the queries' tile
 // from shared memory each time; without exponentials, tensor-memory loads and
@@ -38,8 +39,8 @@
 // S), so an S of 128 keys has one buffer a tile: 5370 cycles, the softmax then
 // waits for every product.  A second loader warp, four unpacked stages and
 // longer or shorter sleeps in the waits changed nothing.  Heads of 256 have room
-// for one tile, two unpacked stages and one packed: 212 us for three chunks of
-// up to 512 tokens on up to 8000 keys, 16/2 heads, 0.58 PFLOP/s (958 us in
+// for one tile, two unpacked stages and one packed: 184 us for three chunks of
+// up to 512 tokens on up to 8000 keys, 16/2 heads, 0.67 PFLOP/s (958 us in
 // passes of 16 rows).
 //
 // The schedule, the pieces of units that a CTA's share cuts and the join are

@@ -12,7 +12,7 @@
 // Both passes are bound by memory: the forward reads and writes each element
 // once, the backward reads x and dy and writes dx.  8192 tokens, 32 + 32 heads
 // of 128 in bf16: forward 44.8 us for 273 MB, 6.1 TB/s, 0.90 of a copy's rate;
-// backward 64.8 us for 407 MB, 6.3 TB/s, 0.93.  8 tokens take 2.8 us, a launch.
+// backward 64.6 us for 407 MB, 6.3 TB/s, 0.93.  8 tokens take 2.6 us, a launch.
 //
 // Layout.  A head's channels are cut into chunks of 8.  A lane holds two
 // chunks of a head -- the two partners of a rotation, chunk l and chunk
@@ -86,7 +86,8 @@ __device__ __forceinline__ void write_dw_part(const NormParams& p, const float* 
 // work is `inner` blocks of heads (SG * U heads each) of one token.
 // CTAs per SM: 5 forward, 4 backward (128 registers for its sums of dw);
 // measured at 8192 tokens x 64 heads against 3..5 CTAs (backward with 5: 97.7
-// us, with 4: 64.8).
+// us, with 4: 64.6; bf16: fp32 takes the same numbers, without a measurement
+// of its own).
 __host__ __device__ constexpr int norm_ctas(bool bwd) { return bwd ? 4 : 5; }
 
 template <class T, bool BWD>
@@ -94,11 +95,11 @@ struct NormVec {
   static constexpr int U = sizeof(T) == 2 && !BWD ? 2 : 1;  // heads per lane and step
   // bf16 backward: x and dy come through a ring of asynchronous copies, each
   // lane its own four chunks, so three steps are on their way without taking
-  // registers: 64.8 us where the next step's loads in registers, one step
+  // registers: 64.6 us where the next step's loads in registers, one step
   // ahead, took 79.3 (8192 tokens x 64 heads); the forward is the other way
-  // round, 46.3 and 44.8.  In fp32 two stages are what
-  // 48 KB hold, and loads in registers are the faster ones (11.4 and 13.0 us
-  // for 1531 tokens x 16 heads of 64).
+  // round, 46.3 and 44.8.  In fp32 a stage takes twice the room: a ring of
+  // two took 13.0 us where loads in registers took 11.4 (1531 tokens x 16
+  // heads of 64; today 10.7); deeper ones were not tried.
   static constexpr int STAGES = BWD && sizeof(T) == 2 ? 4 : 0;
   static constexpr int RING = STAGES * 64 * NR_THREADS;
 };
