@@ -32,7 +32,10 @@ using namespace kv4;
 // rows 405 and 98, and 48 rows 87 where 64 take 76 here; 16/16 heads of 64, 64
 // rows 125 and 100; 16/2 heads of 256, 48 rows 60 where 64 take 45 here.  With
 // two sequences of 2048 keys, too little for the whole device, the two meet
-// at about 96 to 128 rows (64 rows: 17.6 and 21.9 us).
+// at about 96 to 128 rows (64 rows: 17.6 and 21.9 us).  The number is the
+// call's average, since the host does not know the lengths: where they differ
+// much, some rows run on the kernel that suits them less.  All measured with
+// equal lengths.
 constexpr int64_t PROMPT_FROM = 64;
 bool prompt_kernel(bool fp32, int64_t rows) { return !fp32 && rows >= PROMPT_FROM; }
 
