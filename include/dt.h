@@ -518,6 +518,109 @@ DT_API dt_status dt_tp_kv4_attention_workspace_size(const dt_dtensor* q, const d
                                                     const dt_dtensor* page_table, int32_t head_dim, int32_t group,
                                                     int32_t tp_mesh_dim, size_t* bytes);
 
+/* ---- between blocks ----
+ *
+ * Operands of rows: [..., channels], each on its own Replicate or Shard(0) on
+ * every mesh dim (so a call may gather or scatter tokens on its way), leading
+ * dims collapsible to one token dim, unit inner stride, fewer than 2^31 - 2^16
+ * tokens (DT_ERR_CAPACITY).  All arithmetic is fp32 and each result is rounded
+ * once.  Outputs must not have materialised replicas.
+ */
+
+/*
+ * What lies between a block's output and the next block's input, in one pass:
+ *   s = x, its parts added in rank order when x is Partial(sum) on tp
+ *   u = s / sqrt(mean(s^2) + eps) * post_weight          (norm after the block)
+ *   f = keep ? u * gate / (1 - dropout) : 0
+ *   h = residual_scale * residual + f
+ *   y = h / sqrt(mean(h^2) + eps) * pre_weight           (norm before the next)
+ *   x           bf16 or fp32; may be Partial(sum) on tp
+ *   residual    x's shape; bf16 or fp32 (fp32 when x is); NULL: none
+ *   post_weight [channels] Replicate, bf16 or fp32; NULL: no norm of x
+ *   gate        [channels] or [..., channels] Replicate, bf16 or fp32; its rows
+ *               divide the tokens, each for as many consecutive ones; NULL: none
+ *   pre_weight  [channels] Replicate, given exactly when y is
+ *   rng         int32 [4] Replicate, needed with dropout > 0 and read on the
+ *               device: a captured graph replays with new ones
+ *   h           dtype of the residual (without one bf16 or fp32, fp32 when x
+ *               is); NULL: not written
+ *   y           dtype of x
+ * y comes from h before its rounding.  Element i = token * channels + channel
+ * is kept when word i % 4 of Philox4x32-10 at the counter (i / 4 in 64 bits,
+ * rng[2], rng[3]) under the key (rng[0], rng[1]) is at least
+ * floor(dropout * 2^32): the mask depends on the element alone, not on the
+ * layout, and is not stored.  What a dropped element holds does not reach h.
+ */
+DT_API dt_status dt_tp_block_norm(const dt_dtensor* x, const dt_dtensor* residual, const dt_dtensor* post_weight,
+                                  const dt_dtensor* gate, const dt_dtensor* pre_weight, const dt_dtensor* rng,
+                                  const dt_dtensor* h, const dt_dtensor* y, float eps, float residual_scale,
+                                  float dropout, int32_t tp_mesh_dim, int32_t* d_status, dt_stream_t stream);
+
+/*
+ * Its gradients, from dh and dy (gradients of h and y, of their dtypes; dh may
+ * be NULL, dy is given exactly when pre_weight is) and the forward's inputs
+ * with the same rng:
+ *   dx         shape and dtype of x, Replicate or Shard(0) (every part of a
+ *              Partial x has this gradient); NULL: not written
+ *   dresidual  dtype of the residual; NULL: not written
+ *   dpost_weight, dgate, dpre_weight   shapes of their operands, bf16 or fp32,
+ *              given exactly when these are; summed over tokens in an order
+ *              fixed by the shapes (the same inputs give the same bits)
+ * workspace: 256-byte aligned device memory of the queried size (gate_rows 0
+ * without a gate) for the sums over tokens; not needed without weights.
+ */
+DT_API dt_status dt_tp_block_norm_backward(const dt_dtensor* dh, const dt_dtensor* dy, const dt_dtensor* x,
+                                           const dt_dtensor* residual, const dt_dtensor* post_weight,
+                                           const dt_dtensor* gate, const dt_dtensor* pre_weight, const dt_dtensor* rng,
+                                           const dt_dtensor* dx, const dt_dtensor* dresidual,
+                                           const dt_dtensor* dpost_weight, const dt_dtensor* dgate,
+                                           const dt_dtensor* dpre_weight, float eps, float residual_scale, float dropout,
+                                           int32_t tp_mesh_dim, void* workspace, size_t workspace_bytes,
+                                           int32_t* d_status, dt_stream_t stream);
+DT_API dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, int64_t channels, int64_t gate_rows,
+                                                          size_t* bytes);
+
+/* ---- behind the head ---- */
+
+/*
+ * Log probabilities over a sharded vocabulary, without gathering the logits:
+ *   l = log_softmax(scale * logits)
+ *   logits        [..., V] bf16 or fp32, Shard(-1) (as a column-parallel head
+ *                 leaves them) or Replicate on tp, Replicate on the other mesh
+ *                 dims, leading dims collapsible, unit inner stride
+ *   ids           int32 [...] or [..., C], C at most 64, Replicate
+ *   logprobs      fp32, shape of ids: l at the given ids (both NULL: none)
+ *   lse           fp32 [...]: log of the sum of exp(scale * logits); or NULL
+ *   entropy       fp32 [...]: -sum exp(l) l; or NULL
+ *   top_ids, top_logprobs   int32 and fp32 [..., k], k at most 32: the k largest
+ *                 logits, largest first, ties to the lowest id; or both NULL
+ * All small tensors are Replicate and contiguous.  scale > 0.  An id that is
+ * ignore_index gives 0; another one outside [0, V) gives 0 and sets
+ * DT_DEV_ERR_INDEX.  Logits of -inf have probability 0; a row of nothing else
+ * gives lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or
+ * +inf gives NaN (in the order of the alternatives NaN is above all).
+ */
+DT_API dt_status dt_tp_log_probs(const dt_dtensor* logits, const dt_dtensor* ids, const dt_dtensor* logprobs,
+                                 const dt_dtensor* lse, const dt_dtensor* entropy, const dt_dtensor* top_logprobs,
+                                 const dt_dtensor* top_ids, float scale, int32_t ignore_index, int32_t tp_mesh_dim,
+                                 int32_t* d_status, dt_stream_t stream);
+
+/*
+ * The gradient with respect to the logits, from dlogprobs (fp32, shape of ids;
+ * both NULL: none), dentropy (fp32 [...]; NULL: none) and what the forward
+ * returned (lse; entropy where dentropy is given):
+ *   dlogits  shape, dtype and placement of logits; it may be logits itself
+ *            (the same slots and strides)
+ * Ids that were given twice add up; those that gave 0 above add nothing.  A row
+ * whose gradients are all 0, and one whose lse is -inf, get 0 whatever its
+ * logits hold.
+ */
+DT_API dt_status dt_tp_log_probs_backward(const dt_dtensor* dlogprobs, const dt_dtensor* dentropy,
+                                          const dt_dtensor* logits, const dt_dtensor* ids, const dt_dtensor* lse,
+                                          const dt_dtensor* entropy, const dt_dtensor* dlogits, float scale,
+                                          int32_t ignore_index, int32_t tp_mesh_dim, int32_t* d_status,
+                                          dt_stream_t stream);
+
 /* ---- utilities ---- */
 
 /* Static description of a status code. */

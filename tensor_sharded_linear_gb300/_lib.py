@@ -61,6 +61,8 @@ EXPORTS = [
     "dt_cuda_core_gemm_count", "dt_tp_mlp_static_workspace",
     "dt_tp_qk_norm_rope", "dt_tp_qk_norm_rope_backward", "dt_tp_qk_norm_rope_backward_workspace_size",
     "dt_kv4_record_words", "dt_tp_kv4_append", "dt_tp_kv4_attention", "dt_tp_kv4_attention_workspace_size",
+    "dt_tp_block_norm", "dt_tp_block_norm_backward", "dt_tp_block_norm_backward_workspace_size", "dt_tp_log_probs",
+    "dt_tp_log_probs_backward",
 ]
 
 _lib = None
@@ -125,12 +127,19 @@ def load(path: str = LIB_PATH) -> C.CDLL:
             "dt_tp_kv4_attention": (st, [D] * 7 + [C.c_int32, C.c_int32, C.c_float, C.c_int32, C.c_int32, C.c_int32,
                                                    C.c_void_p, C.c_size_t, C.c_void_p, C.c_void_p]),
             "dt_tp_kv4_attention_workspace_size": (st, [D] * 3 + [C.c_int32] * 3 + [P(C.c_size_t)]),
+            "dt_tp_block_norm": (st, [D] * 8 + [C.c_float] * 3 + [C.c_int32, C.c_void_p, C.c_void_p]),
+            "dt_tp_block_norm_backward": (st, [D] * 13 + [C.c_float] * 3 + [C.c_int32, C.c_void_p, C.c_size_t,
+                                                                            C.c_void_p, C.c_void_p]),
+            "dt_tp_block_norm_backward_workspace_size": (st, [C.c_int64] * 3 + [P(C.c_size_t)]),
+            "dt_tp_log_probs": (st, [D] * 7 + [C.c_float, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
+            "dt_tp_log_probs_backward": (st, [D] * 7 + [C.c_float, C.c_int32, C.c_int32, C.c_void_p, C.c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
             fn.restype = res
             fn.argtypes = args
-        for name in ("dt_tp_qk_norm_rope", "dt_tp_qk_norm_rope_backward", "dt_tp_kv4_append", "dt_tp_kv4_attention"):
+        for name in ("dt_tp_qk_norm_rope", "dt_tp_qk_norm_rope_backward", "dt_tp_kv4_append", "dt_tp_kv4_attention",
+                     "dt_tp_block_norm", "dt_tp_block_norm_backward", "dt_tp_log_probs", "dt_tp_log_probs_backward"):
             _untyped[name] = lib[name]  # an object of its own beside the typed one; the result is an int
         _lib = lib
         return lib

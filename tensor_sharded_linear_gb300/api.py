@@ -18,7 +18,7 @@ from __future__ import annotations
 
 import ctypes as C
 from dataclasses import dataclass
-from typing import Optional, Sequence
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -725,6 +725,129 @@ def tp_cached_attention(x: DTensor, wq: DTensor, wk: DTensor, wv: DTensor, wo: D
                           **kw)
     a = tp_kv4_attention(q, cache, page_table, kv_lens, q_starts, scale=scale, causal=causal, window=window, **kw)
     return row_parallel_linear(a, wo, mode=mode, tp_dim=tp_dim, out_dtype=out_dtype, out=out)
+
+
+# ---------------------------------------------------------------- between blocks, and behind the head
+
+def _row_like(x: DTensor, dtype=None) -> DTensor:
+    """An empty tensor of x's rows: placed as x, Replicate where x is Partial."""
+    pls = [Replicate() if isinstance(p, Partial) else p for p in x.placements]
+    return DTensor.empty(x.mesh, pls, x.gshape, dtype or x.dtype, device=x.slots[0].device)
+
+
+def tp_block_norm(x: DTensor, residual: Optional[DTensor] = None, post_weight: Optional[DTensor] = None,
+                  gate: Optional[DTensor] = None, pre_weight: Optional[DTensor] = None, *, eps: float = 1e-6,
+                  residual_scale: float = 1.0, dropout: float = 0.0, rng: Optional[DTensor] = None, tp_dim="tp",
+                  out=None):
+    """What lies between a block's output x and the next block's input, in one pass:
+
+    u = norm(x) * post_weight, f = dropout(u * gate), h = residual_scale * residual + f,
+    y = norm(h) * pre_weight; parts that are None are left out.
+
+    x [..., channels] may be Partial on tp (a row-parallel layer's PARTIAL
+    output); x, residual, h and y are each Replicate or Shard(0), so the call
+    can reduce, scatter and gather tokens on its way.  ``gate`` [channels], or
+    with rows that divide the tokens.  ``dropout`` takes ``rng``, int32 [4]
+    (key and offset of the generator); the same rng gives the same mask.
+    Returns (h, y), y None without ``pre_weight``; ``out`` = (h, y) to write
+    into, either None where it is not wanted.  Without it both lie as the
+    residual (or x) does, h in its dtype."""
+    if out is None:
+        like = residual if residual is not None else x
+        out = (_row_like(like), None if pre_weight is None else _row_like(like, x.dtype))
+    h, y = out
+    L.check(L.untyped("dt_tp_block_norm")(_ref(x), _ref(residual), _ref(post_weight), _ref(gate), _ref(pre_weight),
+                                          _ref(rng), _ref(h), _ref(y), C.c_float(eps), C.c_float(residual_scale),
+                                          C.c_float(dropout), _tp_index(x.mesh, tp_dim), None, _stream_arg()),
+            "tp_block_norm")
+    return h, y
+
+
+def tp_block_norm_backward_workspace_bytes(x: DTensor, post_weight: Optional[DTensor] = None,
+                                           gate: Optional[DTensor] = None,
+                                           pre_weight: Optional[DTensor] = None) -> int:
+    """dt_tp_block_norm_backward_workspace_size (0 without weights and gate)."""
+    if post_weight is None and gate is None and pre_weight is None:
+        return 0
+    tokens = rows = 1
+    for s in x.gshape[:-1]:
+        tokens *= s
+    for s in gate.gshape[:-1] if gate is not None else (0,):
+        rows *= s
+    n = C.c_size_t()
+    L.check(L.load().dt_tp_block_norm_backward_workspace_size(tokens, x.gshape[-1], rows, C.byref(n)),
+            "tp_block_norm_backward_workspace_size")
+    return n.value
+
+
+def tp_block_norm_backward(dh: Optional[DTensor], dy: Optional[DTensor], x: DTensor,
+                           residual: Optional[DTensor] = None, post_weight: Optional[DTensor] = None,
+                           gate: Optional[DTensor] = None, pre_weight: Optional[DTensor] = None, *, eps: float = 1e-6,
+                           residual_scale: float = 1.0, dropout: float = 0.0, rng: Optional[DTensor] = None,
+                           tp_dim="tp", out=None, workspace: Optional[torch.Tensor] = None):
+    """Gradients of ``tp_block_norm`` from those of h and y and its inputs.
+
+    Returns (dx, dresidual, dpost_weight, dgate, dpre_weight), None where the
+    operand is; dx is that of every part of a Partial x.  ``out``: the five to
+    write into (dx and dresidual None where not wanted)."""
+    if out is None:
+        out = (_row_like(x), None if residual is None else _row_like(residual),
+               *(None if w is None else _like(w) for w in (post_weight, gate, pre_weight)))
+    if workspace is None:
+        workspace = _workspace(tp_block_norm_backward_workspace_bytes(x, post_weight, gate, pre_weight),
+                               x.slots[0].device)
+    L.check(L.untyped("dt_tp_block_norm_backward")(
+        _ref(dh), _ref(dy), _ref(x), _ref(residual), _ref(post_weight), _ref(gate), _ref(pre_weight), _ref(rng),
+        *(_ref(o) for o in out), C.c_float(eps), C.c_float(residual_scale), C.c_float(dropout),
+        _tp_index(x.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()), "tp_block_norm_backward")
+    return tuple(out)
+
+
+class TokenLogProbs(NamedTuple):
+    """What ``tp_log_probs`` returns; None where it was not asked for."""
+    logprobs: Optional[DTensor]
+    lse: DTensor
+    entropy: Optional[DTensor]
+    top_logprobs: Optional[DTensor]
+    top_ids: Optional[DTensor]
+
+
+def tp_log_probs(logits: DTensor, ids: Optional[DTensor] = None, *, scale: float = 1.0, top: int = 0,
+                 entropy: bool = False, ignore_index: int = -100, tp_dim="tp", out=None) -> TokenLogProbs:
+    """log_softmax(scale * logits) at the given ids, over a vocabulary sharded on tp.
+
+    logits [..., V] as a column-parallel head leaves them (Shard(-1)) or
+    Replicate; ids int32 [...] or [..., C].  ``top`` alternatives per token (ties
+    to the lowest id), the entropy on request, and always lse, which the
+    gradient takes.  An id that is ``ignore_index`` gives 0.  ``out``: the five
+    results to write into."""
+    if out is None:
+        lead, dev = logits.gshape[:-1], logits.slots[0].device
+
+        def empty(shape, dtype=torch.float32):
+            return DTensor.empty(logits.mesh, [Replicate()] * logits.mesh.ndim, shape, dtype, device=dev)
+
+        out = (None if ids is None else empty(ids.gshape), empty(lead), empty(lead) if entropy else None,
+               empty(lead + (top,)) if top else None, empty(lead + (top,), torch.int32) if top else None)
+    L.check(L.untyped("dt_tp_log_probs")(_ref(logits), _ref(ids), *(_ref(o) for o in out), C.c_float(scale),
+                                         int(ignore_index), _tp_index(logits.mesh, tp_dim), None, _stream_arg()),
+            "tp_log_probs")
+    return TokenLogProbs(*out)
+
+
+def tp_log_probs_backward(dlogprobs: Optional[DTensor], dentropy: Optional[DTensor], logits: DTensor,
+                          ids: Optional[DTensor], lse: DTensor, entropy: Optional[DTensor] = None, *,
+                          scale: float = 1.0, ignore_index: int = -100, tp_dim="tp",
+                          out: Optional[DTensor] = None) -> DTensor:
+    """The gradient of ``tp_log_probs`` with respect to the logits, from those of
+    the log probabilities and (with ``entropy``) of the entropy, and the forward's
+    lse.  ``out`` may be logits itself."""
+    d = out if out is not None else _like(logits)
+    L.check(L.untyped("dt_tp_log_probs_backward")(_ref(dlogprobs), _ref(dentropy), _ref(logits), _ref(ids), _ref(lse),
+                                                  _ref(entropy), _ref(d), C.c_float(scale), int(ignore_index),
+                                                  _tp_index(logits.mesh, tp_dim), None, _stream_arg()),
+            "tp_log_probs_backward")
+    return d
 
 
 # ---------------------------------------------------------------- DTorch-style layers
