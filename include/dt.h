@@ -594,7 +594,8 @@ DT_API dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, int64_
  *   entropy       fp32 [...]: -sum exp(l) l; or NULL
  *   top_ids, top_logprobs   int32 and fp32 [..., k], k at most 32: the k largest
  *                 logits, largest first, ties to the lowest id; or both NULL
- * All small tensors are Replicate and contiguous.  scale > 0.  An id that is
+ * All small tensors are Replicate and contiguous.  scale 2^-20 .. 2^20; with
+ * alternatives V is at most 2^24 (DT_ERR_CAPACITY).  An id that is
  * ignore_index gives 0; another one outside [0, V) gives 0 and sets
  * DT_DEV_ERR_INDEX.  Logits of -inf have probability 0; a row of nothing else
  * gives lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or

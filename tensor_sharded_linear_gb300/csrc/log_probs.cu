@@ -21,26 +21,51 @@ namespace {
 
 constexpr int LP_MAX_TOP = 32;
 constexpr int LP_MAX_GIVEN = 64;
+constexpr int LP_WARPS = 8;
+constexpr int LP_THREADS = 32 * LP_WARPS;
+constexpr int LP_MAX_CLUSTER = 8;
+constexpr int64_t LP_MAX_TOP_VOCAB = 1 << 24;
+constexpr float LOG2E = 1.44269504088896341f;
 
-// Columns [begin, begin of the next shard) of every token.
+// A unit of work is 2 KB of one shard's row, on 16-byte boundaries of memory:
+// four vectors a lane, each 512 contiguous bytes over the warp.  Of a row that
+// starts off a boundary the first and last units are partly outside it; these
+// elements are neither read nor written.
+constexpr int LP_VECS = 4;
+template <class T>
+struct Unit {
+  static constexpr int VE = 16 / sizeof(T);      // elements of a vector
+  static constexpr int BLOCK = 32 * VE;          // of a vector over the warp
+  static constexpr int SIZE = LP_VECS * BLOCK;
+};
+
+// Columns [begin, begin + n) of every token.
 struct VocabShard {
   char* ptr;
   int64_t ld;  // elements between tokens
-  int64_t begin;
+  int32_t begin, n;
+  int32_t unit, pad;  // units of a row before this shard
 };
 
 struct LogProbArgs {
-  VocabShard z[DT_MAX_SLOTS], dz[DT_MAX_SLOTS];
-  int32_t shards, dz_shards;
-  int64_t tokens, vocab;
+  int32_t shards;
+  int32_t units;  // of a row
+  int64_t tokens;
+  int32_t vocab;
   const int32_t* ids;  // [tokens, given]; NULL: none
   int32_t given, ignore, top;
   float scale;
   float *logp, *lse, *entropy, *top_logp;  // backward: lse and entropy are read
   int32_t* top_ids;
   const float *dlogp, *dentropy;
+  int32_t parts;  // CTAs of a row (forward: a cluster)
   int32_t* status;
 };
+template <int CAP>
+struct LogProbParams : LogProbArgs {
+  VocabShard z[CAP], dz[CAP];
+};
+constexpr int LP_SMALL = 8;  // shards of most launches; a parameter block for 64 takes longer to launch
 
 // Bits whose order as unsigned numbers is that of the values; -0 equals +0, NaN is above all.
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -58,121 +83,461 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
-
-constexpr int LP_THREADS = 256;
-
-template <class F>
-__device__ __forceinline__ void cta_reduce(uint64_t* buf, uint64_t& v, F&& join) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (int o = 16; o; o >>= 1) v = join(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if (lane == 0) buf[warp] = v;
-  __syncthreads();
-  v = buf[0];
-  for (int w = 1; w < LP_THREADS / 32; ++w) v = join(v, buf[w]);
+__device__ __forceinline__ uint32_t max_nan_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
 
 template <class T>
-__device__ __forceinline__ float logit(const LogProbArgs& p, int64_t t, int64_t j) {
+struct Vec;  // 16 bytes of logits
+template <>
+struct Vec<__nv_bfloat16> {
+  uint4 u;
+  __device__ __forceinline__ void get(f2 (&v)[4]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = f2{__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u)};
+  }
+  __device__ __forceinline__ void put(const f2 (&v)[4]) {
+    u = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                   pack_bf16(v[3].x, v[3].y));
+  }
+  __device__ __forceinline__ float max() const {
+    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+};
+template <>
+struct Vec<float> {
+  uint4 u;
+  __device__ __forceinline__ void get(f2 (&v)[2]) const {
+    v[0] = f2{__uint_as_float(u.x), __uint_as_float(u.y)}, v[1] = f2{__uint_as_float(u.z), __uint_as_float(u.w)};
+  }
+  __device__ __forceinline__ void put(const f2 (&v)[2]) {
+    u = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
+  }
+  __device__ __forceinline__ float max() const {
+    return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
+                   max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+};
+__device__ __forceinline__ float element(const Vec<__nv_bfloat16>& v, int i) {
+  const uint32_t w = i < 2 ? v.u.x : i < 4 ? v.u.y : i < 6 ? v.u.z : v.u.w;
+  return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
+}
+__device__ __forceinline__ float element(const Vec<float>& v, int i) {
+  return __uint_as_float(i == 0 ? v.u.x : i == 1 ? v.u.y : i == 2 ? v.u.z : v.u.w);
+}
+
+// Where a unit lies: the first element of lane 0's first vector is column
+// `at` of the shard's row, -VE < at < n.
+template <class T>
+struct Place {
+  const T* row;  // column 0 of the shard's row
+  int32_t shard, at, n;
+  __device__ __forceinline__ int column(int vec, int lane) const {
+    return at + vec * Unit<T>::BLOCK + lane * Unit<T>::VE;
+  }
+  __device__ __forceinline__ bool inside() const { return at >= 0 && at + Unit<T>::SIZE <= n; }
+};
+template <class T, class S>
+__device__ __forceinline__ Place<T> place(const S* shards, int count, int unit, int64_t t, int& s) {
+  while (s + 1 < count && shards[s + 1].unit <= unit) ++s;
+  Place<T> p;
+  p.row = reinterpret_cast<const T*>(shards[s].ptr) + t * shards[s].ld;
+  const int off = (int)(reinterpret_cast<uintptr_t>(p.row) & 15) / (int)sizeof(T);
+  p.shard = s;
+  p.at = (unit - shards[s].unit) * Unit<T>::SIZE - off;
+  p.n = shards[s].n;
+  return p;
+}
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p)
+               : "memory");
+  return v;
+}
+// The lane's vector `vec` of a unit; -inf for what lies outside the row.
+template <class T>
+__device__ __forceinline__ Vec<T> load_vec(const Place<T>& p, int vec, int lane) {
+  Vec<T> v;
+  const int c = p.column(vec, lane);
+  if (c >= 0 && c + Unit<T>::VE <= p.n) {
+    v.u = load16(p.row + c);
+    return v;
+  }
+  constexpr int N = Unit<T>::VE / 2;
+  f2 x[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i].x = c + 2 * i >= 0 && c + 2 * i < p.n ? to_f32(p.row[c + 2 * i]) : -INFINITY;
+    x[i].y = c + 2 * i + 1 >= 0 && c + 2 * i + 1 < p.n ? to_f32(p.row[c + 2 * i + 1]) : -INFINITY;
+  }
+  v.put(x);
+  return v;
+}
+template <class T>
+__device__ __forceinline__ void load_unit(const Place<T>& p, int lane, Vec<T> (&v)[LP_VECS]) {
+  if (p.inside()) {
+#pragma unroll
+    for (int i = 0; i < LP_VECS; ++i) v[i].u = load16(p.row + p.column(i, lane));
+  } else {
+#pragma unroll
+    for (int i = 0; i < LP_VECS; ++i) v[i] = load_vec(p, i, lane);
+  }
+}
+
+template <class T, class P>
+__device__ __forceinline__ float logit(const P& p, int64_t t, int j) {
   int s = 0;
   while (s + 1 < p.shards && p.z[s + 1].begin <= j) ++s;
   return to_f32(reinterpret_cast<const T*>(p.z[s].ptr)[t * p.z[s].ld + (j - p.z[s].begin)]);
 }
 
 // The id at place i: its column, or -1 (and the status bit unless it is the one to be ignored).
-__device__ __forceinline__ int64_t given_id(const LogProbArgs& p, int64_t i, bool report) {
+__device__ __forceinline__ int given_id(const LogProbArgs& p, int64_t i, bool report) {
   const int32_t id = load_plain(p.ids + i);
   if (id >= 0 && id < p.vocab) return id;
   if (report && id != p.ignore) atomicOr(p.status, DT_DEV_ERR_INDEX);
   return -1;
 }
 
-template <class T>
-__global__ void __launch_bounds__(LP_THREADS) log_probs_kernel(const __grid_constant__ LogProbArgs p) {
-  __shared__ uint64_t buf[LP_THREADS / 32];
+// A running softmax: the largest logit m, s = sum exp2((z - m) c), and
+// e = sum exp2((z - m) c) (z - m).  m starts at the lowest finite number, so
+// that -inf - m is -inf; differences are kept above -1e28 where they are
+// multiplied, so that 0 times them is 0.
+struct Soft {
+  float m = -3.402823466e38f, s = 0.f, e = 0.f;
+  __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
+    const float d = fmaxf(m - to, -1e28f), f = exp2_fast(d * c);
+    e = f * fmaf(d, s, e);
+    s *= f;
+    m = to;
+  }
+  __device__ __forceinline__ void join(Soft o, float c) {
+    const float top = max_nan(m, o.m);
+    raise(top, c);
+    o.raise(top, c);
+    s += o.s;
+    e += o.e;
+  }
+  __device__ __forceinline__ Soft shuffled(int o) const {
+    Soft r;
+    r.m = __shfl_xor_sync(0xffffffffu, m, o);
+    r.s = __shfl_xor_sync(0xffffffffu, s, o);
+    r.e = __shfl_xor_sync(0xffffffffu, e, o);
+    return r;
+  }
+};
+
+template <class T, bool ENT>
+__device__ __forceinline__ void soft_unit(Soft& a, const Vec<T> (&v)[LP_VECS], float most, float c) {
+  most = max_nan(a.m, most);
+  if (!(most == a.m)) a.raise(most, c);
+  constexpr int N = Unit<T>::VE / 2;
+  const f2 m2 = both(-a.m), c2 = both(c);
+  f2 s[2] = {both(0.f), both(0.f)}, e[2] = {both(0.f), both(0.f)};
+#pragma unroll
+  for (int i = 0; i < LP_VECS; ++i) {
+    f2 z[N];
+    v[i].get(z);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const f2 d = z[k] + m2, t = d * c2, x = f2{exp2_fast(t.x), exp2_fast(t.y)};
+      s[k & 1] = s[k & 1] + x;
+      if (ENT) e[k & 1] = fma2(x, f2{fmaxf(d.x, -1e28f), fmaxf(d.y, -1e28f)}, e[k & 1]);
+    }
+  }
+  const f2 s1 = s[0] + s[1], e1 = e[0] + e[1];
+  a.s += s1.x + s1.y;
+  if (ENT) a.e += e1.x + e1.y;
+}
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t first_ctas(const void* p) {  // the same object in the cluster's first CTA
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
+  return r;
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, uint64_t v) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
+}
+__device__ __forceinline__ void store_cluster(uint32_t a, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// One cluster of CTAs per token (a cluster of one when there are tokens
+// enough): each warp takes every so many units, the CTAs' sums and candidates
+// meet in the first one's shared memory, which writes the results.
+//
+// Alternatives.  The pass over the row leaves the largest logit of each block
+// of 512 bytes and of 32 or 64 groups of lanes.  The k-th largest of the groups
+// is at most the k-th largest logit, so every alternative is in a block that
+// reaches it; these (hardly more than k when values differ) are read again, now
+// from L2, and elements that reach it go through a sorted list per warp, then
+// through a count of the larger ones.  The order is that of (value, lowest id)
+// as one 64-bit number, so the result does not depend on who came first.
+template <class T, bool TOP, bool ENT, int CAP>
+__global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_constant__ LogProbParams<CAP> p) {
+  __shared__ Soft soft[LP_WARPS];
+  __shared__ Soft meet[LP_MAX_CLUSTER];                      // in the first CTA
+  __shared__ uint64_t recv[LP_MAX_CLUSTER * LP_MAX_TOP];     // in the first CTA
+  __shared__ uint64_t cand[LP_WARPS * LP_MAX_TOP];
+  __shared__ __align__(16) uint32_t group[64];
+  __shared__ uint32_t reach;
+  __shared__ int listed, found;
+  extern __shared__ uint32_t block_key[];  // TOP: [blocks of this CTA], then the list of those to be read again
   wait_for_previous_kernel();
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    float m = -INFINITY, s = 0.f, e = 0.f;
-    auto each = [&](auto&& body) {
-      for (int k = 0; k < p.shards; ++k) {
-        const T* z = reinterpret_cast<const T*>(p.z[k].ptr) + t * p.z[k].ld;
-        const int64_t n = (k + 1 < p.shards ? p.z[k + 1].begin : p.vocab) - p.z[k].begin;
-        for (int64_t j = threadIdx.x; j < n; j += LP_THREADS) body(to_f32(z[j]), p.z[k].begin + j);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int ctas = p.parts, rank = ctas > 1 ? (int)cluster_rank() : 0;
+  if (ctas > 1) cluster_arrive();
+  const int64_t t = blockIdx.x / ctas;
+  const float c = p.scale * LOG2E;
+  const int step = ctas * warps, first = rank * warps + warp;
+  if (TOP && threadIdx.x == 0) listed = found = 0;
+  Soft a;
+  int shard = 0, k_unit = 0;
+  Vec<T> v[LP_VECS];
+  Place<T> at;
+  if (first < p.units) {
+    at = place<T>(p.z, p.shards, first, t, shard);
+    load_unit(at, lane, v);
+  }
+  for (int u = first; u < p.units; u += step, ++k_unit) {
+    Vec<T> next[LP_VECS];
+    if (u + step < p.units) {
+      at = place<T>(p.z, p.shards, u + step, t, shard);
+      load_unit(at, lane, next);
+    }
+    float most;
+#pragma unroll
+    for (int i = 0; i < LP_VECS; ++i) {
+      const float b = v[i].max();
+      most = i ? max_nan(most, b) : b;
+      if (TOP) {
+        const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(b));
+        if (lane == 0) block_key[(k_unit * warps + warp) * LP_VECS + i] = key;
       }
-    };
-    each([&](float z, int64_t) { m = max_nan(m, z); });
-    uint64_t v = __float_as_uint(m);
-    cta_reduce(buf, v, [](uint64_t a, uint64_t b) {
-      return (uint64_t)__float_as_uint(max_nan(__uint_as_float((uint32_t)a), __uint_as_float((uint32_t)b)));
-    });
-    m = __uint_as_float((uint32_t)v);
-    const bool none = m == -INFINITY;  // no token is possible
-    each([&](float z, int64_t) {
-      const float d = none ? -INFINITY : (z - m) * p.scale, x = __expf(d);
-      s += x;
-      e += x * fmaxf(d, -1e30f);
-    });
-    auto add = [](uint64_t a, uint64_t b) {
-      return (uint64_t)__float_as_uint(__uint_as_float((uint32_t)a) + __uint_as_float((uint32_t)b));
-    };
-    v = __float_as_uint(s);
-    cta_reduce(buf, v, add);
-    s = __uint_as_float((uint32_t)v);
-    v = __float_as_uint(e);
-    cta_reduce(buf, v, add);
-    e = __uint_as_float((uint32_t)v);
-    const float ln = logf(s);
-    auto logp = [&](float z) { return none ? -INFINITY : (z - m) * p.scale - ln; };
+    }
+    soft_unit<T, ENT>(a, v, most, c);
+#pragma unroll
+    for (int i = 0; i < LP_VECS; ++i) v[i] = next[i];
+  }
+  const int per_group = warps >= 2 ? warps / 2 : 1, groups = 32 * warps / per_group;
+  if (TOP) {
+    // (a lane without any element: below every key)
+    uint32_t g = first < p.units ? order_key(a.m == Soft().m ? -INFINITY : a.m) : 0;
+    for (int o = 1; o < per_group; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (lane % per_group == 0) group[(warp * 32 + lane) / per_group] = g;
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) a.join(a.shuffled(o), c);
+  if (lane == 0) soft[warp] = a;
+  __syncthreads();
+  a = soft[0];
+  for (int w = 1; w < warps; ++w) a.join(soft[w], c);
+  if (TOP) {
+    if ((int)threadIdx.x < groups) {
+      const uint32_t mine = group[threadIdx.x];
+      int above = 0;
+      for (int i = 0; i < groups; ++i) {
+        const uint32_t o = group[i];
+        above += o > mine || (o == mine && i < (int)threadIdx.x);
+      }
+      if (above == p.top - 1) reach = mine;
+    }
+    __syncthreads();
+    const uint32_t low = reach;
+    const int my_units = first - warp < p.units ? (p.units - (first - warp) + step - 1) / step : 0;  // rounds of the CTA
+    const int blocks = my_units * warps * LP_VECS;
+    uint32_t* list = block_key + blocks;
+    for (int i = threadIdx.x; i < blocks; i += blockDim.x) {
+      const int u = rank * warps + i / LP_VECS % warps + i / (LP_VECS * warps) * step;
+      if (u < p.units && block_key[i] >= low) list[atomicAdd(&listed, 1)] = i;
+    }
+    __syncthreads();
+    uint64_t best = 0, worst = 0;  // lane i: the i-th best so far; the k-th
+    for (int l = warp; l < listed; l += warps) {
+      const int i = (int)list[l], u = rank * warps + i / LP_VECS % warps + i / (LP_VECS * warps) * step;
+      int s = 0;
+      const Place<T> q = place<T>(p.z, p.shards, u, t, s);
+      const Vec<T> x = load_vec(q, i % LP_VECS, lane);
+      const int col = q.column(i % LP_VECS, lane);
+#pragma unroll 1
+      for (int e = 0; e < Unit<T>::VE; ++e) {
+        const uint32_t key = order_key(element(x, e));
+        const uint64_t me = (uint64_t)key << 32 | (0xFFFFFFFFu - (uint32_t)(p.z[q.shard].begin + col + e));
+        unsigned in = __ballot_sync(0xffffffffu, col + e >= 0 && col + e < q.n && key >= low && me > worst);
+        while (in) {
+          const uint64_t n = __shfl_sync(0xffffffffu, me, __ffs(in) - 1);
+          in &= in - 1;
+          if (n <= worst) continue;
+          const int pos = __popc(__ballot_sync(0xffffffffu, best > n));
+          const uint64_t up = __shfl_up_sync(0xffffffffu, best, 1);
+          best = lane < pos ? best : lane == pos ? n : up;
+          worst = __shfl_sync(0xffffffffu, best, p.top - 1);
+        }
+      }
+    }
+    const unsigned have = __ballot_sync(0xffffffffu, lane < p.top && best != 0);
+    int base = 0;
+    if (lane == 0) base = atomicAdd(&found, __popc(have));
+    base = __shfl_sync(0xffffffffu, base, 0);
+    if (have >> lane & 1) cand[base + __popc(have & ((1u << lane) - 1))] = best;
+    __syncthreads();
+  }
+  auto count_larger = [](const uint64_t* x, int n, uint64_t mine) {
+    int above = 0;
+    for (int i = 0; i < n; ++i) above += x[i] > mine;
+    return above;
+  };
+  int total = TOP ? found : 0;
+  const uint64_t* from = cand;
+  if (ctas > 1) {
+    cluster_wait();  // the first CTA is there
     if (threadIdx.x == 0) {
-      if (p.lse) p.lse[t] = none ? -INFINITY : m * p.scale + ln;
-      if (p.entropy) p.entropy[t] = none ? 0.f : ln - e / s;
+      store_cluster(first_ctas(&meet[rank].m), a.m);
+      store_cluster(first_ctas(&meet[rank].s), a.s);
+      store_cluster(first_ctas(&meet[rank].e), a.e);
     }
-    for (int c = threadIdx.x; c < p.given; c += LP_THREADS) {
-      const int64_t id = given_id(p, t * p.given + c, true);
-      p.logp[t * p.given + c] = id >= 0 ? logp(logit<T>(p, t, id)) : 0.f;
+    if (TOP) {  // this CTA's k best, and zeros where it has fewer
+      for (int i = threadIdx.x; i < total; i += blockDim.x) {
+        const int r = count_larger(cand, total, cand[i]);
+        if (r < p.top) store_cluster(first_ctas(&recv[rank * p.top + r]), cand[i]);
+      }
+      for (int i = total + (int)threadIdx.x; i < p.top; i += blockDim.x)
+        store_cluster(first_ctas(&recv[rank * p.top + i]), (uint64_t)0);
     }
-    uint64_t last = ~0ull;
-    for (int k = 0; k < p.top; ++k) {
-      uint64_t best = 0;
-      each([&](float z, int64_t j) {
-        const uint64_t x = (uint64_t)order_key(z) << 32 | (0xFFFFFFFFu - (uint32_t)j);
-        if (x < last && x > best) best = x;
-      });
-      cta_reduce(buf, best, [](uint64_t a, uint64_t b) { return a > b ? a : b; });
-      last = best;
-      if (threadIdx.x == 0) {
-        p.top_logp[t * p.top + k] = logp(key_value((uint32_t)(best >> 32)));
-        p.top_ids[t * p.top + k] = (int32_t)(0xFFFFFFFFu - (uint32_t)best);
+    cluster_arrive();
+    cluster_wait();
+    if (rank != 0) return;
+    a = meet[0];
+    for (int r = 1; r < ctas; ++r) a.join(meet[r], c);
+    from = recv;
+    total = ctas * p.top;
+  }
+  const bool none = a.s == 0.f;  // no token is possible
+  const float ln = logf(a.s);
+  auto logp = [&](float z) { return none ? -INFINITY : (z - a.m) * p.scale - ln; };
+  if (threadIdx.x == 0) {
+    if (p.lse) p.lse[t] = none ? -INFINITY : fmaf(a.m, p.scale, ln);
+    if (ENT) p.entropy[t] = none ? 0.f : ln - p.scale * (a.e / a.s);
+  }
+  for (int i = threadIdx.x; i < p.given; i += blockDim.x) {
+    const int id = given_id(p, t * p.given + i, true);
+    p.logp[t * p.given + i] = id >= 0 ? logp(logit<T>(p, t, id)) : 0.f;
+  }
+  if (TOP) {
+    for (int i = threadIdx.x; i < total; i += blockDim.x) {
+      const uint64_t mine = from[i];
+      const int r = mine ? count_larger(from, total, mine) : p.top;
+      if (r < p.top) {
+        p.top_logp[t * p.top + r] = logp(key_value((uint32_t)(mine >> 32)));
+        p.top_ids[t * p.top + r] = (int32_t)(0xFFFFFFFFu - (uint32_t)mine);
       }
     }
   }
 }
 
-template <class T>
-__global__ void __launch_bounds__(LP_THREADS) log_probs_backward_kernel(const __grid_constant__ LogProbArgs p) {
+// A CTA takes a run of units of one token.  The given ids' elements are
+// written last, by the threads that stand for them, so that the pass itself
+// is the same for all.
+template <class T, bool ENT, int CAP>
+__global__ void __launch_bounds__(LP_THREADS, 4) log_probs_backward_kernel(const __grid_constant__ LogProbParams<CAP> p) {
   wait_for_previous_kernel();
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    float g = 0.f;
-    for (int c = 0; c < p.given; ++c) {
-      const int64_t id = given_id(p, t * p.given + c, threadIdx.x == 0);
-      if (id >= 0) g += load_plain(p.dlogp + t * p.given + c);
-    }
-    const float lse = load_plain(p.lse + t), ge = p.dentropy ? load_plain(p.dentropy + t) : 0.f;
-    const float h = p.dentropy ? load_plain(p.entropy + t) : 0.f;
-    const bool none = lse == -INFINITY;
-    for (int k = 0; k < p.shards; ++k) {
-      const T* z = reinterpret_cast<const T*>(p.z[k].ptr) + t * p.z[k].ld;
-      T* dz = reinterpret_cast<T*>(p.dz[k].ptr) + t * p.dz[k].ld;
-      const int64_t n = (k + 1 < p.shards ? p.z[k + 1].begin : p.vocab) - p.z[k].begin;
-      for (int64_t j = threadIdx.x; j < n; j += LP_THREADS) {
-        const float l = to_f32(z[j]) * p.scale - lse, q = __expf(l);
-        float d = -q * g - ge * q * (fmaxf(l, -1e30f) + h);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x / p.parts;
+  const int part = (int)(blockIdx.x - t * p.parts);
+  const int u0 = (int)((int64_t)p.units * part / p.parts), u1 = (int)((int64_t)p.units * (part + 1) / p.parts);
+  float g = 0.f;
+  bool zero = true;
+  for (int c = 0; c < p.given; ++c) {
+    const int id = given_id(p, t * p.given + c, part == 0 && threadIdx.x == 0);
+    const float v = id >= 0 ? load_plain(p.dlogp + t * p.given + c) : 0.f;
+    zero = zero && v == 0.f;
+    g += v;
+  }
+  const float lse = load_plain(p.lse + t);
+  const float ge = ENT ? load_plain(p.dentropy + t) : 0.f, h = ENT ? load_plain(p.entropy + t) : 0.f;
+  zero = (zero && ge == 0.f) || lse == -INFINITY;
+  // dlogit = exp(l) (a + b l) with l = scale z - lse, and scale g_c on top at the given ids
+  const float a = -p.scale * (g + ge * h), b = -p.scale * ge;
+  auto value = [&](float z) {
+    const float l = fmaf(z, p.scale, -lse), x = exp2_fast(l * LOG2E);
+    return x * (ENT ? fmaf(fmaxf(l, -1e28f), b, a) : a);
+  };
+  // the given ids of this CTA's units: their gradients, before the logits may be overwritten
+  T* to = nullptr;
+  float at_id = 0.f;
+  if ((int)threadIdx.x < p.given && !zero) {
+    const int id = given_id(p, t * p.given + threadIdx.x, false);
+    if (id >= 0) {
+      int s = 0;
+      while (s + 1 < p.shards && p.z[s + 1].begin <= id) ++s;
+      const T* row = reinterpret_cast<const T*>(p.z[s].ptr) + t * p.z[s].ld;
+      const int col = id - p.z[s].begin, off = (int)(reinterpret_cast<uintptr_t>(row) & 15) / (int)sizeof(T);
+      const int u = p.z[s].unit + (col + off) / Unit<T>::SIZE;
+      if (u >= u0 && u < u1) {
+        float mine = 0.f;
         for (int c = 0; c < p.given; ++c)
-          if (load_plain(p.ids + t * p.given + c) == p.z[k].begin + j) d += load_plain(p.dlogp + t * p.given + c);
-        from_f32(dz + j, none || (g == 0.f && ge == 0.f && p.given <= 1) ? 0.f : d * p.scale);
+          if (load_plain(p.ids + t * p.given + c) == id) mine += load_plain(p.dlogp + t * p.given + c);
+        to = reinterpret_cast<T*>(p.dz[s].ptr) + t * p.dz[s].ld + col;
+        at_id = fmaf(p.scale, mine, value(to_f32(row[col])));
       }
     }
   }
+  __syncthreads();
+  constexpr int N = Unit<T>::VE / 2;
+  int shard = 0;
+  for (int u = u0 + warp; u < u1; u += LP_WARPS) {
+    const Place<T> at = place<T>(p.z, p.shards, u, t, shard);
+    T* out = reinterpret_cast<T*>(p.dz[at.shard].ptr) + t * p.dz[at.shard].ld;
+    // the gradient's row starts as far from a 16-byte boundary as the logits' in all but odd views
+    const bool alike = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(at.row)) & 15) == 0;
+    Vec<T> v[LP_VECS];
+    if (!zero) load_unit(at, lane, v);
+#pragma unroll
+    for (int i = 0; i < LP_VECS; ++i) {
+      f2 x[N];
+      if (!zero) {
+        v[i].get(x);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const f2 l = fma2(x[k], both(p.scale), both(-lse)), e = l * both(LOG2E);
+          const f2 q = f2{exp2_fast(e.x), exp2_fast(e.y)};
+          x[k] = q * (ENT ? fma2(f2{fmaxf(l.x, -1e28f), fmaxf(l.y, -1e28f)}, both(b), both(a)) : both(a));
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < N; ++k) x[k] = both(0.f);
+      }
+      v[i].put(x);
+      const int c = at.column(i, lane);
+      if (alike && c >= 0 && c + Unit<T>::VE <= at.n) {
+        __stcs(reinterpret_cast<uint4*>(out + c), v[i].u);
+      } else {
+#pragma unroll
+        for (int k = 0; k < Unit<T>::VE; ++k)
+          if (c + k >= 0 && c + k < at.n) from_f32(out + c + k, k & 1 ? x[k / 2].y : x[k / 2].x);
+      }
+    }
+  }
+  __syncthreads();
+  if (to) from_f32(to, at_id);
 }
 
 // ---------------------------------------------------------------- host
@@ -221,7 +586,7 @@ dt_status vocab_operand(const dt_dtensor* in, const char* what, int tp, bool out
       }
     }
     if (output && tokens > 1 && ld < v.shape[last]) return fail(DT_ERR_UNSUPPORTED, "%s: rows of an output overlap", what);
-    out[(*shards)++] = VocabShard{v.ptr, ld, v.goff[last]};
+    out[(*shards)++] = VocabShard{v.ptr, ld, (int32_t)v.goff[last], (int32_t)v.shape[last], 0, 0};
   }
   return DT_OK;
 }
@@ -244,24 +609,89 @@ dt_status beside(const dt_dtensor* in, const char* what, const Layout& of, int d
   return DT_OK;
 }
 
-dt_status common_checks(const LogProbArgs& p, const Layout& l) {
-  if (!(p.scale > 0.f) || !std::isfinite(p.scale)) return fail(DT_ERR_INVALID_ARG, "scale must be positive and finite");
+dt_status common_checks(const LogProbArgs& p) {
+  if (!(p.scale >= 0x1p-20f && p.scale <= 0x1p20f)) return fail(DT_ERR_INVALID_ARG, "scale must be in [2^-20, 2^20]");
   if (p.given > LP_MAX_GIVEN) return fail(DT_ERR_CAPACITY, "%d ids per token (at most %d)", p.given, LP_MAX_GIVEN);
   if (p.tokens > 0 && p.vocab == 0) return fail(DT_ERR_SHAPE, "logits of an empty vocabulary");
-  (void)l;
   return DT_OK;
 }
 
-template <class K, class P>
-cudaError_t launch_rows(K kernel, const P& p, cudaStream_t s) {
-  const int grid = (int)std::min<int64_t>(p.tokens, (int64_t)device_sm_count() * 8);
-  return launch_early(kernel, dim3(grid), LP_THREADS, 0, s, p);
+// The shards' units, for rows that start on 16-byte boundaries or not.
+int64_t count_units(VocabShard* z, int shards, int64_t tokens, int esize) {
+  int64_t units = 0;
+  const int size = LP_VECS * 32 * 16 / esize;
+  for (int s = 0; s < shards; ++s) {
+    z[s].unit = (int32_t)units;
+    const bool even = reinterpret_cast<uintptr_t>(z[s].ptr) % 16 == 0 && (tokens == 1 || z[s].ld * esize % 16 == 0);
+    units += ((int64_t)z[s].n + (even ? 0 : 16 / esize - 1) + size - 1) / size;
+  }
+  return units;
+}
+
+template <class P>
+cudaError_t launch_log_probs(void (*kernel)(P), const P& p, int threads, size_t smem, cudaStream_t s) {
+  if (smem > 32 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(p.tokens * p.parts));
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = p.parts;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = p.parts > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <class T, int CAP>
+cudaError_t forward(const LogProbArgs& a, const VocabShard* z, cudaStream_t s) {
+  LogProbParams<CAP> p;
+  static_cast<LogProbArgs&>(p) = a;
+  std::copy(z, z + a.shards, p.z);
+  // Few tokens: a cluster for each, as long as all CTAs are resident at once
+  // and every warp has a unit.
+  const int64_t resident = 4 * (int64_t)device_sm_count();
+  p.parts = 1;
+  while (p.parts < LP_MAX_CLUSTER && p.tokens * p.parts * 2 <= resident && p.units >= 2 * p.parts * LP_WARPS) p.parts *= 2;
+  auto smem = [&] {
+    const int64_t step = (int64_t)p.parts * LP_WARPS;
+    return a.top ? (size_t)((p.units + step - 1) / step * LP_WARPS * LP_VECS * 2 * sizeof(uint32_t)) : 0;
+  };
+  while (p.parts < LP_MAX_CLUSTER && smem() > 128 * 1024) p.parts *= 2;
+  int warps = 1;
+  while (warps < LP_WARPS && warps < p.units) warps *= 2;
+#define DT_LP(TOP, ENT) \
+  if ((a.top > 0) == TOP && (a.entropy != nullptr) == ENT) \
+    return launch_log_probs(log_probs_kernel<T, TOP, ENT, CAP>, p, 32 * warps, smem(), s);
+  DT_LP(false, false) DT_LP(false, true) DT_LP(true, false) DT_LP(true, true)
+#undef DT_LP
+  return cudaErrorInvalidValue;
+}
+
+template <class T, int CAP>
+cudaError_t backward(const LogProbArgs& a, const VocabShard* z, const VocabShard* dz, cudaStream_t s) {
+  LogProbParams<CAP> p;
+  static_cast<LogProbArgs&>(p) = a;
+  std::copy(z, z + a.shards, p.z);
+  std::copy(dz, dz + a.shards, p.dz);
+  // parts of at most 8 units a warp, fewer while that leaves CTAs idle
+  p.parts = std::max(1, (p.units + 8 * LP_WARPS - 1) / (8 * LP_WARPS));
+  while (p.tokens * p.parts < 4 * (int64_t)device_sm_count() && p.units >= 2 * p.parts * LP_WARPS) p.parts *= 2;
+  const dim3 grid((unsigned)(p.tokens * p.parts));
+  if ((int64_t)grid.x != p.tokens * p.parts) return cudaErrorInvalidValue;
+  return a.dentropy ? launch_early(log_probs_backward_kernel<T, true, CAP>, grid, LP_THREADS, 0, s, p)
+                    : launch_early(log_probs_backward_kernel<T, false, CAP>, grid, LP_THREADS, 0, s, p);
 }
 
 void sizes(const Layout& l, LogProbArgs* p) {
   p->tokens = 1;
   for (int d = 0; d + 1 < l.ndim; ++d) p->tokens *= l.gshape[d];
-  p->vocab = l.gshape[l.ndim - 1];
+  p->vocab = (int32_t)l.gshape[l.ndim - 1];
 }
 
 template <class T>
@@ -281,10 +711,11 @@ extern "C" dt_status dt_tp_log_probs(const dt_dtensor* logits, const dt_dtensor*
   return no_throw([&]() -> dt_status {
     clear_error();
     LogProbArgs p{};
+    VocabShard z[DT_MAX_SLOTS];
     Layout lz;
     dt_status st;
     if (!logits) return fail(DT_ERR_INVALID_ARG, "logits is NULL");
-    if ((st = vocab_operand(logits, "logits", tp_mesh_dim, false, p.z, &p.shards, &lz)) != DT_OK) return st;
+    if ((st = vocab_operand(logits, "logits", tp_mesh_dim, false, z, &p.shards, &lz)) != DT_OK) return st;
     sizes(lz, &p);
     p.scale = scale;
     p.ignore = ignore_index;
@@ -320,17 +751,22 @@ extern "C" dt_status dt_tp_log_probs(const dt_dtensor* logits, const dt_dtensor*
       p.top_logp = writable<float>(ptr);
       if (k > LP_MAX_TOP) return fail(DT_ERR_CAPACITY, "%lld alternatives (at most %d)", (long long)k, LP_MAX_TOP);
       if (p.tokens > 0 && k > p.vocab) return fail(DT_ERR_SHAPE, "more alternatives than tokens in the vocabulary");
+      if (k > 0 && p.vocab > LP_MAX_TOP_VOCAB)
+        return fail(DT_ERR_CAPACITY, "alternatives from a vocabulary of more than 2^24");
       p.top = (int32_t)k;
       if (k > 0) anchor = ptr;
     }
-    if ((st = common_checks(p, lz)) != DT_OK) return st;
+    if ((st = common_checks(p)) != DT_OK) return st;
     if (p.tokens == 0 || !anchor) return DT_OK;
     if ((st = bind_device_of(anchor)) != DT_OK) return st;
     p.status = device_status_word(d_status);
     if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = lz.dtype == DT_BF16 ? launch_rows(log_probs_kernel<__nv_bfloat16>, p, s)
-                                              : launch_rows(log_probs_kernel<float>, p, s);
+    p.units = (int32_t)count_units(z, p.shards, p.tokens, lz.esize);
+    const bool small = p.shards <= LP_SMALL;
+    const cudaError_t e =
+        lz.dtype == DT_BF16 ? (small ? forward<__nv_bfloat16, LP_SMALL>(p, z, s) : forward<__nv_bfloat16, DT_MAX_SLOTS>(p, z, s))
+                            : (small ? forward<float, LP_SMALL>(p, z, s) : forward<float, DT_MAX_SLOTS>(p, z, s));
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "log_probs launch: %s", cudaGetErrorString(e));
     count_launch();
     return DT_OK;
@@ -345,6 +781,8 @@ extern "C" dt_status dt_tp_log_probs_backward(const dt_dtensor* dlogprobs, const
   return no_throw([&]() -> dt_status {
     clear_error();
     LogProbArgs p{};
+    VocabShard z[DT_MAX_SLOTS], dz[DT_MAX_SLOTS];
+    int32_t dz_shards = 0;
     Layout lz, ld;
     dt_status st;
     if (!logits || !dlogits) return fail(DT_ERR_INVALID_ARG, "logits or dlogits is NULL");
@@ -352,14 +790,14 @@ extern "C" dt_status dt_tp_log_probs_backward(const dt_dtensor* dlogprobs, const
     if ((ids != nullptr) != (dlogprobs != nullptr)) return fail(DT_ERR_INVALID_ARG, "ids and dlogprobs go together");
     if (!dlogprobs && !dentropy) return fail(DT_ERR_INVALID_ARG, "neither dlogprobs nor dentropy");
     if (dentropy && !entropy) return fail(DT_ERR_INVALID_ARG, "dentropy needs entropy");
-    if ((st = vocab_operand(logits, "logits", tp_mesh_dim, false, p.z, &p.shards, &lz)) != DT_OK) return st;
-    if ((st = vocab_operand(dlogits, "dlogits", tp_mesh_dim, true, p.dz, &p.dz_shards, &ld)) != DT_OK) return st;
+    if ((st = vocab_operand(logits, "logits", tp_mesh_dim, false, z, &p.shards, &lz)) != DT_OK) return st;
+    if ((st = vocab_operand(dlogits, "dlogits", tp_mesh_dim, true, dz, &dz_shards, &ld)) != DT_OK) return st;
     if ((st = same_mesh(ld, lz, "dlogits")) != DT_OK) return st;
     bool same = ld.ndim == lz.ndim;
     for (int d = 0; same && d < lz.ndim; ++d) same = ld.gshape[d] == lz.gshape[d];
     if (!same) return fail(DT_ERR_SHAPE, "dlogits must have the shape of logits");
     if (ld.dtype != lz.dtype) return fail(DT_ERR_INVALID_ARG, "dlogits must have the dtype of logits");
-    if (p.shards != p.dz_shards) return fail(DT_ERR_PLACEMENT, "dlogits must be placed as logits");
+    if (p.shards != dz_shards) return fail(DT_ERR_PLACEMENT, "dlogits must be placed as logits");
     sizes(lz, &p);
     p.scale = scale;
     p.ignore = ignore_index;
@@ -381,14 +819,18 @@ extern "C" dt_status dt_tp_log_probs_backward(const dt_dtensor* dlogprobs, const
       if ((st = beside(dentropy, "dentropy", lz, DT_FP32, false, false, &one, &ptr)) != DT_OK) return st;
       p.dentropy = static_cast<const float*>(ptr);
     }
-    if ((st = common_checks(p, lz)) != DT_OK) return st;
+    if ((st = common_checks(p)) != DT_OK) return st;
     if (p.tokens == 0) return DT_OK;
-    if ((st = bind_device_of(p.dz[0].ptr)) != DT_OK) return st;
+    if ((st = bind_device_of(dz[0].ptr)) != DT_OK) return st;
     p.status = device_status_word(d_status);
     if (!p.status) return fail(DT_ERR_CUDA, "no device status word");
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const cudaError_t e = lz.dtype == DT_BF16 ? launch_rows(log_probs_backward_kernel<__nv_bfloat16>, p, s)
-                                              : launch_rows(log_probs_backward_kernel<float>, p, s);
+    p.units = (int32_t)count_units(z, p.shards, p.tokens, lz.esize);
+    const bool small = p.shards <= LP_SMALL;
+    const cudaError_t e = lz.dtype == DT_BF16 ? (small ? backward<__nv_bfloat16, LP_SMALL>(p, z, dz, s)
+                                                       : backward<__nv_bfloat16, DT_MAX_SLOTS>(p, z, dz, s))
+                                              : (small ? backward<float, LP_SMALL>(p, z, dz, s)
+                                                       : backward<float, DT_MAX_SLOTS>(p, z, dz, s));
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "log_probs_backward launch: %s", cudaGetErrorString(e));
     count_launch();
     return DT_OK;
