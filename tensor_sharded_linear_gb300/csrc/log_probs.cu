@@ -108,9 +108,19 @@ struct Vec<__nv_bfloat16> {
     u = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
                    pack_bf16(v[3].x, v[3].y));
   }
-  __device__ __forceinline__ float max() const {
-    const uint32_t m = max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+  // the largest of the even and of the odd elements, and what that is as a number
+  __device__ __forceinline__ uint32_t most() const {
+    return max_nan_bf16x2(max_nan_bf16x2(u.x, u.y), max_nan_bf16x2(u.z, u.w));
+  }
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) { return max_nan_bf16x2(a, b); }
+  static __device__ __forceinline__ float number(uint32_t m) {
     return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
+  // nothing below -1e28 (as bf16); NaN stays
+  __device__ __forceinline__ void lift() {
+    constexpr uint32_t LOW = 0xee01ee01u;
+    u = make_uint4(max_nan_bf16x2(u.x, LOW), max_nan_bf16x2(u.y, LOW), max_nan_bf16x2(u.z, LOW),
+                   max_nan_bf16x2(u.w, LOW));
   }
 };
 template <>
@@ -122,9 +132,15 @@ struct Vec<float> {
   __device__ __forceinline__ void put(const f2 (&v)[2]) {
     u = make_uint4(__float_as_uint(v[0].x), __float_as_uint(v[0].y), __float_as_uint(v[1].x), __float_as_uint(v[1].y));
   }
-  __device__ __forceinline__ float max() const {
+  __device__ __forceinline__ float most() const {
     return max_nan(max_nan(__uint_as_float(u.x), __uint_as_float(u.y)),
                    max_nan(__uint_as_float(u.z), __uint_as_float(u.w)));
+  }
+  static __device__ __forceinline__ float larger(float a, float b) { return max_nan(a, b); }
+  static __device__ __forceinline__ float number(float m) { return m; }
+  __device__ __forceinline__ void lift() {
+    auto up = [](uint32_t w) { return __float_as_uint(max_nan(__uint_as_float(w), -1e28f)); };
+    u = make_uint4(up(u.x), up(u.y), up(u.z), up(u.w));
   }
 };
 __device__ __forceinline__ float element(const Vec<__nv_bfloat16>& v, int i) {
@@ -156,6 +172,13 @@ __device__ __forceinline__ Place<T> place(const S* shards, int count, int unit, 
   p.at = (unit - shards[s].unit) * Unit<T>::SIZE - off;
   p.n = shards[s].n;
   return p;
+}
+// On to unit `unit`, `step` further.
+template <class T, class S>
+__device__ __forceinline__ void move_on(Place<T>& p, const S* shards, int count, int unit, int step, int64_t t) {
+  int s = p.shard;
+  if (s + 1 < count && shards[s + 1].unit <= unit) p = place<T>(shards, count, unit, t, s);
+  else p.at += step * Unit<T>::SIZE;
 }
 __device__ __forceinline__ uint4 load16(const void* p) {
   uint4 v;
@@ -210,50 +233,74 @@ __device__ __forceinline__ int given_id(const LogProbArgs& p, int64_t i, bool re
   return -1;
 }
 
-// A running softmax: the largest logit m, s = sum exp2((z - m) c), and
-// e = sum exp2((z - m) c) (z - m).  m starts at the lowest finite number, so
-// that -inf - m is -inf; differences are kept above -1e28 where they are
-// multiplied, so that 0 times them is 0.
+// A running softmax in powers of two: the largest logit m, s = sum 2^t and
+// e = sum t 2^t over the logits so far, t = c z - fl(c m): one multiply-add a
+// logit, and the product's rounding, common to all of them, drops out at the
+// end (`rounding`).  Where |m| > 1e27, t = (z - m) c, which does not overflow;
+// m starts at the lowest finite number.  Factors stay above -1e28, so that 0
+// times them is 0.
 struct Soft {
   float m = -3.402823466e38f, s = 0.f, e = 0.f;
+  static __device__ __forceinline__ bool usual(float m) { return fabsf(m) <= 1e27f; }
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
-    const float d = fmaxf(m - to, -1e28f), f = exp2_fast(d * c);
-    e = f * fmaf(d, s, e);
+    const float d = usual(m) && usual(to) ? __fsub_rn(__fmul_rn(m, c), __fmul_rn(to, c)) : (m - to) * c;
+    const float down = fmaxf(d, -1e28f), f = exp2_fast(down);
+    e = f * fmaf(down, s, e);
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ void join(Soft o, float c) {
-    const float top = max_nan(m, o.m);
+  __device__ __forceinline__ float rounding(float c) const { return usual(m) ? fmaf(m, c, -__fmul_rn(m, c)) : 0.f; }
+  template <int N>
+  __device__ __forceinline__ void join_lanes(float c) {  // over groups of N lanes
+    float top = m;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, o));
     raise(top, c);
-    o.raise(top, c);
-    s += o.s;
-    e += o.e;
-  }
-  __device__ __forceinline__ Soft shuffled(int o) const {
-    Soft r;
-    r.m = __shfl_xor_sync(0xffffffffu, m, o);
-    r.s = __shfl_xor_sync(0xffffffffu, s, o);
-    r.e = __shfl_xor_sync(0xffffffffu, e, o);
-    return r;
+#pragma unroll
+    for (int o = N / 2; o; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      e += __shfl_xor_sync(0xffffffffu, e, o);
+    }
   }
 };
+// t of two logits under any m
+__device__ __forceinline__ f2 difference(f2 z, float m, float c) {
+  if (Soft::usual(m)) return fma2(z, both(c), both(-__fmul_rn(m, c)));
+  return (z + both(-m)) * both(c);
+}
 
 template <class T, bool ENT>
-__device__ __forceinline__ void soft_unit(Soft& a, const Vec<T> (&v)[LP_VECS], float most, float c) {
+__device__ __forceinline__ void soft_unit(Soft& a, Vec<T> (&v)[LP_VECS], float most, float c) {
   most = max_nan(a.m, most);
   if (!(most == a.m)) a.raise(most, c);
   constexpr int N = Unit<T>::VE / 2;
-  const f2 m2 = both(-a.m), c2 = both(c);
   f2 s[2] = {both(0.f), both(0.f)}, e[2] = {both(0.f), both(0.f)};
+  if (__all_sync(0xffffffffu, Soft::usual(a.m))) {
+    const f2 r2 = both(-__fmul_rn(a.m, c)), c2 = both(c);
 #pragma unroll
-  for (int i = 0; i < LP_VECS; ++i) {
-    f2 z[N];
-    v[i].get(z);
+    for (int i = 0; i < LP_VECS; ++i) {
+      if (ENT) v[i].lift();  // (2^t is 0 there either way)
+      f2 z[N];
+      v[i].get(z);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-      const f2 d = z[k] + m2, t = d * c2, x = f2{exp2_fast(t.x), exp2_fast(t.y)};
-      s[k & 1] = s[k & 1] + x;
-      if (ENT) e[k & 1] = fma2(x, f2{fmaxf(d.x, -1e28f), fmaxf(d.y, -1e28f)}, e[k & 1]);
+      for (int k = 0; k < N; ++k) {
+        const f2 t = fma2(z[k], c2, r2), x = f2{exp2_fast(t.x), exp2_fast(t.y)};
+        s[k & 1] = s[k & 1] + x;
+        if (ENT) e[k & 1] = fma2(x, t, e[k & 1]);
+      }
+    }
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < LP_VECS; ++i) {
+      f2 z[N];
+      v[0].get(z);
+      v[0] = v[1], v[1] = v[2], v[2] = v[3];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        const f2 t = difference(z[k], a.m, c), x = f2{exp2_fast(t.x), exp2_fast(t.y)};
+        s[0] = s[0] + x;
+        if (ENT) e[0] = fma2(x, f2{fmaxf(t.x, -1e28f), fmaxf(t.y, -1e28f)}, e[0]);
+      }
     }
   }
   const f2 s1 = s[0] + s[1], e1 = e[0] + e[1];
@@ -280,23 +327,73 @@ __device__ __forceinline__ void store_cluster(uint32_t a, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-// One cluster of CTAs per token (a cluster of one when there are tokens
-// enough): each warp takes every so many units, the CTAs' sums and candidates
-// meet in the first one's shared memory, which writes the results.
+// How many of the n numbers at x (16-byte aligned) are larger.
+__device__ __forceinline__ int count_larger(const uint64_t* x, int n, uint64_t mine) {
+  int above = 0;
+#pragma unroll 8
+  for (int i = 0; i + 1 < n; i += 2) {
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(x + i);
+    above += (v.x > mine) + (v.y > mine);
+  }
+  return n & 1 ? above + (x[n - 1] > mine) : above;
+}
+
+// The largest so far, in order over a warp's lanes (lane i: the i-th; 0: none).
+struct TopList {
+  uint64_t best = 0, worst = 0;  // worst: the k-th
+  __device__ __forceinline__ void insert(uint64_t n, int k, int lane) {
+    if (n <= worst) return;
+    const int pos = __popc(__ballot_sync(0xffffffffu, best > n));
+    const uint64_t up = __shfl_up_sync(0xffffffffu, best, 1);
+    best = lane < pos ? best : lane == pos ? n : up;
+    worst = __shfl_sync(0xffffffffu, best, k - 1);
+  }
+  // The elements of a vector over the warp whose key is at least `low`; lane
+  // 0's first one is column `col0` of a shard's row of n, token `begin` + col0.
+  template <class T>
+  __device__ __forceinline__ void take(const Vec<T>& x, int col0, int n, int begin, uint32_t low, int k, int lane) {
+    constexpr int VE = Unit<T>::VE;
+    const uint32_t key = order_key(Vec<T>::number(x.most()));
+    const uint64_t at_most = (uint64_t)key << 32 | (0xFFFFFFFFu - (uint32_t)max(begin + col0 + lane * VE, 0));
+    unsigned lanes = __ballot_sync(0xffffffffu, key >= low && at_most > worst);
+    while (lanes) {  // one lane's vector at a time, an element a lane
+      const int from = __ffs(lanes) - 1;
+      lanes &= lanes - 1;
+      Vec<T> y;
+      y.u.x = __shfl_sync(0xffffffffu, x.u.x, from), y.u.y = __shfl_sync(0xffffffffu, x.u.y, from);
+      y.u.z = __shfl_sync(0xffffffffu, x.u.z, from), y.u.w = __shfl_sync(0xffffffffu, x.u.w, from);
+      const int col = col0 + from * VE + lane;
+      const uint32_t mine = order_key(element(y, lane % VE));
+      const uint64_t me = (uint64_t)mine << 32 | (0xFFFFFFFFu - (uint32_t)(begin + col));
+      unsigned in = __ballot_sync(0xffffffffu, lane < VE && col >= 0 && col < n && mine >= low && me > worst);
+      while (in) {
+        insert(__shfl_sync(0xffffffffu, me, __ffs(in) - 1), k, lane);
+        in &= in - 1;
+      }
+    }
+  }
+};
+
+// One cluster of CTAs per token (of one CTA when there are tokens enough): each
+// warp takes every so many units, the CTAs' sums and candidates meet in the
+// first one's shared memory, and that one writes the results.
 //
 // Alternatives.  The pass over the row leaves the largest logit of each block
-// of 512 bytes and of 32 or 64 groups of lanes.  The k-th largest of the groups
-// is at most the k-th largest logit, so every alternative is in a block that
-// reaches it; these (hardly more than k when values differ) are read again, now
-// from L2, and elements that reach it go through a sorted list per warp, then
+// of 1 KB and of 32 or 64 groups of lanes.  The k-th largest of the groups is at
+// most the k-th largest logit, so every alternative is in a block that reaches
+// it; these (hardly more than k when values differ) are read again, now from
+// L2, and elements that reach it go through a sorted list per warp, then
 // through a count of the larger ones.  The order is that of (value, lowest id)
 // as one 64-bit number, so the result does not depend on who came first.
+constexpr int LP_BLOCK_VECS = 2;
+constexpr int LP_UNIT_BLOCKS = LP_VECS / LP_BLOCK_VECS;
+
 template <class T, bool TOP, bool ENT, int CAP>
 __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_constant__ LogProbParams<CAP> p) {
   __shared__ Soft soft[LP_WARPS];
-  __shared__ Soft meet[LP_MAX_CLUSTER];                      // in the first CTA
-  __shared__ uint64_t recv[LP_MAX_CLUSTER * LP_MAX_TOP];     // in the first CTA
-  __shared__ uint64_t cand[LP_WARPS * LP_MAX_TOP];
+  __shared__ Soft meet[LP_MAX_CLUSTER];                                   // in the first CTA
+  __shared__ __align__(16) uint64_t recv[LP_MAX_CLUSTER * LP_MAX_TOP];    // in the first CTA
+  __shared__ __align__(16) uint64_t cand[LP_WARPS * LP_MAX_TOP];
   __shared__ __align__(16) uint32_t group[64];
   __shared__ uint32_t reach;
   __shared__ int listed, found;
@@ -309,102 +406,124 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
   const float c = p.scale * LOG2E;
   const int step = ctas * warps, first = rank * warps + warp;
   if (TOP && threadIdx.x == 0) listed = found = 0;
-  Soft a;
-  int shard = 0, k_unit = 0;
-  Vec<T> v[LP_VECS];
-  Place<T> at;
-  if (first < p.units) {
-    at = place<T>(p.z, p.shards, first, t, shard);
-    load_unit(at, lane, v);
+  // the first CTA's threads stand for the given ids (one CTA of one warp: two each)
+  int id[2] = {-1, -1};
+  float z_id[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (rank == 0 && i < p.given) {
+      id[j] = given_id(p, t * p.given + i, true);
+      if (id[j] >= 0) z_id[j] = logit<T>(p, t, id[j]);
+    }
   }
-  for (int u = first; u < p.units; u += step, ++k_unit) {
-    Vec<T> next[LP_VECS];
-    if (u + step < p.units) {
-      at = place<T>(p.z, p.shards, u + step, t, shard);
-      load_unit(at, lane, next);
-    }
-    float most;
+  Soft a;
+  int rounds = 0;
+  auto work = [&](Vec<T>(&v)[LP_VECS]) {
+    auto most = v[0].most();
+    if (TOP) {
 #pragma unroll
-    for (int i = 0; i < LP_VECS; ++i) {
-      const float b = v[i].max();
-      most = i ? max_nan(most, b) : b;
-      if (TOP) {
-        const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(b));
-        if (lane == 0) block_key[(k_unit * warps + warp) * LP_VECS + i] = key;
+      for (int b = 0; b < LP_UNIT_BLOCKS; ++b) {
+        auto m = v[b * LP_BLOCK_VECS].most();
+#pragma unroll
+        for (int i = 1; i < LP_BLOCK_VECS; ++i) m = Vec<T>::larger(m, v[b * LP_BLOCK_VECS + i].most());
+        most = b ? Vec<T>::larger(most, m) : m;
+        const uint32_t key = __reduce_max_sync(0xffffffffu, order_key(Vec<T>::number(m)));
+        if (lane == 0) block_key[(rounds * warps + warp) * LP_UNIT_BLOCKS + b] = key;
       }
-    }
-    soft_unit<T, ENT>(a, v, most, c);
+      ++rounds;
+    } else {
 #pragma unroll
-    for (int i = 0; i < LP_VECS; ++i) v[i] = next[i];
+      for (int i = 1; i < LP_VECS; ++i) most = Vec<T>::larger(most, v[i].most());
+    }
+    soft_unit<T, ENT>(a, v, Vec<T>::number(most), c);
+  };
+  if (first < p.units) {
+    int s = 0;
+    Place<T> at = place<T>(p.z, p.shards, first, t, s);
+    Vec<T> v[LP_VECS], w[LP_VECS];
+    load_unit(at, lane, v);
+    for (int u = first;; u += 2 * step) {
+      const bool more = u + step < p.units;
+      if (more) {
+        move_on(at, p.z, p.shards, u + step, step, t);
+        load_unit(at, lane, w);
+      }
+      work(v);
+      if (!more) break;
+      const bool again = u + 2 * step < p.units;
+      if (again) {
+        move_on(at, p.z, p.shards, u + 2 * step, step, t);
+        load_unit(at, lane, v);
+      }
+      work(w);
+      if (!again) break;
+    }
   }
   const int per_group = warps >= 2 ? warps / 2 : 1, groups = 32 * warps / per_group;
   if (TOP) {
-    // (a lane without any element: below every key)
+    // (no element: below every key; m as it started: at most -inf is known to be there)
     uint32_t g = first < p.units ? order_key(a.m == Soft().m ? -INFINITY : a.m) : 0;
     for (int o = 1; o < per_group; o <<= 1) g = max(g, __shfl_xor_sync(0xffffffffu, g, o));
     if (lane % per_group == 0) group[(warp * 32 + lane) / per_group] = g;
   }
-#pragma unroll
-  for (int o = 16; o; o >>= 1) a.join(a.shuffled(o), c);
+  a.join_lanes<32>(c);
   if (lane == 0) soft[warp] = a;
   __syncthreads();
-  a = soft[0];
-  for (int w = 1; w < warps; ++w) a.join(soft[w], c);
+  a = lane % LP_WARPS < warps ? soft[lane % LP_WARPS] : Soft();
+  a.join_lanes<LP_WARPS>(c);
   if (TOP) {
     if ((int)threadIdx.x < groups) {
       const uint32_t mine = group[threadIdx.x];
       int above = 0;
-      for (int i = 0; i < groups; ++i) {
-        const uint32_t o = group[i];
-        above += o > mine || (o == mine && i < (int)threadIdx.x);
+#pragma unroll 8
+      for (int i = 0; i < groups; i += 4) {
+        const uint4 o = *reinterpret_cast<const uint4*>(group + i);
+        const int me = threadIdx.x - i;
+        above += (o.x > mine || (o.x == mine && 0 < me)) + (o.y > mine || (o.y == mine && 1 < me)) +
+                 (o.z > mine || (o.z == mine && 2 < me)) + (o.w > mine || (o.w == mine && 3 < me));
       }
       if (above == p.top - 1) reach = mine;
     }
     __syncthreads();
     const uint32_t low = reach;
-    const int my_units = first - warp < p.units ? (p.units - (first - warp) + step - 1) / step : 0;  // rounds of the CTA
-    const int blocks = my_units * warps * LP_VECS;
+    const int row = warps * LP_UNIT_BLOCKS;  // blocks of a round of the CTA
+    const int blocks = rank * warps < p.units ? (p.units - rank * warps + step - 1) / step * row : 0;
     uint32_t* list = block_key + blocks;
-    for (int i = threadIdx.x; i < blocks; i += blockDim.x) {
-      const int u = rank * warps + i / LP_VECS % warps + i / (LP_VECS * warps) * step;
-      if (u < p.units && block_key[i] >= low) list[atomicAdd(&listed, 1)] = i;
-    }
+    auto unit_of = [&](int i) { return rank * warps + i % row / LP_UNIT_BLOCKS + i / row * step; };
+    for (int i = threadIdx.x; i < blocks; i += blockDim.x)
+      if (unit_of(i) < p.units && block_key[i] >= low) list[atomicAdd(&listed, 1)] = i;
     __syncthreads();
-    uint64_t best = 0, worst = 0;  // lane i: the i-th best so far; the k-th
-    for (int l = warp; l < listed; l += warps) {
-      const int i = (int)list[l], u = rank * warps + i / LP_VECS % warps + i / (LP_VECS * warps) * step;
-      int s = 0;
-      const Place<T> q = place<T>(p.z, p.shards, u, t, s);
-      const Vec<T> x = load_vec(q, i % LP_VECS, lane);
-      const int col = q.column(i % LP_VECS, lane);
-#pragma unroll 1
-      for (int e = 0; e < Unit<T>::VE; ++e) {
-        const uint32_t key = order_key(element(x, e));
-        const uint64_t me = (uint64_t)key << 32 | (0xFFFFFFFFu - (uint32_t)(p.z[q.shard].begin + col + e));
-        unsigned in = __ballot_sync(0xffffffffu, col + e >= 0 && col + e < q.n && key >= low && me > worst);
-        while (in) {
-          const uint64_t n = __shfl_sync(0xffffffffu, me, __ffs(in) - 1);
-          in &= in - 1;
-          if (n <= worst) continue;
-          const int pos = __popc(__ballot_sync(0xffffffffu, best > n));
-          const uint64_t up = __shfl_up_sync(0xffffffffu, best, 1);
-          best = lane < pos ? best : lane == pos ? n : up;
-          worst = __shfl_sync(0xffffffffu, best, p.top - 1);
-        }
+    TopList best;
+    for (int l = warp; l < listed; l += 2 * warps) {  // two blocks' loads at once
+      Vec<T> x[2][LP_BLOCK_VECS];
+      int col[2], n[2], begin[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (l + h * warps >= listed) break;
+        const int i = (int)list[l + h * warps];
+        int s = 0;
+        const Place<T> q = place<T>(p.z, p.shards, unit_of(i), t, s);
+        const int vec = i % LP_UNIT_BLOCKS * LP_BLOCK_VECS;
+#pragma unroll
+        for (int k = 0; k < LP_BLOCK_VECS; ++k) x[h][k] = load_vec(q, vec + k, lane);
+        col[h] = q.column(vec, 0), n[h] = q.n, begin[h] = p.z[q.shard].begin;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (l + h * warps >= listed) break;
+#pragma unroll
+        for (int k = 0; k < LP_BLOCK_VECS; ++k)
+          best.take(x[h][k], col[h] + k * Unit<T>::BLOCK, n[h], begin[h], low, p.top, lane);
       }
     }
-    const unsigned have = __ballot_sync(0xffffffffu, lane < p.top && best != 0);
+    const unsigned have = __ballot_sync(0xffffffffu, lane < p.top && best.best != 0);
     int base = 0;
     if (lane == 0) base = atomicAdd(&found, __popc(have));
     base = __shfl_sync(0xffffffffu, base, 0);
-    if (have >> lane & 1) cand[base + __popc(have & ((1u << lane) - 1))] = best;
+    if (have >> lane & 1) cand[base + __popc(have & ((1u << lane) - 1))] = best.best;
     __syncthreads();
   }
-  auto count_larger = [](const uint64_t* x, int n, uint64_t mine) {
-    int above = 0;
-    for (int i = 0; i < n; ++i) above += x[i] > mine;
-    return above;
-  };
   int total = TOP ? found : 0;
   const uint64_t* from = cand;
   if (ctas > 1) {
@@ -425,21 +544,22 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
     cluster_arrive();
     cluster_wait();
     if (rank != 0) return;
-    a = meet[0];
-    for (int r = 1; r < ctas; ++r) a.join(meet[r], c);
+    a = lane % LP_MAX_CLUSTER < ctas ? meet[lane % LP_MAX_CLUSTER] : Soft();
+    a.join_lanes<LP_MAX_CLUSTER>(c);
     from = recv;
     total = ctas * p.top;
   }
   const bool none = a.s == 0.f;  // no token is possible
-  const float ln = logf(a.s);
+  const float ln_s = logf(a.s), ln = fmaf(-0.693147180559945f, a.rounding(c), ln_s);
   auto logp = [&](float z) { return none ? -INFINITY : (z - a.m) * p.scale - ln; };
   if (threadIdx.x == 0) {
     if (p.lse) p.lse[t] = none ? -INFINITY : fmaf(a.m, p.scale, ln);
-    if (ENT) p.entropy[t] = none ? 0.f : ln - p.scale * (a.e / a.s);
+    if (ENT) p.entropy[t] = none ? 0.f : fmaf(-0.693147180559945f, a.e / a.s, ln_s);
   }
-  for (int i = threadIdx.x; i < p.given; i += blockDim.x) {
-    const int id = given_id(p, t * p.given + i, true);
-    p.logp[t * p.given + i] = id >= 0 ? logp(logit<T>(p, t, id)) : 0.f;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int i = threadIdx.x + j * blockDim.x;
+    if (i < p.given) p.logp[t * p.given + i] = id[j] >= 0 ? logp(z_id[j]) : 0.f;
   }
   if (TOP) {
     for (int i = threadIdx.x; i < total; i += blockDim.x) {
@@ -660,7 +780,7 @@ cudaError_t forward(const LogProbArgs& a, const VocabShard* z, cudaStream_t s) {
   while (p.parts < LP_MAX_CLUSTER && p.tokens * p.parts * 2 <= resident && p.units >= 2 * p.parts * LP_WARPS) p.parts *= 2;
   auto smem = [&] {
     const int64_t step = (int64_t)p.parts * LP_WARPS;
-    return a.top ? (size_t)((p.units + step - 1) / step * LP_WARPS * LP_VECS * 2 * sizeof(uint32_t)) : 0;
+    return a.top ? (size_t)((p.units + step - 1) / step * LP_WARPS * LP_UNIT_BLOCKS * 2 * sizeof(uint32_t)) : 0;
   };
   while (p.parts < LP_MAX_CLUSTER && smem() > 128 * 1024) p.parts *= 2;
   int warps = 1;
