@@ -33,7 +33,9 @@
 namespace dt {
 namespace {
 
-constexpr int BN_MAX_BLOCKS = 320;  // CTAs of a backward launch, and rows of each of its sums in the workspace
+// CTAs of a backward launch at most, and so rows of each of its sums in the
+// workspace: few channels need more CTAs to fill an SM.
+inline int max_backward_blocks(int64_t n) { return n > 2048 ? 320 : n > 1024 ? 640 : 1280; }
 
 struct BlockArgs {
   RowTable x, r, h, y;    // forward: h and y are written; backward: they are dh and dy
@@ -267,6 +269,446 @@ __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const _
   }
 }
 
+// ---------------------------------------------------------------- channels in vectors of 8
+
+// Rows of a multiple of 8 channels on 16-byte boundaries: a CTA per row, a
+// thread holds VPT vectors of 8 channels of it, `blockDim.x` vectors apart.
+constexpr int row_threads(int vpt) { return vpt == 1 ? 1024 : 512; }
+
+// The sum over a CTA, in an order fixed by its size; the same in every thread.
+// `buf` [2][K][32] is zero behind the CTA's warps.
+template <int K>
+__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[K][32], int& turn) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    if (lane == 0 && warps > 1) buf[turn][k][warp] = v[k];
+  }
+  if (warps == 1) return;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    v[k] = 0.f;
+    for (int w = 0; w < warps; w += 4) {
+      const float4 x = *reinterpret_cast<const float4*>(&buf[turn][k][w]);
+      v[k] += (x.x + x.y) + (x.z + x.w);
+    }
+  }
+  turn ^= 1;
+}
+template <int K>
+__device__ __forceinline__ void clear_sums(float (*buf)[K][32]) {
+  for (int i = threadIdx.x; i < 2 * K * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+  __syncthreads();
+}
+
+// 8 channels of a vector over channels (bf16 or fp32, 16-byte aligned).
+__device__ __forceinline__ void load_w8(const void* w, int dtype, int64_t c, f2 (&v)[4]) {
+  if (dtype == DT_BF16) {
+    Raw8<__nv_bfloat16> x;
+    x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
+    x.get2(v);
+  } else {
+    Raw8<float> x;
+    x.load_keep(static_cast<const float*>(w) + c);
+    x.get2(v);
+  }
+}
+
+// Dropout of 8 channels from channel c of token t: bit i keeps channel c + i.
+struct Dropout {
+  uint32_t key[4], below;
+  bool on;
+  __device__ __forceinline__ explicit Dropout(const BlockArgs& p) : below(p.drop_below), on(p.rng != nullptr) {
+    for (int i = 0; i < 4; ++i) key[i] = on ? (uint32_t)load_plain(p.rng + i) : 0;
+  }
+  __device__ __forceinline__ uint32_t bits(int64_t t, int n, int c) const {
+    const uint64_t i = ((uint64_t)t * n + c) >> 2;
+    const uint4 a = philox(i, key[2], key[3], key[0], key[1]), b = philox(i + 1, key[2], key[3], key[0], key[1]);
+    return (a.x >= below) | (a.y >= below) << 1 | (a.z >= below) << 2 | (a.w >= below) << 3 | (b.x >= below) << 4 |
+           (b.y >= below) << 5 | (b.z >= below) << 6 | (b.w >= below) << 7;
+  }
+};
+__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i, float scale) {  // pair i of the 8
+  return f2{bits >> (2 * i) & 1 ? v.x * scale : 0.f, bits >> (2 * i + 1) & 1 ? v.y * scale : 0.f};
+}
+
+template <class T>
+struct Pieces {
+  static constexpr int N = sizeof(T) / 2;  // 16-byte pieces of 8 elements
+};
+// A row's vector into a stage of the ring (`to`: this thread's first piece, `step` apart).
+template <class T>
+__device__ __forceinline__ void fetch8(uint4* to, const char* row, int c, int step) {
+  const T* from = reinterpret_cast<const T*>(row) + c;
+#pragma unroll
+  for (int i = 0; i < Pieces<T>::N; ++i) copy16_async(to + i * step, reinterpret_cast<const uint4*>(from) + i);
+}
+
+// RING: x (one part) and the residual come through a ring of asynchronous
+// copies of STAGES rows, each thread its own pieces, so that the next rows are
+// on their way without taking registers or barriers.  Else (parts to be added,
+// rows too large for a ring) plain loads, all of a row at once.
+constexpr int BN_STAGES = 3;
+
+template <class XT, class RT, int VPT, bool RING, class P>
+__global__ void __launch_bounds__(row_threads(VPT), VPT == 2 ? 2 : 1) block_norm_row_kernel(const __grid_constant__ P p) {
+  __shared__ __align__(16) float buf[2][1][32];
+  extern __shared__ uint4 ring[];
+  wait_for_previous_kernel();
+  clear_sums(buf);
+  int turn = 0;
+  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
+  const float inv_n = 1.f / (float)n;
+  const Dropout drop(p);
+  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, PIECES = VPT * (PX + PR);
+  const bool res = p.r.count > 0, out_h = p.h.count > 0, out_y = p.y.count > 0;
+  int ax = 0, ar = 0, ah = 0, ay = 0;
+  auto channel = [&](int v) { return (v * nt + tid) * 8; };
+  uint4* const mine = ring + tid;
+  int put = 0, get = 0;
+  auto fetch = [&](int64_t t) {
+    if (t < p.tokens) {
+      const char* x = row_at(p.blocks[row_block(p.blocks, p.x, t, ax)], t, sizeof(XT));
+      const char* r = res ? row_at(p.blocks[row_block(p.blocks, p.r, t, ar)], t, sizeof(RT)) : nullptr;
+      uint4* to = mine + put * PIECES * nt;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = channel(v);
+        if (c >= n) break;
+        fetch8<XT>(to + v * PX * nt, x, c, nt);
+        if (res) fetch8<RT>(to + (VPT * PX + v * PR) * nt, r, c, nt);
+      }
+    }
+    copies_commit();
+    if (++put == BN_STAGES) put = 0;
+  };
+  if (RING)
+    for (int i = 0; i + 1 < BN_STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x);
+  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
+    f2 u[VPT][4], h[VPT][4];
+    Raw8<RT> r[VPT];
+    if constexpr (RING) {
+      fetch(t + (int64_t)(BN_STAGES - 1) * gridDim.x);
+      copies_wait<BN_STAGES - 1>();
+      const uint4* from = mine + get * PIECES * nt;
+      if (++get == BN_STAGES) get = 0;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        Raw8<XT> x;
+        x.zero(), r[v].zero();
+        if (channel(v) < n) {
+          x.set(from + v * PX * nt, nt);
+          if (res) r[v].set(from + (VPT * PX + v * PR) * nt, nt);
+        }
+        x.get2(u[v]);
+      }
+    } else {
+      const int bx = row_block(p.blocks, p.x, t, ax);
+      const char* rr = res ? row_at(p.blocks[row_block(p.blocks, p.r, t, ar)], t, sizeof(RT)) : nullptr;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        r[v].zero();
+        if (res && channel(v) < n) r[v].load(reinterpret_cast<const RT*>(rr) + channel(v));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) u[v][i] = both(0.f);
+      }
+#pragma unroll 4
+      for (int k = 0; k < p.x.parts; ++k) {
+        const XT* x = reinterpret_cast<const XT*>(row_at(p.blocks[bx + k * p.x.count], t, sizeof(XT)));
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          Raw8<XT> w;
+          w.zero();
+          if (channel(v) < n) w.load(x + channel(v));
+          f2 s[4];
+          w.get2(s);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] + s[i];
+        }
+      }
+    }
+    float sum[1];
+    auto total = [&](const f2(&a)[VPT][4]) {
+      f2 s = both(0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(a[v][i], a[v][i], s);
+      sum[0] = s.x + s.y;
+      row_sum(sum, buf, turn);
+      return rsqrtf(sum[0] * inv_n + p.eps);
+    };
+    const float rx = p.post ? total(u) : 1.f;
+    const int64_t seg = p.gate ? (uint32_t)t / (uint32_t)p.gate_per : 0;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = channel(v);
+      if (c < n) {
+        f2 w[4];
+        if (p.post) {
+          load_w8(p.post, p.post_dtype, c, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] * both(rx) * w[i];
+        }
+        if (p.gate) {
+          load_w8(p.gate, p.gate_dtype, seg * n + c, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] * w[i];
+        }
+        if (drop.on) {
+          const uint32_t bits = drop.bits(t, n, c);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) u[v][i] = kept(u[v][i], bits, i, p.drop_scale);
+        }
+      }
+      r[v].get2(h[v]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) h[v][i] = res ? fma2(both(p.scale), h[v][i], u[v][i]) : u[v][i];
+    }
+    if (out_h) {
+      RT* o = reinterpret_cast<RT*>(row_at(p.blocks[row_block(p.blocks, p.h, t, ah)], t, sizeof(RT)));
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (channel(v) < n) store8(o + channel(v), h[v]);
+    }
+    if (out_y) {
+      const float rh = total(h);
+      XT* o = reinterpret_cast<XT*>(row_at(p.blocks[row_block(p.blocks, p.y, t, ay)], t, sizeof(XT)));
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = channel(v);
+        if (c >= n) break;
+        f2 w[4];
+        load_w8(p.pre, p.pre_dtype, c, w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = h[v][i] * both(rh) * w[i];
+        store8(o + c, w);
+      }
+    }
+  }
+  if (RING) copies_wait<0>();
+}
+
+// Gradients.  A CTA takes a run of consecutive tokens and keeps the sums over
+// them in registers; x, the residual, dh and dy come through the ring and are
+// read from it twice, before and after the means, instead of being held.  The
+// means' sums are taken at once: with a = gate post keep x / (1 - p), h =
+// scale residual + r(x) a and g = dh + r(h) z - k h, the sum of a g is that of
+// a dh, a z and a h, so one meeting of the CTA does after that of r(x).
+constexpr int bwd_stages(int pieces) { return pieces > 8 ? 2 : 3; }
+
+template <class XT, class RT, int VPT, class P>
+__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 2 : 1)
+    block_norm_row_backward_kernel(const __grid_constant__ P p) {
+  __shared__ __align__(16) float buf[2][5][32];
+  extern __shared__ uint4 ring[];
+  wait_for_previous_kernel();
+  clear_sums(buf);
+  int turn = 0;
+  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
+  const float inv_n = 1.f / (float)n;
+  const Dropout drop(p);
+  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, PIECES = 2 * VPT * (PX + PR);
+  constexpr int STAGES = bwd_stages(PIECES / VPT);
+  const bool res = p.r.count > 0, has_h = p.h.count > 0, has_y = p.y.count > 0;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
+  int ax = 0, ar = 0, ah = 0, ay = 0, adx = 0, adr = 0;
+  auto channel = [&](int v) { return (v * nt + tid) * 8; };
+  uint4* const mine = ring + tid;
+  int put = 0, get = 0;
+  auto fetch = [&](int64_t t) {
+    if (t < t1) {
+      auto row = [&](const RowTable& r, int& a, int es) {
+        return r.count ? row_at(p.blocks[row_block(p.blocks, r, t, a)], t, es) : nullptr;
+      };
+      const char *x = row(p.x, ax, sizeof(XT)), *r = row(p.r, ar, sizeof(RT)), *h = row(p.h, ah, sizeof(RT)),
+                 *y = row(p.y, ay, sizeof(XT));
+      uint4* to = mine + put * PIECES * nt;
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        const int c = channel(v);
+        if (c >= n) break;
+        fetch8<XT>(to + v * PX * nt, x, c, nt);
+        if (has_y) fetch8<XT>(to + (VPT + v) * PX * nt, y, c, nt);
+        if (res) fetch8<RT>(to + (2 * VPT * PX + v * PR) * nt, r, c, nt);
+        if (has_h) fetch8<RT>(to + (2 * VPT * PX + (VPT + v) * PR) * nt, h, c, nt);
+      }
+    }
+    copies_commit();
+    if (++put == STAGES) put = 0;
+  };
+  for (int i = 0; i + 1 < STAGES; ++i) fetch(t0 + i);
+  f2 s_pre[VPT][4], s_post[VPT][4], s_gate[VPT][4];
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_pre[v][i] = s_post[v][i] = s_gate[v][i] = both(0.f);
+  auto write_sums = [&](float* to, const f2(&s)[VPT][4]) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      if (channel(v) < n) {
+        float4* o = reinterpret_cast<float4*>(to + channel(v));
+        o[0] = make_float4(s[v][0].x, s[v][0].y, s[v][1].x, s[v][1].y);
+        o[1] = make_float4(s[v][2].x, s[v][2].y, s[v][3].x, s[v][3].y);
+      }
+  };
+  int64_t seg = p.gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0, seg_end = (seg + 1) * p.gate_per;
+  for (int64_t t = t0; t < t1; ++t) {
+    fetch(t + STAGES - 1);
+    copies_wait<STAGES - 1>();
+    const uint4* from = mine + get * PIECES * nt;
+    if (++get == STAGES) get = 0;
+    if (t == seg_end) {
+      ++seg;
+      seg_end += p.gate_per;
+    }
+    auto load_x = [&](int v, f2(&x)[4]) {
+      Raw8<XT> w;
+      w.set(from + v * PX * nt, nt);
+      w.get2(x);
+    };
+    float rx = 1.f, rh = 1.f, kh = 0.f, kx = 0.f;
+    if (p.post) {
+      f2 s = both(0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        if (channel(v) >= n) break;
+        f2 x[4];
+        load_x(v, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(x[i], x[i], s);
+      }
+      float sum[5] = {s.x + s.y, 0.f, 0.f, 0.f, 0.f};
+      row_sum(sum, buf, turn);
+      rx = rsqrtf(sum[0] * inv_n + p.eps);
+    }
+    uint32_t bits[VPT];
+    // a vector's x, a, h, z and dh
+    auto values = [&](int v, f2(&x)[4], f2(&a)[4], f2(&h)[4], f2(&z)[4], f2(&dy)[4], f2(&dh)[4], f2(&post)[4],
+                      f2(&gate)[4]) {
+      const int c = channel(v);
+      load_x(v, x);
+      if (p.post) load_w8(p.post, p.post_dtype, c, post);
+      if (p.gate) load_w8(p.gate, p.gate_dtype, seg * n + c, gate);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = x[i];
+        if (p.post) a[i] = a[i] * post[i];
+        if (p.gate) a[i] = a[i] * gate[i];
+        if (drop.on) a[i] = kept(a[i], bits[v], i, p.drop_scale);
+      }
+      if (res) {
+        Raw8<RT> w;
+        w.set(from + (2 * VPT * PX + v * PR) * nt, nt);
+        w.get2(h);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 f = a[i] * both(rx);
+        h[i] = res ? fma2(both(p.scale), h[i], f) : f;
+        dh[i] = dy[i] = z[i] = both(0.f);
+      }
+      if (has_h) {
+        Raw8<RT> w;
+        w.set(from + (2 * VPT * PX + (VPT + v) * PR) * nt, nt);
+        w.get2(dh);
+      }
+      if (has_y) {
+        Raw8<XT> w;
+        w.set(from + (VPT + v) * PX * nt, nt);
+        w.get2(dy);
+        load_w8(p.pre, p.pre_dtype, c, z);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = z[i] * dy[i];
+      }
+    };
+    f2 q[5] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (channel(v) >= n) break;
+      if (drop.on) bits[v] = drop.bits(t, n, channel(v));
+      if (!has_y && !p.post) continue;
+      f2 x[4], a[4], h[4], z[4], dy[4], dh[4], post[4], gate[4];
+      values(v, x, a, h, z, dy, dh, post, gate);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        q[0] = fma2(h[i], h[i], q[0]);
+        q[1] = fma2(h[i], z[i], q[1]);
+        q[2] = fma2(a[i], dh[i], q[2]);
+        q[3] = fma2(a[i], z[i], q[3]);
+        q[4] = fma2(a[i], h[i], q[4]);
+      }
+    }
+    if (has_y || p.post) {
+      float sum[5];
+#pragma unroll
+      for (int i = 0; i < 5; ++i) sum[i] = q[i].x + q[i].y;
+      row_sum(sum, buf, turn);
+      if (has_y) {
+        rh = rsqrtf(sum[0] * inv_n + p.eps);
+        kh = rh * rh * rh * (sum[1] * inv_n);
+      }
+      kx = p.post ? rx * rx * rx * ((sum[2] + rh * sum[3] - kh * sum[4]) * inv_n) : 0.f;
+    }
+    char* dx = p.dx.count ? row_at(p.blocks[row_block(p.blocks, p.dx, t, adx)], t, sizeof(XT)) : nullptr;
+    char* dr = p.dr.count ? row_at(p.blocks[row_block(p.blocks, p.dr, t, adr)], t, sizeof(RT)) : nullptr;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = channel(v);
+      if (c >= n) break;
+      f2 x[4], a[4], h[4], z[4], dy[4], dh[4], post[4], gate[4];
+      values(v, x, a, h, z, dy, dh, post, gate);
+      f2 o[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f2 g = dh[i];
+        if (has_y) {
+          g = fma2(z[i], both(rh), fma2(h[i], both(-kh), g));
+          s_pre[v][i] = fma2(dy[i], h[i] * both(rh), s_pre[v][i]);
+        }
+        dh[i] = g * both(p.scale);
+        const f2 e = drop.on ? kept(g, bits[v], i, p.drop_scale) : g;
+        f2 xr = p.post ? x[i] * both(rx) : x[i];
+        if (drop.on) xr = kept(xr, bits[v], i, 1.f);  // (what is dropped may be NaN)
+        f2 w = e;
+        if (p.gate) {
+          a[i] = e * (p.post ? xr * post[i] : xr);
+          s_gate[v][i] = s_gate[v][i] + a[i];
+          w = e * gate[i];
+        }
+        if (p.post) {
+          s_post[v][i] = fma2(w, xr, s_post[v][i]);
+          o[i] = fma2(w * post[i], both(rx), x[i] * both(-kx));
+        } else {
+          o[i] = w;
+        }
+      }
+      if (dr) store8(reinterpret_cast<RT*>(dr) + c, dh);
+      if (dx) store8(reinterpret_cast<XT*>(dx) + c, o);
+      if (p.gate && p.gate_per == 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          store_any(p.dgate, p.dgate_dtype, t * n + c + 2 * i, a[i].x);
+          store_any(p.dgate, p.dgate_dtype, t * n + c + 2 * i + 1, a[i].y);
+        }
+      }
+    }
+    if (p.gate && p.gate_per != 1 && (t + 1 == t1 || t + 1 == seg_end)) {
+      write_sums(p.part_gate + ((int64_t)blockIdx.x + seg) * n, s_gate);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s_gate[v][i] = both(0.f);
+    }
+  }
+  if (p.pre) write_sums(p.part_pre + (int64_t)blockIdx.x * n, s_pre);
+  if (p.post) write_sums(p.part_post + (int64_t)blockIdx.x * n, s_post);
+  copies_wait<0>();
+}
+
 // ---------------------------------------------------------------- host
 
 struct BlockCall {
@@ -294,18 +736,91 @@ dt_status channel_vector(const dt_dtensor* w, const char* what, const Layout& of
   return DT_OK;
 }
 
-int block_backward_grid(int64_t tokens) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(tokens, std::min(2 * device_sm_count(), BN_MAX_BLOCKS)));
-}
-
 // Rows of the gate's sums in the workspace beyond one per CTA.
 int64_t gate_part_rows(int64_t tokens, int64_t gate_rows) { return gate_rows == tokens ? 0 : gate_rows; }
 
+// How a launch covers its rows.
+struct Shape {
+  int threads = 0, vpt = 0, grid = 0;  // vpt 0: the kernels for any size
+  bool ring = false;
+  size_t smem = 0;
+};
+
+int round_up(int64_t a, int b) { return (int)((a + b - 1) / b * b); }
+
+Shape forward_shape(const BlockArgs& p, bool vec, bool small) {
+  Shape s;
+  const int sms = device_sm_count();
+  const int64_t vectors = p.n / 8;
+  if (!vec || vectors > 4 * 512) {
+    s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * 8);
+    return s;
+  }
+  // a vector a thread where there are few tokens (the shortest way through a
+  // row) or few channels; else two, four for the widest
+  s.vpt = vectors <= 256 || (p.tokens <= sms && vectors <= 1024) ? 1 : vectors <= 1024 ? 2 : 4;
+  s.threads = round_up((vectors + s.vpt - 1) / s.vpt, 32);
+  const size_t stage = (size_t)s.threads * s.vpt * 8 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype));
+  s.ring = small && p.x.parts == 1 && stage * BN_STAGES <= 200 * 1024;
+  s.smem = s.ring ? stage * BN_STAGES : 0;
+  int ctas = std::max(1, std::min(32, 1024 / s.threads));
+  if (s.ring) ctas = std::max(1, std::min<int>(ctas, (int)(220 * 1024 / (s.smem + 1280))));
+  s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * ctas);
+  return s;
+}
+
+Shape backward_shape(const BlockArgs& p, bool vec, bool small) {
+  Shape s;
+  const int sms = device_sm_count();
+  const int64_t vectors = p.n / 8;
+  int64_t most = 2 * sms;
+  const int pieces = 2 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype)) / 2;  // 16-byte pieces of a vector
+  if (vec && small && p.x.parts == 1 && vectors <= 1024) {
+    s.vpt = vectors <= 256 ? 1 : 2;
+    s.threads = round_up((vectors + s.vpt - 1) / s.vpt, 32);
+    s.smem = (size_t)s.threads * s.vpt * pieces * 16 * bwd_stages(pieces);
+    s.ring = true;
+    if (s.smem > 220 * 1024) s = Shape();
+    else most = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(512 / s.threads, 220 * 1024 / (s.smem + 2048)), 8)) * sms;
+  }
+  // four tokens a CTA at least, for its sums are written and read again
+  most = std::min<int64_t>(most, std::max<int64_t>(sms, (p.tokens + 3) / 4));
+  s.grid = (int)std::max<int64_t>(1, std::min<int64_t>({p.tokens, most, max_backward_blocks(p.n)}));
+  return s;
+}
+
+template <class K, class P>
+cudaError_t launch_rows(K kernel, const P& p, const Shape& s, cudaStream_t stream) {
+  if (s.smem > 40 * 1024)
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem)) return e;
+  return launch_early(kernel, dim3(s.grid), s.threads, s.smem, stream, p);
+}
+
+template <class XT, class RT, class P>
+cudaError_t launch_typed(const P& p, bool bwd, const Shape& s, cudaStream_t stream) {
+  constexpr bool SMALL = P::kCap == BlockSmall::kCap;
+  if constexpr (SMALL) {
+    if (bwd)
+      return s.vpt == 1 ? launch_rows(block_norm_row_backward_kernel<XT, RT, 1, P>, p, s, stream)
+                        : launch_rows(block_norm_row_backward_kernel<XT, RT, 2, P>, p, s, stream);
+    if (s.ring)
+      return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, true, P>, p, s, stream)
+             : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, true, P>, p, s, stream)
+                          : launch_rows(block_norm_row_kernel<XT, RT, 4, true, P>, p, s, stream);
+  }
+  return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, false, P>, p, s, stream)
+         : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, false, P>, p, s, stream)
+                      : launch_rows(block_norm_row_kernel<XT, RT, 4, false, P>, p, s, stream);
+}
+
 template <class P>
-cudaError_t launch_block(const P& p, bool bwd, cudaStream_t s) {
-  const int grid = bwd ? p.grid : (int)std::min<int64_t>(p.tokens, (int64_t)device_sm_count() * 8);
-  return bwd ? launch_early(block_norm_any_kernel<P, true>, dim3(grid), BN_ANY_THREADS, 0, s, p)
-             : launch_early(block_norm_any_kernel<P, false>, dim3(grid), BN_ANY_THREADS, 0, s, p);
+cudaError_t launch_block(const P& p, bool bwd, const Shape& s, cudaStream_t stream) {
+  if (!s.vpt)
+    return bwd ? launch_early(block_norm_any_kernel<P, true>, dim3(s.grid), BN_ANY_THREADS, 0, stream, p)
+               : launch_early(block_norm_any_kernel<P, false>, dim3(s.grid), BN_ANY_THREADS, 0, stream, p);
+  if (p.x.dtype == DT_FP32) return launch_typed<float, float>(p, bwd, s, stream);
+  if (p.h.dtype == DT_FP32) return launch_typed<__nv_bfloat16, float>(p, bwd, s, stream);
+  return launch_typed<__nv_bfloat16, __nv_bfloat16>(p, bwd, s, stream);
 }
 
 dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, int32_t* d_status, cudaStream_t stream) {
@@ -347,7 +862,6 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   auto rows = [&](const dt_dtensor* in, const char* what, bool output, bool of_stream, RowTable* t) {
     if (!in) {
       *t = RowTable{};
-      t->dtype = (int16_t)(of_stream && stream_dtype >= 0 ? stream_dtype : X.dtype);
       return DT_OK;
     }
     RowOperand o;
@@ -373,6 +887,9 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
     if ((st = rows(A.dx, "dx", true, false, &p.dx)) != DT_OK) return st;
     if ((st = rows(A.dresidual, "dresidual", true, true, &p.dr)) != DT_OK) return st;
   }
+  // what is not there has the type of what is like it
+  for (RowTable* t : {&p.r, &p.h, &p.dr}) t->dtype = (int16_t)(stream_dtype < 0 ? X.dtype : stream_dtype);
+  for (RowTable* t : {&p.y, &p.dx}) t->dtype = (int16_t)X.dtype;
   p.tokens = X.tokens;
   p.n = (int32_t)X.n;
   p.gate_rows = 1;
@@ -421,7 +938,11 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   if (!anchor && p.dgate && X.n > 0 && p.tokens > 0) anchor = p.dgate;
   if (X.n == 0 || !anchor) return DT_OK;
   if ((st = bind_device_of(anchor)) != DT_OK) return st;
-  p.grid = block_backward_grid(p.tokens);
+  vec = vec && X.n % 8 == 0;
+  for (const void* v : {p.post, p.gate, p.pre}) vec = vec && reinterpret_cast<uintptr_t>(v) % 16 == 0;
+  const bool small = used <= BlockSmall::kCap;
+  const Shape shape = bwd ? backward_shape(p, vec, small) : forward_shape(p, vec, small);
+  p.grid = shape.grid;
   if (sums) {
     const int64_t rows_pre = p.dpre ? p.grid : 0, rows_post = p.dpost ? p.grid : 0;
     const int64_t rows_gate = p.dgate && p.gate_per != 1 ? p.grid + p.gate_rows : 0;
@@ -435,14 +956,14 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   }
   cudaError_t e = cudaSuccess;
   if (p.tokens > 0) {
-    if (used <= BlockSmall::kCap) {
+    if (small) {
       BlockSmall s;
       static_cast<BlockArgs&>(s) = p;
       std::copy(p.blocks, p.blocks + used, s.blocks);
       std::fill(s.blocks + used, s.blocks + BlockSmall::kCap, RowBlock{});
-      e = launch_block(s, bwd, stream);
+      e = launch_block(s, bwd, shape, stream);
     } else {
-      e = launch_block(p, bwd, stream);
+      e = launch_block(p, bwd, shape, stream);
     }
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "block_norm launch: %s", cudaGetErrorString(e));
     count_launch();
@@ -496,6 +1017,6 @@ extern "C" dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, in
     return fail(DT_ERR_INVALID_ARG, "tokens %lld, channels %lld, gate_rows %lld", (long long)tokens,
                 (long long)channels, (long long)gate_rows);
   if (gate_rows > std::max<int64_t>(tokens, 1)) return fail(DT_ERR_SHAPE, "more gate rows than tokens");
-  *bytes = (size_t)(3 * BN_MAX_BLOCKS + gate_part_rows(tokens, gate_rows)) * channels * sizeof(float);
+  *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * channels * sizeof(float);
   return DT_OK;
 }
