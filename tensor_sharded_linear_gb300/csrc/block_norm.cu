@@ -271,36 +271,61 @@ __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const _
 
 // ---------------------------------------------------------------- channels in vectors of 8
 
-// Rows of a multiple of 8 channels on 16-byte boundaries: a CTA per row, a
-// thread holds VPT vectors of 8 channels of it, `blockDim.x` vectors apart.
-constexpr int row_threads(int vpt) { return vpt == 1 ? 1024 : 512; }
+// Rows of a multiple of 8 channels on 16-byte boundaries: a CTA takes a run of
+// consecutive rows, one at a time; a thread holds VPT vectors of 8 channels of
+// it, `blockDim.x` vectors apart.
+constexpr int BN_MAX_WARPS = 32;
 
 // The sum over a CTA, in an order fixed by its size; the same in every thread.
-// `buf` [2][K][32] is zero behind the CTA's warps.
-template <int K>
-__device__ __forceinline__ void row_sum(float (&v)[K], float (*buf)[K][32], int& turn) {
+// `buf` is zero behind the CTA's warps.  It alternates between two halves, so
+// one meeting of the CTA is enough.
+__device__ __forceinline__ float row_sum(float v, float (*buf)[BN_MAX_WARPS], int& turn) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-    if (lane == 0 && warps > 1) buf[turn][k][warp] = v[k];
-  }
-  if (warps == 1) return;
+  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (warps == 1) return v;
+  if (lane == 0) buf[turn][warp] = v;
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    v[k] = 0.f;
-    for (int w = 0; w < warps; w += 4) {
-      const float4 x = *reinterpret_cast<const float4*>(&buf[turn][k][w]);
-      v[k] += (x.x + x.y) + (x.z + x.w);
-    }
+  v = 0.f;
+  for (int w = 0; w < warps; w += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(&buf[turn][w]);
+    v += (x.x + x.y) + (x.z + x.w);
   }
   turn ^= 1;
+  return v;
 }
-template <int K>
-__device__ __forceinline__ void clear_sums(float (*buf)[K][32]) {
-  for (int i = threadIdx.x; i < 2 * K * 32; i += blockDim.x) (&buf[0][0][0])[i] = 0.f;
+
+// Eight sums over a CTA of at most 16 warps at once: the lanes split the
+// values among them on the way (fifteen exchanges instead of forty), lane l
+// ends up with value l / 4 of the warp, and then of the CTA.
+__device__ __forceinline__ void row_sums(float (&v)[8], float (*buf)[8][16], int& turn) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+#pragma unroll
+  for (int o = 16, k = 4; k; o >>= 1, k >>= 1) {
+    const bool high = lane & o;
+#pragma unroll
+    for (int i = 0; i < k; ++i) {
+      const float keep = high ? v[i + k] : v[i], send = high ? v[i] : v[i + k];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  float x = v[0];
+  x += __shfl_xor_sync(0xffffffffu, x, 2);
+  x += __shfl_xor_sync(0xffffffffu, x, 1);
+  if (warps > 1) {
+    if ((lane & 3) == 0) buf[turn][lane >> 2][warp] = x;
+    __syncthreads();
+    const float4 y = *reinterpret_cast<const float4*>(&buf[turn][lane >> 2][4 * (lane & 3)]);
+    x = (y.x + y.y) + (y.z + y.w);
+    x += __shfl_xor_sync(0xffffffffu, x, 2);
+    x += __shfl_xor_sync(0xffffffffu, x, 1);
+    turn ^= 1;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, x, 4 * i);
+}
+__device__ __forceinline__ void clear(float* buf, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) buf[i] = 0.f;
   __syncthreads();
 }
 
@@ -324,15 +349,19 @@ struct Dropout {
   __device__ __forceinline__ explicit Dropout(const BlockArgs& p) : below(p.drop_below), on(p.rng != nullptr) {
     for (int i = 0; i < 4; ++i) key[i] = on ? (uint32_t)load_plain(p.rng + i) : 0;
   }
+  __device__ __forceinline__ void words(int64_t t, int n, int c, uint4& a, uint4& b) const {
+    const uint64_t i = ((uint64_t)t * (uint32_t)n + (uint32_t)c) >> 2;
+    a = philox(i, key[2], key[3], key[0], key[1]), b = philox(i + 1, key[2], key[3], key[0], key[1]);
+  }
   __device__ __forceinline__ uint32_t bits(int64_t t, int n, int c) const {
-    const uint64_t i = ((uint64_t)t * n + c) >> 2;
-    const uint4 a = philox(i, key[2], key[3], key[0], key[1]), b = philox(i + 1, key[2], key[3], key[0], key[1]);
+    uint4 a, b;
+    words(t, n, c, a, b);
     return (a.x >= below) | (a.y >= below) << 1 | (a.z >= below) << 2 | (a.w >= below) << 3 | (b.x >= below) << 4 |
            (b.y >= below) << 5 | (b.z >= below) << 6 | (b.w >= below) << 7;
   }
 };
-__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i, float scale) {  // pair i of the 8
-  return f2{bits >> (2 * i) & 1 ? v.x * scale : 0.f, bits >> (2 * i + 1) & 1 ? v.y * scale : 0.f};
+__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i) {  // pair i of the 8
+  return f2{bits & (1u << (2 * i)) ? v.x : 0.f, bits & (2u << (2 * i)) ? v.y : 0.f};
 }
 
 template <class T>
@@ -347,365 +376,474 @@ __device__ __forceinline__ void fetch8(uint4* to, const char* row, int c, int st
   for (int i = 0; i < Pieces<T>::N; ++i) copy16_async(to + i * step, reinterpret_cast<const uint4*>(from) + i);
 }
 
-// RING: x (one part) and the residual come through a ring of asynchronous
-// copies of STAGES rows, each thread its own pieces, so that the next rows are
-// on their way without taking registers or barriers.  Else (parts to be added,
-// rows too large for a ring) plain loads, all of a row at once.
-constexpr int BN_STAGES = 3;
-
-template <class XT, class RT, int VPT, bool RING, class P>
-__global__ void __launch_bounds__(row_threads(VPT), VPT == 2 ? 2 : 1) block_norm_row_kernel(const __grid_constant__ P p) {
-  __shared__ __align__(16) float buf[2][1][32];
-  extern __shared__ uint4 ring[];
-  wait_for_previous_kernel();
-  clear_sums(buf);
-  int turn = 0;
-  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
-  const float inv_n = 1.f / (float)n;
-  const Dropout drop(p);
-  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, PIECES = VPT * (PX + PR);
-  const bool res = p.r.count > 0, out_h = p.h.count > 0, out_y = p.y.count > 0;
-  int ax = 0, ar = 0, ah = 0, ay = 0;
-  auto channel = [&](int v) { return (v * nt + tid) * 8; };
-  uint4* const mine = ring + tid;
-  int put = 0, get = 0;
-  auto fetch = [&](int64_t t) {
-    if (t < p.tokens) {
-      const char* x = row_at(p.blocks[row_block(p.blocks, p.x, t, ax)], t, sizeof(XT));
-      const char* r = res ? row_at(p.blocks[row_block(p.blocks, p.r, t, ar)], t, sizeof(RT)) : nullptr;
-      uint4* to = mine + put * PIECES * nt;
+// Rows of K tensors, one token after the other: all blocks are looked up again
+// where one of them ends.  Steps between rows fit 31 bits (else the kernels for
+// any size run).
+template <int K>
+struct RowCursors {
+  char* ptr[K];  // NULL: no such tensor
+  int32_t step[K];
+  int32_t left;  // tokens from this one to the end of a block
+  template <class P>
+  __device__ __forceinline__ void find(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
+    int64_t until = end;
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = channel(v);
-        if (c >= n) break;
-        fetch8<XT>(to + v * PX * nt, x, c, nt);
-        if (res) fetch8<RT>(to + (VPT * PX + v * PR) * nt, r, c, nt);
-      }
+    for (int k = 0; k < K; ++k) {
+      const RowTable& r = *tables[k];
+      ptr[k] = nullptr;
+      step[k] = 0;
+      if (!r.count || t >= end) continue;
+      int at = 0;
+      const RowBlock& b = p.blocks[row_block(p.blocks, r, t, at)];
+      const int esize = r.dtype == DT_BF16 ? 2 : 4;
+      ptr[k] = row_at(b, t, esize);
+      step[k] = (int32_t)b.ld * esize;
+      if (at + 1 < r.count) until = min(until, p.blocks[r.first + at + 1].begin);
     }
-    copies_commit();
-    if (++put == BN_STAGES) put = 0;
-  };
-  if (RING)
-    for (int i = 0; i + 1 < BN_STAGES; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x);
-  for (int64_t t = blockIdx.x; t < p.tokens; t += gridDim.x) {
-    f2 u[VPT][4], h[VPT][4];
-    Raw8<RT> r[VPT];
-    if constexpr (RING) {
-      fetch(t + (int64_t)(BN_STAGES - 1) * gridDim.x);
-      copies_wait<BN_STAGES - 1>();
-      const uint4* from = mine + get * PIECES * nt;
-      if (++get == BN_STAGES) get = 0;
+    left = (int32_t)(until - t);
+  }
+  // to token t, the next one
+  template <class P>
+  __device__ __forceinline__ void next(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
+    if (--left > 0) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        Raw8<XT> x;
-        x.zero(), r[v].zero();
-        if (channel(v) < n) {
-          x.set(from + v * PX * nt, nt);
-          if (res) r[v].set(from + (VPT * PX + v * PR) * nt, nt);
-        }
-        x.get2(u[v]);
-      }
-    } else {
-      const int bx = row_block(p.blocks, p.x, t, ax);
-      const char* rr = res ? row_at(p.blocks[row_block(p.blocks, p.r, t, ar)], t, sizeof(RT)) : nullptr;
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        r[v].zero();
-        if (res && channel(v) < n) r[v].load(reinterpret_cast<const RT*>(rr) + channel(v));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[v][i] = both(0.f);
-      }
-#pragma unroll 4
-      for (int k = 0; k < p.x.parts; ++k) {
-        const XT* x = reinterpret_cast<const XT*>(row_at(p.blocks[bx + k * p.x.count], t, sizeof(XT)));
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          Raw8<XT> w;
-          w.zero();
-          if (channel(v) < n) w.load(x + channel(v));
-          f2 s[4];
-          w.get2(s);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] + s[i];
-        }
-      }
-    }
-    float sum[1];
-    auto total = [&](const f2(&a)[VPT][4]) {
-      f2 s = both(0.f);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma2(a[v][i], a[v][i], s);
-      sum[0] = s.x + s.y;
-      row_sum(sum, buf, turn);
-      return rsqrtf(sum[0] * inv_n + p.eps);
-    };
-    const float rx = p.post ? total(u) : 1.f;
-    const int64_t seg = p.gate ? (uint32_t)t / (uint32_t)p.gate_per : 0;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = channel(v);
-      if (c < n) {
-        f2 w[4];
-        if (p.post) {
-          load_w8(p.post, p.post_dtype, c, w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] * both(rx) * w[i];
-        }
-        if (p.gate) {
-          load_w8(p.gate, p.gate_dtype, seg * n + c, w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[v][i] = u[v][i] * w[i];
-        }
-        if (drop.on) {
-          const uint32_t bits = drop.bits(t, n, c);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) u[v][i] = kept(u[v][i], bits, i, p.drop_scale);
-        }
-      }
-      r[v].get2(h[v]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) h[v][i] = res ? fma2(both(p.scale), h[v][i], u[v][i]) : u[v][i];
-    }
-    if (out_h) {
-      RT* o = reinterpret_cast<RT*>(row_at(p.blocks[row_block(p.blocks, p.h, t, ah)], t, sizeof(RT)));
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-        if (channel(v) < n) store8(o + channel(v), h[v]);
-    }
-    if (out_y) {
-      const float rh = total(h);
-      XT* o = reinterpret_cast<XT*>(row_at(p.blocks[row_block(p.blocks, p.y, t, ay)], t, sizeof(XT)));
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = channel(v);
-        if (c >= n) break;
-        f2 w[4];
-        load_w8(p.pre, p.pre_dtype, c, w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = h[v][i] * both(rh) * w[i];
-        store8(o + c, w);
-      }
+      for (int k = 0; k < K; ++k) ptr[k] += step[k];
+    } else if (t < end) {
+      find(p, tables, t, end);
     }
   }
-  if (RING) copies_wait<0>();
+};
+
+// body(w, v): v's vectors of a weight's channels; the type is looked at once, so
+// that the loads of all vectors can be on their way together.
+template <int VPT, class C, class F>
+__device__ __forceinline__ void each_w8(const void* weight, int dtype, C&& channel, F&& body) {
+  f2 w[4];
+  if (dtype == DT_BF16) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      Raw8<__nv_bfloat16> x;
+      x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + channel(v)));
+      x.get2(w);
+      body(w, v);
+    }
+  } else {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      Raw8<float> x;
+      x.load_keep(static_cast<const float*>(weight) + channel(v));
+      x.get2(w);
+      body(w, v);
+    }
+  }
 }
 
-// Gradients.  A CTA takes a run of consecutive tokens and keeps the sums over
-// them in registers; x, the residual, dh and dy come through the ring and are
-// read from it twice, before and after the means, instead of being held.  The
-// means' sums are taken at once: with a = gate post keep x / (1 - p), h =
-// scale residual + r(x) a and g = dh + r(h) z - k h, the sum of a g is that of
-// a dh, a z and a h, so one meeting of the CTA does after that of r(x).
-constexpr int bwd_stages(int pieces) { return pieces > 8 ? 2 : 3; }
+// Threads of forward CTAs that an SM's registers are shared among, measured
+// together with the vectors a thread at 8192 x 4096 with dropout: four vectors
+// and 640 threads 51.6 us, two and 768 57.7, eight and 512 64.7.
+constexpr int forward_resident(int vpt, bool ahead, int er) {
+  return vpt == 1 ? 1024 : vpt == 2 ? (ahead ? 768 : 1024) : ahead ? (er == 4 ? 512 : 640) : 768;
+}
 
-template <class XT, class RT, int VPT, class P>
-__global__ void __launch_bounds__(VPT == 1 ? 256 : 512, VPT == 1 ? 2 : 1)
-    block_norm_row_backward_kernel(const __grid_constant__ P p) {
-  __shared__ __align__(16) float buf[2][5][32];
-  extern __shared__ uint4 ring[];
-  wait_for_previous_kernel();
-  clear_sums(buf);
+// Forward.  AHEAD (x in one part): the next row's loads are on their way while
+// a row is worked on, x's from where it has been unpacked, the residual's from
+// where it has been added.  Else the parts' loads go out four at a time.
+// Threads without a last vector load the row's first one instead and drop it.
+template <class XT, class RT, int VPT, bool AHEAD, class P>
+__global__ void __launch_bounds__(forward_resident(VPT, AHEAD, sizeof(RT)))
+    block_norm_row_kernel(const __grid_constant__ P p) {
+  __shared__ __align__(16) float buf[2][BN_MAX_WARPS];
+  clear(&buf[0][0], 2 * BN_MAX_WARPS);
   int turn = 0;
   const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
   const float inv_n = 1.f / (float)n;
-  const Dropout drop(p);
-  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, PIECES = 2 * VPT * (PX + PR);
-  constexpr int STAGES = bwd_stages(PIECES / VPT);
-  const bool res = p.r.count > 0, has_h = p.h.count > 0, has_y = p.y.count > 0;
   const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
-  int ax = 0, ar = 0, ah = 0, ay = 0, adx = 0, adr = 0;
+  // x alone (its parts are looked up where they are read), the residual alone
+  // (its loads go out later), the outputs
+  const RowTable *const tx[1] = {&p.x}, *const tr[1] = {&p.r}, *const to[2] = {&p.h, &p.y};
+  RowCursors<1> cx, cr;
+  RowCursors<2> out;
+  cx.find(p, tx, t0, t1);
+  cr.find(p, tr, t0, t1);
+  out.find(p, to, t0, t1);
+  const int parts = p.x.parts;
+  int at = 0;
+  // vectors below the last two are there in every thread
+  const bool last = tid + (VPT - 1) * nt < n / 8, last_but_one = tid + (VPT - 2) * nt < n / 8;
+  auto has = [&](int v) { return v < VPT - 2 || (v == VPT - 1 ? last : last_but_one); };
+  auto channel = [&](int v) { return has(v) ? (tid + v * nt) * 8 : 0; };
+  const bool res = p.r.count > 0;
+  wait_for_previous_kernel();  // (until here: parameters and shared memory alone)
+  const Dropout drop(p);
+  Raw8<XT> x[VPT];
+  Raw8<RT> r[VPT];
+  auto load_x = [&](const char* row) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) x[v].load(reinterpret_cast<const XT*>(row) + channel(v));
+  };
+  auto load_r = [&] {
+    if (!res) return;
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) r[v].load(reinterpret_cast<const RT*>(cr.ptr[0]) + channel(v));
+  };
+  if (AHEAD && t0 < t1) {
+    load_x(cx.ptr[0]);
+    load_r();
+  }
+  const int64_t seg0 = p.gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0;
+  int64_t seg_end = (seg0 + 1) * p.gate_per;
+  const char* gate = static_cast<const char*>(p.gate);
+  const int64_t gate_step = (int64_t)n * (p.gate_dtype == DT_BF16 ? 2 : 4);
+  if (gate) gate += seg0 * gate_step;
+  // a vector a thread: its weights stay in registers
+  constexpr bool KEEP = VPT == 1;
+  f2 w_post[4], w_gate[4], w_pre[4];
+  if (KEEP) {
+    if (p.post) load_w8(p.post, p.post_dtype, channel(0), w_post);
+    if (gate) load_w8(gate, p.gate_dtype, channel(0), w_gate);
+    if (p.pre) load_w8(p.pre, p.pre_dtype, channel(0), w_pre);
+  }
+  auto weigh = [&](const void* weight, int dtype, const f2(&w)[4], auto&& body) {
+    if constexpr (KEEP) body(w, 0);
+    else each_w8<VPT>(weight, dtype, channel, body);
+  };
+  for (int64_t t = t0; t < t1; ++t) {
+    f2 h[VPT][4];
+    auto unpack = [&](int v, f2(&w)[4]) {
+      x[v].get2(w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = has(v) ? w[i] : both(0.f);
+    };
+    if constexpr (AHEAD) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) unpack(v, h[v]);
+      if (t + 1 < t1) {
+        cx.next(p, tx, t + 1, t1);
+        load_x(cx.ptr[0]);
+      }
+    } else {
+      load_r();
+      const int block = row_block(p.blocks, p.x, t, at);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = both(0.f);
+#pragma unroll 4
+      for (int k = 0; k < parts; ++k) {
+        load_x(k ? row_at(p.blocks[block + k * p.x.count], t, sizeof(XT)) : cx.ptr[0]);
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+          f2 w[4];
+          unpack(v, w);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) h[v][i] = k ? h[v][i] + w[i] : w[i];
+        }
+      }
+      cx.next(p, tx, t + 1, t1);
+    }
+    auto total = [&] {
+      f2 s = both(0.f);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s = fma2(h[v][i], h[v][i], s);
+      return rsqrtf(row_sum(s.x + s.y, buf, turn) * inv_n + p.eps);
+    };
+    if (p.post) {
+      const f2 rx = both(total());
+      weigh(p.post, p.post_dtype, w_post, [&](const f2(&w)[4], int v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = h[v][i] * rx * w[i];
+      });
+    }
+    if (gate) {
+      if (t == seg_end) {
+        gate += gate_step;
+        seg_end += p.gate_per;
+        if (KEEP) load_w8(gate, p.gate_dtype, channel(0), w_gate);
+      }
+      weigh(gate, p.gate_dtype, w_gate, [&](const f2(&w)[4], int v) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = h[v][i] * w[i];
+      });
+    }
+    if (drop.on) {
+      // the words in a loop of two vectors a round: unrolled, the code does not stay in the instruction cache
+      uint64_t keep = 0;
+#pragma unroll 2
+      for (int v = 0; v < VPT; ++v) keep |= (uint64_t)drop.bits(t, n, (tid + v * nt) * 8) << (8 * v);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = kept(h[v][i] * both(p.drop_scale), (uint32_t)(keep >> (8 * v)), i);
+    }
+    if (res) {
+      const f2 scale = both(p.scale);
+#pragma unroll
+      for (int v = 0; v < VPT; ++v) {
+        f2 w[4];
+        r[v].get2(w);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[v][i] = has(v) ? fma2(scale, w[i], h[v][i]) : h[v][i];
+      }
+      cr.next(p, tr, t + 1, t1);
+      if (AHEAD && t + 1 < t1) load_r();
+    }
+    if (out.ptr[0]) {
+#pragma unroll
+      for (int v = 0; v < VPT; ++v)
+        if (has(v)) store8(reinterpret_cast<RT*>(out.ptr[0]) + channel(v), h[v]);
+    }
+    if (out.ptr[1]) {
+      const f2 rh = both(total());
+      weigh(p.pre, p.pre_dtype, w_pre, [&](const f2(&w)[4], int v) {
+        f2 y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = h[v][i] * rh * w[i];
+        if (has(v)) store8(reinterpret_cast<XT*>(out.ptr[1]) + channel(v), y);
+      });
+    }
+    out.next(p, to, t + 1, t1);
+  }
+}
+
+// Gradients.  A CTA keeps the sums over its tokens and the weights in
+// registers; x, dy, the residual and dh come through a ring of S rows.  Three
+// things keep the work per element small.
+//  - The means' sums are taken at once: with a = w s (w = gate post / (1 - p),
+//    0 where dropped), h = scale residual + r(s) a and g = dh + r(h) z - k h,
+//    the sum of a g is made of those of a dh, a z and a h; and (S > 1) the next
+//    row's sum of s^2 goes with them, so the CTA meets once a row.
+//  - dgate and dpost are one sum: with q = sum over the tokens of a gate row
+//    of g s r(s) (kept elements), dgate = post q / (1 - p), and dpost adds up
+//    gate q / (1 - p).
+//  - What an operand is missing for is 0 (or, of w, 1) and computed all the same.
+template <class XT, class RT, int VPT, int S, class P>
+__global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __grid_constant__ P p) {
+  __shared__ __align__(16) float buf[2][8][16];
+  extern __shared__ uint4 ring[];
+  clear(&buf[0][0][0], 2 * 8 * 16);
+  int turn = 0;
+  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
+  const float inv_n = 1.f / (float)n;
+  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, STAGE = 2 * VPT * (PX + PR);
+  constexpr bool HOLD = VPT == 1;  // a row's values stay in registers between the two looks at it
+  const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
+  const RowTable *const tin[4] = {&p.x, &p.y, &p.r, &p.h}, *const tout[2] = {&p.dx, &p.dr};
+  RowCursors<4> in;
+  RowCursors<2> out;
+  in.find(p, tin, t0, t1);
+  out.find(p, tout, t0, t1);
+  const bool has_y = p.y.count > 0, res = p.r.count > 0, has_h = p.h.count > 0, post = p.post, gate = p.gate;
+  wait_for_previous_kernel();  // (until here: parameters and shared memory alone)
+  const Dropout drop(p);
   auto channel = [&](int v) { return (v * nt + tid) * 8; };
   uint4* const mine = ring + tid;
-  int put = 0, get = 0;
-  auto fetch = [&](int64_t t) {
-    if (t < t1) {
-      auto row = [&](const RowTable& r, int& a, int es) {
-        return r.count ? row_at(p.blocks[row_block(p.blocks, r, t, a)], t, es) : nullptr;
-      };
-      const char *x = row(p.x, ax, sizeof(XT)), *r = row(p.r, ar, sizeof(RT)), *h = row(p.h, ah, sizeof(RT)),
-                 *y = row(p.y, ay, sizeof(XT));
-      uint4* to = mine + put * PIECES * nt;
+  int64_t tf = t0;
+  auto fetch = [&](uint4* to) {
+    if (tf < t1) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) {
         const int c = channel(v);
         if (c >= n) break;
-        fetch8<XT>(to + v * PX * nt, x, c, nt);
-        if (has_y) fetch8<XT>(to + (VPT + v) * PX * nt, y, c, nt);
-        if (res) fetch8<RT>(to + (2 * VPT * PX + v * PR) * nt, r, c, nt);
-        if (has_h) fetch8<RT>(to + (2 * VPT * PX + (VPT + v) * PR) * nt, h, c, nt);
+        fetch8<XT>(to + v * PX * nt, in.ptr[0], c, nt);
+        if (has_y) fetch8<XT>(to + (VPT + v) * PX * nt, in.ptr[1], c, nt);
+        if (res) fetch8<RT>(to + (2 * VPT * PX + v * PR) * nt, in.ptr[2], c, nt);
+        if (has_h) fetch8<RT>(to + (2 * VPT * PX + (VPT + v) * PR) * nt, in.ptr[3], c, nt);
       }
+      ++tf;
+      in.next(p, tin, tf, t1);
     }
     copies_commit();
-    if (++put == STAGES) put = 0;
   };
-  for (int i = 0; i + 1 < STAGES; ++i) fetch(t0 + i);
-  f2 s_pre[VPT][4], s_post[VPT][4], s_gate[VPT][4];
+  for (int i = 0; i < S; ++i) {  // places that no copy fills are 0
+    uint4* to = mine + i * STAGE * nt;
 #pragma unroll
-  for (int v = 0; v < VPT; ++v)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_pre[v][i] = s_post[v][i] = s_gate[v][i] = both(0.f);
-  auto write_sums = [&](float* to, const f2(&s)[VPT][4]) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      if (channel(v) < n) {
-        float4* o = reinterpret_cast<float4*>(to + channel(v));
-        o[0] = make_float4(s[v][0].x, s[v][0].y, s[v][1].x, s[v][1].y);
-        o[1] = make_float4(s[v][2].x, s[v][2].y, s[v][3].x, s[v][3].y);
-      }
-  };
-  int64_t seg = p.gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0, seg_end = (seg + 1) * p.gate_per;
-  for (int64_t t = t0; t < t1; ++t) {
-    fetch(t + STAGES - 1);
-    copies_wait<STAGES - 1>();
-    const uint4* from = mine + get * PIECES * nt;
-    if (++get == STAGES) get = 0;
-    if (t == seg_end) {
-      ++seg;
-      seg_end += p.gate_per;
+    for (int k = 0; k < STAGE; ++k) {
+      const int v = k < 2 * VPT * PX ? k / PX % VPT : (k - 2 * VPT * PX) / PR % VPT;
+      const bool there = k < VPT * PX ? true : k < 2 * VPT * PX ? has_y : k < 2 * VPT * PX + VPT * PR ? res : has_h;
+      if (!there || channel(v) >= n) to[k * nt] = make_uint4(0, 0, 0, 0);
     }
-    auto load_x = [&](int v, f2(&x)[4]) {
-      Raw8<XT> w;
-      w.set(from + v * PX * nt, nt);
-      w.get2(x);
-    };
-    float rx = 1.f, rh = 1.f, kh = 0.f, kx = 0.f;
-    if (p.post) {
-      f2 s = both(0.f);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        if (channel(v) >= n) break;
-        f2 x[4];
-        load_x(v, x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma2(x[i], x[i], s);
-      }
-      float sum[5] = {s.x + s.y, 0.f, 0.f, 0.f, 0.f};
-      row_sum(sum, buf, turn);
-      rx = rsqrtf(sum[0] * inv_n + p.eps);
-    }
-    uint32_t bits[VPT];
-    // a vector's x, a, h, z and dh
-    auto values = [&](int v, f2(&x)[4], f2(&a)[4], f2(&h)[4], f2(&z)[4], f2(&dy)[4], f2(&dh)[4], f2(&post)[4],
-                      f2(&gate)[4]) {
-      const int c = channel(v);
-      load_x(v, x);
-      if (p.post) load_w8(p.post, p.post_dtype, c, post);
-      if (p.gate) load_w8(p.gate, p.gate_dtype, seg * n + c, gate);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = x[i];
-        if (p.post) a[i] = a[i] * post[i];
-        if (p.gate) a[i] = a[i] * gate[i];
-        if (drop.on) a[i] = kept(a[i], bits[v], i, p.drop_scale);
-      }
-      if (res) {
-        Raw8<RT> w;
-        w.set(from + (2 * VPT * PX + v * PR) * nt, nt);
-        w.get2(h);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 f = a[i] * both(rx);
-        h[i] = res ? fma2(both(p.scale), h[i], f) : f;
-        dh[i] = dy[i] = z[i] = both(0.f);
-      }
-      if (has_h) {
-        Raw8<RT> w;
-        w.set(from + (2 * VPT * PX + (VPT + v) * PR) * nt, nt);
-        w.get2(dh);
-      }
-      if (has_y) {
-        Raw8<XT> w;
-        w.set(from + (VPT + v) * PX * nt, nt);
-        w.get2(dy);
-        load_w8(p.pre, p.pre_dtype, c, z);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) z[i] = z[i] * dy[i];
-      }
-    };
-    f2 q[5] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (channel(v) >= n) break;
-      if (drop.on) bits[v] = drop.bits(t, n, channel(v));
-      if (!has_y && !p.post) continue;
-      f2 x[4], a[4], h[4], z[4], dy[4], dh[4], post[4], gate[4];
-      values(v, x, a, h, z, dy, dh, post, gate);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q[0] = fma2(h[i], h[i], q[0]);
-        q[1] = fma2(h[i], z[i], q[1]);
-        q[2] = fma2(a[i], dh[i], q[2]);
-        q[3] = fma2(a[i], z[i], q[3]);
-        q[4] = fma2(a[i], h[i], q[4]);
-      }
-    }
-    if (has_y || p.post) {
-      float sum[5];
-#pragma unroll
-      for (int i = 0; i < 5; ++i) sum[i] = q[i].x + q[i].y;
-      row_sum(sum, buf, turn);
-      if (has_y) {
-        rh = rsqrtf(sum[0] * inv_n + p.eps);
-        kh = rh * rh * rh * (sum[1] * inv_n);
-      }
-      kx = p.post ? rx * rx * rx * ((sum[2] + rh * sum[3] - kh * sum[4]) * inv_n) : 0.f;
-    }
-    char* dx = p.dx.count ? row_at(p.blocks[row_block(p.blocks, p.dx, t, adx)], t, sizeof(XT)) : nullptr;
-    char* dr = p.dr.count ? row_at(p.blocks[row_block(p.blocks, p.dr, t, adr)], t, sizeof(RT)) : nullptr;
+  }
+  for (int i = 0; i < S; ++i) fetch(mine + i * STAGE * nt);
+  f2 s_pre[VPT][4], s_post[VPT][4], q_gate[VPT][4], w_pre[VPT][4], w[VPT][4];
+  int64_t seg = gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0, seg_end = (seg + 1) * p.gate_per;
+  auto weights = [&] {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = channel(v);
       if (c >= n) break;
-      f2 x[4], a[4], h[4], z[4], dy[4], dh[4], post[4], gate[4];
-      values(v, x, a, h, z, dy, dh, post, gate);
+      f2 a[4], b[4];
+      if (post) load_w8(p.post, p.post_dtype, c, a);
+      if (gate) load_w8(p.gate, p.gate_dtype, seg * n + c, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        w[v][i] = both(p.drop_scale);
+        if (post) w[v][i] = w[v][i] * a[i];
+        if (gate) w[v][i] = w[v][i] * b[i];
+      }
+    }
+  };
+#pragma unroll
+  for (int v = 0; v < VPT; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s_pre[v][i] = s_post[v][i] = q_gate[v][i] = w_pre[v][i] = w[v][i] = both(0.f);
+  weights();
+  if (has_y) {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v)
+      if (channel(v) < n) load_w8(p.pre, p.pre_dtype, channel(v), w_pre[v]);
+  }
+  auto write_sums = [&](float* to, int v, const f2(&s)[4]) {
+    float4* o = reinterpret_cast<float4*>(to + channel(v));
+    o[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
+    o[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
+  };
+  // the end of a gate row's tokens (or, without a gate, of the CTA's)
+  auto close = [&] {
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = channel(v);
+      if (c >= n) break;
+      f2 a[4], b[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = b[i] = both(1.f);
+        q_gate[v][i] = q_gate[v][i] * both(p.drop_scale);
+      }
+      if (post) load_w8(p.post, p.post_dtype, c, a);
+      if (gate) load_w8(p.gate, p.gate_dtype, seg * n + c, b);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = a[i] * q_gate[v][i];
+        s_post[v][i] = fma2(b[i], q_gate[v][i], s_post[v][i]);
+        q_gate[v][i] = both(0.f);
+      }
+      if (!gate) continue;
+      if (p.gate_per != 1) write_sums(p.part_gate + ((int64_t)blockIdx.x + seg) * n, v, a);
+      else if (p.dgate_dtype == DT_BF16) store8(static_cast<__nv_bfloat16*>(p.dgate) + seg * n + c, a);
+      else store8(static_cast<float*>(p.dgate) + seg * n + c, a);
+    }
+  };
+  auto square = [&](const uint4* from) {  // this thread's share of the sum of s^2
+    f2 s = both(0.f);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      Raw8<XT> r;
+      r.set(from + v * PX * nt, nt);
+      f2 x[4];
+      r.get2(x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s = fma2(x[i], x[i], s);
+    }
+    return s.x + s.y;
+  };
+  float rx = 1.f;
+  int slot = 0;
+  const f2 scale = both(p.scale);
+  for (int64_t t = t0; t < t1; ++t) {
+    uint4* const from = mine + slot * STAGE * nt;
+    if (++slot == S) slot = 0;
+    copies_wait<(S > 1 ? S - 2 : 0)>();  // this row and (S > 1) the next
+    float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (post && (S == 1 || t == t0)) {
+      q[0] = square(from);
+      row_sums(q, buf, turn);
+      rx = rsqrtf(q[0] * inv_n + p.eps);
+    }
+    uint32_t bits[VPT];
+    f2 x[4], h[4], dy[4], dh[4];  // of one vector
+    auto values = [&](int v) {
+      Raw8<XT> xw, yw;
+      Raw8<RT> rw, hw;
+      xw.set(from + v * PX * nt, nt);
+      yw.set(from + (VPT + v) * PX * nt, nt);
+      rw.set(from + (2 * VPT * PX + v * PR) * nt, nt);
+      hw.set(from + (2 * VPT * PX + (VPT + v) * PR) * nt, nt);
+      xw.get2(x), yw.get2(dy), rw.get2(h), hw.get2(dh);
+    };
+    auto branch = [&](int v, int i) {  // a
+      const f2 a = x[i] * w[v][i];
+      return drop.on ? kept(a, bits[v], i) : a;
+    };
+    f2 sum[5] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      if (drop.on) bits[v] = drop.bits(t, n, channel(v));
+      values(v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 a = branch(v, i), z = dy[i] * w_pre[v][i];
+        h[i] = fma2(scale, h[i], a * both(rx));
+        sum[0] = fma2(h[i], h[i], sum[0]);
+        sum[1] = fma2(h[i], z, sum[1]);
+        sum[2] = fma2(a, dh[i], sum[2]);
+        sum[3] = fma2(a, z, sum[3]);
+        sum[4] = fma2(a, h[i], sum[4]);
+      }
+    }
+    float rh = 0.f, kh = 0.f, kx = 0.f, next_rx = 1.f;
+    if (has_y || post) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) q[i] = sum[i].x + sum[i].y;
+      q[5] = q[6] = q[7] = 0.f;
+      if (S > 1 && post && t + 1 < t1) q[5] = square(mine + slot * STAGE * nt);
+      row_sums(q, buf, turn);
+      if (has_y) {
+        rh = rsqrtf(q[0] * inv_n + p.eps);
+        kh = rh * rh * rh * (q[1] * inv_n);
+      }
+      if (post) {
+        kx = rx * rx * rx * ((q[2] + rh * q[3] - kh * q[4]) * inv_n);
+        next_rx = rsqrtf(q[5] * inv_n + p.eps);
+      }
+    }
+    const f2 rx2 = both(rx), rh2 = both(rh), kh2 = both(-kh), kx2 = both(-kx);
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+      const int c = channel(v);
+      if (!HOLD) {
+        values(v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) h[i] = fma2(scale, h[i], branch(v, i) * rx2);
+      }
       f2 o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        f2 g = dh[i];
-        if (has_y) {
-          g = fma2(z[i], both(rh), fma2(h[i], both(-kh), g));
-          s_pre[v][i] = fma2(dy[i], h[i] * both(rh), s_pre[v][i]);
+        f2 g = dh[i], xr = x[i] * rx2;
+        if (has_y) {  // (a choice: kh may not be finite where h is 0)
+          g = fma2(dy[i] * w_pre[v][i], rh2, fma2(h[i], kh2, g));
+          s_pre[v][i] = fma2(dy[i], h[i] * rh2, s_pre[v][i]);
         }
-        dh[i] = g * both(p.scale);
-        const f2 e = drop.on ? kept(g, bits[v], i, p.drop_scale) : g;
-        f2 xr = p.post ? x[i] * both(rx) : x[i];
-        if (drop.on) xr = kept(xr, bits[v], i, 1.f);  // (what is dropped may be NaN)
-        f2 w = e;
-        if (p.gate) {
-          a[i] = e * (p.post ? xr * post[i] : xr);
-          s_gate[v][i] = s_gate[v][i] + a[i];
-          w = e * gate[i];
-        }
-        if (p.post) {
-          s_post[v][i] = fma2(w, xr, s_post[v][i]);
-          o[i] = fma2(w * post[i], both(rx), x[i] * both(-kx));
-        } else {
-          o[i] = w;
-        }
+        dh[i] = g * scale;
+        if (drop.on) g = kept(g, bits[v], i), xr = kept(xr, bits[v], i);  // (what is dropped may be NaN)
+        q_gate[v][i] = fma2(g, xr, q_gate[v][i]);
+        o[i] = g * w[v][i];
+        if (post) o[i] = fma2(o[i], rx2, x[i] * kx2);
       }
-      if (dr) store8(reinterpret_cast<RT*>(dr) + c, dh);
-      if (dx) store8(reinterpret_cast<XT*>(dx) + c, o);
-      if (p.gate && p.gate_per == 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          store_any(p.dgate, p.dgate_dtype, t * n + c + 2 * i, a[i].x);
-          store_any(p.dgate, p.dgate_dtype, t * n + c + 2 * i + 1, a[i].y);
-        }
+      if (c < n) {
+        if (out.ptr[1]) store8(reinterpret_cast<RT*>(out.ptr[1]) + c, dh);
+        if (out.ptr[0]) store8(reinterpret_cast<XT*>(out.ptr[0]) + c, o);
       }
     }
-    if (p.gate && p.gate_per != 1 && (t + 1 == t1 || t + 1 == seg_end)) {
-      write_sums(p.part_gate + ((int64_t)blockIdx.x + seg) * n, s_gate);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s_gate[v][i] = both(0.f);
+    out.next(p, tout, t + 1, t1);
+    fetch(from);
+    if (S > 1) rx = next_rx;
+    if (t + 1 == t1) {
+      close();
+    } else if (gate && t + 1 == seg_end) {
+      close();
+      ++seg;
+      seg_end += p.gate_per;
+      weights();
     }
   }
-  if (p.pre) write_sums(p.part_pre + (int64_t)blockIdx.x * n, s_pre);
-  if (p.post) write_sums(p.part_post + (int64_t)blockIdx.x * n, s_post);
+#pragma unroll
+  for (int v = 0; v < VPT; ++v) {
+    if (channel(v) >= n) break;
+    if (has_y) write_sums(p.part_pre + (int64_t)blockIdx.x * n, v, s_pre[v]);
+    if (post) write_sums(p.part_post + (int64_t)blockIdx.x * n, v, s_post[v]);
+  }
   copies_wait<0>();
 }
 
@@ -742,11 +880,14 @@ int64_t gate_part_rows(int64_t tokens, int64_t gate_rows) { return gate_rows == 
 // How a launch covers its rows.
 struct Shape {
   int threads = 0, vpt = 0, grid = 0;  // vpt 0: the kernels for any size
-  bool ring = false;
+  int stages = 0;  // backward: rows of the ring
+  bool ahead = false;  // forward: the next row's loads go out early
   size_t smem = 0;
 };
 
 int round_up(int64_t a, int b) { return (int)((a + b - 1) / b * b); }
+constexpr int64_t BN_SMEM = 224 * 1024;  // of an SM, for rings
+constexpr int64_t BN_STATIC = 2048;      // a CTA's other shared memory, at most
 
 Shape forward_shape(const BlockArgs& p, bool vec, bool small) {
   Shape s;
@@ -756,15 +897,16 @@ Shape forward_shape(const BlockArgs& p, bool vec, bool small) {
     s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * 8);
     return s;
   }
-  // a vector a thread where there are few tokens (the shortest way through a
-  // row) or few channels; else two, four for the widest
-  s.vpt = vectors <= 256 || (p.tokens <= sms && vectors <= 1024) ? 1 : vectors <= 1024 ? 2 : 4;
-  s.threads = round_up((vectors + s.vpt - 1) / s.vpt, 32);
-  const size_t stage = (size_t)s.threads * s.vpt * 8 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype));
-  s.ring = small && p.x.parts == 1 && stage * BN_STAGES <= 200 * 1024;
-  s.smem = s.ring ? stage * BN_STAGES : 0;
-  int ctas = std::max(1, std::min(32, 1024 / s.threads));
-  if (s.ring) ctas = std::max(1, std::min<int>(ctas, (int)(220 * 1024 / (s.smem + 1280))));
+  // Few tokens: a vector a thread, the shortest way through a row.  Else four,
+  // for what a row costs besides its vectors is paid by each warp, or two where
+  // that leaves a fifth fewer threads idle.
+  auto threads = [&](int vpt) { return round_up((vectors + vpt - 1) / vpt, 32); };
+  s.vpt = 4;
+  if (p.tokens <= 2 * sms && vectors <= 1024) s.vpt = 1;
+  else if (vectors <= 64 || (vectors <= 1024 && 8 * threads(2) < 13 * threads(4))) s.vpt = vectors <= 32 ? 1 : 2;
+  s.threads = threads(s.vpt);
+  s.ahead = small && p.x.parts == 1 && p.tokens > 2 * sms;
+  const int ctas = std::max(1, std::min(32, forward_resident(s.vpt, s.ahead, dtype_size(p.h.dtype)) / s.threads));
   s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * ctas);
   return s;
 }
@@ -774,14 +916,14 @@ Shape backward_shape(const BlockArgs& p, bool vec, bool small) {
   const int sms = device_sm_count();
   const int64_t vectors = p.n / 8;
   int64_t most = 2 * sms;
-  const int pieces = 2 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype)) / 2;  // 16-byte pieces of a vector
   if (vec && small && p.x.parts == 1 && vectors <= 1024) {
-    s.vpt = vectors <= 256 ? 1 : 2;
+    s.vpt = vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 85.9 us, one 91.0)
     s.threads = round_up((vectors + s.vpt - 1) / s.vpt, 32);
-    s.smem = (size_t)s.threads * s.vpt * pieces * 16 * bwd_stages(pieces);
-    s.ring = true;
-    if (s.smem > 220 * 1024) s = Shape();
-    else most = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(512 / s.threads, 220 * 1024 / (s.smem + 2048)), 8)) * sms;
+    const int64_t stage = (int64_t)s.threads * s.vpt * 16 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype));
+    const int64_t ctas = std::min(8, 512 / s.threads);
+    s.stages = s.vpt == 1 && (5 * stage + BN_STATIC) * ctas <= BN_SMEM ? 5 : (3 * stage + BN_STATIC) * ctas <= BN_SMEM ? 3 : 1;
+    s.smem = stage * s.stages;
+    most = std::max<int64_t>(1, std::min<int64_t>(ctas, BN_SMEM / (int64_t)(s.smem + BN_STATIC))) * sms;
   }
   // four tokens a CTA at least, for its sums are written and read again
   most = std::min<int64_t>(most, std::max<int64_t>(sms, (p.tokens + 3) / 4));
@@ -798,12 +940,14 @@ cudaError_t launch_rows(K kernel, const P& p, const Shape& s, cudaStream_t strea
 
 template <class XT, class RT, class P>
 cudaError_t launch_typed(const P& p, bool bwd, const Shape& s, cudaStream_t stream) {
-  constexpr bool SMALL = P::kCap == BlockSmall::kCap;
-  if constexpr (SMALL) {
-    if (bwd)
-      return s.vpt == 1 ? launch_rows(block_norm_row_backward_kernel<XT, RT, 1, P>, p, s, stream)
-                        : launch_rows(block_norm_row_backward_kernel<XT, RT, 2, P>, p, s, stream);
-    if (s.ring)
+#define DT_BN_BACK(VPT, S) \
+  if (s.vpt == VPT && s.stages == S) return launch_rows(block_norm_row_backward_kernel<XT, RT, VPT, S, P>, p, s, stream);
+  if constexpr (P::kCap == BlockSmall::kCap) {
+    if (bwd) {
+      DT_BN_BACK(1, 5) DT_BN_BACK(1, 3) DT_BN_BACK(2, 3) DT_BN_BACK(2, 1)
+      return cudaErrorInvalidValue;
+    }
+    if (s.ahead)
       return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, true, P>, p, s, stream)
              : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, true, P>, p, s, stream)
                           : launch_rows(block_norm_row_kernel<XT, RT, 4, true, P>, p, s, stream);
@@ -811,6 +955,7 @@ cudaError_t launch_typed(const P& p, bool bwd, const Shape& s, cudaStream_t stre
   return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, false, P>, p, s, stream)
          : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, false, P>, p, s, stream)
                       : launch_rows(block_norm_row_kernel<XT, RT, 4, false, P>, p, s, stream);
+#undef DT_BN_BACK
 }
 
 template <class P>
@@ -939,6 +1084,7 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   if (X.n == 0 || !anchor) return DT_OK;
   if ((st = bind_device_of(anchor)) != DT_OK) return st;
   vec = vec && X.n % 8 == 0;
+  for (int i = 0; i < used; ++i) vec = vec && p.blocks[i].ld < (1 << 29);  // steps between rows in 31 bits
   for (const void* v : {p.post, p.gate, p.pre}) vec = vec && reinterpret_cast<uintptr_t>(v) % 16 == 0;
   const bool small = used <= BlockSmall::kCap;
   const Shape shape = bwd ? backward_shape(p, vec, small) : forward_shape(p, vec, small);
