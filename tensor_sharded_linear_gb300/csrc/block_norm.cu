@@ -27,62 +27,15 @@
 #include <algorithm>
 #include <cmath>
 
-#include "heads_sm103.cuh"
-#include "row_operands.h"
+#include "block_norm.h"
+#include "block_norm.cuh"
 
 namespace dt {
 namespace {
 
-// CTAs of a backward launch at most, and so rows of each of its sums in the
-// workspace: few channels need more CTAs to fill an SM.
+// Runs of tokens of a backward launch at most, and so rows of each of its sums
+// in the workspace: few channels need more CTAs to fill an SM.
 inline int max_backward_blocks(int64_t n) { return n > 2048 ? 320 : n > 1024 ? 640 : 1280; }
-
-struct BlockArgs {
-  RowTable x, r, h, y;    // forward: h and y are written; backward: they are dh and dy
-  RowTable dx, dr;        // backward
-  const void *post, *gate, *pre;
-  void *dpost, *dgate, *dpre;
-  int32_t post_dtype, gate_dtype, pre_dtype, dpost_dtype, dgate_dtype, dpre_dtype;
-  const int32_t* rng;     // NULL: no dropout
-  uint32_t drop_below;    // words below this are dropped
-  float drop_scale;       // 1 / (1 - p)
-  float eps, scale;
-  int64_t tokens;
-  int32_t n;
-  int64_t gate_rows, gate_per;  // rows of the gate, consecutive tokens of each
-  // backward: sums per CTA, [CTA][n] for pre and post, [CTA + gate row][n] for the gate
-  float *part_pre, *part_post, *part_gate;
-  int32_t grid;
-};
-
-// The launch's tables of row blocks; most launches need few.
-template <int CAP>
-struct BlockParams : BlockArgs {
-  static constexpr int kCap = CAP;
-  RowBlock blocks[CAP];
-};
-using BlockSmall = BlockParams<40>;
-using BlockLarge = BlockParams<6 * DT_MAX_SLOTS>;
-
-__device__ __forceinline__ float load_any(const void* p, int dtype, int64_t i) {
-  return dtype == DT_BF16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
-}
-__device__ __forceinline__ void store_any(void* p, int dtype, int64_t i, float v) {
-  if (dtype == DT_BF16) static_cast<__nv_bfloat16*>(p)[i] = __float2bfloat16_rn(v);
-  else static_cast<float*>(p)[i] = v;
-}
-
-// Philox4x32-10: the four words of counter (lo, hi, c2, c3) under key (k0, k1).
-__device__ __forceinline__ uint4 philox(uint64_t counter, uint32_t c2, uint32_t c3, uint32_t k0, uint32_t k1) {
-  uint4 c = make_uint4((uint32_t)counter, (uint32_t)(counter >> 32), c2, c3);
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
-    const uint64_t a = (uint64_t)c.x * 0xD2511F53u, b = (uint64_t)c.z * 0xCD9E8D57u;
-    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b, (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
-    k0 += 0x9E3779B9u, k1 += 0xBB67AE85u;
-  }
-  return c;
-}
 
 // K sums over a CTA's threads, in an order fixed by its size; the same in
 // every thread.  `buf` alternates between two halves, so one barrier is enough.
@@ -219,632 +172,63 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
       const float a = value(c, s, keep), g = grad(c, a);
       if (dr) store_any(dr, p.dr.dtype, c, p.scale * g);
       auto add = [&](float* to, bool begin, float v) { *to = begin ? v : *to + v; };
-      if (p.pre) add(p.part_pre + (int64_t)blockIdx.x * n + c, first, load_any(y, p.y.dtype, c) * a * rh);
+      if (p.pre) add(p.part_pre + (int64_t)blockIdx.x * p.pitch + c, first, load_any(y, p.y.dtype, c) * a * rh);
       const float e = keep ? g * p.drop_scale : 0.f, w = e * gate(c);
       if (p.gate) {
         const float d = keep ? e * s * rx * post(c) : 0.f;
         if (p.gate_per == 1) store_any(p.dgate, p.dgate_dtype, t * n + c, d);
-        else add(p.part_gate + ((int64_t)blockIdx.x + seg) * n + c, first_gate, d);
+        else add(p.part_gate + ((int64_t)blockIdx.x + seg) * p.pitch + c, first_gate, d);
       }
-      if (p.post) add(p.part_post + (int64_t)blockIdx.x * n + c, first, keep ? w * s * rx : 0.f);
+      if (p.post) add(p.part_post + (int64_t)blockIdx.x * p.pitch + c, first, keep ? w * s * rx : 0.f);
       if (dx) store_any(dx, p.dx.dtype, c, p.post ? rx * w * post(c) - kx * s : w);
     }
   }
 }
 
-// dpre, dpost and the gate's rows from the CTAs' sums: 32 channels a block,
-// each warp every 32nd CTA's, then the warps'; a fixed order.
-constexpr int BN_SUM_THREADS = 1024;
+// dpre, dpost and the gate's rows from the sums of the runs of tokens.  A block
+// takes 64 channels: 16 lanes hold four each, half-warps take every 32nd run's
+// sums, eight of them at once, and theirs are added at the end; a fixed order.
+constexpr int BN_SUM_THREADS = 512, BN_SUM_CHANNELS = 64;
 __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const __grid_constant__ BlockArgs p) {
-  __shared__ float acc[32][33];
+  __shared__ float acc[32][BN_SUM_CHANNELS + 1];
   wait_for_previous_kernel();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
   const int64_t rows = p.gate && p.gate_per != 1 ? p.gate_rows : 0;
+  const int64_t c0 = (int64_t)blockIdx.x * BN_SUM_CHANNELS;
   for (int64_t which = blockIdx.y; which < 2 + rows; which += gridDim.y) {
     void* out = which == 0 ? p.dpre : which == 1 ? p.dpost : p.dgate;
     if (!out) continue;
     const int dtype = which == 0 ? p.dpre_dtype : which == 1 ? p.dpost_dtype : p.dgate_dtype;
-    const float* part = which == 0 ? p.part_pre : which == 1 ? p.part_post : p.part_gate;
-    int64_t b0 = 0, b1 = p.tokens ? p.grid : 0, row = 0;
-    if (which >= 2) {  // the CTAs that hold tokens of this row, and their sums' places
+    int64_t b0 = 0, b1 = p.tokens ? p.runs : 0, row = 0;
+    if (which >= 2) {  // the runs that hold tokens of this row, and their sums' places
       row = which - 2;
       if (p.tokens) {
-        b0 = ((row * p.gate_per + 1) * p.grid - 1) / p.tokens + row;
-        b1 = ((row + 1) * p.gate_per * p.grid - 1) / p.tokens + 1 + row;
+        b0 = ((row * p.gate_per + 1) * p.runs - 1) / p.tokens + row;
+        b1 = ((row + 1) * p.gate_per * p.runs - 1) / p.tokens + 1 + row;
       }
     }
-    int64_t c = (int64_t)blockIdx.x * 32 + lane;
-    float s = 0.f;
-    if (c < p.n) {
-#pragma unroll 4
-      for (int64_t b = b0 + warp; b < b1; b += 32) s += part[b * p.n + c];
+    const int64_t c = c0 + lane * 4;
+    const float* part = (which == 0 ? p.part_pre : which == 1 ? p.part_post : p.part_gate) + b0 * p.pitch + c;
+    const int count = c < p.n ? (int)(b1 - b0) : 0;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int b = group; b < count; b += 32 * 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = b + 32 * k < count ? load_plain(reinterpret_cast<const float4*>(part + (int64_t)(b + 32 * k) * p.pitch))
+                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
     }
-    acc[warp][lane] = s;
+    acc[group][lane * 4] = s.x, acc[group][lane * 4 + 1] = s.y, acc[group][lane * 4 + 2] = s.z, acc[group][lane * 4 + 3] = s.w;
     __syncthreads();
-    s = acc[lane][warp];
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    c = (int64_t)blockIdx.x * 32 + warp;
-    if (lane == 0 && c < p.n) store_any(out, dtype, row * p.n + c, s);
+    const int ch = threadIdx.x / 8, k0 = threadIdx.x % 8;  // eight threads a channel
+    float v = (acc[k0][ch] + acc[k0 + 8][ch]) + (acc[k0 + 16][ch] + acc[k0 + 24][ch]);
+#pragma unroll
+    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (k0 == 0 && c0 + ch < p.n) store_any(out, dtype, row * p.n + c0 + ch, v);
     __syncthreads();
   }
-}
-
-// ---------------------------------------------------------------- channels in vectors of 8
-
-// Rows of a multiple of 8 channels on 16-byte boundaries: a CTA takes a run of
-// consecutive rows, one at a time; a thread holds VPT vectors of 8 channels of
-// it, `blockDim.x` vectors apart.
-constexpr int BN_MAX_WARPS = 32;
-
-// The sum over a CTA, in an order fixed by its size; the same in every thread.
-// `buf` is zero behind the CTA's warps.  It alternates between two halves, so
-// one meeting of the CTA is enough.
-__device__ __forceinline__ float row_sum(float v, float (*buf)[BN_MAX_WARPS], int& turn) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (warps == 1) return v;
-  if (lane == 0) buf[turn][warp] = v;
-  __syncthreads();
-  v = 0.f;
-  for (int w = 0; w < warps; w += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(&buf[turn][w]);
-    v += (x.x + x.y) + (x.z + x.w);
-  }
-  turn ^= 1;
-  return v;
-}
-
-// Eight sums over a CTA of at most 16 warps at once: the lanes split the
-// values among them on the way (fifteen exchanges instead of forty), lane l
-// ends up with value l / 4 of the warp, and then of the CTA.
-__device__ __forceinline__ void row_sums(float (&v)[8], float (*buf)[8][16], int& turn) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int o = 16, k = 4; k; o >>= 1, k >>= 1) {
-    const bool high = lane & o;
-#pragma unroll
-    for (int i = 0; i < k; ++i) {
-      const float keep = high ? v[i + k] : v[i], send = high ? v[i] : v[i + k];
-      v[i] = keep + __shfl_xor_sync(0xffffffffu, send, o);
-    }
-  }
-  float x = v[0];
-  x += __shfl_xor_sync(0xffffffffu, x, 2);
-  x += __shfl_xor_sync(0xffffffffu, x, 1);
-  if (warps > 1) {
-    if ((lane & 3) == 0) buf[turn][lane >> 2][warp] = x;
-    __syncthreads();
-    const float4 y = *reinterpret_cast<const float4*>(&buf[turn][lane >> 2][4 * (lane & 3)]);
-    x = (y.x + y.y) + (y.z + y.w);
-    x += __shfl_xor_sync(0xffffffffu, x, 2);
-    x += __shfl_xor_sync(0xffffffffu, x, 1);
-    turn ^= 1;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __shfl_sync(0xffffffffu, x, 4 * i);
-}
-__device__ __forceinline__ void clear(float* buf, int n) {
-  for (int i = threadIdx.x; i < n; i += blockDim.x) buf[i] = 0.f;
-  __syncthreads();
-}
-
-// 8 channels of a vector over channels (bf16 or fp32, 16-byte aligned).
-__device__ __forceinline__ void load_w8(const void* w, int dtype, int64_t c, f2 (&v)[4]) {
-  if (dtype == DT_BF16) {
-    Raw8<__nv_bfloat16> x;
-    x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
-    x.get2(v);
-  } else {
-    Raw8<float> x;
-    x.load_keep(static_cast<const float*>(w) + c);
-    x.get2(v);
-  }
-}
-
-// Dropout of 8 channels from channel c of token t: bit i keeps channel c + i.
-struct Dropout {
-  uint32_t key[4], below;
-  bool on;
-  __device__ __forceinline__ explicit Dropout(const BlockArgs& p) : below(p.drop_below), on(p.rng != nullptr) {
-    for (int i = 0; i < 4; ++i) key[i] = on ? (uint32_t)load_plain(p.rng + i) : 0;
-  }
-  __device__ __forceinline__ void words(int64_t t, int n, int c, uint4& a, uint4& b) const {
-    const uint64_t i = ((uint64_t)t * (uint32_t)n + (uint32_t)c) >> 2;
-    a = philox(i, key[2], key[3], key[0], key[1]), b = philox(i + 1, key[2], key[3], key[0], key[1]);
-  }
-  __device__ __forceinline__ uint32_t bits(int64_t t, int n, int c) const {
-    uint4 a, b;
-    words(t, n, c, a, b);
-    return (a.x >= below) | (a.y >= below) << 1 | (a.z >= below) << 2 | (a.w >= below) << 3 | (b.x >= below) << 4 |
-           (b.y >= below) << 5 | (b.z >= below) << 6 | (b.w >= below) << 7;
-  }
-};
-__device__ __forceinline__ f2 kept(f2 v, uint32_t bits, int i) {  // pair i of the 8
-  return f2{bits & (1u << (2 * i)) ? v.x : 0.f, bits & (2u << (2 * i)) ? v.y : 0.f};
-}
-
-template <class T>
-struct Pieces {
-  static constexpr int N = sizeof(T) / 2;  // 16-byte pieces of 8 elements
-};
-// A row's vector into a stage of the ring (`to`: this thread's first piece, `step` apart).
-template <class T>
-__device__ __forceinline__ void fetch8(uint4* to, const char* row, int c, int step) {
-  const T* from = reinterpret_cast<const T*>(row) + c;
-#pragma unroll
-  for (int i = 0; i < Pieces<T>::N; ++i) copy16_async(to + i * step, reinterpret_cast<const uint4*>(from) + i);
-}
-
-// Rows of K tensors, one token after the other: all blocks are looked up again
-// where one of them ends.  Steps between rows fit 31 bits (else the kernels for
-// any size run).
-template <int K>
-struct RowCursors {
-  char* ptr[K];  // NULL: no such tensor
-  int32_t step[K];
-  int32_t left;  // tokens from this one to the end of a block
-  template <class P>
-  __device__ __forceinline__ void find(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
-    int64_t until = end;
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const RowTable& r = *tables[k];
-      ptr[k] = nullptr;
-      step[k] = 0;
-      if (!r.count || t >= end) continue;
-      int at = 0;
-      const RowBlock& b = p.blocks[row_block(p.blocks, r, t, at)];
-      const int esize = r.dtype == DT_BF16 ? 2 : 4;
-      ptr[k] = row_at(b, t, esize);
-      step[k] = (int32_t)b.ld * esize;
-      if (at + 1 < r.count) until = min(until, p.blocks[r.first + at + 1].begin);
-    }
-    left = (int32_t)(until - t);
-  }
-  // to token t, the next one
-  template <class P>
-  __device__ __forceinline__ void next(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
-    if (--left > 0) {
-#pragma unroll
-      for (int k = 0; k < K; ++k) ptr[k] += step[k];
-    } else if (t < end) {
-      find(p, tables, t, end);
-    }
-  }
-};
-
-// body(w, v): v's vectors of a weight's channels; the type is looked at once, so
-// that the loads of all vectors can be on their way together.
-template <int VPT, class C, class F>
-__device__ __forceinline__ void each_w8(const void* weight, int dtype, C&& channel, F&& body) {
-  f2 w[4];
-  if (dtype == DT_BF16) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      Raw8<__nv_bfloat16> x;
-      x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(weight) + channel(v)));
-      x.get2(w);
-      body(w, v);
-    }
-  } else {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      Raw8<float> x;
-      x.load_keep(static_cast<const float*>(weight) + channel(v));
-      x.get2(w);
-      body(w, v);
-    }
-  }
-}
-
-// Threads of forward CTAs that an SM's registers are shared among, measured
-// together with the vectors a thread at 8192 x 4096 with dropout: four vectors
-// and 640 threads 51.6 us, two and 768 57.7, eight and 512 64.7.
-constexpr int forward_resident(int vpt, bool ahead, int er) {
-  return vpt == 1 ? 1024 : vpt == 2 ? (ahead ? 768 : 1024) : ahead ? (er == 4 ? 512 : 640) : 768;
-}
-
-// Forward.  AHEAD (x in one part): the next row's loads are on their way while
-// a row is worked on, x's from where it has been unpacked, the residual's from
-// where it has been added.  Else the parts' loads go out four at a time.
-// Threads without a last vector load the row's first one instead and drop it.
-template <class XT, class RT, int VPT, bool AHEAD, class P>
-__global__ void __launch_bounds__(forward_resident(VPT, AHEAD, sizeof(RT)))
-    block_norm_row_kernel(const __grid_constant__ P p) {
-  __shared__ __align__(16) float buf[2][BN_MAX_WARPS];
-  clear(&buf[0][0], 2 * BN_MAX_WARPS);
-  int turn = 0;
-  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
-  const float inv_n = 1.f / (float)n;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
-  // x alone (its parts are looked up where they are read), the residual alone
-  // (its loads go out later), the outputs
-  const RowTable *const tx[1] = {&p.x}, *const tr[1] = {&p.r}, *const to[2] = {&p.h, &p.y};
-  RowCursors<1> cx, cr;
-  RowCursors<2> out;
-  cx.find(p, tx, t0, t1);
-  cr.find(p, tr, t0, t1);
-  out.find(p, to, t0, t1);
-  const int parts = p.x.parts;
-  int at = 0;
-  // vectors below the last two are there in every thread
-  const bool last = tid + (VPT - 1) * nt < n / 8, last_but_one = tid + (VPT - 2) * nt < n / 8;
-  auto has = [&](int v) { return v < VPT - 2 || (v == VPT - 1 ? last : last_but_one); };
-  auto channel = [&](int v) { return has(v) ? (tid + v * nt) * 8 : 0; };
-  const bool res = p.r.count > 0;
-  wait_for_previous_kernel();  // (until here: parameters and shared memory alone)
-  const Dropout drop(p);
-  Raw8<XT> x[VPT];
-  Raw8<RT> r[VPT];
-  auto load_x = [&](const char* row) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) x[v].load(reinterpret_cast<const XT*>(row) + channel(v));
-  };
-  auto load_r = [&] {
-    if (!res) return;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) r[v].load(reinterpret_cast<const RT*>(cr.ptr[0]) + channel(v));
-  };
-  if (AHEAD && t0 < t1) {
-    load_x(cx.ptr[0]);
-    load_r();
-  }
-  const int64_t seg0 = p.gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0;
-  int64_t seg_end = (seg0 + 1) * p.gate_per;
-  const char* gate = static_cast<const char*>(p.gate);
-  const int64_t gate_step = (int64_t)n * (p.gate_dtype == DT_BF16 ? 2 : 4);
-  if (gate) gate += seg0 * gate_step;
-  // a vector a thread: its weights stay in registers
-  constexpr bool KEEP = VPT == 1;
-  f2 w_post[4], w_gate[4], w_pre[4];
-  if (KEEP) {
-    if (p.post) load_w8(p.post, p.post_dtype, channel(0), w_post);
-    if (gate) load_w8(gate, p.gate_dtype, channel(0), w_gate);
-    if (p.pre) load_w8(p.pre, p.pre_dtype, channel(0), w_pre);
-  }
-  auto weigh = [&](const void* weight, int dtype, const f2(&w)[4], auto&& body) {
-    if constexpr (KEEP) body(w, 0);
-    else each_w8<VPT>(weight, dtype, channel, body);
-  };
-  for (int64_t t = t0; t < t1; ++t) {
-    f2 h[VPT][4];
-    auto unpack = [&](int v, f2(&w)[4]) {
-      x[v].get2(w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = has(v) ? w[i] : both(0.f);
-    };
-    if constexpr (AHEAD) {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) unpack(v, h[v]);
-      if (t + 1 < t1) {
-        cx.next(p, tx, t + 1, t1);
-        load_x(cx.ptr[0]);
-      }
-    } else {
-      load_r();
-      const int block = row_block(p.blocks, p.x, t, at);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = both(0.f);
-#pragma unroll 4
-      for (int k = 0; k < parts; ++k) {
-        load_x(k ? row_at(p.blocks[block + k * p.x.count], t, sizeof(XT)) : cx.ptr[0]);
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) {
-          f2 w[4];
-          unpack(v, w);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) h[v][i] = k ? h[v][i] + w[i] : w[i];
-        }
-      }
-      cx.next(p, tx, t + 1, t1);
-    }
-    auto total = [&] {
-      f2 s = both(0.f);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s = fma2(h[v][i], h[v][i], s);
-      return rsqrtf(row_sum(s.x + s.y, buf, turn) * inv_n + p.eps);
-    };
-    if (p.post) {
-      const f2 rx = both(total());
-      weigh(p.post, p.post_dtype, w_post, [&](const f2(&w)[4], int v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = h[v][i] * rx * w[i];
-      });
-    }
-    if (gate) {
-      if (t == seg_end) {
-        gate += gate_step;
-        seg_end += p.gate_per;
-        if (KEEP) load_w8(gate, p.gate_dtype, channel(0), w_gate);
-      }
-      weigh(gate, p.gate_dtype, w_gate, [&](const f2(&w)[4], int v) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = h[v][i] * w[i];
-      });
-    }
-    if (drop.on) {
-      // the words in a loop of two vectors a round: unrolled, the code does not stay in the instruction cache
-      uint64_t keep = 0;
-#pragma unroll 2
-      for (int v = 0; v < VPT; ++v) keep |= (uint64_t)drop.bits(t, n, (tid + v * nt) * 8) << (8 * v);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = kept(h[v][i] * both(p.drop_scale), (uint32_t)(keep >> (8 * v)), i);
-    }
-    if (res) {
-      const f2 scale = both(p.scale);
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        f2 w[4];
-        r[v].get2(w);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = has(v) ? fma2(scale, w[i], h[v][i]) : h[v][i];
-      }
-      cr.next(p, tr, t + 1, t1);
-      if (AHEAD && t + 1 < t1) load_r();
-    }
-    if (out.ptr[0]) {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v)
-        if (has(v)) store8(reinterpret_cast<RT*>(out.ptr[0]) + channel(v), h[v]);
-    }
-    if (out.ptr[1]) {
-      const f2 rh = both(total());
-      weigh(p.pre, p.pre_dtype, w_pre, [&](const f2(&w)[4], int v) {
-        f2 y[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = h[v][i] * rh * w[i];
-        if (has(v)) store8(reinterpret_cast<XT*>(out.ptr[1]) + channel(v), y);
-      });
-    }
-    out.next(p, to, t + 1, t1);
-  }
-}
-
-// Gradients.  A CTA keeps the sums over its tokens and the weights in
-// registers; x, dy, the residual and dh come through a ring of S rows.  Three
-// things keep the work per element small.
-//  - The means' sums are taken at once: with a = w s (w = gate post / (1 - p),
-//    0 where dropped), h = scale residual + r(s) a and g = dh + r(h) z - k h,
-//    the sum of a g is made of those of a dh, a z and a h; and (S > 1) the next
-//    row's sum of s^2 goes with them, so the CTA meets once a row.
-//  - dgate and dpost are one sum: with q = sum over the tokens of a gate row
-//    of g s r(s) (kept elements), dgate = post q / (1 - p), and dpost adds up
-//    gate q / (1 - p).
-//  - What an operand is missing for is 0 (or, of w, 1) and computed all the same.
-template <class XT, class RT, int VPT, int S, class P>
-__global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __grid_constant__ P p) {
-  __shared__ __align__(16) float buf[2][8][16];
-  extern __shared__ uint4 ring[];
-  clear(&buf[0][0][0], 2 * 8 * 16);
-  int turn = 0;
-  const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
-  const float inv_n = 1.f / (float)n;
-  constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N, STAGE = 2 * VPT * (PX + PR);
-  constexpr bool HOLD = VPT == 1;  // a row's values stay in registers between the two looks at it
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
-  const RowTable *const tin[4] = {&p.x, &p.y, &p.r, &p.h}, *const tout[2] = {&p.dx, &p.dr};
-  RowCursors<4> in;
-  RowCursors<2> out;
-  in.find(p, tin, t0, t1);
-  out.find(p, tout, t0, t1);
-  const bool has_y = p.y.count > 0, res = p.r.count > 0, has_h = p.h.count > 0, post = p.post, gate = p.gate;
-  wait_for_previous_kernel();  // (until here: parameters and shared memory alone)
-  const Dropout drop(p);
-  auto channel = [&](int v) { return (v * nt + tid) * 8; };
-  uint4* const mine = ring + tid;
-  int64_t tf = t0;
-  auto fetch = [&](uint4* to) {
-    if (tf < t1) {
-#pragma unroll
-      for (int v = 0; v < VPT; ++v) {
-        const int c = channel(v);
-        if (c >= n) break;
-        fetch8<XT>(to + v * PX * nt, in.ptr[0], c, nt);
-        if (has_y) fetch8<XT>(to + (VPT + v) * PX * nt, in.ptr[1], c, nt);
-        if (res) fetch8<RT>(to + (2 * VPT * PX + v * PR) * nt, in.ptr[2], c, nt);
-        if (has_h) fetch8<RT>(to + (2 * VPT * PX + (VPT + v) * PR) * nt, in.ptr[3], c, nt);
-      }
-      ++tf;
-      in.next(p, tin, tf, t1);
-    }
-    copies_commit();
-  };
-  for (int i = 0; i < S; ++i) {  // places that no copy fills are 0
-    uint4* to = mine + i * STAGE * nt;
-#pragma unroll
-    for (int k = 0; k < STAGE; ++k) {
-      const int v = k < 2 * VPT * PX ? k / PX % VPT : (k - 2 * VPT * PX) / PR % VPT;
-      const bool there = k < VPT * PX ? true : k < 2 * VPT * PX ? has_y : k < 2 * VPT * PX + VPT * PR ? res : has_h;
-      if (!there || channel(v) >= n) to[k * nt] = make_uint4(0, 0, 0, 0);
-    }
-  }
-  for (int i = 0; i < S; ++i) fetch(mine + i * STAGE * nt);
-  f2 s_pre[VPT][4], s_post[VPT][4], q_gate[VPT][4], w_pre[VPT][4], w[VPT][4];
-  int64_t seg = gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0, seg_end = (seg + 1) * p.gate_per;
-  auto weights = [&] {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = channel(v);
-      if (c >= n) break;
-      f2 a[4], b[4];
-      if (post) load_w8(p.post, p.post_dtype, c, a);
-      if (gate) load_w8(p.gate, p.gate_dtype, seg * n + c, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[v][i] = both(p.drop_scale);
-        if (post) w[v][i] = w[v][i] * a[i];
-        if (gate) w[v][i] = w[v][i] * b[i];
-      }
-    }
-  };
-#pragma unroll
-  for (int v = 0; v < VPT; ++v)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_pre[v][i] = s_post[v][i] = q_gate[v][i] = w_pre[v][i] = w[v][i] = both(0.f);
-  weights();
-  if (has_y) {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v)
-      if (channel(v) < n) load_w8(p.pre, p.pre_dtype, channel(v), w_pre[v]);
-  }
-  auto write_sums = [&](float* to, int v, const f2(&s)[4]) {
-    float4* o = reinterpret_cast<float4*>(to + channel(v));
-    o[0] = make_float4(s[0].x, s[0].y, s[1].x, s[1].y);
-    o[1] = make_float4(s[2].x, s[2].y, s[3].x, s[3].y);
-  };
-  // the end of a gate row's tokens (or, without a gate, of the CTA's)
-  auto close = [&] {
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = channel(v);
-      if (c >= n) break;
-      f2 a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = b[i] = both(1.f);
-        q_gate[v][i] = q_gate[v][i] * both(p.drop_scale);
-      }
-      if (post) load_w8(p.post, p.post_dtype, c, a);
-      if (gate) load_w8(p.gate, p.gate_dtype, seg * n + c, b);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = a[i] * q_gate[v][i];
-        s_post[v][i] = fma2(b[i], q_gate[v][i], s_post[v][i]);
-        q_gate[v][i] = both(0.f);
-      }
-      if (!gate) continue;
-      if (p.gate_per != 1) write_sums(p.part_gate + ((int64_t)blockIdx.x + seg) * n, v, a);
-      else if (p.dgate_dtype == DT_BF16) store8(static_cast<__nv_bfloat16*>(p.dgate) + seg * n + c, a);
-      else store8(static_cast<float*>(p.dgate) + seg * n + c, a);
-    }
-  };
-  auto square = [&](const uint4* from) {  // this thread's share of the sum of s^2
-    f2 s = both(0.f);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      Raw8<XT> r;
-      r.set(from + v * PX * nt, nt);
-      f2 x[4];
-      r.get2(x);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(x[i], x[i], s);
-    }
-    return s.x + s.y;
-  };
-  float rx = 1.f;
-  int slot = 0;
-  const f2 scale = both(p.scale);
-  for (int64_t t = t0; t < t1; ++t) {
-    uint4* const from = mine + slot * STAGE * nt;
-    if (++slot == S) slot = 0;
-    copies_wait<(S > 1 ? S - 2 : 0)>();  // this row and (S > 1) the next
-    float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (post && (S == 1 || t == t0)) {
-      q[0] = square(from);
-      row_sums(q, buf, turn);
-      rx = rsqrtf(q[0] * inv_n + p.eps);
-    }
-    uint32_t bits[VPT];
-    f2 x[4], h[4], dy[4], dh[4];  // of one vector
-    auto values = [&](int v) {
-      Raw8<XT> xw, yw;
-      Raw8<RT> rw, hw;
-      xw.set(from + v * PX * nt, nt);
-      yw.set(from + (VPT + v) * PX * nt, nt);
-      rw.set(from + (2 * VPT * PX + v * PR) * nt, nt);
-      hw.set(from + (2 * VPT * PX + (VPT + v) * PR) * nt, nt);
-      xw.get2(x), yw.get2(dy), rw.get2(h), hw.get2(dh);
-    };
-    auto branch = [&](int v, int i) {  // a
-      const f2 a = x[i] * w[v][i];
-      return drop.on ? kept(a, bits[v], i) : a;
-    };
-    f2 sum[5] = {both(0.f), both(0.f), both(0.f), both(0.f), both(0.f)};
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      if (drop.on) bits[v] = drop.bits(t, n, channel(v));
-      values(v);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 a = branch(v, i), z = dy[i] * w_pre[v][i];
-        h[i] = fma2(scale, h[i], a * both(rx));
-        sum[0] = fma2(h[i], h[i], sum[0]);
-        sum[1] = fma2(h[i], z, sum[1]);
-        sum[2] = fma2(a, dh[i], sum[2]);
-        sum[3] = fma2(a, z, sum[3]);
-        sum[4] = fma2(a, h[i], sum[4]);
-      }
-    }
-    float rh = 0.f, kh = 0.f, kx = 0.f, next_rx = 1.f;
-    if (has_y || post) {
-#pragma unroll
-      for (int i = 0; i < 5; ++i) q[i] = sum[i].x + sum[i].y;
-      q[5] = q[6] = q[7] = 0.f;
-      if (S > 1 && post && t + 1 < t1) q[5] = square(mine + slot * STAGE * nt);
-      row_sums(q, buf, turn);
-      if (has_y) {
-        rh = rsqrtf(q[0] * inv_n + p.eps);
-        kh = rh * rh * rh * (q[1] * inv_n);
-      }
-      if (post) {
-        kx = rx * rx * rx * ((q[2] + rh * q[3] - kh * q[4]) * inv_n);
-        next_rx = rsqrtf(q[5] * inv_n + p.eps);
-      }
-    }
-    const f2 rx2 = both(rx), rh2 = both(rh), kh2 = both(-kh), kx2 = both(-kx);
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-      const int c = channel(v);
-      if (!HOLD) {
-        values(v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fma2(scale, h[i], branch(v, i) * rx2);
-      }
-      f2 o[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        f2 g = dh[i], xr = x[i] * rx2;
-        if (has_y) {  // (a choice: kh may not be finite where h is 0)
-          g = fma2(dy[i] * w_pre[v][i], rh2, fma2(h[i], kh2, g));
-          s_pre[v][i] = fma2(dy[i], h[i] * rh2, s_pre[v][i]);
-        }
-        dh[i] = g * scale;
-        if (drop.on) g = kept(g, bits[v], i), xr = kept(xr, bits[v], i);  // (what is dropped may be NaN)
-        q_gate[v][i] = fma2(g, xr, q_gate[v][i]);
-        o[i] = g * w[v][i];
-        if (post) o[i] = fma2(o[i], rx2, x[i] * kx2);
-      }
-      if (c < n) {
-        if (out.ptr[1]) store8(reinterpret_cast<RT*>(out.ptr[1]) + c, dh);
-        if (out.ptr[0]) store8(reinterpret_cast<XT*>(out.ptr[0]) + c, o);
-      }
-    }
-    out.next(p, tout, t + 1, t1);
-    fetch(from);
-    if (S > 1) rx = next_rx;
-    if (t + 1 == t1) {
-      close();
-    } else if (gate && t + 1 == seg_end) {
-      close();
-      ++seg;
-      seg_end += p.gate_per;
-      weights();
-    }
-  }
-#pragma unroll
-  for (int v = 0; v < VPT; ++v) {
-    if (channel(v) >= n) break;
-    if (has_y) write_sums(p.part_pre + (int64_t)blockIdx.x * n, v, s_pre[v]);
-    if (post) write_sums(p.part_post + (int64_t)blockIdx.x * n, v, s_post[v]);
-  }
-  copies_wait<0>();
 }
 
 // ---------------------------------------------------------------- host
@@ -877,23 +261,17 @@ dt_status channel_vector(const dt_dtensor* w, const char* what, const Layout& of
 // Rows of the gate's sums in the workspace beyond one per CTA.
 int64_t gate_part_rows(int64_t tokens, int64_t gate_rows) { return gate_rows == tokens ? 0 : gate_rows; }
 
-// How a launch covers its rows.
-struct Shape {
-  int threads = 0, vpt = 0, grid = 0;  // vpt 0: the kernels for any size
-  int stages = 0;  // backward: rows of the ring
-  bool ahead = false;  // forward: the next row's loads go out early
-  size_t smem = 0;
-};
-
 int round_up(int64_t a, int b) { return (int)((a + b - 1) / b * b); }
 constexpr int64_t BN_SMEM = 224 * 1024;  // of an SM, for rings
-constexpr int64_t BN_STATIC = 2048;      // a CTA's other shared memory, at most
+constexpr int64_t BN_STATIC = 2560;      // a CTA's other shared memory, at most
 
-Shape forward_shape(const BlockArgs& p, bool vec, bool small) {
-  Shape s;
+// vec: no step between rows is beyond what the kernels on vectors count in;
+// even: rows of a multiple of 8 channels on 16-byte boundaries; small: few row blocks.
+BlockShape forward_shape(const BlockArgs& p, bool vec, bool even, bool small) {
+  BlockShape s;
   const int sms = device_sm_count();
-  const int64_t vectors = p.n / 8;
-  if (!vec || vectors > 4 * 512) {
+  const int64_t vectors = ((int64_t)p.n + 7) / 8;
+  if (!vec || vectors > 4 * 512 || (!even && !small)) {
     s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * 8);
     return s;
   }
@@ -905,67 +283,49 @@ Shape forward_shape(const BlockArgs& p, bool vec, bool small) {
   if (p.tokens <= 2 * sms && vectors <= 1024) s.vpt = 1;
   else if (vectors <= 64 || (vectors <= 1024 && 8 * threads(2) < 13 * threads(4))) s.vpt = vectors <= 32 ? 1 : 2;
   s.threads = threads(s.vpt);
-  s.ahead = small && p.x.parts == 1 && p.tokens > 2 * sms;
-  const int ctas = std::max(1, std::min(32, forward_resident(s.vpt, s.ahead, dtype_size(p.h.dtype)) / s.threads));
+  s.even = even;
+  s.ahead = small && even && p.x.parts == 1 && p.tokens > 2 * sms;
+  const int ctas = std::max(1, std::min(32, block_forward_resident(s.vpt, s.ahead, dtype_size(p.h.dtype)) / s.threads));
   s.grid = (int)std::min<int64_t>(p.tokens, (int64_t)sms * ctas);
   return s;
 }
 
-Shape backward_shape(const BlockArgs& p, bool vec, bool small) {
-  Shape s;
+BlockShape backward_shape(const BlockArgs& p, bool vec, bool even, bool small, int* runs) {
+  BlockShape s;
   const int sms = device_sm_count();
-  const int64_t vectors = p.n / 8;
+  const int64_t vectors = ((int64_t)p.n + 7) / 8;
   int64_t most = 2 * sms;
-  if (vec && small && p.x.parts == 1 && vectors <= 1024) {
+  if (vec && small && vectors <= 2048) {
+    s.cluster = vectors <= 1024 ? 1 : 2;
     s.vpt = vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 85.9 us, one 91.0)
-    s.threads = round_up((vectors + s.vpt - 1) / s.vpt, 32);
-    const int64_t stage = (int64_t)s.threads * s.vpt * 16 * (dtype_size(p.x.dtype) + dtype_size(p.h.dtype));
+    s.threads = round_up((vectors + s.vpt * s.cluster - 1) / (s.vpt * s.cluster), 32);
+    s.even = even;
+    const int64_t stage = (int64_t)s.threads * s.vpt * 8 *
+                          ((p.x.parts + 1) * dtype_size(p.x.dtype) + 2 * dtype_size(p.h.dtype));
     const int64_t ctas = std::min(8, 512 / s.threads);
-    s.stages = s.vpt == 1 && (5 * stage + BN_STATIC) * ctas <= BN_SMEM ? 5 : (3 * stage + BN_STATIC) * ctas <= BN_SMEM ? 3 : 1;
+    s.stages = !even || p.x.parts > 1                                      ? 1
+               : s.vpt == 1 && (5 * stage + BN_STATIC) * ctas <= BN_SMEM ? 5
+               : (3 * stage + BN_STATIC) * ctas <= BN_SMEM               ? 3
+                                                                         : 1;
     s.smem = stage * s.stages;
-    most = std::max<int64_t>(1, std::min<int64_t>(ctas, BN_SMEM / (int64_t)(s.smem + BN_STATIC))) * sms;
+    if (stage + BN_STATIC > BN_SMEM) s = BlockShape();
+    else most = std::min<int64_t>(ctas, BN_SMEM / (int64_t)(s.smem + BN_STATIC)) * sms / s.cluster;
   }
-  // four tokens a CTA at least, for its sums are written and read again
-  most = std::min<int64_t>(most, std::max<int64_t>(sms, (p.tokens + 3) / 4));
-  s.grid = (int)std::max<int64_t>(1, std::min<int64_t>({p.tokens, most, max_backward_blocks(p.n)}));
+  // four tokens a run at least, for its sums are written and read again
+  most = std::min<int64_t>(most, std::max<int64_t>(sms / s.cluster, (p.tokens + 3) / 4));
+  *runs = (int)std::max<int64_t>(1, std::min<int64_t>({p.tokens, most, max_backward_blocks(p.n)}));
+  s.grid = *runs * s.cluster;
   return s;
 }
 
-template <class K, class P>
-cudaError_t launch_rows(K kernel, const P& p, const Shape& s, cudaStream_t stream) {
-  if (s.smem > 40 * 1024)
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem)) return e;
-  return launch_early(kernel, dim3(s.grid), s.threads, s.smem, stream, p);
-}
-
-template <class XT, class RT, class P>
-cudaError_t launch_typed(const P& p, bool bwd, const Shape& s, cudaStream_t stream) {
-#define DT_BN_BACK(VPT, S) \
-  if (s.vpt == VPT && s.stages == S) return launch_rows(block_norm_row_backward_kernel<XT, RT, VPT, S, P>, p, s, stream);
-  if constexpr (P::kCap == BlockSmall::kCap) {
-    if (bwd) {
-      DT_BN_BACK(1, 5) DT_BN_BACK(1, 3) DT_BN_BACK(2, 3) DT_BN_BACK(2, 1)
-      return cudaErrorInvalidValue;
-    }
-    if (s.ahead)
-      return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, true, P>, p, s, stream)
-             : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, true, P>, p, s, stream)
-                          : launch_rows(block_norm_row_kernel<XT, RT, 4, true, P>, p, s, stream);
-  }
-  return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, false, P>, p, s, stream)
-         : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, false, P>, p, s, stream)
-                      : launch_rows(block_norm_row_kernel<XT, RT, 4, false, P>, p, s, stream);
-#undef DT_BN_BACK
-}
-
 template <class P>
-cudaError_t launch_block(const P& p, bool bwd, const Shape& s, cudaStream_t stream) {
+cudaError_t launch_block(const P& p, bool bwd, const BlockShape& s, cudaStream_t stream) {
   if (!s.vpt)
     return bwd ? launch_early(block_norm_any_kernel<P, true>, dim3(s.grid), BN_ANY_THREADS, 0, stream, p)
                : launch_early(block_norm_any_kernel<P, false>, dim3(s.grid), BN_ANY_THREADS, 0, stream, p);
-  if (p.x.dtype == DT_FP32) return launch_typed<float, float>(p, bwd, s, stream);
-  if (p.h.dtype == DT_FP32) return launch_typed<__nv_bfloat16, float>(p, bwd, s, stream);
-  return launch_typed<__nv_bfloat16, __nv_bfloat16>(p, bwd, s, stream);
+  if (p.x.dtype == DT_FP32) return block_rows_fp32(p, bwd, s, stream);
+  if (p.h.dtype == DT_FP32) return block_rows_mixed(p, bwd, s, stream);
+  return block_rows_bf16(p, bwd, s, stream);
 }
 
 dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, int32_t* d_status, cudaStream_t stream) {
@@ -993,12 +353,12 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   int used = 0;
   RowOperand X;
   const void* anchor = nullptr;  // something that the call writes
-  bool vec = true;
+  bool even = true;
   auto add = [&](const RowOperand& o, RowTable* t) {
     *t = RowTable{(int16_t)used, (int16_t)o.count, (int16_t)o.parts, (int16_t)o.dtype};
     std::copy(o.block, o.block + o.count * o.parts, p.blocks + used);
     used += o.count * o.parts;
-    vec = vec && o.vec16;
+    even = even && o.vec16;
   };
   if ((st = row_operand(A.x, "x", A.tp, false, true, &X, &lx)) != DT_OK) return st;
   add(X, &p.x);
@@ -1083,22 +443,24 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   if (!anchor && p.dgate && X.n > 0 && p.tokens > 0) anchor = p.dgate;
   if (X.n == 0 || !anchor) return DT_OK;
   if ((st = bind_device_of(anchor)) != DT_OK) return st;
-  vec = vec && X.n % 8 == 0;
+  even = even && X.n % 8 == 0;
+  for (const void* v : {p.post, p.gate, p.pre}) even = even && reinterpret_cast<uintptr_t>(v) % 16 == 0;
+  even = even && (p.gate_per != 1 || reinterpret_cast<uintptr_t>(p.dgate) % 16 == 0);
+  bool vec = true;
   for (int i = 0; i < used; ++i) vec = vec && p.blocks[i].ld < (1 << 29);  // steps between rows in 31 bits
-  for (const void* v : {p.post, p.gate, p.pre}) vec = vec && reinterpret_cast<uintptr_t>(v) % 16 == 0;
   const bool small = used <= BlockSmall::kCap;
-  const Shape shape = bwd ? backward_shape(p, vec, small) : forward_shape(p, vec, small);
-  p.grid = shape.grid;
+  const BlockShape shape = bwd ? backward_shape(p, vec, even, small, &p.runs) : forward_shape(p, vec, even, small);
+  p.pitch = round_up(X.n, 8);
   if (sums) {
-    const int64_t rows_pre = p.dpre ? p.grid : 0, rows_post = p.dpost ? p.grid : 0;
-    const int64_t rows_gate = p.dgate && p.gate_per != 1 ? p.grid + p.gate_rows : 0;
-    const size_t need = (size_t)(rows_pre + rows_post + rows_gate) * X.n * sizeof(float);
+    const int64_t rows_pre = p.dpre ? p.runs : 0, rows_post = p.dpost ? p.runs : 0;
+    const int64_t rows_gate = p.dgate && p.gate_per != 1 ? p.runs + p.gate_rows : 0;
+    const size_t need = (size_t)(rows_pre + rows_post + rows_gate) * p.pitch * sizeof(float);
     if (!ws || ws_bytes < need)
       return fail(DT_ERR_INVALID_ARG, "workspace of %zu bytes, %zu needed", ws ? ws_bytes : (size_t)0, need);
     if (reinterpret_cast<uintptr_t>(ws) % 256) return fail(DT_ERR_ALIGNMENT, "workspace must be 256-byte aligned");
     p.part_pre = static_cast<float*>(ws);
-    p.part_post = p.part_pre + rows_pre * X.n;
-    p.part_gate = p.part_post + rows_post * X.n;
+    p.part_post = p.part_pre + rows_pre * p.pitch;
+    p.part_gate = p.part_post + rows_post * p.pitch;
   }
   cudaError_t e = cudaSuccess;
   if (p.tokens > 0) {
@@ -1116,8 +478,8 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   }
   if (sums) {
     const int64_t which = 2 + (p.dgate && p.gate_per != 1 ? p.gate_rows : 0);
-    e = launch_early(block_norm_sums_kernel, dim3((unsigned)((X.n + 31) / 32), (unsigned)std::min<int64_t>(which, 4096)),
-                     BN_SUM_THREADS, 0, stream, static_cast<const BlockArgs&>(p));
+    const dim3 grid((unsigned)((X.n + BN_SUM_CHANNELS - 1) / BN_SUM_CHANNELS), (unsigned)std::min<int64_t>(which, 4096));
+    e = launch_early(block_norm_sums_kernel, grid, BN_SUM_THREADS, 0, stream, static_cast<const BlockArgs&>(p));
     if (e != cudaSuccess) return fail(DT_ERR_CUDA, "block_norm sums launch: %s", cudaGetErrorString(e));
     count_launch();
   }
@@ -1163,6 +525,6 @@ extern "C" dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, in
     return fail(DT_ERR_INVALID_ARG, "tokens %lld, channels %lld, gate_rows %lld", (long long)tokens,
                 (long long)channels, (long long)gate_rows);
   if (gate_rows > std::max<int64_t>(tokens, 1)) return fail(DT_ERR_SHAPE, "more gate rows than tokens");
-  *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * channels * sizeof(float);
+  *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * ((channels + 7) / 8 * 8) * sizeof(float);
   return DT_OK;
 }

@@ -13,6 +13,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "cluster_sm103.cuh"
 #include "heads_sm103.cuh"
 #include "row_operands.h"
 
@@ -308,25 +309,6 @@ __device__ __forceinline__ void soft_unit(Soft& a, Vec<T> (&v)[LP_VECS], float m
   if (ENT) a.e += e1.x + e1.y;
 }
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t first_ctas(const void* p) {  // the same object in the cluster's first CTA
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_u32(p)));
-  return r;
-}
-__device__ __forceinline__ void store_cluster(uint32_t a, uint64_t v) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(v) : "memory");
-}
-__device__ __forceinline__ void store_cluster(uint32_t a, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
-}
-
 // How many of the n numbers at x (16-byte aligned) are larger.
 __device__ __forceinline__ int count_larger(const uint64_t* x, int n, uint64_t mine) {
   int above = 0;
@@ -529,17 +511,17 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
   if (ctas > 1) {
     cluster_wait();  // the first CTA is there
     if (threadIdx.x == 0) {
-      store_cluster(first_ctas(&meet[rank].m), a.m);
-      store_cluster(first_ctas(&meet[rank].s), a.s);
-      store_cluster(first_ctas(&meet[rank].e), a.e);
+      store_cluster(in_cta(&meet[rank].m, 0), a.m);
+      store_cluster(in_cta(&meet[rank].s, 0), a.s);
+      store_cluster(in_cta(&meet[rank].e, 0), a.e);
     }
     if (TOP) {  // this CTA's k best, and zeros where it has fewer
       for (int i = threadIdx.x; i < total; i += blockDim.x) {
         const int r = count_larger(cand, total, cand[i]);
-        if (r < p.top) store_cluster(first_ctas(&recv[rank * p.top + r]), cand[i]);
+        if (r < p.top) store_cluster(in_cta(&recv[rank * p.top + r], 0), cand[i]);
       }
       for (int i = total + (int)threadIdx.x; i < p.top; i += blockDim.x)
-        store_cluster(first_ctas(&recv[rank * p.top + i]), (uint64_t)0);
+        store_cluster(in_cta(&recv[rank * p.top + i], 0), (uint64_t)0);
     }
     cluster_arrive();
     cluster_wait();
