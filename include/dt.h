@@ -549,7 +549,8 @@ DT_API dt_status dt_tp_kv4_attention_workspace_size(const dt_dtensor* q, const d
  * is kept when word i % 4 of Philox4x32-10 at the counter (i / 4 in 64 bits,
  * rng[2], rng[3]) under the key (rng[0], rng[1]) is at least
  * floor(dropout * 2^32): the mask depends on the element alone, not on the
- * layout, and is not stored.  What a dropped element holds does not reach h.
+ * layout, and is not stored.  Without post_weight, what a dropped element of x
+ * holds reaches nothing.  With eps 0 a row of zeros gives NaN.
  */
 DT_API dt_status dt_tp_block_norm(const dt_dtensor* x, const dt_dtensor* residual, const dt_dtensor* post_weight,
                                   const dt_dtensor* gate, const dt_dtensor* pre_weight, const dt_dtensor* rng,

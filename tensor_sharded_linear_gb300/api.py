@@ -798,7 +798,7 @@ def tp_block_norm_backward(dh: Optional[DTensor], dy: Optional[DTensor], x: DTen
                                x.slots[0].device)
     L.check(L.untyped("dt_tp_block_norm_backward")(
         _ref(dh), _ref(dy), _ref(x), _ref(residual), _ref(post_weight), _ref(gate), _ref(pre_weight), _ref(rng),
-        *(_ref(o) for o in out), C.c_float(eps), C.c_float(residual_scale), C.c_float(dropout),
+        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), _ref(out[4]), C.c_float(eps), C.c_float(residual_scale), C.c_float(dropout),
         _tp_index(x.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()), "tp_block_norm_backward")
     return tuple(out)
 
@@ -829,10 +829,11 @@ def tp_log_probs(logits: DTensor, ids: Optional[DTensor] = None, *, scale: float
 
         out = (None if ids is None else empty(ids.gshape), empty(lead), empty(lead) if entropy else None,
                empty(lead + (top,)) if top else None, empty(lead + (top,), torch.int32) if top else None)
-    L.check(L.untyped("dt_tp_log_probs")(_ref(logits), _ref(ids), *(_ref(o) for o in out), C.c_float(scale),
-                                         int(ignore_index), _tp_index(logits.mesh, tp_dim), None, _stream_arg()),
-            "tp_log_probs")
-    return TokenLogProbs(*out)
+    lp, lse, ent, top_lp, top_ids = out
+    L.check(L.untyped("dt_tp_log_probs")(_ref(logits), _ref(ids), _ref(lp), _ref(lse), _ref(ent), _ref(top_lp),
+                                         _ref(top_ids), C.c_float(scale), int(ignore_index),
+                                         _tp_index(logits.mesh, tp_dim), None, _stream_arg()), "tp_log_probs")
+    return TokenLogProbs(lp, lse, ent, top_lp, top_ids)
 
 
 def tp_log_probs_backward(dlogprobs: Optional[DTensor], dentropy: Optional[DTensor], logits: DTensor,
@@ -848,6 +849,25 @@ def tp_log_probs_backward(dlogprobs: Optional[DTensor], dentropy: Optional[DTens
                                                   _tp_index(logits.mesh, tp_dim), None, _stream_arg()),
             "tp_log_probs_backward")
     return d
+
+
+def tp_head_log_probs(x: DTensor, w_head: DTensor, ids: Optional[DTensor] = None, *, residual: Optional[DTensor] = None,
+                      post_weight: Optional[DTensor] = None, gate: Optional[DTensor] = None,
+                      pre_weight: Optional[DTensor] = None, eps: float = 1e-6, residual_scale: float = 1.0,
+                      scale: float = 1.0, top: int = 0, entropy: bool = False, ignore_index: int = -100, tp_dim="tp",
+                      logits_dtype=None) -> TokenLogProbs:
+    """The end of a decoder: the last block's ``tp_block_norm``, the column-parallel head, ``tp_log_probs``.
+
+    x [..., hidden] is the last block's output (Partial, token-sharded or
+    Replicate), ``w_head`` [hidden, vocabulary] is Shard(1).  The logits stay on
+    their shards, in ``logits_dtype`` (x's without one).  With none of residual,
+    weights and gate x goes into the head as it is."""
+    if any(o is not None for o in (residual, post_weight, gate, pre_weight)):
+        h, y = tp_block_norm(x, residual, post_weight, gate, pre_weight, eps=eps, residual_scale=residual_scale,
+                             tp_dim=tp_dim)
+        x = h if y is None else y
+    logits = column_parallel_linear(x, w_head, tp_dim=tp_dim, out_dtype=logits_dtype)
+    return tp_log_probs(logits, ids, scale=scale, top=top, entropy=entropy, ignore_index=ignore_index, tp_dim=tp_dim)
 
 
 # ---------------------------------------------------------------- DTorch-style layers
