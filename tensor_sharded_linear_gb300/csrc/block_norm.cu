@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
   if (p.rng)
     for (int i = 0; i < 4; ++i) rng[i] = (uint32_t)load_plain(p.rng + i);
   // forward: tokens one after the other over the CTAs; backward: a run of consecutive tokens per CTA
-  const int64_t t0 = BWD ? (int64_t)blockIdx.x * p.tokens / gridDim.x : blockIdx.x;
-  const int64_t t1 = BWD ? (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x : p.tokens;
+  const int64_t t0 = BWD ? run_begin(p, blockIdx.x) : blockIdx.x;
+  const int64_t t1 = BWD ? run_begin(p, blockIdx.x + 1) : p.tokens;
   int ax = 0, ar = 0, ah = 0, ay = 0, adx = 0, adr = 0;
   for (int64_t t = t0; t < t1; t += BWD ? 1 : gridDim.x) {
     const int bx = row_block(p.blocks, p.x, t, ax);
@@ -203,8 +203,8 @@ __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const _
     if (which >= 2) {  // the runs that hold tokens of this row, and their sums' places
       row = which - 2;
       if (p.tokens) {
-        b0 = ((row * p.gate_per + 1) * p.runs - 1) / p.tokens + row;
-        b1 = ((row + 1) * p.gate_per * p.runs - 1) / p.tokens + 1 + row;
+        b0 = run_of(p, row * p.gate_per) + row;
+        b1 = run_of(p, (row + 1) * p.gate_per - 1) + 1 + row;
       }
     }
     const int64_t c = c0 + lane * 4;
@@ -450,7 +450,10 @@ dt_status block_call(bool bwd, const BlockCall& A, void* ws, size_t ws_bytes, in
   for (int i = 0; i < used; ++i) vec = vec && p.blocks[i].ld < (1 << 29);  // steps between rows in 31 bits
   const bool small = used <= BlockSmall::kCap;
   const BlockShape shape = bwd ? backward_shape(p, vec, even, small, &p.runs) : forward_shape(p, vec, even, small);
+  if (!bwd) p.runs = shape.grid;
   p.pitch = round_up(X.n, 8);
+  p.run_tokens = (int32_t)(p.tokens / std::max(p.runs, 1));
+  p.run_more = (int32_t)(p.tokens % std::max(p.runs, 1));
   if (sums) {
     const int64_t rows_pre = p.dpre ? p.runs : 0, rows_post = p.dpost ? p.runs : 0;
     const int64_t rows_gate = p.dgate && p.gate_per != 1 ? p.runs + p.gate_rows : 0;

@@ -206,7 +206,7 @@ template <int K>
 struct RowCursors {
   char* ptr[K];  // NULL: no such tensor
   int32_t step[K];
-  int32_t left;  // tokens from this one to the end of a block
+  int32_t left = 0;  // tokens from this one to the end of a block
   template <class P>
   __device__ __forceinline__ void find(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
     int64_t until = end;
@@ -225,7 +225,7 @@ struct RowCursors {
     }
     left = (int32_t)(until - t);
   }
-  // to token t, the next one
+  // to token t, the first one or the one behind the present one
   template <class P>
   __device__ __forceinline__ void next(const P& p, const RowTable* const (&tables)[K], int64_t t, int64_t end) {
     if (--left > 0) {
@@ -249,15 +249,12 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
   int turn = 0;
   const int n = p.n, nt = blockDim.x, tid = threadIdx.x;
   const float inv_n = 1.f / (float)n;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tokens / gridDim.x, t1 = (int64_t)(blockIdx.x + 1) * p.tokens / gridDim.x;
+  const int64_t t0 = run_begin(p, blockIdx.x), t1 = run_begin(p, blockIdx.x + 1);
   // x alone (its parts are looked up where they are read), the residual alone
   // (its loads go out later), the outputs
   const RowTable *const tx[1] = {&p.x}, *const tr[1] = {&p.r}, *const to[2] = {&p.h, &p.y};
   RowCursors<1> cx, cr;
   RowCursors<2> out;
-  cx.find(p, tx, t0, t1);
-  cr.find(p, tr, t0, t1);
-  out.find(p, to, t0, t1);
   const int parts = p.x.parts;
   int at = 0;
   // vectors below the last two are there in every thread
@@ -274,32 +271,30 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 #pragma unroll
     for (int v = 0; v < VPT; ++v) load8<EVEN>(x[v], reinterpret_cast<const XT*>(row), channel(v), n);
   };
-  auto load_r = [&] {
+  auto load_r = [&](int64_t t) {
     if (!res) return;
+    cr.next(p, tr, t, t1);
 #pragma unroll
     for (int v = 0; v < VPT; ++v) load8<EVEN>(r[v], reinterpret_cast<const RT*>(cr.ptr[0]), channel(v), n);
   };
-  if (AHEAD && t0 < t1) {
-    load_x(cx.ptr[0]);
-    load_r();
-  }
-  const int64_t seg0 = p.gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0;
-  int64_t seg_end = (seg0 + 1) * p.gate_per;
   const char* gate = static_cast<const char*>(p.gate);
-  const int64_t gate_step = (int64_t)n * (p.gate_dtype == DT_BF16 ? 2 : 4);
-  if (gate) gate += seg0 * gate_step;
+  int64_t gate_end = t0;  // of the tokens of the gate's present row
   // a vector a thread: its weights stay in registers
   constexpr bool KEEP = VPT == 1;
   f2 w_post[4], w_gate[4], w_pre[4];
   if (KEEP) {
     if (p.post) load_w8<EVEN>(p.post, p.post_dtype, channel(0), n, w_post);
-    if (gate) load_w8<EVEN>(gate, p.gate_dtype, channel(0), n, w_gate);
     if (p.pre) load_w8<EVEN>(p.pre, p.pre_dtype, channel(0), n, w_pre);
   }
   auto weigh = [&](const void* weight, int dtype, const f2(&w)[4], auto&& body) {
     if constexpr (KEEP) body(w, 0);
     else each_w8<VPT, EVEN>(weight, dtype, n, channel, body);
   };
+  if (AHEAD) {
+    cx.next(p, tx, t0, t1);
+    load_x(cx.ptr[0]);
+    load_r(t0);
+  }
   for (int64_t t = t0; t < t1; ++t) {
     f2 h[VPT][4];
     auto unpack = [&](int v, f2(&w)[4]) {
@@ -307,6 +302,12 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = has(v) ? w[i] : both(0.f);
     };
+    if (gate && t >= gate_end) {
+      const int64_t row = (uint32_t)t / (uint32_t)p.gate_per;
+      gate = static_cast<const char*>(p.gate) + row * n * (p.gate_dtype == DT_BF16 ? 2 : 4);
+      gate_end = (row + 1) * p.gate_per;
+      if (KEEP) load_w8<EVEN>(gate, p.gate_dtype, channel(0), n, w_gate);
+    }
     if constexpr (AHEAD) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v) unpack(v, h[v]);
@@ -315,7 +316,8 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
         load_x(cx.ptr[0]);
       }
     } else {
-      load_r();
+      load_r(t);
+      cx.next(p, tx, t, t1);
       const int block = row_block(p.blocks, p.x, t, at);
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
@@ -332,7 +334,6 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
           for (int i = 0; i < 4; ++i) h[v][i] = k ? h[v][i] + w[i] : w[i];
         }
       }
-      cx.next(p, tx, t + 1, t1);
     }
     auto total = [&] {
       f2 s = both(0.f);
@@ -350,11 +351,6 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
       });
     }
     if (gate) {
-      if (t == seg_end) {
-        gate += gate_step;
-        seg_end += p.gate_per;
-        if (KEEP) load_w8<EVEN>(gate, p.gate_dtype, channel(0), n, w_gate);
-      }
       weigh(gate, p.gate_dtype, w_gate, [&](const f2(&w)[4], int v) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[v][i] = h[v][i] * w[i];
@@ -379,9 +375,9 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 #pragma unroll
         for (int i = 0; i < 4; ++i) h[v][i] = has(v) ? fma2(scale, w[i], h[v][i]) : h[v][i];
       }
-      cr.next(p, tr, t + 1, t1);
-      if (AHEAD && t + 1 < t1) load_r();
     }
+    if (AHEAD && t + 1 < t1) load_r(t + 1);
+    out.next(p, to, t, t1);
     if (out.ptr[0]) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
@@ -396,7 +392,6 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
         if (has(v)) store8<EVEN>(reinterpret_cast<XT*>(out.ptr[1]), channel(v), n, y);
       });
     }
-    out.next(p, to, t + 1, t1);
   }
 }
 
@@ -433,7 +428,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
   // pieces of a stage: x's parts, dy, the residual, dh
   const int at_y = parts * VPT * PX * nt, at_r = at_y + VPT * PX * nt, at_h = at_r + VPT * PR * nt,
             stage = at_h + VPT * PR * nt;
-  const int64_t t0 = (int64_t)run * p.tokens / p.runs, t1 = (int64_t)(run + 1) * p.tokens / p.runs;
+  const int64_t t0 = run_begin(p, run), t1 = run_begin(p, run + 1);
   const RowTable *const tin[4] = {&p.x, &p.y, &p.r, &p.h}, *const tout[2] = {&p.dx, &p.dr};
   RowCursors<4> in;
   RowCursors<2> out;

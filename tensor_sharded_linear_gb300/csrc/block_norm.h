@@ -24,7 +24,19 @@ struct BlockArgs {
   // pre and post, [run + gate row][pitch] for the gate
   float *part_pre, *part_post, *part_gate;
   int32_t runs, pitch;
+  // tokens of a run: run_tokens, and one more in the first run_more runs
+  int32_t run_tokens, run_more;
 };
+
+#ifdef __CUDACC__
+__device__ __forceinline__ int64_t run_begin(const BlockArgs& p, int run) {
+  return (int64_t)run * p.run_tokens + min(run, p.run_more);
+}
+__device__ __forceinline__ int64_t run_of(const BlockArgs& p, int64_t t) {
+  const int64_t longer = (int64_t)p.run_more * (p.run_tokens + 1);
+  return t < longer ? t / (p.run_tokens + 1) : p.run_more + (t - longer) / max(p.run_tokens, 1);
+}
+#endif
 
 // The launch's tables of row blocks; most launches need few.
 template <int CAP>
