@@ -430,7 +430,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
   const int n = p.n, nt = blockDim.x, tid = threadIdx.x, parts = ONE ? 1 : p.x.parts;
   const float inv_n = 1.f / (float)n;
   constexpr int PX = Pieces<XT>::N, PR = Pieces<RT>::N;
-  constexpr bool HOLD = VPT == 1;  // a row's values stay in registers between the two looks at it
+  constexpr bool HOLD = VPT == 1;  // a row's values stay in registers between the two looks at it (else h alone)
   // pieces of a stage: x's parts, dy, the residual, dh
   const int at_y = parts * VPT * PX * nt, at_r = at_y + VPT * PX * nt, at_h = at_r + VPT * PR * nt,
             stage = at_h + VPT * PR * nt;
@@ -479,7 +479,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
     }
   }
   for (int i = 0; i < S; ++i) fetch(mine + i * stage);
-  f2 s_pre[VPT][4], s_post[VPT][4], q_gate[VPT][4], w_pre[VPT][4], w[VPT][4];
+  f2 s_pre[VPT][4], q_gate[VPT][4], w_pre[VPT][4], w[VPT][4];
+  bool closed = false;  // a sum of this run's is in the workspace
   int64_t seg = gate ? (uint32_t)t0 / (uint32_t)p.gate_per : 0, seg_end = (seg + 1) * p.gate_per;
   auto gate_row = [&] { return static_cast<const char*>(p.gate) + seg * n * (p.gate_dtype == DT_BF16 ? 2 : 4); };
   auto weights = [&] {
@@ -501,7 +502,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
 #pragma unroll
   for (int v = 0; v < VPT; ++v)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s_pre[v][i] = s_post[v][i] = q_gate[v][i] = w_pre[v][i] = w[v][i] = both(0.f);
+    for (int i = 0; i < 4; ++i) s_pre[v][i] = q_gate[v][i] = w_pre[v][i] = w[v][i] = both(0.f);
   weights();
   if (has_y) {
 #pragma unroll
@@ -530,14 +531,25 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         a[i] = a[i] * q_gate[v][i];
-        s_post[v][i] = fma2(b[i], q_gate[v][i], s_post[v][i]);
+        b[i] = b[i] * q_gate[v][i];
         q_gate[v][i] = both(0.f);
+      }
+      if (post) {  // (this thread's own place)
+        float* to = p.part_post + (int64_t)run * p.pitch;
+        if (closed) {
+          f2 had[4];
+          load_w8<true>(to, DT_FP32, c, n, had);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) b[i] = b[i] + had[i];
+        }
+        write_sums(to, v, b);
       }
       if (!gate) continue;
       if (p.gate_per != 1) write_sums(p.part_gate + ((int64_t)run + seg) * p.pitch, v, a);
       else if (p.dgate_dtype == DT_BF16) store8<EVEN>(static_cast<__nv_bfloat16*>(p.dgate) + seg * n, c, n, a);
       else store8<EVEN>(static_cast<float*>(p.dgate) + seg * n, c, n, a);
     }
+    closed = true;
   };
   auto load_x = [&](const uint4* from, int v, f2(&x)[4]) {
     if (parts == 1) {
@@ -613,15 +625,14 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
       rx = rsqrtf(q[0] * inv_n + p.eps);
     }
     uint32_t bits[VPT] = {};
-    f2 x[4], h[4], dy[4], dh[4];  // of one vector
+    f2 x[4], h[VPT][4], dy[4], dh[4];  // x, dy and dh of one vector
     auto values = [&](int v) {
       load_x(from, v, x);
       Raw8<XT> yw;
-      Raw8<RT> rw, hw;
+      Raw8<RT> hw;
       yw.set(from + at_y + v * PX * nt, nt);
-      rw.set(from + at_r + v * PR * nt, nt);
       hw.set(from + at_h + v * PR * nt, nt);
-      yw.get2(dy), rw.get2(h), hw.get2(dh);
+      yw.get2(dy), hw.get2(dh);
     };
     auto branch = [&](int v, int i) {  // a
       const f2 a = x[i] * w[v][i];
@@ -632,15 +643,18 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
     for (int v = 0; v < VPT; ++v) {
       if (drop.on) bits[v] = drop.bits<EVEN>(t, n, channel(v));
       values(v);
+      Raw8<RT> rw;
+      rw.set(from + at_r + v * PR * nt, nt);
+      rw.get2(h[v]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 a = branch(v, i), z = dy[i] * w_pre[v][i];
-        h[i] = fma2(scale, h[i], a * both(rx));
-        sum[0] = fma2(h[i], h[i], sum[0]);
-        sum[1] = fma2(h[i], z, sum[1]);
+        h[v][i] = fma2(scale, h[v][i], a * both(rx));
+        sum[0] = fma2(h[v][i], h[v][i], sum[0]);
+        sum[1] = fma2(h[v][i], z, sum[1]);
         sum[2] = fma2(a, dh[i], sum[2]);
         sum[3] = fma2(a, z, sum[3]);
-        sum[4] = fma2(a, h[i], sum[4]);
+        sum[4] = fma2(a, h[v][i], sum[4]);
       }
     }
     float rh = 0.f, kh = 0.f, kx = 0.f, next_rx = 1.f;
@@ -663,18 +677,14 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
       const int c = channel(v);
-      if (!HOLD) {
-        values(v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = fma2(scale, h[i], branch(v, i) * rx2);
-      }
+      if (!HOLD) values(v);
       f2 o[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         f2 g = dh[i], xr = x[i] * rx2;
         if (has_y) {  // (a choice: kh may not be finite where h is 0)
-          g = fma2(dy[i] * w_pre[v][i], rh2, fma2(h[i], kh2, g));
-          s_pre[v][i] = fma2(dy[i], h[i] * rh2, s_pre[v][i]);
+          g = fma2(dy[i] * w_pre[v][i], rh2, fma2(h[v][i], kh2, g));
+          s_pre[v][i] = fma2(dy[i], h[v][i] * rh2, s_pre[v][i]);
         }
         dh[i] = g * scale;
         if (drop.on) g = kept(g, bits[v], i), xr = kept(xr, bits[v], i);  // (what is dropped may be NaN)
@@ -703,7 +713,6 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
   for (int v = 0; v < VPT; ++v) {
     if (channel(v) >= n) break;
     if (has_y) write_sums(p.part_pre + (int64_t)run * p.pitch, v, s_pre[v]);
-    if (post) write_sums(p.part_post + (int64_t)run * p.pitch, v, s_post[v]);
   }
   if (EVEN) copies_wait<0>();
 }
