@@ -229,8 +229,9 @@ __device__ __forceinline__ float logit(const P& p, int64_t t, int j) {
 // The id at place i: its column, or -1 (and the status bit unless it is the one to be ignored).
 __device__ __forceinline__ int given_id(const LogProbArgs& p, int64_t i, bool report) {
   const int32_t id = load_plain(p.ids + i);
+  if (id == p.ignore) return -1;  // (which may be a column)
   if (id >= 0 && id < p.vocab) return id;
-  if (report && id != p.ignore) atomicOr(p.status, DT_DEV_ERR_INDEX);
+  if (report) atomicOr(p.status, DT_DEV_ERR_INDEX);
   return -1;
 }
 
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     if (rank != 0 || (int)(threadIdx.x + j * blockDim.x) >= p.given) continue;
-    if (id[j] >= 0 && id[j] < p.vocab) {
+    if (id[j] >= 0 && id[j] < p.vocab && id[j] != p.ignore) {
       z_id[j] = logit<T>(p, t, id[j]);
     } else {
       if (id[j] != p.ignore) atomicOr(p.status, DT_DEV_ERR_INDEX);

@@ -210,6 +210,29 @@ def test_ids_outside_the_vocabulary():
     assert (d[[1, 2, 4]] == 0).all() and (d[[0, 3]] != 0).all()
 
 
+@pytest.mark.parametrize("ignore", [0, 999, -1])
+def test_an_ignored_id_may_be_a_column(ignore):
+    rng = np.random.default_rng(5)
+    mesh = tsl.DeviceMesh((2,), ("tp",))
+    t, v = 12, 1000
+    z = logits(rng, t, v, "fp32")
+    given = rng.integers(1, v - 1, (t, 3))
+    given[::2, 1] = ignore
+    given[3] = ignore  # a token of nothing else
+    zd = vocab(z, mesh, "fp32")
+    r = tsl.tp_log_probs(zd, ints(given, mesh), ignore_index=ignore)
+    seen = np.where(given == ignore, -100, given)
+    check_forward(r, z, seen, 1.0, 0)
+    g = draw(rng, (t, 3), "fp32")
+    d = tsl.tp_log_probs_backward(whole(g, mesh, torch.float32), None, zd, ints(given, mesh), r.lse, ignore_index=ignore)
+    e, mag = decoder.log_probs_backward(z, seen, g, host(r.lse))
+    rel = (12 + 2 * (np.abs(z) + np.abs(host(r.lse))[:, None]) + 3 * 3) * E24  # as above
+    assert (np.abs(side(d) - e) <= HALF["fp32"] * np.abs(e) + rel * mag + 2.0 ** -130).all()
+    assert not side(d)[3].any()
+    torch.cuda.synchronize()
+    assert tsl.read_device_status() == 0
+
+
 def test_the_same_id_given_twice():
     rng = np.random.default_rng(8)
     mesh = tsl.DeviceMesh((2,), ("tp",))
