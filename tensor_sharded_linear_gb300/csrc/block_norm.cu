@@ -527,7 +527,7 @@ extern "C" dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, in
   if (tokens < 0 || channels < 0 || gate_rows < 0 || channels > (1 << 30) || tokens >= MAX_ROWS)
     return fail(DT_ERR_INVALID_ARG, "tokens %lld, channels %lld, gate_rows %lld", (long long)tokens,
                 (long long)channels, (long long)gate_rows);
-  if (gate_rows > std::max<int64_t>(tokens, 1)) return fail(DT_ERR_SHAPE, "more gate rows than tokens");
+  if (tokens > 0 && gate_rows > tokens) return fail(DT_ERR_SHAPE, "more gate rows than tokens");
   *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * ((channels + 7) / 8 * 8) * sizeof(float);
   return DT_OK;
 }

@@ -146,6 +146,14 @@ def test_block_norm_workspace_query(lib):
     assert tsl.tp_block_norm_backward_workspace_bytes(dt((10, 64)), dt((64,)), dt((5, 64))) == base + 5 * 64 * 4
 
 
+def test_block_norm_workspace_of_an_empty_batch_with_gate_rows(lib):
+    """Five empty sequences, a gate row each: their gradients are zeros, from a workspace all the same."""
+    n = C.c_size_t()
+    assert lib.dt_tp_block_norm_backward_workspace_size(0, 64, 5, C.byref(n)) == L.OK
+    assert tsl.tp_block_norm_backward_workspace_bytes(dt((5, 0, 64)), None, dt((5, 64))) == n.value
+    assert n.value >= (3 + 5) * 64 * 4
+
+
 Z = (6, 50)
 
 

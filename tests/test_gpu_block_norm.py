@@ -316,6 +316,15 @@ def test_no_tokens_give_zero_weight_gradients():
     assert all((d == 0).all() for d in out)
 
 
+def test_empty_sequences_give_zero_gate_gradients():
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    empty = lambda: whole(torch.zeros(5, 0, 64), mesh, torch.bfloat16)  # noqa: E731
+    w, gate = whole(torch.ones(64), mesh), whole(torch.ones(5, 64), mesh)
+    out = (empty(), None, None, whole(torch.full((5, 64), 3.0), mesh), whole(torch.full((64,), 3.0), mesh))
+    tsl.tp_block_norm_backward(None, empty(), empty(), None, None, gate, w, out=out)
+    assert all((d.slots[0] == 0).all() for d in out[3:])
+
+
 def test_offsets_past_32_bits():
     """Rows beyond 2^32 bytes and elements beyond 2^32, dropout's counter among them."""
     n, t = 8192, (1 << 32) // 8192 + 3
