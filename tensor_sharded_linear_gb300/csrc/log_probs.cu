@@ -629,10 +629,11 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_backward_kernel(const
   const float ge = ENT ? load_plain(p.dentropy + t) : 0.f, h = ENT ? load_plain(p.entropy + t) : 0.f;
   zero = (zero && ge == 0.f) || lse == -INFINITY;
   // dlogit = exp(l) (a + b l) with l = scale z - lse, and scale g_c on top at the given ids
+  // (below -256 exp(l) is 0, which the other factor, kept finite, does not change)
   const float a = -p.scale * (g + ge * h), b = -p.scale * ge;
   auto value = [&](float z) {
     const float l = fmaf(z, p.scale, -lse), x = exp2_fast(l * LOG2E);
-    return x * (ENT ? fmaf(fmaxf(l, -1e28f), b, a) : a);
+    return x * (ENT ? fmaf(fmaxf(l, -256.f), b, a) : a);
   };
   // the given ids of this CTA's units: their gradients, before the logits may be overwritten
   T* to = nullptr;
@@ -673,7 +674,7 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_backward_kernel(const
         for (int k = 0; k < N; ++k) {
           const f2 l = fma2(x[k], both(p.scale), both(-lse)), e = l * both(LOG2E);
           const f2 q = f2{exp2_fast(e.x), exp2_fast(e.y)};
-          x[k] = q * (ENT ? fma2(f2{fmaxf(l.x, -1e28f), fmaxf(l.y, -1e28f)}, both(b), both(a)) : both(a));
+          x[k] = q * (ENT ? fma2(f2{fmaxf(l.x, -256.f), fmaxf(l.y, -256.f)}, both(b), both(a)) : both(a));
         }
       } else {
 #pragma unroll

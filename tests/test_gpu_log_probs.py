@@ -233,6 +233,20 @@ def test_an_ignored_id_may_be_a_column(ignore):
     assert tsl.read_device_status() == 0
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_hidden_columns_under_large_entropy_gradients(dtype):
+    """-inf and the lowest value have no gradient, however large scale and the entropy's gradient are."""
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    z = np.zeros((3, 40))
+    z[:, 20:30], z[:, 30:] = -np.inf, torch.finfo(DT[dtype]).min
+    zd = vocab(z, mesh, dtype)
+    r = tsl.tp_log_probs(zd, scale=2.0 ** 20, entropy=True)
+    g = whole(torch.full((3,), 1e9), mesh)
+    d = side(tsl.tp_log_probs_backward(None, g, zd, None, r.lse, r.entropy, scale=2.0 ** 20))
+    # the others are alike, each at the mean of log p: what is left is a rounding of ln 20 times scale g / 20
+    assert (d[:, 20:] == 0).all() and (np.abs(d[:, :20]) <= 2.0 ** 20 * 1e9 / 20 * 16 * E24).all()
+
+
 def test_the_same_id_given_twice():
     rng = np.random.default_rng(8)
     mesh = tsl.DeviceMesh((2,), ("tp",))
