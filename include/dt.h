@@ -551,6 +551,7 @@ DT_API dt_status dt_tp_kv4_attention_workspace_size(const dt_dtensor* q, const d
  * floor(dropout * 2^32): the mask depends on the element alone, not on the
  * layout, and is not stored.  Without post_weight, what a dropped element of x
  * holds reaches nothing.  With eps 0 a row of zeros gives NaN.
+ * h may be the residual itself, and y x itself (the same slots and strides).
  */
 DT_API dt_status dt_tp_block_norm(const dt_dtensor* x, const dt_dtensor* residual, const dt_dtensor* post_weight,
                                   const dt_dtensor* gate, const dt_dtensor* pre_weight, const dt_dtensor* rng,
@@ -567,6 +568,8 @@ DT_API dt_status dt_tp_block_norm(const dt_dtensor* x, const dt_dtensor* residua
  *   dpost_weight, dgate, dpre_weight   shapes of their operands, bf16 or fp32,
  *              given exactly when these are; summed over tokens in an order
  *              fixed by the shapes (the same inputs give the same bits)
+ * dx may be x or dy itself, dresidual the residual or dh itself (the same slots
+ * and strides).
  * workspace: 256-byte aligned device memory of the queried size (gate_rows 0
  * without a gate) for the sums over tokens; not needed without weights.
  */

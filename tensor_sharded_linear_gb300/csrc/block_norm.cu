@@ -170,7 +170,6 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
       const float s = sum_x(c);
       const bool keep = kept(c);
       const float a = value(c, s, keep), g = grad(c, a);
-      if (dr) store_any(dr, p.dr.dtype, c, p.scale * g);
       auto add = [&](float* to, bool begin, float v) { *to = begin ? v : *to + v; };
       if (p.pre) add(p.part_pre + (int64_t)blockIdx.x * p.pitch + c, first, load_any(y, p.y.dtype, c) * a * rh);
       const float e = keep ? g * p.drop_scale : 0.f, w = e * gate(c);
@@ -180,6 +179,7 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
         else add(p.part_gate + ((int64_t)blockIdx.x + seg) * p.pitch + c, first_gate, d);
       }
       if (p.post) add(p.part_post + (int64_t)blockIdx.x * p.pitch + c, first, keep ? w * s * rx : 0.f);
+      if (dr) store_any(dr, p.dr.dtype, c, p.scale * g);
       if (dx) store_any(dx, p.dx.dtype, c, p.post ? rx * w * post(c) - kx * s : w);
     }
   }

@@ -316,6 +316,35 @@ def test_no_tokens_give_zero_weight_gradients():
     assert all((d == 0).all() for d in out)
 
 
+IN_PLACE = [dict(t=7, n=512), dict(t=700, n=4096, drop=0.1), dict(t=600, n=1001, p=2, place=S0, out=S0, gate=3),
+            dict(t=9, n=20000), dict(t=300, n=1152, dtype="fp32"), dict(t=320, n=16384, gate=-1)]
+
+
+@pytest.mark.parametrize("c", IN_PLACE, ids=ids)
+def test_results_in_place_of_operands(c):
+    """The same bits as with outputs of their own."""
+    def fresh():
+        return Case(27, **c)
+
+    def same(a, b):
+        assert all(torch.equal(u, v) for u, v in zip(a.slots, b.slots))
+
+    one = fresh()
+    h, y = one.forward()
+    want = one.backward()
+    case = fresh()
+    got_h, got_y = tsl.tp_block_norm(*case.operands(), out=(case.r, case.x), **case.kw)
+    same(got_h, h)
+    same(got_y, y)
+    for over in (lambda k: (k.x, k.r), lambda k: (k.gy, k.gh), lambda k: (k.gy, k.r)):
+        case = fresh()
+        dx, dr = over(case)
+        out = tsl.tp_block_norm_backward(case.gh, case.gy, *case.operands(), out=(dx, dr, *case.bwd_out[2:]), **case.kw)
+        for a, b in zip(out, want):
+            if b is not None:
+                same(a, b)
+
+
 def test_empty_sequences_give_zero_gate_gradients():
     mesh = tsl.DeviceMesh((1,), ("tp",))
     empty = lambda: whole(torch.zeros(5, 0, 64), mesh, torch.bfloat16)  # noqa: E731
