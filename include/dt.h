@@ -599,7 +599,7 @@ DT_API dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, int64_
  *   top_ids, top_logprobs   int32 and fp32 [..., k], k at most 32: the k largest
  *                 logits, largest first, ties to the lowest id; or both NULL
  * All small tensors are Replicate and contiguous.  scale 2^-20 .. 2^20; with
- * alternatives V is at most 2^24 (DT_ERR_CAPACITY).  An id that is
+ * alternatives V is at most 2^24, or 2^21 of 2^28 tokens (DT_ERR_CAPACITY).  An id that is
  * ignore_index gives 0; another one outside [0, V) gives 0 and sets
  * DT_DEV_ERR_INDEX.  Logits of -inf have probability 0; a row of nothing else
  * gives lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or

@@ -913,6 +913,8 @@ extern "C" dt_status dt_tp_log_probs(const dt_dtensor* logits, const dt_dtensor*
       if (p.tokens > 0 && k > p.vocab) return fail(DT_ERR_SHAPE, "more alternatives than tokens in the vocabulary");
       if (k > 0 && p.vocab > LP_MAX_TOP_VOCAB)
         return fail(DT_ERR_CAPACITY, "alternatives from a vocabulary of more than 2^24");
+      if (k > 0 && p.vocab > LP_MAX_TOP_VOCAB / 8 && p.tokens > INT32_MAX / LP_MAX_CLUSTER)
+        return fail(DT_ERR_CAPACITY, "alternatives of 2^28 tokens from a vocabulary of more than 2^21");
       p.top = (int32_t)k;
       if (k > 0) anchor = ptr;
     }

@@ -38,7 +38,7 @@ class Fake:
         self.buf = (C.c_char * 64)()
         addr = (C.addressof(self.buf) + 15) // 16 * 16
         d = L.DTensorDesc()
-        d.layout = tsl.api._layout(MESH, [pl], shape, {L.BF16: BF, L.FP32: F32}[dtype], False)
+        d.layout = tsl.api._layout(MESH, [pl], shape, {L.BF16: BF, L.FP32: F32, L.INT32: I32}[dtype], False)
         d.nslots = 1 if pl == R else 2
         self.ptrs = (C.c_void_p * 2)(addr, addr)
         d.slots = C.cast(self.ptrs, C.POINTER(C.c_void_p))
@@ -189,6 +189,15 @@ def test_log_probs_refusals(lib, i):
     kw, want = LP_BAD[i]
     n0 = lib.dt_launch_count()
     assert lp(lib, **kw) == want, lib.dt_last_error()
+    assert lib.dt_last_error() and lib.dt_launch_count() == n0
+
+
+def test_log_probs_clusters_for_too_many_tokens(lib):
+    """Rows whose alternatives need a cluster each, more of them than a grid has CTAs for."""
+    t = 2 ** 28
+    side = dict(ids=None, logp=None, lse=None, ent=None, top=Fake((t, 1), dtype=L.FP32), tids=Fake((t, 1), dtype=L.INT32))
+    n0 = lib.dt_launch_count()
+    assert lp(lib, z=Fake((t, 2 ** 21 + 1), S1), **side) == CAP
     assert lib.dt_last_error() and lib.dt_launch_count() == n0
 
 
