@@ -185,14 +185,19 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
   }
 }
 
-// dpre, dpost and the gate's rows from the sums of the runs of tokens.  A block
-// takes 64 channels: 16 lanes hold four each, half-warps take every 32nd run's
-// sums, eight of them at once, and theirs are added at the end; a fixed order.
-constexpr int BN_SUM_THREADS = 512, BN_SUM_CHANNELS = 64;
+// dpre, dpost and the gate's rows from the sums of the runs of tokens: a few MB
+// that are still in L2, bound by latency.  A block takes 32 channels, four a
+// lane; its 64 groups of eight lanes take every 64th run's sums, six of them at
+// once (all of 384 runs), and theirs are added at the end; a fixed order.
+// (8192 x 4096, 304 runs, with the kernel before: 77.0 us; 64 channels and 32
+// groups with six at once 77.4, with eight 79.3.  1533 x 1000: 18.8, 19.1, 21.6.)
+constexpr int BN_SUM_THREADS = 512, BN_SUM_CHANNELS = 32, BN_SUM_LOADS = 6;
+constexpr int BN_SUM_LANES = BN_SUM_CHANNELS / 4, BN_SUM_GROUPS = BN_SUM_THREADS / BN_SUM_LANES;
+constexpr int BN_SUM_SHARE = BN_SUM_THREADS / BN_SUM_CHANNELS;  // threads a channel at the end
 __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const __grid_constant__ BlockArgs p) {
-  __shared__ float acc[32][BN_SUM_CHANNELS + 1];
+  __shared__ float acc[BN_SUM_GROUPS][BN_SUM_CHANNELS + 1];
   wait_for_previous_kernel();
-  const int lane = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int lane = threadIdx.x % BN_SUM_LANES, group = threadIdx.x / BN_SUM_LANES;
   const int64_t rows = p.gate && p.gate_per != 1 ? p.gate_rows : 0;
   const int64_t c0 = (int64_t)blockIdx.x * BN_SUM_CHANNELS;
   for (int64_t which = blockIdx.y; which < 2 + rows; which += gridDim.y) {
@@ -211,21 +216,25 @@ __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const _
     const float* part = (which == 0 ? p.part_pre : which == 1 ? p.part_post : p.part_gate) + b0 * p.pitch + c;
     const int count = c < p.n ? (int)(b1 - b0) : 0;
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int b = group; b < count; b += 32 * 8) {
-      float4 v[8];
+    for (int b = group; b < count; b += BN_SUM_GROUPS * BN_SUM_LOADS) {
+      float4 v[BN_SUM_LOADS];
 #pragma unroll
-      for (int k = 0; k < 8; ++k)
-        v[k] = b + 32 * k < count ? load_plain(reinterpret_cast<const float4*>(part + (int64_t)(b + 32 * k) * p.pitch))
-                                  : make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < BN_SUM_LOADS; ++k) {
+        const int at = b + BN_SUM_GROUPS * k;
+        v[k] = at < count ? load_plain(reinterpret_cast<const float4*>(part + at * (int64_t)p.pitch))
+                          : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
+      for (int k = 0; k < BN_SUM_LOADS; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
     }
     acc[group][lane * 4] = s.x, acc[group][lane * 4 + 1] = s.y, acc[group][lane * 4 + 2] = s.z, acc[group][lane * 4 + 3] = s.w;
     __syncthreads();
-    const int ch = threadIdx.x / 8, k0 = threadIdx.x % 8;  // eight threads a channel
-    float v = (acc[k0][ch] + acc[k0 + 8][ch]) + (acc[k0 + 16][ch] + acc[k0 + 24][ch]);
+    const int ch = threadIdx.x / BN_SUM_SHARE, k0 = threadIdx.x % BN_SUM_SHARE;
+    static_assert(BN_SUM_GROUPS == 4 * BN_SUM_SHARE, "four sums a thread");
+    float v = (acc[k0][ch] + acc[k0 + BN_SUM_SHARE][ch]) +
+              (acc[k0 + 2 * BN_SUM_SHARE][ch] + acc[k0 + 3 * BN_SUM_SHARE][ch]);
 #pragma unroll
-    for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = BN_SUM_SHARE / 2; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (k0 == 0 && c0 + ch < p.n) store_any(out, dtype, row * p.n + c0 + ch, v);
     __syncthreads();
   }
@@ -297,7 +306,7 @@ BlockShape backward_shape(const BlockArgs& p, bool vec, bool even, bool small, i
   int64_t most = 2 * sms;
   if (vec && small && vectors <= 2048) {
     s.cluster = vectors <= 1024 ? 1 : 2;
-    s.vpt = vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 85.9 us, one 91.0)
+    s.vpt = vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 79.0 us, one 88.9)
     s.threads = round_up((vectors + s.vpt * s.cluster - 1) / (s.vpt * s.cluster), 32);
     s.even = even;
     const int64_t stage = (int64_t)s.threads * s.vpt * 8 *
