@@ -90,13 +90,35 @@ __device__ __forceinline__ void clear(float* buf, int n) {
   __syncthreads();
 }
 
-// 8 channels of a row of n, in fp32 or as loaded: one or two 16-byte accesses
-// (EVEN), or element by element, with 0 behind the row's end.
-template <class T, class V>
-__device__ __forceinline__ void load8_uneven(const T* row, int c, int n, V&& load, Raw8<T>& r) {
+// How rows lie: of a multiple of 8 channels on 16-byte boundaries (EVEN), or
+// not: wide accesses and shifts (WIDE), or element by element (SINGLE), which
+// takes fewer registers and so is what the gradients do.  4000 rows of 8191
+// channels, both norms: wide 151 us in bf16 and 176 in fp32, element by element
+// 202 and 307; their gradients 412 and 421, 350 and 413.
+enum class Rows { EVEN, WIDE, SINGLE };
+
+// Words of a run of bytes that starts o bytes (a multiple of 2) into w.
+template <int N, int M>
+__device__ __forceinline__ void shifted(uint32_t (&w)[M], int o, uint32_t (&out)[N]) {
+  if (o & 8) {
+#pragma unroll
+    for (int i = 0; i + 2 < M; ++i) w[i] = w[i + 2];
+  }
+  if (o & 4) {
+#pragma unroll
+    for (int i = 0; i + 1 < M; ++i) w[i] = w[i + 1];
+  }
+  const int bits = (o & 2) * 8;
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(w[i], i + 1 < M ? w[i + 1] : 0, bits);
+}
+
+// 8 channels of a row of n, in fp32 or as loaded, with 0 behind the row's end.
+template <class T>
+__device__ __forceinline__ void load8_single(const T* row, int c, int n, Raw8<T>& r) {
   T e[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) e[i] = c + i < n ? load(row + c + i) : T(0.f);
+  for (int i = 0; i < 8; ++i) e[i] = c + i < n ? load_plain(row + c + i) : T(0.f);
   if constexpr (sizeof(T) == 2) {
     uint32_t w[4];
 #pragma unroll
@@ -107,21 +129,82 @@ __device__ __forceinline__ void load8_uneven(const T* row, int c, int n, V&& loa
     r.a = make_float4(e[0], e[1], e[2], e[3]), r.b = make_float4(e[4], e[5], e[6], e[7]);
   }
 }
-template <bool EVEN, class T>
+// The same by 16-byte accesses, one more than on their boundaries, where these
+// do not reach beyond the row.
+template <class T>
+__device__ __forceinline__ void load8_wide(const T* row, int c, int n, Raw8<T>& r) {
+  constexpr int P = sizeof(T) / 2, E = 16 / sizeof(T);
+  const int o = (int)(reinterpret_cast<uintptr_t>(row) & 15), before = o / (int)sizeof(T);
+  if (c < before || c - before + (P + 1) * E > n) {
+    load8_single(row, c, n, r);
+    return;
+  }
+  uint32_t w[4 * P + 4], out[4 * P];
+  const uint4* from = reinterpret_cast<const uint4*>(reinterpret_cast<const char*>(row + c) - o);
+#pragma unroll
+  for (int i = 0; i <= P; ++i) {
+    const uint4 u = load_plain(from + i);
+    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+  }
+  shifted(w, o, out);
+  if constexpr (P == 1) {
+    r.u = make_uint4(out[0], out[1], out[2], out[3]);
+  } else {
+    r.a = make_float4(__uint_as_float(out[0]), __uint_as_float(out[1]), __uint_as_float(out[2]), __uint_as_float(out[3]));
+    r.b = make_float4(__uint_as_float(out[4]), __uint_as_float(out[5]), __uint_as_float(out[6]), __uint_as_float(out[7]));
+  }
+}
+template <Rows ROWS, class T>
 __device__ __forceinline__ void load8(Raw8<T>& r, const T* row, int c, int n) {
-  if constexpr (EVEN) r.load(row + c);
-  else load8_uneven(row, c, n, [](const T* p) { return load_plain(p); }, r);
+  if constexpr (ROWS == Rows::EVEN) r.load(row + c);
+  else if constexpr (ROWS == Rows::WIDE) load8_wide(row, c, n, r);
+  else load8_single(row, c, n, r);
+}
+// Off 16-byte boundaries: a lane writes the 16 bytes that its last channels and
+// the next lane's first ones share, and (fp32) those that are its own; what has
+// no such neighbour goes element by element.  All lanes of the warp come here,
+// lane l for channel c of lane 0 + 8 l; those with c >= n write nothing.
+template <class T>
+__device__ __forceinline__ void store8_wide(T* row, int c, int n, const f2 (&v)[4]) {
+  constexpr int P = sizeof(T) / 2, E = 16 / sizeof(T);
+  const int lane = threadIdx.x & 31, o = (int)(reinterpret_cast<uintptr_t>(row) & 15);
+  uint32_t w[4 * P + 4], out[4 * P];
+#pragma unroll
+  for (int i = 0; i < 4 * P; ++i) {
+    if constexpr (P == 1) w[i] = pack_bf16(v[i].x, v[i].y);
+    else w[i] = __float_as_uint(i & 1 ? v[i >> 1].y : v[i >> 1].x);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[4 * P + i] = __shfl_down_sync(0xffffffffu, w[i], 1);
+  // elements below `head` share 16 bytes with the lane before, those from `tail` on with the next
+  const int head = o ? E - o / (int)sizeof(T) : 0, tail = head + (P - 1) * E;
+  const bool full = c + 8 <= n, shared = o ? lane < 31 && c + 16 <= n : full;
+  shifted(w, o ? 16 - o : 0, out);
+  char* to = reinterpret_cast<char*>(row + c) + (o ? 16 - o : 0);
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (i + 1 < P ? full : shared)
+      __stcs(reinterpret_cast<uint4*>(to) + i, make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]));
+  const bool mine = !(full && lane > 0);
+  if ((mine && head > 0) || !shared) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c + i < n && (i < head ? mine : i < tail ? !full : !shared))
+        from_f32(row + c + i, i & 1 ? v[i >> 1].y : v[i >> 1].x);
+  }
 }
 // KEEP: without the hint that it is not read again soon.  y is, by the next
 // block's product (13403 x 1152: 30.4 us instead of 32.4; h, dx and dr with it
 // make 8192 x 4096 slower).
-template <bool EVEN, bool KEEP = false, class T>
+template <Rows ROWS, bool KEEP = false, class T>
 __device__ __forceinline__ void store8(T* row, int c, int n, const f2 (&v)[4]) {
-  if constexpr (EVEN && KEEP && sizeof(T) == 2) {
+  if constexpr (ROWS == Rows::EVEN && KEEP && sizeof(T) == 2) {
     *reinterpret_cast<uint4*>(row + c) = make_uint4(pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
                                                     pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
-  } else if constexpr (EVEN) {
+  } else if constexpr (ROWS == Rows::EVEN) {
     dt::store8(row + c, v);
+  } else if constexpr (ROWS == Rows::WIDE) {
+    store8_wide(row, c, n, v);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
@@ -129,35 +212,35 @@ __device__ __forceinline__ void store8(T* row, int c, int n, const f2 (&v)[4]) {
   }
 }
 // of a vector over channels, bf16 or fp32
-template <bool EVEN>
+template <Rows ROWS>
 __device__ __forceinline__ void load_w8(const void* w, int dtype, int c, int n, f2 (&v)[4]) {
   if (dtype == DT_BF16) {
     Raw8<__nv_bfloat16> x;
-    if constexpr (EVEN) x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
-    else load8<false>(x, static_cast<const __nv_bfloat16*>(w), c, n);
+    if constexpr (ROWS == Rows::EVEN) x.u = load_plain(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(w) + c));
+    else load8<ROWS>(x, static_cast<const __nv_bfloat16*>(w), c, n);
     x.get2(v);
   } else {
     Raw8<float> x;
-    if constexpr (EVEN) x.load_keep(static_cast<const float*>(w) + c);
-    else load8<false>(x, static_cast<const float*>(w), c, n);
+    if constexpr (ROWS == Rows::EVEN) x.load_keep(static_cast<const float*>(w) + c);
+    else load8<ROWS>(x, static_cast<const float*>(w), c, n);
     x.get2(v);
   }
 }
 // body(w, v): v's vectors of a weight's channels; the type is looked at once, so
 // that the loads of all vectors can be on their way together.
-template <int VPT, bool EVEN, class C, class F>
+template <int VPT, Rows ROWS, class C, class F>
 __device__ __forceinline__ void each_w8(const void* weight, int dtype, int n, C&& channel, F&& body) {
   f2 w[4];
   if (dtype == DT_BF16) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      load_w8<EVEN>(weight, DT_BF16, channel(v), n, w);
+      load_w8<ROWS>(weight, DT_BF16, channel(v), n, w);
       body(w, v);
     }
   } else {
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-      load_w8<EVEN>(weight, DT_FP32, channel(v), n, w);
+      load_w8<ROWS>(weight, DT_FP32, channel(v), n, w);
       body(w, v);
     }
   }
@@ -198,7 +281,7 @@ __device__ __forceinline__ void fetch8(uint4* to, const char* row, int c, int n,
     for (int i = 0; i < Pieces<T>::N; ++i) copy16_async(to + i * step, reinterpret_cast<const uint4*>(from + c) + i);
   } else {
     Raw8<T> r;
-    load8<false>(r, from, c, n);
+    load8<Rows::SINGLE>(r, from, c, n);
     const uint4* w = reinterpret_cast<const uint4*>(&r);
 #pragma unroll
     for (int i = 0; i < Pieces<T>::N; ++i) to[i * step] = w[i];
@@ -250,6 +333,7 @@ struct RowCursors {
 template <class XT, class RT, int VPT, bool AHEAD, bool EVEN, class P>
 __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT)))
     block_norm_row_kernel(const __grid_constant__ P p) {
+  constexpr Rows ROWS = EVEN ? Rows::EVEN : Rows::WIDE;
   __shared__ __align__(16) float buf[2][BN_MAX_WARPS];
   clear(&buf[0][0], 2 * BN_MAX_WARPS);
   int turn = 0;
@@ -275,13 +359,13 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
   Raw8<RT> r[VPT];
   auto load_x = [&](const char* row) {
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) load8<EVEN>(x[v], reinterpret_cast<const XT*>(row), channel(v), n);
+    for (int v = 0; v < VPT; ++v) load8<ROWS>(x[v], reinterpret_cast<const XT*>(row), channel(v), n);
   };
   auto load_r = [&](int64_t t) {
     if (!res) return;
     cr.next(p, tr, t, t1);
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) load8<EVEN>(r[v], reinterpret_cast<const RT*>(cr.ptr[0]), channel(v), n);
+    for (int v = 0; v < VPT; ++v) load8<ROWS>(r[v], reinterpret_cast<const RT*>(cr.ptr[0]), channel(v), n);
   };
   const char* gate = static_cast<const char*>(p.gate);
   int64_t gate_end = t0;  // of the tokens of the gate's present row
@@ -289,12 +373,12 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
   constexpr bool KEEP = VPT == 1;
   f2 w_post[4], w_gate[4], w_pre[4];
   if (KEEP) {
-    if (p.post) load_w8<EVEN>(p.post, p.post_dtype, channel(0), n, w_post);
-    if (p.pre) load_w8<EVEN>(p.pre, p.pre_dtype, channel(0), n, w_pre);
+    if (p.post) load_w8<ROWS>(p.post, p.post_dtype, channel(0), n, w_post);
+    if (p.pre) load_w8<ROWS>(p.pre, p.pre_dtype, channel(0), n, w_pre);
   }
   auto weigh = [&](const void* weight, int dtype, const f2(&w)[4], auto&& body) {
     if constexpr (KEEP) body(w, 0);
-    else each_w8<VPT, EVEN>(weight, dtype, n, channel, body);
+    else each_w8<VPT, ROWS>(weight, dtype, n, channel, body);
   };
   if (AHEAD) {
     cx.next(p, tx, t0, t1);
@@ -312,7 +396,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
       const int64_t row = (uint32_t)t / (uint32_t)p.gate_per;
       gate = static_cast<const char*>(p.gate) + row * n * (p.gate_dtype == DT_BF16 ? 2 : 4);
       gate_end = (row + 1) * p.gate_per;
-      if (KEEP) load_w8<EVEN>(gate, p.gate_dtype, channel(0), n, w_gate);
+      if (KEEP) load_w8<ROWS>(gate, p.gate_dtype, channel(0), n, w_gate);
     }
     if constexpr (AHEAD) {
 #pragma unroll
@@ -387,7 +471,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
     if (out.ptr[0]) {
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
-        if (has(v)) store8<EVEN>(reinterpret_cast<RT*>(out.ptr[0]), channel(v), n, h[v]);
+        if (!EVEN || has(v)) store8<ROWS>(reinterpret_cast<RT*>(out.ptr[0]), (tid + v * nt) * 8, n, h[v]);
     }
     if (out.ptr[1]) {
       const f2 rh = both(total());
@@ -395,7 +479,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
         f2 y[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[i] = h[v][i] * rh * w[i];
-        if (has(v)) store8<EVEN, true>(reinterpret_cast<XT*>(out.ptr[1]), channel(v), n, y);
+        if (!EVEN || has(v)) store8<ROWS, true>(reinterpret_cast<XT*>(out.ptr[1]), (tid + v * nt) * 8, n, y);
       });
     }
   }
@@ -418,6 +502,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 // DROP false: no code for dropout (8192 x 4096: 79.4 us, with it 83.5).
 template <class XT, class RT, int VPT, int S, int CLUSTER, bool ONE, bool EVEN, bool DROP, class P>
 __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __grid_constant__ P p) {
+  constexpr Rows ROWS = EVEN ? Rows::EVEN : Rows::SINGLE;
   __shared__ __align__(16) float buf[2][8][16];
   __shared__ float meet[2][2][8];  // the cluster's CTAs' sums
   extern __shared__ uint4 ring[];
@@ -491,8 +576,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
       const int c = channel(v);
       if (c >= n) break;
       f2 a[4], b[4];
-      if (post) load_w8<EVEN>(p.post, p.post_dtype, c, n, a);
-      if (gate) load_w8<EVEN>(gate_row(), p.gate_dtype, c, n, b);
+      if (post) load_w8<ROWS>(p.post, p.post_dtype, c, n, a);
+      if (gate) load_w8<ROWS>(gate_row(), p.gate_dtype, c, n, b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         w[v][i] = both(p.drop_scale);
@@ -509,7 +594,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
   if (has_y) {
 #pragma unroll
     for (int v = 0; v < VPT; ++v)
-      if (channel(v) < n) load_w8<EVEN>(p.pre, p.pre_dtype, channel(v), n, w_pre[v]);
+      if (channel(v) < n) load_w8<ROWS>(p.pre, p.pre_dtype, channel(v), n, w_pre[v]);
   }
   auto write_sums = [&](float* to, int v, const f2(&s)[4]) {  // (rows of a multiple of 8 numbers)
     float4* o = reinterpret_cast<float4*>(to + channel(v));
@@ -528,8 +613,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
         a[i] = b[i] = both(1.f);
         q_gate[v][i] = q_gate[v][i] * both(p.drop_scale);
       }
-      if (post) load_w8<EVEN>(p.post, p.post_dtype, c, n, a);
-      if (gate) load_w8<EVEN>(gate_row(), p.gate_dtype, c, n, b);
+      if (post) load_w8<ROWS>(p.post, p.post_dtype, c, n, a);
+      if (gate) load_w8<ROWS>(gate_row(), p.gate_dtype, c, n, b);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         a[i] = a[i] * q_gate[v][i];
@@ -540,7 +625,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
         float* to = p.part_post + (int64_t)run * p.pitch;
         if (closed) {
           f2 had[4];
-          load_w8<true>(to, DT_FP32, c, n, had);
+          load_w8<Rows::EVEN>(to, DT_FP32, c, n, had);
 #pragma unroll
           for (int i = 0; i < 4; ++i) b[i] = b[i] + had[i];
         }
@@ -548,8 +633,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
       }
       if (!gate) continue;
       if (p.gate_per != 1) write_sums(p.part_gate + ((int64_t)run + seg) * p.pitch, v, a);
-      else if (p.dgate_dtype == DT_BF16) store8<EVEN>(static_cast<__nv_bfloat16*>(p.dgate) + seg * n, c, n, a);
-      else store8<EVEN>(static_cast<float*>(p.dgate) + seg * n, c, n, a);
+      else if (p.dgate_dtype == DT_BF16) store8<ROWS>(static_cast<__nv_bfloat16*>(p.dgate) + seg * n, c, n, a);
+      else store8<ROWS>(static_cast<float*>(p.dgate) + seg * n, c, n, a);
     }
     closed = true;
   };
@@ -695,8 +780,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
         if (post) o[i] = fma2(o[i], rx2, x[i] * kx2);
       }
       if (c < n) {
-        if (out.ptr[1]) store8<EVEN>(reinterpret_cast<RT*>(out.ptr[1]), c, n, dh);
-        if (out.ptr[0]) store8<EVEN>(reinterpret_cast<XT*>(out.ptr[0]), c, n, o);
+        if (out.ptr[1]) store8<ROWS>(reinterpret_cast<RT*>(out.ptr[1]), c, n, dh);
+        if (out.ptr[0]) store8<ROWS>(reinterpret_cast<XT*>(out.ptr[0]), c, n, o);
       }
     }
     out.next(p, tout, t + 1, t1);

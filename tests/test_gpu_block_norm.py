@@ -316,6 +316,26 @@ def test_no_tokens_give_zero_weight_gradients():
     assert all((d == 0).all() for d in out)
 
 
+@pytest.mark.parametrize("dtype,stream", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("n", [9, 255, 263, 1003, 4096])
+def test_rows_at_every_distance_from_a_16_byte_boundary(n, dtype, stream):
+    """Rows 1 to 8 elements off the boundary, with other numbers between them that have to stay."""
+    for offset in range(1, 9):
+        case = Case(28 + offset, 11, n, p=2, place=S0, out=S0, dtype=dtype, stream=stream, gate=-1, extra=offset % 3,
+                    offset=offset, wdtype=dtype)
+        beside = []
+        for d in case.fwd_out:
+            for s in d.slots:
+                flat = torch.as_strided(s, (s.untyped_storage().size() // s.element_size(),), (1,), 0)
+                flat.fill_(7)
+                mask = torch.ones_like(flat, dtype=torch.bool)
+                torch.as_strided(mask, s.shape, s.stride(), s.storage_offset()).fill_(False)
+                beside.append((flat, mask))
+        case.check_forward(*case.forward())
+        for flat, mask in beside:
+            assert (flat[mask] == 7).all()
+
+
 IN_PLACE = [dict(t=7, n=512), dict(t=700, n=4096, drop=0.1), dict(t=600, n=1001, p=2, place=S0, out=S0, gate=3),
             dict(t=9, n=20000), dict(t=300, n=1152, dtype="fp32"), dict(t=320, n=16384, gate=-1)]
 
