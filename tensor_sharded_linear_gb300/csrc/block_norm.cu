@@ -64,7 +64,10 @@ struct CtaSum {
 
 constexpr int BN_ANY_THREADS = 256;
 
-// One element a thread and step; the later passes over a row come from L1 or L2.
+// For more than 16384 channels, steps between rows of 2^29 elements and more, and
+// what does not fit the other kernels' tables or shared memory.  One element a
+// thread and step; the later passes over a row come from L1 or L2 and compute its
+// values again (1600 x 20000 bf16, both norms: 452 us, gradients 2.9 ms).
 template <class P, bool BWD>
 __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __grid_constant__ P p) {
   __shared__ float buf[2][5][BN_ANY_THREADS / 32];

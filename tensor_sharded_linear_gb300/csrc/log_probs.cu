@@ -360,7 +360,15 @@ struct TopList {
 
 // One cluster of CTAs per token (of one CTA when there are tokens enough): each
 // warp takes every so many units, the CTAs' sums meet in the first one's shared
-// memory, and that one writes the results.
+// memory, and that one writes the results.  One pass, each logit read once; two
+// units' loads a warp are under way, 32 warps an SM.  With the entropy an element
+// costs a multiply-add and a power of two, two sums and its unpacking: 8 warp
+// instructions for 32 of them, 0.67 of the issue slots.
+//   4096 x 128256 bf16 in 8 shards                153.5 us, 1.01 of a copy's rate; with the entropy 163.4, 0.95
+//   64 x 128256 fp32, 5 alternatives               12.7 us: the pass is half of it, then the alternatives' steps
+//   777 x 50257 bf16, 10 alternatives              20.2 us, 0.57: the same
+//   1 x 128256 bf16, 20 alternatives, entropy       8.7 us: 2 units a warp, then six meetings of the cluster or CTA
+// (With 3 CTAs an SM and more registers: 175.7, 19.1, 19.2 and 8.3 us for the last four.)
 //
 // Alternatives.  The pass over the row leaves the largest logit of each block
 // of 1 KB and of 64 groups of the cluster's lanes (32 in a CTA of one warp).
@@ -607,8 +615,10 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
   }
 }
 
-// A CTA takes a run of units of one token.  The given ids' elements are
-// written last, by the threads that stand for them, so that the pass itself
+// A CTA takes a run of units of one token; bound by HBM (4096 x 128256 bf16 in 8
+// shards, a tenth of the rows without gradient and not read: 292 us, 1.00 of a
+// copy's rate; with the entropy's 312; 301 x 50257 fp32 20.5, 0.87).  The given
+// ids' elements are written last, by the threads that stand for them, so that the pass itself
 // is the same for all.
 template <class T, bool ENT, int CAP>
 __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_backward_kernel(const __grid_constant__ LogProbParams<CAP> p) {
