@@ -368,7 +368,7 @@ struct TopList {
 //   64 x 128256 fp32, 5 alternatives               12.7 us: the pass is half of it, then the alternatives' steps
 //   777 x 50257 bf16, 10 alternatives              20.2 us, 0.57: the same
 //   1 x 128256 bf16, 20 alternatives, entropy       8.7 us: 2 units a warp, then six meetings of the cluster or CTA
-// (With 3 CTAs an SM and more registers: 175.7, 19.1, 19.2 and 8.3 us for the last four.)
+// (With 3 CTAs an SM and more registers: 175.7 us with the entropy, 19.1, 19.2 and 8.3.)
 //
 // Alternatives.  The pass over the row leaves the largest logit of each block
 // of 1 KB and of 64 groups of the cluster's lanes (32 in a CTA of one warp).
