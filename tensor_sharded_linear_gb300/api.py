@@ -798,8 +798,8 @@ def tp_block_norm_backward(dh: Optional[DTensor], dy: Optional[DTensor], x: DTen
                                x.slots[0].device)
     L.check(L.untyped("dt_tp_block_norm_backward")(
         _ref(dh), _ref(dy), _ref(x), _ref(residual), _ref(post_weight), _ref(gate), _ref(pre_weight), _ref(rng),
-        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), _ref(out[4]), C.c_float(eps), C.c_float(residual_scale), C.c_float(dropout),
-        _tp_index(x.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()), "tp_block_norm_backward")
+        _ref(out[0]), _ref(out[1]), _ref(out[2]), _ref(out[3]), _ref(out[4]), C.c_float(eps), C.c_float(residual_scale),
+        C.c_float(dropout), _tp_index(x.mesh, tp_dim), *_ws_untyped(workspace), None, _stream_arg()), "tp_block_norm_backward")
     return tuple(out)
 
 

@@ -230,7 +230,8 @@ __global__ void __launch_bounds__(BN_SUM_THREADS) block_norm_sums_kernel(const _
 #pragma unroll
       for (int k = 0; k < BN_SUM_LOADS; ++k) s.x += v[k].x, s.y += v[k].y, s.z += v[k].z, s.w += v[k].w;
     }
-    acc[group][lane * 4] = s.x, acc[group][lane * 4 + 1] = s.y, acc[group][lane * 4 + 2] = s.z, acc[group][lane * 4 + 3] = s.w;
+    float* const mine = acc[group] + lane * 4;
+    mine[0] = s.x, mine[1] = s.y, mine[2] = s.z, mine[3] = s.w;
     __syncthreads();
     const int ch = threadIdx.x / BN_SUM_SHARE, k0 = threadIdx.x % BN_SUM_SHARE;
     static_assert(BN_SUM_GROUPS == 4 * BN_SUM_SHARE, "four sums a thread");
@@ -540,6 +541,7 @@ extern "C" dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, in
     return fail(DT_ERR_INVALID_ARG, "tokens %lld, channels %lld, gate_rows %lld", (long long)tokens,
                 (long long)channels, (long long)gate_rows);
   if (tokens > 0 && gate_rows > tokens) return fail(DT_ERR_SHAPE, "more gate rows than tokens");
-  *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * ((channels + 7) / 8 * 8) * sizeof(float);
+  *bytes = (size_t)(3 * max_backward_blocks(channels) + gate_part_rows(tokens, gate_rows)) * ((channels + 7) / 8 * 8) *
+           sizeof(float);
   return DT_OK;
 }
