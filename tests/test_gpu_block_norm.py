@@ -365,6 +365,33 @@ def test_results_in_place_of_operands(c):
                 same(a, b)
 
 
+@pytest.mark.parametrize("n,wdtype", [(1001, "bf16"), (77, "fp32"), (1024, "bf16"), (20001, "bf16")])
+def test_a_gate_for_every_token(n, wdtype):
+    """Its gradient has the tokens' rows, off 16-byte boundaries too, and goes out without sums over tokens."""
+    case = Case(40, 23, n, p=2, place=S0, out=R, gate=23, wdtype=wdtype, drop=0.2)
+    case.check_forward(*case.forward())
+    case.check_backward(case.backward())
+
+
+@pytest.mark.parametrize("n", [512, 1001])
+def test_one_row_for_all_tokens(n):
+    """Rows without a step between them (x and the residual broadcast), and one replica of several."""
+    case = Case(41, 9, n, gate=-1)
+    for d in (case.x, case.r):
+        d.slots[0].copy_(d.slots[0][:1].clone().expand(9, n))
+    want = [d.slots[0] for d in case.forward()] + [d.slots[0] for d in case.backward()]
+    mesh = tsl.DeviceMesh((2,), ("tp",))
+
+    def again(d, broadcast=False):
+        t = d.slots[0]
+        t = t[:1].expand(9, n) if broadcast else t
+        return tsl.DTensor([t, t.clone()], mesh, [R], d.gshape, d.dtype, materialize_replicas=True)
+
+    ops = (again(case.x, True), again(case.r, True), again(case.post), again(case.gate), again(case.pre))
+    out = tsl.tp_block_norm(*ops, **case.kw) + tsl.tp_block_norm_backward(again(case.gh), again(case.gy), *ops, **case.kw)
+    assert all(torch.equal(a.slots[0], b) for a, b in zip(out, want))
+
+
 def test_empty_sequences_give_zero_gate_gradients():
     mesh = tsl.DeviceMesh((1,), ("tp",))
     empty = lambda: whole(torch.zeros(5, 0, 64), mesh, torch.bfloat16)  # noqa: E731
