@@ -237,21 +237,29 @@ __device__ __forceinline__ int given_id(const LogProbArgs& p, int64_t i, bool re
 
 // A running softmax in powers of two: the largest logit m, s = sum 2^t and
 // e = sum t 2^t over the logits so far, t = c z - fl(c m): one multiply-add a
-// logit, and the product's rounding, common to all of them, drops out at the
-// end (`rounding`).  Where |m| > 1e27, t = (z - m) c, which does not overflow;
-// m starts at the lowest finite number.  Factors stay above -1e28, so that 0
-// times them is 0.
+// logit.  The product's rounding c m - fl(c m) is in every t and drops out at the
+// end (`rounding`); it has to stay small, for the largest logit's 2^t is 2 to
+// that, and does while |c m| <= 2^22, whose last place is a quarter: an eighth.
+// Beyond (m starts there, at the lowest finite number) t = (z - m) c, which has
+// no such rounding and does not overflow, and a maximum that goes from one form
+// to the other takes the difference of the two roundings along.  Factors stay
+// above -1e28, so that 0 times them is 0.
 struct Soft {
   float m = -3.402823466e38f, s = 0.f, e = 0.f;
-  static __device__ __forceinline__ bool usual(float m) { return fabsf(m) <= 1e27f; }
+  static __device__ __forceinline__ bool usual(float m, float c) { return fabsf(__fmul_rn(m, c)) <= 0x1p22f; }
+  static __device__ __forceinline__ float rounding(float m, float c) {
+    return usual(m, c) ? fmaf(m, c, -__fmul_rn(m, c)) : 0.f;
+  }
+  __device__ __forceinline__ float rounding(float c) const { return rounding(m, c); }
   __device__ __forceinline__ void raise(float to, float c) {  // to >= m, or NaN
-    const float d = usual(m) && usual(to) ? __fsub_rn(__fmul_rn(m, c), __fmul_rn(to, c)) : (m - to) * c;
+    const float from = __fmul_rn(m, c), up = __fmul_rn(to, c);
+    float d = __fsub_rn(from, up);
+    if (!(fmaxf(fabsf(from), fabsf(up)) <= 0x1p22f)) d = (m - to) * c + (rounding(to, c) - rounding(m, c));
     const float down = fmaxf(d, -1e28f), f = exp2_fast(down);
     e = f * fmaf(down, s, e);
     s *= f;
     m = to;
   }
-  __device__ __forceinline__ float rounding(float c) const { return usual(m) ? fmaf(m, c, -__fmul_rn(m, c)) : 0.f; }
   template <int N>
   __device__ __forceinline__ void join_lanes(float c) {  // over groups of N lanes
     float top = m;
@@ -267,7 +275,7 @@ struct Soft {
 };
 // t of two logits under any m
 __device__ __forceinline__ f2 difference(f2 z, float m, float c) {
-  if (Soft::usual(m)) return fma2(z, both(c), both(-__fmul_rn(m, c)));
+  if (Soft::usual(m, c)) return fma2(z, both(c), both(-__fmul_rn(m, c)));
   return (z + both(-m)) * both(c);
 }
 
@@ -277,7 +285,7 @@ __device__ __forceinline__ void soft_unit(Soft& a, Vec<T> (&v)[LP_VECS], float m
   if (!(most == a.m)) a.raise(most, c);
   constexpr int N = Unit<T>::VE / 2;
   f2 s[2] = {both(0.f), both(0.f)}, e[2] = {both(0.f), both(0.f)};
-  if (__all_sync(0xffffffffu, Soft::usual(a.m))) {
+  if (__all_sync(0xffffffffu, Soft::usual(a.m, c))) {
     const f2 r2 = both(-__fmul_rn(a.m, c)), c2 = both(c);
 #pragma unroll
     for (int i = 0; i < LP_VECS; ++i) {
