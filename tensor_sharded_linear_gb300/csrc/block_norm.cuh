@@ -332,7 +332,8 @@ struct RowCursors {
 // where it has been unpacked, the residual's from where it has been added (a ring
 // of rows in shared memory, which takes the weights' L1, 53 us instead of 51.6 at
 // the first size below).  Else the parts' loads go out four at a time.  Threads
-// without a last vector load the row's first one instead and drop it.
+// without a last vector work on the row's first one instead, with its weights,
+// and leave it out of sums and stores (whatever it holds then, NaN too).
 //   8192 x 4096 bf16, dropout, residual, norm     51.4 us, 0.77 of a copy's rate
 //     (43.8 us without dropout's arithmetic, ten rounds for four elements)
 //   2048 x 8192 bf16 in 8 parts, both norms       65.7 us, 0.83 (waits for the parts)
@@ -395,11 +396,6 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
   }
   for (int64_t t = t0; t < t1; ++t) {
     f2 h[VPT][4];
-    auto unpack = [&](int v, f2(&w)[4]) {
-      x[v].get2(w);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = has(v) ? w[i] : both(0.f);
-    };
     if (gate && t >= gate_end) {
       const int64_t row = (uint32_t)t / (uint32_t)p.gate_per;
       gate = static_cast<const char*>(p.gate) + row * n * (p.gate_dtype == DT_BF16 ? 2 : 4);
@@ -408,7 +404,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
     }
     if constexpr (AHEAD) {
 #pragma unroll
-      for (int v = 0; v < VPT; ++v) unpack(v, h[v]);
+      for (int v = 0; v < VPT; ++v) x[v].get2(h[v]);
       if (t + 1 < t1) {
         cx.next(p, tx, t + 1, t1);
         load_x(cx.ptr[0]);
@@ -427,7 +423,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
           f2 w[4];
-          unpack(v, w);
+          x[v].get2(w);
 #pragma unroll
           for (int i = 0; i < 4; ++i) h[v][i] = k ? h[v][i] + w[i] : w[i];
         }
@@ -436,9 +432,11 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
     auto total = [&] {
       f2 s = both(0.f);
 #pragma unroll
-      for (int v = 0; v < VPT; ++v)
+      for (int v = 0; v < VPT; ++v) {
+        if (!has(v)) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) s = fma2(h[v][i], h[v][i], s);
+      }
       return rsqrtf(row_sum(s.x + s.y, buf, turn) * inv_n + p.eps);
     };
     if (p.post) {
@@ -471,7 +469,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
         f2 w[4];
         r[v].get2(w);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) h[v][i] = has(v) ? fma2(scale, w[i], h[v][i]) : h[v][i];
+        for (int i = 0; i < 4; ++i) h[v][i] = fma2(scale, w[i], h[v][i]);
       }
     }
     if (AHEAD && t + 1 < t1) load_r(t + 1);

@@ -1,0 +1,59 @@
+"""Block norms under weights and gates that are not finite: what the formula keeps finite stays finite."""
+import numpy as np
+import pytest
+import torch
+
+import tensor_sharded_linear_gb300 as tsl
+from heads_helpers import DT, draw, strided, whole
+from oracle import decoder
+
+pytestmark = pytest.mark.gpu
+HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
+R = tsl.Replicate()
+INF, NAN = float("inf"), float("nan")
+
+
+def same(a, e, tol):
+    with np.errstate(invalid="ignore"):
+        ok = (a == e) | (np.isnan(a) & np.isnan(e)) | (np.abs(a - e) <= tol)
+    assert ok.all(), [(i.tolist(), a[tuple(i)], e[tuple(i)]) for i in np.argwhere(~ok)[:5]]
+
+
+@pytest.mark.parametrize("dtype,stream", [("bf16", "bf16"), ("bf16", "fp32"), ("fp32", "fp32")])
+@pytest.mark.parametrize("t", [3, 320])  # (few tokens: a vector a thread; many: rows read ahead)
+@pytest.mark.parametrize("n,offset", [(9, 0), (40, 0), (1000, 0), (1152, 0), (1160, 1), (2568, 0), (4096, 0)])
+def test_weights_of_the_first_channels(n, offset, t, dtype, stream):
+    """An infinite or NaN weight of channels 0 to 7: channel counts with and without threads that have no last vector.
+
+    Where dropout drops the channel, the row is that of a finite weight; where h is infinite, y is 0 in the others."""
+    rng = np.random.default_rng(n)
+    mesh = tsl.DeviceMesh((1,), ("tp",))
+    x, r = draw(rng, (t, n), dtype), draw(rng, (t, n), stream)
+    weights = {name: draw(rng, (n,), "fp32") for name in ("post", "gate", "pre")}
+    seed = rng.integers(-2 ** 31, 2 ** 31, 4)
+    keep = decoder.keep_mask(seed, t, n, 0.5)
+
+    def rows(v, d):
+        return tsl.DTensor([strided(torch.from_numpy(v).cuda().to(DT[d]), 0, offset)], mesh, [R], (t, n), DT[d])
+
+    xd, rd, seed = rows(x, dtype), rows(r, stream), whole(torch.tensor(seed, dtype=torch.int32), mesh)
+    for bad, channel in ((INF, 0), (NAN, 7), (-INF, 3)):
+        for which in weights:
+            w = {name: v.copy() for name, v in weights.items()}
+            w[which][channel] = bad
+            h, y = tsl.tp_block_norm(xd, rd, *(whole(v, mesh, torch.float32) for v in w.values()), dropout=0.5, rng=seed)
+            h, y = h.slots[0].double().cpu().numpy(), y.slots[0].double().cpu().numpy()
+            with np.errstate(invalid="ignore", over="ignore", divide="ignore"):
+                e = decoder.Block([x], r, *w.values(), keep=keep, p=0.5)
+                f = np.isfinite(e.h).all(1)
+                # 20 roundings and two norms' sums, as many additions as a thread makes and 16 each; a norm's is of h,
+                # whose terms may cancel, and is the worst row's ratio of magnitudes to values off
+                ratio = ((e.abs_h[f] ** 2).sum(1) / (e.h[f] ** 2).sum(1)).max(initial=1.0)
+                k = (20 + 2 * (-(-n // 32) + 16)) * ratio * 2.0 ** -24
+                same(h, e.h, HALF[stream] * np.abs(e.h) + k * e.abs_h + 1e-37)
+                same(y[f], e.y[f], HALF[dtype] * np.abs(e.y[f]) + k * e.abs_y[f] + 1e-37)
+            if which != "pre":
+                assert np.array_equal(f, ~keep[:, channel])
+                others = np.arange(n) != channel
+                assert np.isnan(y[~f][:, channel]).all()
+                assert (np.isnan(y[~f]) if np.isnan(bad) else y[~f][:, others] == 0).all()
