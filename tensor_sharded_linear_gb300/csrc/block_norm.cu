@@ -275,8 +275,6 @@ dt_status channel_vector(const dt_dtensor* w, const char* what, const Layout& of
 int64_t gate_part_rows(int64_t tokens, int64_t gate_rows) { return gate_rows == tokens ? 0 : gate_rows; }
 
 int round_up(int64_t a, int b) { return (int)((a + b - 1) / b * b); }
-constexpr int64_t BN_SMEM = 224 * 1024;  // of an SM, for rings
-constexpr int64_t BN_STATIC = 2560;      // a CTA's other shared memory, at most
 
 // vec: no step between rows is beyond what the kernels on vectors count in;
 // even: rows of a multiple of 8 channels on 16-byte boundaries; small: few row blocks.

@@ -817,10 +817,10 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
 
 // ---------------------------------------------------------------- launches
 
-template <class K, class... A>
-cudaError_t launch_rows(K kernel, const BlockShape& s, cudaStream_t stream, const A&... args) {
+template <auto KERNEL, class P>
+cudaError_t launch_rows(const BlockShape& s, cudaStream_t stream, const P& p) {
   if (s.smem > 40 * 1024)
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem)) return e;
+    if (cudaError_t e = allow_dynamic_smem<KERNEL, BN_SMEM - BN_STATIC>()) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(s.grid);
   cfg.blockDim = dim3(s.threads);
@@ -834,14 +834,14 @@ cudaError_t launch_rows(K kernel, const BlockShape& s, cudaStream_t stream, cons
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = s.cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
 template <class XT, class RT, bool AHEAD, bool EVEN, class P>
 cudaError_t forward_rows(const P& p, const BlockShape& s, cudaStream_t stream) {
-  return s.vpt == 1   ? launch_rows(block_norm_row_kernel<XT, RT, 1, AHEAD, EVEN, P>, s, stream, p)
-         : s.vpt == 2 ? launch_rows(block_norm_row_kernel<XT, RT, 2, AHEAD, EVEN, P>, s, stream, p)
-                      : launch_rows(block_norm_row_kernel<XT, RT, 4, AHEAD, EVEN, P>, s, stream, p);
+  return s.vpt == 1   ? launch_rows<block_norm_row_kernel<XT, RT, 1, AHEAD, EVEN, P>>(s, stream, p)
+         : s.vpt == 2 ? launch_rows<block_norm_row_kernel<XT, RT, 2, AHEAD, EVEN, P>>(s, stream, p)
+                      : launch_rows<block_norm_row_kernel<XT, RT, 4, AHEAD, EVEN, P>>(s, stream, p);
 }
 template <class XT, class RT>
 cudaError_t block_rows(const BlockSmall& p, bool bwd, const BlockShape& s, cudaStream_t stream) {
@@ -852,7 +852,7 @@ cudaError_t block_rows(const BlockSmall& p, bool bwd, const BlockShape& s, cudaS
 #define DT_BN_BACK(VPT, S, CLUSTER, ONE, EVEN, DROP)                                                       \
   if (s.vpt == VPT && s.stages == S && s.cluster == CLUSTER && (!ONE || p.x.parts == 1) && s.even == EVEN && \
       (DROP || !p.rng))                                                                                    \
-    return launch_rows(block_norm_row_backward_kernel<XT, RT, VPT, S, CLUSTER, ONE, EVEN, DROP, BlockSmall>, s, stream, p);
+    return launch_rows<block_norm_row_backward_kernel<XT, RT, VPT, S, CLUSTER, ONE, EVEN, DROP, BlockSmall>>(s, stream, p);
   DT_BN_BACK(1, 5, 1, true, true, false) DT_BN_BACK(1, 5, 1, true, true, true)
   DT_BN_BACK(1, 3, 1, true, true, false) DT_BN_BACK(1, 3, 1, true, true, true)
   DT_BN_BACK(2, 3, 1, true, true, false) DT_BN_BACK(2, 3, 1, true, true, true)

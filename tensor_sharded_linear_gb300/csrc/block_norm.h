@@ -56,6 +56,8 @@ struct BlockShape {
   bool even = true;    // rows of a multiple of 8 channels on 16-byte boundaries
   size_t smem = 0;
 };
+constexpr int BN_SMEM = 224 * 1024;  // of an SM, for rings
+constexpr int BN_STATIC = 2560;      // a CTA's other shared memory, at most
 // Threads of forward CTAs that an SM's registers are shared among, measured
 // together with the vectors a thread at 8192 x 4096 with dropout: four vectors
 // and 640 threads 51.6 us, two and 768 57.7, eight and 512 64.7.

@@ -1,6 +1,9 @@
 // Clusters of CTAs: ranks, the cluster's barrier in two halves, and stores into
-// the shared memory of another CTA.
+// the shared memory of another CTA; and what launches need beyond the usual
+// shared memory.
 #pragma once
+
+#include <atomic>
 
 #include "ptx_sm103.cuh"
 
@@ -27,6 +30,25 @@ __device__ __forceinline__ void store_cluster(uint32_t a, uint32_t v) {
 }
 __device__ __forceinline__ void store_cluster(uint32_t a, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+}
+
+// Allow a kernel up to BYTES of dynamic shared memory: once per device, and the
+// same for every launch.  The limit is the kernel's, not a launch's: set to what
+// one launch needs, it would refuse a larger one that another thread is about to
+// make.
+template <auto KERNEL, int BYTES>
+cudaError_t allow_dynamic_smem() {
+  static std::atomic<bool> done[64];  // by device; calls come from any thread
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev].load(std::memory_order_acquire)) {
+    e = cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    if (e != cudaSuccess) return e;
+    done[dev].store(true, std::memory_order_release);
+  }
+  return cudaSuccess;
 }
 
 }  // namespace dt

@@ -26,6 +26,7 @@ constexpr int LP_WARPS = 8;
 constexpr int LP_THREADS = 32 * LP_WARPS;
 constexpr int LP_MAX_CLUSTER = 8;
 constexpr int64_t LP_MAX_TOP_VOCAB = 1 << 24;
+constexpr int LP_MAX_SMEM = 128 * 1024;  // a CTA's list of blocks; on clusters of 8 it holds LP_MAX_TOP_VOCAB
 constexpr float LOG2E = 1.44269504088896341f;
 
 // A unit of work is 2 KB of one shard's row, on 16-byte boundaries of memory:
@@ -801,10 +802,10 @@ int64_t count_units(VocabShard* z, int shards, int64_t tokens, int esize) {
   return units;
 }
 
-template <class P>
-cudaError_t launch_log_probs(void (*kernel)(P), const P& p, int threads, size_t smem, cudaStream_t s) {
+template <auto KERNEL, class P>
+cudaError_t launch_log_probs(const P& p, int threads, size_t smem, cudaStream_t s) {
   if (smem > 32 * 1024)
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)) return e;
+    if (cudaError_t e = allow_dynamic_smem<KERNEL, LP_MAX_SMEM>()) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(p.tokens * p.parts));
   cfg.blockDim = dim3(threads);
@@ -818,7 +819,7 @@ cudaError_t launch_log_probs(void (*kernel)(P), const P& p, int threads, size_t 
   at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = p.parts > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, p);
+  return cudaLaunchKernelEx(&cfg, KERNEL, p);
 }
 
 template <class T, int CAP>
@@ -835,7 +836,7 @@ cudaError_t forward(const LogProbArgs& a, const VocabShard* z, cudaStream_t s) {
     const int64_t step = (int64_t)p.parts * LP_WARPS;
     return a.top ? (size_t)((p.units + step - 1) / step * LP_WARPS * LP_UNIT_BLOCKS * 2 * sizeof(uint32_t)) : 0;
   };
-  while (p.parts < LP_MAX_CLUSTER && smem() > 128 * 1024) p.parts *= 2;
+  while (p.parts < LP_MAX_CLUSTER && smem() > LP_MAX_SMEM) p.parts *= 2;
   int warps = 1;
   while (warps < LP_WARPS && warps < p.units) warps *= 2;
   // Many tokens: fewer warps a token, down to 16 units each, as long as the
@@ -845,7 +846,7 @@ cudaError_t forward(const LogProbArgs& a, const VocabShard* z, cudaStream_t s) {
   while (p.parts == 1 && warps > 1 && p.units < 16 * warps && p.tokens * (warps / 2) >= resident * LP_WARPS / 2) warps /= 2;
 #define DT_LP(TOP, ENT) \
   if ((a.top > 0) == TOP && (a.entropy != nullptr) == ENT) \
-    return launch_log_probs(log_probs_kernel<T, TOP, ENT, CAP>, p, 32 * warps, smem(), s);
+    return launch_log_probs<log_probs_kernel<T, TOP, ENT, CAP>>(p, 32 * warps, smem(), s);
   DT_LP(false, false) DT_LP(false, true) DT_LP(true, false) DT_LP(true, true)
 #undef DT_LP
   return cudaErrorInvalidValue;
