@@ -142,8 +142,8 @@ __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __
     }
     float kh = 0.f, kx = 0.f;  // r(h)^3 m(h z), r(s)^3 m(s v)
     auto grad = [&](int c, float a) {  // g, for a value a of h
-      const float z = y ? load_any(y, p.y.dtype, c) * pre(c) : 0.f;
-      return (h ? load_any(h, p.h.dtype, c) : 0.f) + rh * z - kh * a;
+      const float d = h ? load_any(h, p.h.dtype, c) : 0.f;
+      return y ? d + rh * (load_any(y, p.y.dtype, c) * pre(c)) - kh * a : d;
     };
     if (p.pre) {
       float v[5] = {0.f, 0.f, 0.f, 0.f, 0.f};

@@ -767,7 +767,8 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
         kh = rh * rh * rh * (q[1] * inv_n);
       }
       if (post) {
-        kx = rx * rx * rx * ((q[2] + rh * q[3] - kh * q[4]) * inv_n);
+        // (h may hold anything where there is no norm of it)
+        kx = rx * rx * rx * ((has_y ? q[2] + rh * q[3] - kh * q[4] : q[2]) * inv_n);
         next_rx = rsqrtf(q[5] * inv_n + p.eps);
       }
     }

@@ -1,4 +1,4 @@
-"""Block norms under weights and gates that are not finite: what the formula keeps finite stays finite."""
+"""Block norms under weights, gates, residuals and gradients that are not finite: what the formula keeps finite stays so."""
 import numpy as np
 import pytest
 import torch
@@ -6,6 +6,7 @@ import torch
 import tensor_sharded_linear_gb300 as tsl
 from heads_helpers import DT, draw, strided, whole
 from oracle import decoder
+from test_gpu_block_norm import Case
 
 pytestmark = pytest.mark.gpu
 HALF = {"bf16": 2.0 ** -8, "fp32": 2.0 ** -24}
@@ -57,3 +58,28 @@ def test_weights_of_the_first_channels(n, offset, t, dtype, stream):
                 others = np.arange(n) != channel
                 assert np.isnan(y[~f][:, channel]).all()
                 assert (np.isnan(y[~f]) if np.isnan(bad) else y[~f][:, others] == 0).all()
+
+
+def check_gradients(case, dh):
+    """Those of a case whose operands hold what is not finite, in all places where the formula has a value."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        ref = case.ref.backward(dh, case.dy)
+        for name, d in zip(("dx", "dr", "dpost", "dgate", "dpre"), case.backward()):
+            if d is None:
+                continue
+            e, mag = ref[name]
+            half = HALF[case.dtype if name == "dx" else case.stream if name == "dr" else case.wdtype]
+            # as for finite operands: twice the forward's roundings, and sums over tokens
+            k = 2 * case.k + (-(-case.t // 152) + 40) * 2.0 ** -24
+            same(d.slots[0].double().cpu().numpy(), e, half * np.abs(e) + k * mag + 1e-37)
+            assert np.isfinite(e).all() or name == "dr"
+
+
+@pytest.mark.parametrize("drop", [0.0, 0.3])
+@pytest.mark.parametrize("n,dtype", [(1024, "bf16"), (1001, "fp32"), (4096, "bf16"), (12288, "bf16"), (20000, "bf16")])
+def test_gradients_do_not_meet_a_residual_without_a_norm_of_it(n, dtype, drop):
+    """Without pre_weight no gradient depends on h, whatever the residual holds."""
+    case = Case(31, 9, n, dtype=dtype, pre=False, gate=3, drop=drop)
+    for row, v in ((2, INF), (4, NAN), (7, -INF)):
+        case.r.slots[0][row, n // 2:] = v
+    check_gradients(case, case.dh)
