@@ -750,7 +750,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
         h[v][i] = fma2(scale, h[v][i], a * both(rx));
         sum[0] = fma2(h[v][i], h[v][i], sum[0]);
         sum[1] = fma2(h[v][i], z, sum[1]);
-        sum[2] = fma2(a, dh[i], sum[2]);
+        sum[2] = fma2(a, dropout ? kept(dh[i], bits[v], i) : dh[i], sum[2]);  // (0 times what is dropped)
         sum[3] = fma2(a, z, sum[3]);
         sum[4] = fma2(a, h[v][i], sum[4]);
       }

@@ -83,3 +83,15 @@ def test_gradients_do_not_meet_a_residual_without_a_norm_of_it(n, dtype, drop):
     for row, v in ((2, INF), (4, NAN), (7, -INF)):
         case.r.slots[0][row, n // 2:] = v
     check_gradients(case, case.dh)
+
+
+@pytest.mark.parametrize("pre", [True, False])
+@pytest.mark.parametrize("n,dtype", [(1024, "bf16"), (1001, "fp32"), (4096, "bf16"), (12288, "bf16"), (20000, "bf16")])
+def test_gradients_of_dropped_elements_reach_the_residual_alone(n, dtype, pre):
+    """Infinities and NaN of dh in dropped places: the residual's gradient has them there, the others stay finite."""
+    case = Case(32, 9, n, dtype=dtype, pre=pre, gate=3, drop=0.5)
+    dh = case.dh.copy()
+    for row, v in ((1, INF), (4, NAN), (8, -INF)):
+        dh[row, ~case.ref.keep[row]] = v
+    case.gh.slots[0].copy_(torch.from_numpy(dh))
+    check_gradients(case, dh)
