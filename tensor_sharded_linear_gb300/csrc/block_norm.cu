@@ -64,10 +64,12 @@ struct CtaSum {
 
 constexpr int BN_ANY_THREADS = 256;
 
-// For more than 16384 channels, steps between rows of 2^29 elements and more, and
-// what does not fit the other kernels' tables or shared memory.  One element a
-// thread and step; the later passes over a row come from L1 or L2 and compute its
-// values again (1600 x 20000 bf16, both norms: 452 us, gradients 2.9 ms).
+// For more than 16384 channels; steps between rows of 2^29 elements and more; more
+// than 64 row blocks in all operands (gradients, and forward off 16-byte
+// boundaries); gradients with parts of x whose row does not fit the shared memory
+// of two SMs.  One element a thread and step; the later passes over a row come
+// from L1 or L2 and compute its values again (1600 x 20000 bf16, both norms:
+// 452 us, gradients 2.9 ms).
 template <class P, bool BWD>
 __global__ void __launch_bounds__(BN_ANY_THREADS) block_norm_any_kernel(const __grid_constant__ P p) {
   __shared__ float buf[2][5][BN_ANY_THREADS / 32];
@@ -306,21 +308,25 @@ BlockShape backward_shape(const BlockArgs& p, bool vec, bool even, bool small, i
   const int sms = device_sm_count();
   const int64_t vectors = ((int64_t)p.n + 7) / 8;
   int64_t most = 2 * sms;
-  if (vec && small && vectors <= 2048) {
-    s.cluster = vectors <= 1024 ? 1 : 2;
-    s.vpt = vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 79.0 us, one 88.9)
-    s.threads = round_up((vectors + s.vpt * s.cluster - 1) / (s.vpt * s.cluster), 32);
-    s.even = even;
-    const int64_t stage = (int64_t)s.threads * s.vpt * 8 *
+  // one CTA a row, or a pair where there are more channels than a CTA takes, or parts of x that do not fit an SM
+  // (744 x 8192 fp32 in 4 parts: 105 us, the kernel for any size 682)
+  for (int cluster = vectors <= 1024 ? 1 : 2; vec && small && vectors <= 2048 && !s.vpt && cluster <= 2; ++cluster) {
+    const int vpt = cluster == 1 && vectors <= 256 ? 1 : 2;  // (8192 x 4096: two vectors 79.0 us, one 88.9)
+    const int threads = round_up((vectors + vpt * cluster - 1) / (vpt * cluster), 32);
+    const int64_t stage = (int64_t)threads * vpt * 8 *
                           ((p.x.parts + 1) * dtype_size(p.x.dtype) + 2 * dtype_size(p.h.dtype));
-    const int64_t ctas = std::min(8, 512 / s.threads);
-    s.stages = !even || p.x.parts > 1                                      ? 1
-               : s.vpt == 1 && (5 * stage + BN_STATIC) * ctas <= BN_SMEM ? 5
-               : (3 * stage + BN_STATIC) * ctas <= BN_SMEM               ? 3
-                                                                         : 1;
+    if (stage + BN_STATIC > BN_SMEM) continue;
+    const int64_t ctas = std::min(8, 512 / threads);
+    s.cluster = cluster;
+    s.vpt = vpt;
+    s.threads = threads;
+    s.even = even;
+    s.stages = !even || p.x.parts > 1                                    ? 1
+               : vpt == 1 && (5 * stage + BN_STATIC) * ctas <= BN_SMEM ? 5
+               : (3 * stage + BN_STATIC) * ctas <= BN_SMEM             ? 3
+                                                                       : 1;
     s.smem = stage * s.stages;
-    if (stage + BN_STATIC > BN_SMEM) s = BlockShape();
-    else most = std::min<int64_t>(ctas, BN_SMEM / (int64_t)(s.smem + BN_STATIC)) * sms / s.cluster;
+    most = std::min<int64_t>(ctas, BN_SMEM / (int64_t)(s.smem + BN_STATIC)) * sms / cluster;
   }
   // four tokens a run at least, for its sums are written and read again
   most = std::min<int64_t>(most, std::max<int64_t>(sms / s.cluster, (p.tokens + 3) / 4));

@@ -30,6 +30,13 @@ def test_partial_sums(n, p, drop, types):
 
 
 @pytest.mark.parametrize("types", TYPES, ids=ids)
+@pytest.mark.parametrize("n,p", [(8192, 4), (8192, 8), (8192, 16), (6144, 8), (4096, 16), (2048, 32), (16384, 8), (7000, 64)])
+def test_many_partial_sums(n, p, types):
+    """Parts of a row that fill the shared memory of an SM, of two, and more."""
+    run(dict(t=5, n=n, p=p, place=PART, gate=-1, **types))
+
+
+@pytest.mark.parametrize("types", TYPES, ids=ids)
 @pytest.mark.parametrize("n,p", [(1001, 1), (1999, 4), (4093, 1), (8191, 2), (8197, 1), (16383, 3)])
 def test_odd_channels(n, p, types):
     run(dict(t=37, n=n, p=p, place=PART if p > 1 else tsl.Replicate(), gate=-1, drop=0.1, **types))
