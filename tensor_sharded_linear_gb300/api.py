@@ -863,8 +863,11 @@ def tp_head_log_probs(x: DTensor, w_head: DTensor, ids: Optional[DTensor] = None
     their shards, in ``logits_dtype`` (x's without one).  With none of residual,
     weights and gate x goes into the head as it is."""
     if any(o is not None for o in (residual, post_weight, gate, pre_weight)):
+        like = residual if residual is not None else x
+        # what goes into the head, and not the residual stream beside it
+        out = (None, _row_like(like, x.dtype)) if pre_weight is not None else (_row_like(like), None)
         h, y = tp_block_norm(x, residual, post_weight, gate, pre_weight, eps=eps, residual_scale=residual_scale,
-                             tp_dim=tp_dim)
+                             tp_dim=tp_dim, out=out)
         x = h if y is None else y
     logits = column_parallel_linear(x, w_head, tp_dim=tp_dim, out_dtype=logits_dtype)
     return tp_log_probs(logits, ids, scale=scale, top=top, entropy=entropy, ignore_index=ignore_index, tp_dim=tp_dim)
