@@ -453,9 +453,8 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
       });
     }
     if (drop.on) {
-      // the words in a loop of two vectors a round: unrolled, the code does not stay in the instruction cache
-      uint64_t keep = 0;
-#pragma unroll 4
+      uint64_t keep = 0;  // 8 bits a vector
+#pragma unroll
       for (int v = 0; v < VPT; ++v) keep |= (uint64_t)drop.bits<EVEN>(t, n, (tid + v * nt) * 8) << (8 * v);
 #pragma unroll
       for (int v = 0; v < VPT; ++v)
@@ -514,6 +513,7 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 template <class XT, class RT, int VPT, int S, int CLUSTER, bool ONE, bool EVEN, bool DROP, class P>
 __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __grid_constant__ P p) {
   constexpr Rows ROWS = EVEN ? Rows::EVEN : Rows::SINGLE;
+  static_assert(S == 1 || (ONE && EVEN), "parts and rows off 16-byte boundaries: one row at a time");
   __shared__ __align__(16) float buf[2][8][16];
   __shared__ float meet[2][2][8];  // the cluster's CTAs' sums
   extern __shared__ uint4 ring[];
@@ -712,10 +712,7 @@ __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __gr
     if (++slot == S) slot = 0;
     uint4* const next = mine + slot * stage;
     if (EVEN) copies_wait<(S > 1 ? S - 2 : 0)>();  // this row and (S > 1) the next
-    if (parts > 1) {
-      if (S == 1 || t == t0) add_parts(from);
-      if (S > 1 && t + 1 < t1) add_parts(next);
-    }
+    if (parts > 1) add_parts(from);
     float q[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (post && (S == 1 || t == t0)) {
       q[0] = square(from);
