@@ -601,7 +601,8 @@ DT_API dt_status dt_tp_block_norm_backward_workspace_size(int64_t tokens, int64_
  * All small tensors are Replicate and contiguous.  scale 2^-20 .. 2^20; with
  * alternatives V is at most 2^24, or 2^21 of 2^28 tokens (DT_ERR_CAPACITY).  An id that is
  * ignore_index gives 0; another one outside [0, V) gives 0 and sets
- * DT_DEV_ERR_INDEX.  Logits of -inf have probability 0; a row of nothing else
+ * DT_DEV_ERR_INDEX.  Logits may have any finite size (what is beyond fp32 in a
+ * result is an infinity); those of -inf have probability 0, a row of nothing else
  * gives lse = -inf, entropy 0 and log probabilities -inf.  A row with NaN or
  * +inf gives NaN (in the order of the alternatives NaN is above all).
  */
@@ -618,7 +619,9 @@ DT_API dt_status dt_tp_log_probs(const dt_dtensor* logits, const dt_dtensor* ids
  *            (the same slots and strides)
  * Ids that were given twice add up; those that gave 0 above add nothing.  A row
  * whose gradients are all 0, and one whose lse is -inf, get 0 whatever its
- * logits hold.
+ * logits hold.  Probabilities are exp(scale * logits - lse), of an lse in fp32:
+ * accurate while |scale * logits| of the likely ones is small against 2^24, where
+ * lse's last place is 1; beyond they are off by a factor and may overflow.
  */
 DT_API dt_status dt_tp_log_probs_backward(const dt_dtensor* dlogprobs, const dt_dtensor* dentropy,
                                           const dt_dtensor* logits, const dt_dtensor* ids, const dt_dtensor* lse,

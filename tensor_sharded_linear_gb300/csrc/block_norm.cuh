@@ -334,10 +334,11 @@ struct RowCursors {
 // the first size below).  Else the parts' loads go out four at a time.  Threads
 // without a last vector work on the row's first one instead, with its weights,
 // and leave it out of sums and stores (whatever it holds then, NaN too).
-//   8192 x 4096 bf16, dropout, residual, norm     51.4 us, 0.77 of a copy's rate
-//     (43.8 us without dropout's arithmetic, ten rounds for four elements)
-//   2048 x 8192 bf16 in 8 parts, both norms       65.7 us, 0.83 (waits for the parts)
-//   13403 x 1152 bf16, fp32 residual stream, gate 30.4 us, 0.90
+//   8192 x 4096 bf16, dropout, residual, norm     50.7 us, 0.78 of a copy's rate
+//     (42.8 us without dropout's arithmetic, ten rounds for four elements)
+//   2048 x 8192 bf16 in 8 parts, both norms       66.2 us, 0.82 (waits for the parts)
+//   13403 x 1152 bf16, fp32 residual stream, gate 30.0 us, 0.91
+//   8192 x 4096 bf16 in an fp32 stream, both norms 70.0 us, 0.85; fp32 95.1 us, 0.83
 //   8 x 4096 bf16 in 4 parts, both norms           4.1 us, one row's latency
 template <class XT, class RT, int VPT, bool AHEAD, bool EVEN, class P>
 __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT)))
@@ -501,14 +502,19 @@ __global__ void __launch_bounds__(block_forward_resident(VPT, AHEAD, sizeof(RT))
 //  - dgate and dpost are one sum: with q = sum over the tokens of a gate row
 //    of g s r(s) (kept elements), dgate = post q / (1 - p), and dpost adds up
 //    gate q / (1 - p).
-//  - What an operand is missing for is 0 (or, of w, 1) and computed all the same.
+//  - What an operand is missing for is 0 (or, of w, 1) and computed all the same,
+//    but for what may not be finite: h without a norm of it, dh in dropped places.
 // What bounds it: latency at 16 warps an SM (its sums and weights fill the
-// registers); 0.58 of the issue slots and 0.62 of the DRAM cycles are used.
-//   8192 x 4096 bf16, both norms, a gate          77.0 us with the sums' kernel, 0.77 of a copy's rate
-//   1533 x 1000 fp32, both, gates, dropout        18.7 us, four rows a CTA one after the other
-//   1600 x 16384 bf16, both norms, pairs of CTAs  92.3 us, 3.4 TB/s
+// registers); 0.58 of the issue slots and 0.61 of the DRAM cycles are used.
+//   8192 x 4096 bf16, both norms, a gate          76.8 us with the sums' kernel, 0.77 of a copy's rate
+//   1533 x 1000 fp32, both, gates, dropout        18.9 us, four rows a CTA one after the other
+//   1600 x 16384 bf16, both norms, pairs of CTAs  93.1 us, 3.4 TB/s
 // Parts of x (ONE false) are added up in the ring, in fp32, over the first of
-// them.  Rows off 16-byte boundaries (EVEN false) come by plain loads, S = 1.
+// them.  Rows off 16-byte boundaries (EVEN false) come by plain loads.  Both go
+// with S = 1, as do rows of which three do not fit: the next row's loads go out
+// after the present one's stores, and nothing overlaps within a CTA.
+//   744 x 4096 bf16 in 8 parts, both norms        28.6 us, 0.41
+//   8192 x 4096 bf16 in an fp32 stream, both     132 us, 0.67; fp32 201 us, 0.59
 // DROP false: no code for dropout (8192 x 4096: 79.4 us, with it 83.5).
 template <class XT, class RT, int VPT, int S, int CLUSTER, bool ONE, bool EVEN, bool DROP, class P>
 __global__ void __launch_bounds__(512) block_norm_row_backward_kernel(const __grid_constant__ P p) {

@@ -373,8 +373,8 @@ struct TopList {
 // units' loads a warp are under way, 32 warps an SM.  With the entropy an element
 // costs a multiply-add and a power of two, two sums and its unpacking: 8 warp
 // instructions for 32 of them, 0.67 of the issue slots.
-//   4096 x 128256 bf16 in 8 shards                153.5 us, 1.01 of a copy's rate; with the entropy 163.4, 0.95
-//   64 x 128256 fp32, 5 alternatives               12.7 us: the pass is half of it, then the alternatives' steps
+//   4096 x 128256 bf16 in 8 shards                153.5 us, 1.01 of a copy's rate; with the entropy 163.0, 0.95
+//   64 x 128256 fp32, 5 alternatives               12.8 us: the pass is half of it, then the alternatives' steps
 //   777 x 50257 bf16, 10 alternatives              20.2 us, 0.57: the same
 //   1 x 128256 bf16, 20 alternatives, entropy       8.7 us: 2 units a warp, then six meetings of the cluster or CTA
 // (With 3 CTAs an SM and more registers: 175.7 us with the entropy, 19.1, 19.2 and 8.3.)
@@ -624,6 +624,9 @@ __global__ void __launch_bounds__(LP_THREADS, 4) log_probs_kernel(const __grid_c
   }
 }
 
+// l = scale z - lse is as exact as the fp32 lse that the caller has: beyond 2^24 its
+// last place is more than 1, and p = exp(l) off by a factor.
+//
 // A CTA takes a run of units of one token; bound by HBM (4096 x 128256 bf16 in 8
 // shards, a tenth of the rows without gradient and not read: 292 us, 1.00 of a
 // copy's rate; with the entropy's 312; 301 x 50257 fp32 20.5, 0.87).  The given
